@@ -12,11 +12,13 @@ import ctypes as C
 
 from . import _lib
 from ._lib import (ATTN_BF16, ATTN_CAUSAL_BOTTOM_RIGHT, ATTN_CAUSAL_TOP_LEFT, ATTN_DQ_ATOMIC, ATTN_DQ_ORDERED,
-                   ATTN_DQ_SPLIT, ATTN_F16, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t, attn_sdpa_desc_t, attn_view_t, check)
+                   ATTN_DQ_SPLIT, ATTN_F16, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t, attn_qk_norm_desc_t,
+                   attn_sdpa_desc_t, attn_view_t, check)
 
 __all__ = ["sdpa_desc", "nsa_desc", "view_bhsd", "view_tnd", "sdpa_workspace_size", "sdpa_fwd_stats",
            "sdpa_bwd", "nsa_workspace_size", "nsa_selected_attn_bwd", "nsa_block_lists",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd",
+           "qk_norm_rope_desc", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
            "attn_query_status", "AttnError", "ATTN_F16", "ATTN_BF16", "ATTN_MASK_NONE",
            "ATTN_CAUSAL_TOP_LEFT", "ATTN_CAUSAL_BOTTOM_RIGHT"]
 
@@ -212,6 +214,138 @@ def nsa_block_lists(desc, topk, offsets, tokens, *, workspace=None, stream=None)
                                      C.c_void_p(_stream_ptr(stream)))
     check(st, "nsa_block_lists")
     return nblk.value, ws
+
+
+class _Call:
+    """One call on CUDA tensors that all live on one device: checks them, makes that device current for
+    the call, and holds the stream and workspace it runs with.  A workspace made here for a stream other
+    than the current one is recorded on it, so its memory is not reused before the call is done."""
+
+    def __init__(self, where, dtype, device, stream):
+        torch = _torch()
+        self.where, self.dtype, self.device = where, torch.float16 if dtype == ATTN_F16 else torch.bfloat16, device
+        if device.type != "cuda":
+            raise ValueError(f"{where}: CUDA tensors expected, got {device}")
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        if self.stream.device != device:
+            raise ValueError(f"{where}: tensors on {device}, stream on {self.stream.device}")
+
+    def tensor(self, name, t, dtype, shape, contiguous=True):
+        if t.dtype != dtype or tuple(t.shape) != shape or t.device != self.device:
+            raise ValueError(f"{self.where}: {name} must be {dtype} {shape} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{self.where}: {name} must be contiguous")
+        return t
+
+    def ptr(self, name, t, dtype, shape):
+        """Address of a contiguous tensor (None stays None: a NULL pointer)."""
+        return None if t is None else self.tensor(name, t, dtype, shape).data_ptr()
+
+    def view(self, name, x, shape):
+        """x: an attn_view_t, or a [B, H, S, D] tensor of this shape."""
+        return x if isinstance(x, attn_view_t) else view_bhsd(self.tensor(name, x, self.dtype, shape, False))
+
+    def workspace(self, nbytes, workspace):
+        torch = _torch()
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            if self.stream != torch.cuda.current_stream(self.device):
+                workspace.record_stream(self.stream)
+        elif workspace.device != self.device:
+            raise ValueError(f"{self.where}: workspace on {workspace.device}, tensors on {self.device}")
+        return workspace
+
+    def run(self, fn, *args):
+        torch = _torch()
+        if torch.cuda.current_device() == self.device.index:
+            st = fn(*args, self.stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, self.stream.cuda_stream)
+        if st:
+            check(st, self.where)
+
+
+def qk_norm_rope_desc(*, dtype, b, s, h, h_kv, d, rotary_dim=0, interleaved=False, eps=1e-6, weight_fp32=False,
+                      max_pos=0):
+    """An attn_qk_norm_desc_t: b sequences of s tokens (packed tensors: b = 1, s = all tokens), h query and
+    h_kv key heads of dim d (64, 128 or 192).  The first rotary_dim elements of a head (a multiple of 16;
+    0: none) are rotated in pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved, by the rows
+    of cos / sin tables of max_pos rows.  weight_fp32: the norm weights are fp32 (else dtype)."""
+    return attn_qk_norm_desc_t(int(dtype), int(b), int(s), int(h), int(h_kv), int(d), int(rotary_dim),
+                               int(bool(interleaved)), float(eps), int(bool(weight_fp32)), int(max_pos))
+
+
+def qk_norm_rope_workspace_size(desc):
+    """(forward bytes, backward bytes) of device workspace for this descriptor (host only)."""
+    fwd, bwd = C.c_size_t(), C.c_size_t()
+    check(_lib.load().qk_norm_rope_workspace_size(C.byref(desc), C.byref(fwd), C.byref(bwd)),
+          "qk_norm_rope_workspace_size")
+    return fwd.value, bwd.value
+
+
+_NO_VIEW = attn_view_t(None, 0, 0, 0)
+
+
+def _qk_sides(call, desc, named):
+    """Views of (name, query tensor, key tensor) triples; a side without heads has none."""
+    out = []
+    for name, q, k in named:
+        for x, h, n in ((q, desc.h, "q"), (k, desc.h_kv, "k")):
+            out.append(call.view(name % n, x, (desc.b, h, desc.s, desc.d)) if h else _NO_VIEW)
+    return out
+
+
+def _qk_tables(call, desc, q_weight, k_weight, cos, sin, positions):
+    torch = _torch()
+    wt = torch.float32 if desc.weight_fp32 else call.dtype
+    out = [call.ptr(n, w, wt, (desc.d,)) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
+    if not desc.rotary_dim:
+        return out + [None, None, None]
+    shape = (desc.max_pos, desc.rotary_dim // 2)
+    return out + [call.ptr("cos", cos, torch.float32, shape), call.ptr("sin", sin, torch.float32, shape),
+                  call.ptr("positions", positions, torch.int32, (desc.b, desc.s))]
+
+
+def _qk_device(q, k, cos, q_weight, workspace):
+    for t in (q, k, cos, q_weight, workspace):
+        if t is not None and not isinstance(t, attn_view_t):
+            return t.device
+    return _torch().device("cuda", _torch().cuda.current_device())
+
+
+def qk_norm_rope_fwd(desc, q, k, q_weight, k_weight, cos, sin, q_out, k_out, *, positions=None, workspace=None,
+                     stream=None):
+    """RMS norm of every query and key head with the rotary position embedding in the same pass: q, q_out
+    [B, h, S, D], k, k_out [B, h_kv, S, D] (tensors of any strides with a unit innermost one, or
+    attn_view_t views; an output may be its input), weights [D] or None, cos / sin fp32 [max_pos,
+    rotary_dim / 2], positions int32 [B, S] (None: a token's index in its sequence).  Asynchronous on
+    `stream`; returns the workspace, for attn_query_status (positions out of range)."""
+    call = _Call("qk_norm_rope_fwd", desc.dtype, _qk_device(q, k, cos, q_weight, workspace), stream)
+    ws = call.workspace(256, workspace)
+    views = _qk_sides(call, desc, (("%s", q, k), ("%s_out", q_out, k_out)))
+    tables = _qk_tables(call, desc, q_weight, k_weight, cos, sin, positions)
+    call.run(_lib.load().qk_norm_rope_fwd, C.byref(desc), *views[:2], *tables, *views[2:], ws.data_ptr(), ws.numel())
+    return ws
+
+
+def qk_norm_rope_bwd(desc, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, dq, dk, dq_weight=None, dk_weight=None,
+                     *, positions=None, workspace=None, stream=None):
+    """Gradients of qk_norm_rope_fwd: dq, dk (which may be dq_out, dk_out) and the weights' fp32 [D]
+    gradients (None: not wanted) from the call's inputs and the gradients dq_out, dk_out of its outputs,
+    as sdpa_bwd returns them.  Bitwise reproducible.  Asynchronous on `stream`; returns the workspace."""
+    torch = _torch()
+    call = _Call("qk_norm_rope_bwd", desc.dtype, _qk_device(q, k, cos, q_weight, workspace), stream)
+    ws = workspace
+    if ws is None:
+        ws = call.workspace(qk_norm_rope_workspace_size(desc)[1], None)
+    views = _qk_sides(call, desc, (("%s", q, k), ("d%s_out", dq_out, dk_out), ("d%s", dq, dk)))
+    tables = _qk_tables(call, desc, q_weight, k_weight, cos, sin, positions)
+    dws = [call.ptr(n, t, torch.float32, (desc.d,)) for n, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight))]
+    call.run(_lib.load().qk_norm_rope_bwd, C.byref(desc), *views[:4], *tables, *views[4:], *dws, ws.data_ptr(),
+             ws.numel())
+    return ws
 
 
 def attn_query_status(workspace, stream=None):

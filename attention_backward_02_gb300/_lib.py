@@ -25,7 +25,8 @@ EXPORTS = ("sdpa_workspace_size", "sdpa_fwd_stats", "sdpa_bwd", "nsa_workspace_s
            "nsa_selected_attn_bwd", "nsa_block_lists", "attn_query_status", "attn_status_string",
            "attn_set_main_kernel_events", "sdpa_bwd_static_scratch", "attn_static_scratch_status",
            "attn_selftest_wait_timeout", "attn_selftest_occupy", "attn_last_error",
-           "nsa_fwd_workspace_size", "nsa_selected_attn_fwd")
+           "nsa_fwd_workspace_size", "nsa_selected_attn_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd",
+           "qk_norm_rope_bwd")
 
 
 class attn_view_t(C.Structure):
@@ -48,6 +49,12 @@ class attn_nsa_desc_t(C.Structure):
                 ("mask_rows", C.c_int64), ("mask_cols", C.c_int64)]
 
 
+class attn_qk_norm_desc_t(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("b", C.c_int64), ("s", C.c_int64), ("h", C.c_int64), ("h_kv", C.c_int64),
+                ("d", C.c_int64), ("rotary_dim", C.c_int64), ("interleaved", C.c_int), ("eps", C.c_double),
+                ("weight_fp32", C.c_int), ("max_pos", C.c_int64)]
+
+
 _lib = None
 
 
@@ -62,6 +69,7 @@ def load() -> C.CDLL:
     lib = C.CDLL(LIB_PATH)
     P, V, S, I = C.POINTER, C.c_void_p, C.c_size_t, C.c_int
     D, N, view = P(attn_sdpa_desc_t), P(attn_nsa_desc_t), attn_view_t
+    K = P(attn_qk_norm_desc_t)
     sig = {
         "sdpa_workspace_size": [D, P(S), P(S)],
         "sdpa_fwd_stats": [D, view, view, view, view, P(C.c_float), V, S, V],
@@ -79,6 +87,9 @@ def load() -> C.CDLL:
         "attn_static_scratch_status": [V, P(C.c_uint32)],
         "attn_selftest_wait_timeout": [V, S, C.c_double, V],
         "attn_selftest_occupy": [I, S, C.c_double, V],
+        "qk_norm_rope_workspace_size": [K, P(S), P(S)],
+        "qk_norm_rope_fwd": [K, view, view, V, V, V, V, V, view, view, V, S, V],
+        "qk_norm_rope_bwd": [K, view, view, view, view, V, V, V, V, V, view, view, V, V, V, S, V],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

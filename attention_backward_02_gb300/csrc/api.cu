@@ -10,6 +10,7 @@
 
 #include "attnbwd.h"
 #include "plan.h"
+#include "qk_norm.h"
 
 using namespace attn;
 
@@ -597,6 +598,105 @@ attn_status_t nsa_block_lists(const attn_nsa_desc_t *desc, const int32_t *topk, 
         pg.cu_kv[b + 1] = desc->cu_seqlens_kv[b];
     }
     return cuda_status(launch_nsa_block_lists(a, pg, static_cast<cudaStream_t>(stream)));
+}
+
+// --------------------------------------------------- query / key norm and rotation
+
+namespace {
+
+attn_status_t check_qk_desc(const attn_qk_norm_desc_t *d)
+{
+    if (!d) return ATTN_ERR_NULLPTR;
+    if (d->dtype != ATTN_F16 && d->dtype != ATTN_BF16) return ATTN_ERR_INVALID;
+    if (d->b < 1 || d->s < 0 || d->h < 0 || d->h_kv < 0 || d->h + d->h_kv < 1) return ATTN_ERR_INVALID;
+    if (d->rotary_dim < 0 || d->rotary_dim > d->d) return ATTN_ERR_INVALID;
+    if ((d->interleaved != 0 && d->interleaved != 1) || (d->weight_fp32 != 0 && d->weight_fp32 != 1))
+        return ATTN_ERR_INVALID;
+    if (!std::isfinite(d->eps) || !(float(d->eps) > 0.f)) return ATTN_ERR_INVALID;
+    if (d->rotary_dim > 0 && (d->max_pos < 1 || d->max_pos > INT32_MAX)) return ATTN_ERR_INVALID;
+    if (d->d != 64 && d->d != 128 && d->d != 192) return ATTN_ERR_UNSUPPORTED;
+    if (d->rotary_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    // 32-bit work item indices inside the kernels
+    const int64_t lim = int64_t(1) << 31;
+    if (d->h >= lim || d->h_kv >= lim || d->b >= lim || d->s >= lim || d->b * d->s >= lim) return ATTN_ERR_UNSUPPORTED;
+    const int64_t hmax = d->h > d->h_kv ? d->h : d->h_kv;
+    if (d->s > 0 && d->b * d->s > (lim - 1) / hmax) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+size_t qk_part_offset() { return Workspace::align(64 * sizeof(uint32_t)); }
+size_t qk_bwd_bytes(const attn_qk_norm_desc_t *d)
+{
+    return qk_part_offset() + Workspace::align(size_t(kQkBlocks + 2) * size_t(d->d) * sizeof(float));
+}
+
+attn_status_t qk_norm_call(const attn_qk_norm_desc_t *d, bool backward, attn_view_t q, attn_view_t k, attn_view_t dyq,
+                           attn_view_t dyk, const void *wq, const void *wk, const float *cos, const float *sin,
+                           const int32_t *positions, attn_view_t yq, attn_view_t yk, float *dwq, float *dwk,
+                           void *workspace, size_t workspace_bytes, void *stream)
+{
+    attn_status_t st = check_qk_desc(d);
+    if (st) return st;
+    const int64_t rows_q = d->b * d->s * d->h, rows_k = d->b * d->s * d->h_kv;
+    if ((st = check_view(q, rows_q)) || (st = check_view(k, rows_k)) || (st = check_view(yq, rows_q)) ||
+        (st = check_view(yk, rows_k)))
+        return st;
+    if (backward && ((st = check_view(dyq, rows_q)) || (st = check_view(dyk, rows_k)))) return st;
+    if (d->rotary_dim > 0 && d->s > 0) {
+        if (!cos || !sin) return ATTN_ERR_NULLPTR;
+        if (!aligned16(cos) || !aligned16(sin) || (reinterpret_cast<uintptr_t>(positions) & 3)) return ATTN_ERR_ALIGN;
+    }
+    if ((d->h && !aligned16(wq)) || (d->h_kv && !aligned16(wk))) return ATTN_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(dwq) & 3) || (reinterpret_cast<uintptr_t>(dwk) & 3)) return ATTN_ERR_ALIGN;
+    if ((st = check_ws(workspace, workspace_bytes, backward ? qk_bwd_bytes(d) : qk_part_offset()))) return st;
+    QkNormArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.dtype = d->dtype; a.weight_fp32 = d->weight_fp32; a.interleaved = d->interleaved;
+    a.b = d->b; a.s = d->s; a.d = d->d; a.rot = d->rotary_dim; a.max_pos = d->max_pos;
+    a.eps = float(d->eps);
+    a.cos = cos; a.sin = sin; a.pos = positions;
+    char *ws = static_cast<char *>(workspace);
+    a.status = reinterpret_cast<uint32_t *>(ws);
+    QkSide &sq = a.side[0], &sk = a.side[1];
+    sq.x = to_view(q, false); sq.dy = to_view(dyq, false); sq.y = to_view(yq, false);
+    sk.x = to_view(k, false); sk.dy = to_view(dyk, false); sk.y = to_view(yk, false);
+    sq.w = wq; sk.w = wk;
+    sq.h = d->h; sk.h = d->h_kv;
+    sq.dw = d->h ? dwq : nullptr; sk.dw = d->h_kv ? dwk : nullptr;
+    // the query side's shares first, the key side's behind them (split when the blocks are dealt)
+    sq.part = sk.part = reinterpret_cast<float *>(ws + qk_part_offset());
+    return cuda_status(launch_qk_norm(a, backward, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+attn_status_t qk_norm_rope_workspace_size(const attn_qk_norm_desc_t *desc, size_t *fwd_bytes, size_t *bwd_bytes)
+{
+    const attn_status_t st = check_qk_desc(desc);
+    if (st) return st;
+    if (fwd_bytes) *fwd_bytes = qk_part_offset();
+    if (bwd_bytes) *bwd_bytes = qk_bwd_bytes(desc);
+    return ATTN_OK;
+}
+
+attn_status_t qk_norm_rope_fwd(const attn_qk_norm_desc_t *desc, attn_view_t q, attn_view_t k, const void *q_weight,
+                               const void *k_weight, const float *cos, const float *sin, const int32_t *positions,
+                               attn_view_t q_out, attn_view_t k_out, void *workspace, size_t workspace_bytes,
+                               void *stream)
+{
+    const attn_view_t none = {nullptr, 0, 0, 0};
+    return qk_norm_call(desc, false, q, k, none, none, q_weight, k_weight, cos, sin, positions, q_out, k_out, nullptr,
+                        nullptr, workspace, workspace_bytes, stream);
+}
+
+attn_status_t qk_norm_rope_bwd(const attn_qk_norm_desc_t *desc, attn_view_t q, attn_view_t k, attn_view_t dq_out,
+                               attn_view_t dk_out, const void *q_weight, const void *k_weight, const float *cos,
+                               const float *sin, const int32_t *positions, attn_view_t dq, attn_view_t dk,
+                               float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
+                               void *stream)
+{
+    return qk_norm_call(desc, true, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions, dq, dk, dq_weight,
+                        dk_weight, workspace, workspace_bytes, stream);
 }
 
 attn_status_t attn_set_main_kernel_events(void *before, void *after)

@@ -1,8 +1,8 @@
 /*
  * attnbwd.h -- C ABI of the GB300 (sm_103a) attention-backward library.
  *
- * Three computations, each a stateless, asynchronous call on the caller's
- * CUDA stream (passed as void*; NULL is the legacy default stream):
+ * Stateless, asynchronous calls on the caller's CUDA stream (passed as
+ * void*; NULL is the legacy default stream):
  *
  *   sdpa_fwd_stats          O and the fp32 log-sum-exp stats of scaled dot
  *                           product attention (training-mode forward).
@@ -11,6 +11,10 @@
  *   nsa_selected_attn_bwd   dQ, dK, dV of NSA selected attention, where every
  *                           query token attends to selectedBlockCount blocks of
  *                           selectedBlockSize keys chosen by int32 topkIndices.
+ *   qk_norm_rope_fwd, _bwd  RMS norm of every query / key head with the rotary
+ *                           position embedding in the same pass, and its gradient:
+ *                           what makes Q and K for the calls above and takes their
+ *                           dQ and dK.
  *
  * Definitions.  With s_ij = scale * q_i . k_j over the visible keys,
  *   LSE_i = log sum_j exp(s_ij),  P_ij = exp(s_ij - LSE_i),  O_i = sum_j P_ij v_j,
@@ -70,7 +74,8 @@ typedef enum {
 
 /* Bits of the device status word (attn_query_status).                        */
 #define ATTN_DEV_TIMEOUT      0x1u  /* a bounded barrier wait ran out; the CTA quit */
-#define ATTN_DEV_INDEX_RANGE  0x2u  /* a topk index outside [0, S2_b / block_size)   */
+#define ATTN_DEV_INDEX_RANGE  0x2u  /* a topk index outside [0, S2_b / block_size), or a
+                                       position outside [0, max_pos)                 */
 #define ATTN_DEV_INDEX_DUP    0x4u  /* a block listed twice for one (token, kv head) */
 
 typedef enum { ATTN_F16 = 0, ATTN_BF16 = 1 } attn_dtype_t;
@@ -289,6 +294,60 @@ attn_status_t nsa_selected_attn_bwd(const attn_nsa_desc_t *desc, const void *q, 
 attn_status_t nsa_block_lists(const attn_nsa_desc_t *desc, const int32_t *topk, int32_t *offsets,
                               int32_t *tokens, int64_t *nblk_max_out, void *workspace, size_t workspace_bytes,
                               void *stream);
+
+/* Norm and rotation of the query and key heads.  Like the relative-bias calls,
+ * these have no counterpart on the pages: they are what a model runs between
+ * its projections and the attention. */
+typedef struct {
+    attn_dtype_t dtype;     /* q, k, their outputs and gradients               */
+    int64_t b, s;           /* sequences and tokens of each; packed (TND)
+                               tensors: b = 1, s = all tokens, with positions   */
+    int64_t h, h_kv;        /* query / key heads; one of them may be 0: that
+                               side's pointers are then ignored                 */
+    int64_t d;              /* head dim: 64, 128 or 192                         */
+    int64_t rotary_dim;     /* leading elements of a head that are rotated: a
+                               multiple of 16 up to d; 0: norm only             */
+    int interleaved;        /* pairs are (2i, 2i + 1) when 1, (i, i + rotary_dim
+                               / 2) when 0                                      */
+    double eps;             /* added to the mean square; > 0 in fp32            */
+    int weight_fp32;        /* q_weight, k_weight are fp32 when 1, dtype when 0 */
+    int64_t max_pos;        /* rows of cos and sin (ignored with rotary_dim 0)  */
+} attn_qk_norm_desc_t;
+
+/* Workspace bytes of the two calls below.  Either pointer may be NULL.  Host
+ * only; no CUDA call.                                                       */
+attn_status_t qk_norm_rope_workspace_size(const attn_qk_norm_desc_t *desc, size_t *fwd_bytes, size_t *bwd_bytes);
+
+/* For every token and head, with x the head's d elements:
+ *   z = weight * x * r,  r = 1 / sqrt(mean(x^2) + eps),
+ *   y = z with each pair (a, b) of its first rotary_dim elements turned by the
+ *       token's angle: (a cos - b sin, b cos + a sin),
+ * computed in fp32 and rounded once.  q, q_out: [b,h,s,d] views; k, k_out:
+ * [b,h_kv,s,d]; an output view may be its input view (in place), and must not
+ * overlap it otherwise.  q_weight, k_weight: [d], shared by the heads (NULL:
+ * ones).  cos, sin: fp32 [max_pos][rotary_dim / 2], 16-byte aligned;
+ * positions: int32 [b][s] rows of them (NULL: a token's index in its
+ * sequence).  A token whose position is outside [0, max_pos) gets zero
+ * outputs and sets ATTN_DEV_INDEX_RANGE.                                    */
+attn_status_t qk_norm_rope_fwd(const attn_qk_norm_desc_t *desc, attn_view_t q, attn_view_t k, const void *q_weight,
+                               const void *k_weight, const float *cos, const float *sin, const int32_t *positions,
+                               attn_view_t q_out, attn_view_t k_out, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Gradients of the call above from its inputs and the gradients dq_out,
+ * dk_out of its outputs (sdpa_bwd's dQ and dK), with xh = x r and dz = dy
+ * turned back by the token's angle:
+ *   dweight = sum over tokens and heads of dz * xh,
+ *   dx = r (g - xh mean(g * xh)),  g = dz * weight.
+ * dq, dk may be the views of dq_out, dk_out (in place).  dq_weight, dk_weight:
+ * fp32 [d], or NULL when not wanted; summed in a fixed order, so the call is
+ * bitwise reproducible.  A token whose position is out of range gets zero
+ * gradients and adds nothing to the weights'.                              */
+attn_status_t qk_norm_rope_bwd(const attn_qk_norm_desc_t *desc, attn_view_t q, attn_view_t k, attn_view_t dq_out,
+                               attn_view_t dk_out, const void *q_weight, const void *k_weight, const float *cos,
+                               const float *sin, const int32_t *positions, attn_view_t dq, attn_view_t dk,
+                               float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
+                               void *stream);
 
 /* Waits for the stream, then reads the device status word of a workspace a
  * previous call used (bits ATTN_DEV_*; 0 when clean) and clears it.
