@@ -9,17 +9,20 @@ CUDA kernels.
 from __future__ import annotations
 
 import ctypes as C
+import math
 
 from . import _lib
 from ._lib import (ATTN_BF16, ATTN_CAUSAL_BOTTOM_RIGHT, ATTN_CAUSAL_TOP_LEFT, ATTN_DQ_ATOMIC, ATTN_DQ_ORDERED,
-                   ATTN_DQ_SPLIT, ATTN_F16, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t, attn_qk_norm_desc_t,
-                   attn_sdpa_desc_t, attn_view_t, check)
+                   ATTN_DQ_SPLIT, ATTN_F16, ATTN_F32, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t, attn_qk_norm_desc_t,
+                   attn_relbias_t, attn_sdpa_desc_t, attn_view_t, check)
 
 __all__ = ["sdpa_desc", "nsa_desc", "view_bhsd", "view_tnd", "sdpa_workspace_size", "sdpa_fwd_stats",
            "sdpa_bwd", "nsa_workspace_size", "nsa_selected_attn_bwd", "nsa_block_lists",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd",
+           "relbias", "relbias_bucket", "sdpa_relbias_workspace_size", "sdpa_relbias_fwd_stats", "sdpa_relbias_bwd",
            "qk_norm_rope_desc", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
-           "attn_query_status", "AttnError", "ATTN_F16", "ATTN_BF16", "ATTN_MASK_NONE",
+           "attn_query_status", "AttnError", "ATTN_F16", "ATTN_BF16", "ATTN_F32",
+           "ATTN_MASK_NONE",
            "ATTN_CAUSAL_TOP_LEFT", "ATTN_CAUSAL_BOTTOM_RIGHT"]
 
 
@@ -265,6 +268,98 @@ class _Call:
                 st = fn(*args, self.stream.cuda_stream)
         if st:
             check(st, self.where)
+
+
+def relbias(table, *, max_distance=128, bidirectional=True):
+    """An attn_relbias_t: a learned relative position bias.  table [num_buckets, h] (fp32, fp16 or bf16; held by
+    the result): table[bucket(key position - query position), head] is added to the score.  Half of a
+    direction's buckets are exact distances, the rest grow to max_distance; bidirectional: keys after the
+    query have buckets of their own."""
+    torch = _torch()
+    types = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}
+    if table.dtype not in types or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("relbias: a contiguous [num_buckets, h] table of fp32, fp16 or bf16")
+    bias = attn_relbias_t(table.data_ptr(), types[table.dtype], int(table.shape[0]), int(max_distance),
+                          int(bool(bidirectional)))
+    bias.tensor = table
+    return bias
+
+
+def relbias_bucket(bias, delta):
+    """Bucket of a key `delta` positions after its query (host only)."""
+    n = C.c_int64()
+    check(_lib.load().attn_relbias_bucket(C.byref(bias), int(delta), C.byref(n)), "attn_relbias_bucket")
+    return n.value
+
+
+def sdpa_relbias_workspace_size(desc, bias):
+    """(forward bytes, backward bytes) of device workspace for this descriptor and bias (host only)."""
+    fwd, bwd = C.c_size_t(), C.c_size_t()
+    check(_lib.load().sdpa_relbias_workspace_size(C.byref(desc), C.byref(bias), C.byref(fwd), C.byref(bwd)),
+          "sdpa_relbias_workspace_size")
+    return fwd.value, bwd.value
+
+
+def _dense_shapes(desc):
+    """Shapes of the query-side and key-side tensors and of lse (None where packed views are expected)."""
+    if desc.cu_seqlens_q:
+        return None, None, None
+    return ((desc.b, desc.h, desc.s_q, desc.d), (desc.b, desc.h_kv, desc.s_kv, desc.d), (desc.b, desc.h, desc.s_q))
+
+
+def _packed_or(call, name, x, shape):
+    if shape is None and not isinstance(x, attn_view_t):
+        raise ValueError(f"{call.where}: {name}: packed tensors are passed as view_tnd views")
+    return call.view(name, x, shape)
+
+
+def _relbias_call(where, desc, bias, lse, stream):
+    call = _Call(where, desc.dtype, lse.device, stream)
+    if bias.tensor.shape[1] != desc.h or bias.tensor.device != lse.device:
+        raise ValueError(f"{where}: bias table {tuple(bias.tensor.shape)} on {bias.tensor.device}, {desc.h} heads on "
+                         f"{lse.device}")
+    return call
+
+
+def _lse_ptr(call, desc, lse, shape):
+    torch = _torch()
+    if shape is None:
+        shape = (desc.h, int(desc.cu_seqlens_q[desc.b - 1]))
+    if lse.dtype != torch.float32 or lse.numel() != math.prod(shape) or not lse.is_contiguous():
+        raise ValueError(f"{call.where}: lse must be contiguous fp32 of {shape}")
+    return lse.data_ptr()
+
+
+def sdpa_relbias_fwd_stats(desc, bias, q, k, v, o, lse, *, workspace=None, stream=None):
+    """sdpa_fwd_stats with a learned relative position bias (see relbias) in the scores.  q, k, v, o: views or
+    [B, H, S, D] tensors; lse: fp32 [B, h, S_q] (packed: [h, T_q]).  Returns the workspace."""
+    call = _relbias_call("sdpa_relbias_fwd_stats", desc, bias, lse, stream)
+    ws = workspace
+    if ws is None:
+        ws = call.workspace(sdpa_relbias_workspace_size(desc, bias)[0], None)
+    sq, sk, sl = _dense_shapes(desc)
+    views = [_packed_or(call, n, x, s) for n, x, s in (("q", q, sq), ("k", k, sk), ("v", v, sk), ("o", o, sq))]
+    call.run(_lib.load().sdpa_relbias_fwd_stats, C.byref(desc), C.byref(bias), *views, _lse_ptr(call, desc, lse, sl),
+             ws.data_ptr(), ws.numel())
+    return ws
+
+
+def sdpa_relbias_bwd(desc, bias, q, k, v, o, dO, lse, dQ, dK, dV, dtable, *, workspace=None, stream=None):
+    """sdpa_bwd with a learned relative position bias in the scores; also the gradient of the bias table,
+    dtable: fp32 [num_buckets, h], bitwise reproducible.  Returns the workspace."""
+    torch = _torch()
+    call = _relbias_call("sdpa_relbias_bwd", desc, bias, lse, stream)
+    ws = workspace
+    if ws is None:
+        ws = call.workspace(sdpa_relbias_workspace_size(desc, bias)[1], None)
+    sq, sk, sl = _dense_shapes(desc)
+    views = [_packed_or(call, n, x, s) for n, x, s in (
+        ("q", q, sq), ("k", k, sk), ("v", v, sk), ("o", o, sq), ("dO", dO, sq), ("dQ", dQ, sq), ("dK", dK, sk),
+        ("dV", dV, sk))]
+    dt = call.ptr("dtable", dtable, torch.float32, tuple(bias.tensor.shape))
+    call.run(_lib.load().sdpa_relbias_bwd, C.byref(desc), C.byref(bias), *views[:5], _lse_ptr(call, desc, lse, sl),
+             *views[5:], dt, ws.data_ptr(), ws.numel())
+    return ws
 
 
 def qk_norm_rope_desc(*, dtype, b, s, h, h_kv, d, rotary_dim=0, interleaved=False, eps=1e-6, weight_fp32=False,

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libattnbwd.so")
 ATTN_OK, ATTN_ERR_NULLPTR, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED = 0, 1, 2, 3
 ATTN_ERR_WORKSPACE, ATTN_ERR_ALIGN, ATTN_ERR_CUDA, ATTN_ERR_DEVICE = 4, 5, 6, 7
 ATTN_DEV_TIMEOUT, ATTN_DEV_INDEX_RANGE, ATTN_DEV_INDEX_DUP = 0x1, 0x2, 0x4
-ATTN_F16, ATTN_BF16 = 0, 1
+ATTN_F16, ATTN_BF16, ATTN_F32 = 0, 1, 2
 ATTN_MASK_NONE, ATTN_CAUSAL_TOP_LEFT, ATTN_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
 ATTN_DQ_ATOMIC, ATTN_DQ_SPLIT, ATTN_DQ_ORDERED = 0, 1, 2
 
@@ -26,7 +26,8 @@ EXPORTS = ("sdpa_workspace_size", "sdpa_fwd_stats", "sdpa_bwd", "nsa_workspace_s
            "attn_set_main_kernel_events", "sdpa_bwd_static_scratch", "attn_static_scratch_status",
            "attn_selftest_wait_timeout", "attn_selftest_occupy", "attn_last_error",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd",
-           "qk_norm_rope_bwd")
+           "qk_norm_rope_bwd", "attn_relbias_bucket", "sdpa_relbias_workspace_size", "sdpa_relbias_fwd_stats",
+           "sdpa_relbias_bwd")
 
 
 class attn_view_t(C.Structure):
@@ -55,6 +56,11 @@ class attn_qk_norm_desc_t(C.Structure):
                 ("weight_fp32", C.c_int), ("max_pos", C.c_int64)]
 
 
+class attn_relbias_t(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_type", C.c_int), ("num_buckets", C.c_int64),
+                ("max_distance", C.c_int64), ("bidirectional", C.c_int)]
+
+
 _lib = None
 
 
@@ -69,7 +75,7 @@ def load() -> C.CDLL:
     lib = C.CDLL(LIB_PATH)
     P, V, S, I = C.POINTER, C.c_void_p, C.c_size_t, C.c_int
     D, N, view = P(attn_sdpa_desc_t), P(attn_nsa_desc_t), attn_view_t
-    K = P(attn_qk_norm_desc_t)
+    K, R = P(attn_qk_norm_desc_t), P(attn_relbias_t)
     sig = {
         "sdpa_workspace_size": [D, P(S), P(S)],
         "sdpa_fwd_stats": [D, view, view, view, view, P(C.c_float), V, S, V],
@@ -87,6 +93,10 @@ def load() -> C.CDLL:
         "attn_static_scratch_status": [V, P(C.c_uint32)],
         "attn_selftest_wait_timeout": [V, S, C.c_double, V],
         "attn_selftest_occupy": [I, S, C.c_double, V],
+        "attn_relbias_bucket": [R, C.c_int64, P(C.c_int64)],
+        "sdpa_relbias_workspace_size": [D, R, P(S), P(S)],
+        "sdpa_relbias_fwd_stats": [D, R, view, view, view, view, V, V, S, V],
+        "sdpa_relbias_bwd": [D, R, view, view, view, view, view, V, view, view, view, V, V, S, V],
         "qk_norm_rope_workspace_size": [K, P(S), P(S)],
         "qk_norm_rope_fwd": [K, view, view, V, V, V, V, V, view, view, V, S, V],
         "qk_norm_rope_bwd": [K, view, view, view, view, V, V, V, V, V, view, view, V, V, V, S, V],

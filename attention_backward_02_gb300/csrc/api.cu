@@ -11,6 +11,7 @@
 #include "attnbwd.h"
 #include "plan.h"
 #include "qk_norm.h"
+#include "relbias.h"
 
 using namespace attn;
 
@@ -203,18 +204,118 @@ attn_status_t sdpa_workspace_size(const attn_sdpa_desc_t *desc, size_t *fwd_byte
     return ATTN_OK;
 }
 
-attn_status_t sdpa_fwd_stats(const attn_sdpa_desc_t *desc, attn_view_t q, attn_view_t k, attn_view_t v,
+}  // extern "C"
+
+namespace {
+
+// -------------------------------------------------- relative position bias
+
+// Whether distance x has reached step m of the buckets past the exact ones.  Borders that are whole numbers
+// belong to the bucket above: the logarithms' rounding is far below the 1e-9 that is allowed for it.
+bool rel_reached(const RelBias &r, double max_distance, int64_t x, int m)
+{
+    return std::log(double(x) / r.e) / std::log(max_distance / r.e) * (r.n - r.e) + 1e-9 >= double(m);
+}
+
+attn_status_t check_relbias(const attn_relbias_t *b, RelBias *r)
+{
+    if (!b) return ATTN_ERR_NULLPTR;
+    if (b->bidirectional != 0 && b->bidirectional != 1) return ATTN_ERR_INVALID;
+    if (b->table_type != ATTN_F16 && b->table_type != ATTN_BF16 && b->table_type != ATTN_F32) return ATTN_ERR_INVALID;
+    if (b->num_buckets < 2 || (b->bidirectional && (b->num_buckets < 4 || b->num_buckets % 2 != 0)))
+        return ATTN_ERR_INVALID;
+    const int64_t n = b->bidirectional ? b->num_buckets / 2 : b->num_buckets;
+    if (b->max_distance <= n / 2) return ATTN_ERR_INVALID;
+    if (b->num_buckets > kRelMaxBuckets || b->max_distance > kRelMaxDistance) return ATTN_ERR_UNSUPPORTED;
+    std::memset(r, 0, sizeof *r);
+    r->table = b->table;
+    r->table_type = b->table_type;
+    r->buckets = int(b->num_buckets);
+    r->n = int(n);
+    r->e = int(n / 2);
+    r->bidirectional = b->bidirectional;
+    r->nthr = r->n - r->e - 1;
+    const double far = double(b->max_distance);
+    for (int m = 1; m <= r->nthr; ++m) {  // the first distance of step m: a guess, then by the definition
+        int64_t x = int64_t(r->e * std::pow(far / r->e, double(m) / (r->n - r->e)));
+        if (x < r->e) x = r->e;
+        while (x > r->e && rel_reached(*r, far, x - 1, m)) --x;
+        while (!rel_reached(*r, far, x, m)) ++x;
+        r->thr[m - 1] = int32_t(x);
+    }
+    const int w = r->nthr ? r->thr[r->nthr - 1] : r->e;
+    r->lo = -w;
+    r->hi = r->bidirectional ? w : 0;
+    return ATTN_OK;
+}
+
+attn_status_t check_rel_table(const RelBias &r)
+{
+    if (!r.table) return ATTN_ERR_NULLPTR;
+    const uintptr_t size = r.table_type == ATTN_F32 ? 4 : 2;
+    return reinterpret_cast<uintptr_t>(r.table) & (size - 1) ? ATTN_ERR_ALIGN : ATTN_OK;
+}
+
+// Workspace of the calls with a bias, behind `base` bytes of the call without one: the expanded table and, for
+// the backward, its bucket codes and the shares of the table's gradient.
+struct RelLayout {
+    size_t rel, code, part, total;
+};
+
+RelLayout rel_layout(const attn_sdpa_desc_t *d, const DenseShape &sh, const RelBias &r, size_t base, bool backward)
+{
+    RelLayout L;
+    const size_t line = size_t(rel_stride(r));
+    L.rel = base;
+    L.code = L.rel + Workspace::align(size_t(d->h) * line * sizeof(float));
+    L.part = L.code + (backward ? Workspace::align(line * sizeof(uint32_t)) : 0);
+    const size_t rows = size_t(sh.t_kv / 128 + d->b + 1);
+    L.total = L.part + (backward ? Workspace::align(rows * size_t(d->h) * 8 * size_t(r.buckets) * sizeof(float)) : 0);
+    return L;
+}
+
+void fill_rel(RelArgs *a, const attn_sdpa_desc_t *d, const DenseShape &sh, const RelBias &r, const RelLayout &L, void *workspace,
+              bool backward, float *dtable)
+{
+    std::memset(a, 0, sizeof *a);
+    char *ws = static_cast<char *>(workspace);
+    a->b = r;
+    a->h = d->h;
+    a->rel = reinterpret_cast<float *>(ws + L.rel);
+    a->stride = rel_stride(r);
+    a->status = reinterpret_cast<uint32_t *>(ws);
+    if (backward) {
+        a->code = reinterpret_cast<uint32_t *>(ws + L.code);
+        a->part = reinterpret_cast<float *>(ws + L.part);
+        a->part_rows = sh.t_kv / 128 + d->b + 1;
+        a->dtable = dtable;
+    }
+}
+
+// 32-bit entries of the expanded table inside the kernels, and the grid of the small ones
+attn_status_t check_rel_heads(const attn_sdpa_desc_t *d) { return d->h > 65535 ? ATTN_ERR_UNSUPPORTED : ATTN_OK; }
+
+// sdpa_fwd_stats (bias NULL) and sdpa_relbias_fwd_stats
+attn_status_t dense_fwd_call(const attn_sdpa_desc_t *desc, const RelBias *bias, attn_view_t q, attn_view_t k, attn_view_t v,
                              attn_view_t o, float *lse, void *workspace, size_t workspace_bytes, void *stream)
 {
     DenseShape sh;
     attn_status_t st = check_dense_desc(desc, &sh);
     if (st) return st;
+    if (bias && ((st = check_rel_heads(desc)) || (st = check_rel_table(*bias)))) return st;
     if ((st = check_view(q, sh.t_q)) || (st = check_view(o, sh.t_q)) || (st = check_view(k, sh.t_kv)) ||
         (st = check_view(v, sh.t_kv)))
         return st;
     if (sh.t_q && !lse) return ATTN_ERR_NULLPTR;
-    if ((st = check_ws(workspace, workspace_bytes, Workspace::align(64 * sizeof(uint32_t))))) return st;
-    if (sh.t_q == 0) return ATTN_OK;
+    size_t need = Workspace::align(64 * sizeof(uint32_t));
+    RelLayout RL = {};
+    if (bias) {
+        RL = rel_layout(desc, sh, *bias, need, false);
+        need = RL.total;
+    }
+    if ((st = check_ws(workspace, workspace_bytes, need))) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (sh.t_q == 0) return bias ? cuda_status(cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s)) : ATTN_OK;
 
     DenseArgs a;
     std::memset(&a, 0, sizeof a);
@@ -228,20 +329,31 @@ attn_status_t sdpa_fwd_stats(const attn_sdpa_desc_t *desc, attn_view_t q, attn_v
     a.o = to_view(o, sh.packed);
     a.lse_out = lse;
     a.status = static_cast<uint32_t *>(workspace);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     FixedGeo fg;
     static thread_local PackedGeo pg;
     fill_geo(desc, sh, &fg, &pg);
-    return cuda_status(sh.packed ? launch_dense_fwd(a, pg, s) : launch_dense_fwd(a, fg, s));
+    RelArgs rel;
+    if (bias) {
+        fill_rel(&rel, desc, sh, *bias, RL, workspace, false, nullptr);
+        if ((st = cuda_status(launch_rel_expand(rel, s)))) return st;
+    }
+    const RelArgs *rp = bias ? &rel : nullptr;
+    return cuda_status(sh.packed ? launch_dense_fwd(a, pg, s, rp) : launch_dense_fwd(a, fg, s, rp));
 }
 
-attn_status_t sdpa_bwd(const attn_sdpa_desc_t *desc, attn_view_t q, attn_view_t k, attn_view_t v, attn_view_t o,
-                       attn_view_t dO, const float *lse, attn_view_t dQ, attn_view_t dK, attn_view_t dV,
-                       void *workspace, size_t workspace_bytes, void *stream)
+// sdpa_bwd (bias NULL) and sdpa_relbias_bwd
+attn_status_t dense_bwd_call(const attn_sdpa_desc_t *desc, const RelBias *bias, attn_view_t q, attn_view_t k, attn_view_t v,
+                             attn_view_t o, attn_view_t dO, const float *lse, attn_view_t dQ, attn_view_t dK,
+                             attn_view_t dV, float *dtable, void *workspace, size_t workspace_bytes, void *stream)
 {
     DenseShape sh;
     attn_status_t st = check_dense_desc(desc, &sh);
     if (st) return st;
+    if (bias) {
+        if ((st = check_rel_heads(desc)) || (st = check_rel_table(*bias))) return st;
+        if (!dtable) return ATTN_ERR_NULLPTR;
+        if (reinterpret_cast<uintptr_t>(dtable) & 3) return ATTN_ERR_ALIGN;
+    }
     if ((st = check_view(q, sh.t_q)) || (st = check_view(o, sh.t_q)) || (st = check_view(dO, sh.t_q)) ||
         (st = check_view(dQ, sh.t_q)) || (st = check_view(k, sh.t_kv)) || (st = check_view(v, sh.t_kv)) ||
         (st = check_view(dK, sh.t_kv)) || (st = check_view(dV, sh.t_kv)))
@@ -261,7 +373,9 @@ attn_status_t sdpa_bwd(const attn_sdpa_desc_t *desc, attn_view_t q, attn_view_t 
         }
         if ((max_kv + 127) / 128 * desc->b * desc->h_kv > kOrderedMaxUnits) return ATTN_ERR_UNSUPPORTED;
     }
-    if ((st = check_ws(workspace, workspace_bytes, L.total))) return st;
+    RelLayout RL = {};
+    if (bias) RL = rel_layout(desc, sh, *bias, L.total, true);
+    if ((st = check_ws(workspace, workspace_bytes, bias ? RL.total : L.total))) return st;
 
     DenseArgs a;
     std::memset(&a, 0, sizeof a);
@@ -286,26 +400,95 @@ attn_status_t sdpa_bwd(const attn_sdpa_desc_t *desc, attn_view_t q, attn_view_t 
     a.sem = reinterpret_cast<uint32_t *>(ws + L.sem);
     a.sem_stride = L.t_pad / 64;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (sh.t_q == 0 && sh.t_kv == 0) return ATTN_OK;
+    if (sh.t_q == 0 && sh.t_kv == 0 && !bias) return ATTN_OK;
 
     FixedGeo fg;
     static thread_local PackedGeo pg;
     fill_geo(desc, sh, &fg, &pg);
+    RelArgs rel;
+    const RelArgs *rp = bias ? &rel : nullptr;
     cudaError_t e;
-    if (sh.packed) {
-        if ((e = launch_dense_preprocess(a, pg, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = launch_dense_bwd_main(a, pg, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = launch_dq_finalize(a, pg, s)) != cudaSuccess) return cuda_status(e);
-    } else {
-        if ((e = launch_dense_preprocess(a, fg, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = launch_dense_bwd_main(a, fg, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
-        if ((e = launch_dq_finalize(a, fg, s)) != cudaSuccess) return cuda_status(e);
+    if (bias) {
+        fill_rel(&rel, desc, sh, *bias, RL, workspace, true, dtable);
+        if ((e = launch_rel_expand(rel, s)) != cudaSuccess) return cuda_status(e);
     }
+    if (sh.t_q || sh.t_kv) {
+        if (sh.packed) {
+            if ((e = launch_dense_preprocess(a, pg, s)) != cudaSuccess) return cuda_status(e);
+            if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
+            if ((e = launch_dense_bwd_main(a, pg, s, rp)) != cudaSuccess) return cuda_status(e);
+            if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
+            if ((e = launch_dq_finalize(a, pg, s)) != cudaSuccess) return cuda_status(e);
+        } else {
+            if ((e = launch_dense_preprocess(a, fg, s)) != cudaSuccess) return cuda_status(e);
+            if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
+            if ((e = launch_dense_bwd_main(a, fg, s, rp)) != cudaSuccess) return cuda_status(e);
+            if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
+            if ((e = launch_dq_finalize(a, fg, s)) != cudaSuccess) return cuda_status(e);
+        }
+    }
+    return bias ? cuda_status(launch_rel_dtable(rel, s)) : ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t sdpa_fwd_stats(const attn_sdpa_desc_t *desc, attn_view_t q, attn_view_t k, attn_view_t v,
+                             attn_view_t o, float *lse, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return dense_fwd_call(desc, nullptr, q, k, v, o, lse, workspace, workspace_bytes, stream);
+}
+
+attn_status_t sdpa_bwd(const attn_sdpa_desc_t *desc, attn_view_t q, attn_view_t k, attn_view_t v, attn_view_t o,
+                       attn_view_t dO, const float *lse, attn_view_t dQ, attn_view_t dK, attn_view_t dV,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    return dense_bwd_call(desc, nullptr, q, k, v, o, dO, lse, dQ, dK, dV, nullptr, workspace, workspace_bytes, stream);
+}
+
+attn_status_t attn_relbias_bucket(const attn_relbias_t *bias, int64_t delta, int64_t *bucket)
+{
+    RelBias r;
+    const attn_status_t st = check_relbias(bias, &r);
+    if (st) return st;
+    if (!bucket) return ATTN_ERR_NULLPTR;
+    const int64_t far = int64_t(1) << 40;  // beyond any border
+    *bucket = r.bucket(delta < -far ? -far : (delta > far ? far : delta));
     return ATTN_OK;
+}
+
+attn_status_t sdpa_relbias_workspace_size(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, size_t *fwd_bytes,
+                                          size_t *bwd_bytes)
+{
+    DenseShape sh;
+    RelBias r;
+    attn_status_t st = check_dense_desc(desc, &sh);
+    if (st || (st = check_rel_heads(desc)) || (st = check_relbias(bias, &r))) return st;
+    if (fwd_bytes) *fwd_bytes = rel_layout(desc, sh, r, Workspace::align(64 * sizeof(uint32_t)), false).total;
+    if (bwd_bytes) *bwd_bytes = rel_layout(desc, sh, r, dense_layout(desc, sh).total, true).total;
+    return ATTN_OK;
+}
+
+attn_status_t sdpa_relbias_fwd_stats(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q,
+                                     attn_view_t k, attn_view_t v, attn_view_t o, float *lse, void *workspace,
+                                     size_t workspace_bytes, void *stream)
+{
+    RelBias r;
+    const attn_status_t st = check_relbias(bias, &r);
+    if (st) return st;
+    return dense_fwd_call(desc, &r, q, k, v, o, lse, workspace, workspace_bytes, stream);
+}
+
+attn_status_t sdpa_relbias_bwd(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q, attn_view_t k,
+                               attn_view_t v, attn_view_t o, attn_view_t dO, const float *lse, attn_view_t dQ,
+                               attn_view_t dK, attn_view_t dV, float *dtable, void *workspace, size_t workspace_bytes,
+                               void *stream)
+{
+    RelBias r;
+    const attn_status_t st = check_relbias(bias, &r);
+    if (st) return st;
+    return dense_bwd_call(desc, &r, q, k, v, o, dO, lse, dQ, dK, dV, dtable, workspace, workspace_bytes, stream);
 }
 
 // ------------------------------------------------------------------- NSA

@@ -49,6 +49,18 @@
 // rows past the sequence end are masked by row; query rows past it have
 // LSE = +inf in the workspace and so P = 0.
 //
+// Relative position bias (kBias): the bias of a tile is a window of the head's
+// expanded bias (log2 units), element (key row r, query column c) entry r - c +
+// const; the window rides in the Q / dO ring stage.  The gradient of the bias
+// table is the sum of dS over each bucket, taken from the fp32 dS before it is
+// rounded (P and dS are computed in fp32 for both types here): a tile in one end
+// bucket whole adds its dS to one register; otherwise a warp sums its 32 x 32
+// blocks along their diagonals, passing one running sum from lane to lane per
+// column, then adds runs of diagonals of one bucket and the runs to its own row of
+// buckets in shared memory.  Each warp stores its row once per (key tile, head);
+// a kernel behind this one adds them up in a fixed order, so the table's gradient
+// is bitwise reproducible in every dQ mode.
+//
 // Every barrier wait is bounded (about a second).  On a timeout the thread
 // sets ATTN_DEV_TIMEOUT in the status word and an abort flag in shared
 // memory; from then on every wait of the CTA fails fast and all work is
@@ -64,6 +76,7 @@
 #include <vector>
 
 #include "plan.h"
+#include "relbias.h"
 #include "sm103.cuh"
 #include "tc_util.cuh"
 
@@ -105,6 +118,15 @@ struct TcCfg {
     static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
     static constexpr int SMEM = OFF_MISC + 64;
     static constexpr int SMEM_ALLOC = SMEM + 1024;            // room to align the base to 1024
+    // kBias, behind the rest: the ring stages' windows of bias and bucket codes (the window's start is rounded
+    // down to 16 bytes), each P / dS warp's bucket sums, and its finished diagonals
+    static constexpr int WIN_BYTES = (BN + BM + 4) * 4;
+    static constexpr int OFF_WIN = SMEM;                      // NST x (bias, codes)
+    static constexpr int OFF_HIST = OFF_WIN + NST * 2 * WIN_BYTES;
+    static constexpr int OFF_DIAG = OFF_HIST + NSW * kRelMaxBuckets * 4;
+    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * 32 * 4 + 1024;
+    static_assert(WIN_BYTES % 16 == 0 && SMEM % 16 == 0 && SMEM_ALLOC_BIAS <= 227 * 1024, "shared memory budget");
+    static_assert(kRelPad >= BN + BM + 4, "a near tile's window lies within the expanded bias");
     static constexpr int T_S = 0, T_DP = BM, T_P = 2 * BM, T_DV = 2 * BM + BM / 2, T_DK = T_DV + D,
                          T_DQ = T_DK + D;
     static constexpr int T_COLS = 512;
@@ -130,6 +152,7 @@ struct TcParams {
     CUtensorMap tm_q, tm_k, tm_v, tm_do, tm_dq, tm_dk, tm_dv;
     DenseArgs a;
     TcSched sched;
+    RelArgs rel;  // kBias
 };
 
 using namespace tc;
@@ -167,8 +190,9 @@ template <> struct IsPacked<PackedGeo> : std::true_type {};
 }  // namespace
 
 // kOrdered: ordered dQ mode (one accumulator, each query tile's adds in a fixed order; needs the planned
-// unit order and a cooperative launch).  A template parameter, so the other modes carry none of its code.
-template <class T, int D, class Geo, bool kOrdered>
+// unit order and a cooperative launch).  kBias: a relative position bias in the scores, and its gradient.
+// Template parameters, so the other modes carry none of their code.
+template <class T, int D, class Geo, bool kOrdered, bool kBias>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
     dense_bwd_tc_kernel(const __grid_constant__ TcParams p, const Geo geo)
 {
@@ -288,9 +312,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     if (x == 1 && ok && !(ok = mbar_wait(&q_full[0], 0, abort))) flag_abort(abort, a.status);
                     if (!ok) return;
                     const int64_t hq = g * G + it / nq, i0 = int64_t(qt0 + it % nq) * BM;
+                    // relative bias: the tile's window, from its first delta on; of a tile in one end bucket
+                    // the table's first or last entries alone
+                    const int64_t dmin = j0 - i0 - (BM - 1) - (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0);
+                    const RelTile kind = kBias ? rel_tile(p.rel.b, dmin, BN + BM - 1) : kRelPast;
+                    const uint32_t win_bytes = !kBias ? 0u : (kind == kRelNear ? 2u * Cfg::WIN_BYTES : 16u);
                     uint8_t *sQ = smem + Cfg::OFF_Q + st * Cfg::Q_BYTES, *sdO = smem + Cfg::OFF_DO + st * Cfg::Q_BYTES;
                     q_armed = x + 1;
-                    mbar_arrive_expect_tx(&q_full[st], 2 * Cfg::Q_BYTES + 2 * BM * 4);
+                    mbar_arrive_expect_tx(&q_full[st], 2 * Cfg::Q_BYTES + 2 * BM * 4 + win_bytes);
                     for (int c = 0; c < D / 64; ++c) {
                         tma_load_4d(sQ + c * BM * 128, &p.tm_q, &q_full[st], c * 64, int(q_row0 + i0), int(hq), q_b);
                         tma_load_4d(sdO + c * BM * 128, &p.tm_do, &q_full[st], c * 64, int(q_row0 + i0), int(hq), q_b);
@@ -302,6 +331,15 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     }
                     bulk_load(smem + Cfg::OFF_LSE + st * BM * 4, a.lse2 + wrow, BM * 4, &q_full[st]);
                     bulk_load(smem + Cfg::OFF_DVEC + st * BM * 4, a.dvec + wrow, BM * 4, &q_full[st]);
+                    if (kBias) {
+                        const float *rel = p.rel.rel + hq * p.rel.stride;
+                        uint8_t *win = smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES;
+                        const int64_t w0 = kind == kRelNear ? (dmin - (p.rel.b.lo - kRelPad)) & ~int64_t(3)
+                                                            : (kind == kRelPast ? 0 : p.rel.stride - 4);
+                        bulk_load(win, rel + w0, kind == kRelNear ? Cfg::WIN_BYTES : 16, &q_full[st]);
+                        if (kind == kRelNear)
+                            bulk_load(win + Cfg::WIN_BYTES, p.rel.code + w0, Cfg::WIN_BYTES, &q_full[st]);
+                    }
                 };
                 // the first query tile does not need the key tile: load it before waiting for K / V
                 // (except on the very first tile, whose K / V load should start first)
@@ -490,6 +528,59 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             if (tc) tc_fence_after();
         };
 
+        // relative bias: this warp's bucket sums and finished diagonals, and the two end buckets' sums
+        float *hist = reinterpret_cast<float *>(smem + Cfg::OFF_HIST) + (warp - 2) * kRelMaxBuckets;
+        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_DIAG) + (warp - 2) * 32;
+        float sum_past = 0.f, sum_future = 0.f;
+        if (kBias) {
+            for (int n = lane; n < kRelMaxBuckets; n += 32) hist[n] = 0.f;
+            __syncwarp();
+        }
+        // adds v, the sum of one diagonal a lane (consecutive deltas), to the bucket sums: runs of one bucket are
+        // added up towards their first lane, whose bucket no other run has
+        auto add_runs = [&](float v, uint32_t code) {
+            const int rem = min(int(code >> 8 & 31u), 31 - lane);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float t = __shfl_down_sync(0xffffffffu, v, o);
+                if (o <= rem) v += t;
+            }
+            if (lane == 0 || (code >> 16)) hist[code & 255u] += v;
+            __syncwarp();
+        };
+        // the dS of a 32 x 32 block: queries c0 .. c0 + 31 of the tile, this warp's key rows
+        auto add_block = [&](RelTile kind, float run, const uint32_t *wcode, int c0) {
+            if (kind == kRelPast) {
+                sum_past += run;
+            } else if (kind == kRelFuture) {
+                sum_future += run;
+            } else {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
+                __syncwarp();
+                const uint32_t *code = wcode + lg * 32 + BM - 1 - c0 + lane;  // of diagonal lane
+                add_runs(run, code[-31]);
+                add_runs(lane < 31 ? diag[30 - lane] : 0.f, code[1]);
+            }
+        };
+        // end of a (key tile, head): the sums go to their row of the workspace
+        auto flush = [&](int64_t row, int64_t head) {
+            for (int o = 16; o > 0; o >>= 1) {
+                sum_past += __shfl_xor_sync(0xffffffffu, sum_past, o);
+                sum_future += __shfl_xor_sync(0xffffffffu, sum_future, o);
+            }
+            if (lane == 0) {
+                hist[p.rel.b.n - 1] += sum_past;
+                hist[p.rel.b.bidirectional ? p.rel.b.buckets - 1 : 0] += sum_future;
+            }
+            __syncwarp();
+            float *dst = p.rel.part + ((row * a.h + head) * 8 + (warp - 2)) * p.rel.b.buckets;
+            for (int n = lane; n < p.rel.b.buckets; n += 32) {
+                dst[n] = hist[n];
+                hist[n] = 0.f;
+            }
+            __syncwarp();
+            sum_past = sum_future = 0.f;
+        };
+
         ATTN_FOR_EACH_UNIT
         const int64_t shift = a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0;
         for (int64_t jt = first_tile; jt < ntiles; jt += tile_step) {
@@ -499,6 +590,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             query_tiles<BM>(a.mask, j0, lq, lkv, &qt0, &nq);
             const int n_iter = G * nq;
             int iq = 0;  // query tile within the head
+            int64_t hq = g * G;  // kBias: the head
             for (int it = 0; it < n_iter; ++it, ++qi) {
                 const int64_t i0 = int64_t(qt0 + iq) * BM;
                 // Usually LSE / D of this tile have landed (q_full), the GEMMs of tile qi - 2 that read
@@ -519,6 +611,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                 // first visible query column of this key row; everything is masked past the sequence
                 const int64_t cmin64 = !row_ok ? INT64_MAX : (a.mask ? j - shift - i0 : INT64_MIN);
                 const int cmin = int(cmin64 < -1 ? -1 : (cmin64 > BM ? BM : cmin64));
+                const int64_t dmin = j0 - i0 - (BM - 1) - shift;  // kBias: the tile's first delta
+                const RelTile kind = kBias ? rel_tile(p.rel.b, dmin, BN + BM - 1) : kRelPast;
+                const float *win = reinterpret_cast<const float *>(smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES) +
+                                   (kind == kRelNear ? int(uint32_t(dmin - (p.rel.b.lo - kRelPad)) & 3u) : 0);
+                const uint32_t *wcode = reinterpret_cast<const uint32_t *>(win) + Cfg::WIN_BYTES / 4;
 #pragma unroll
                 for (int q = 0; q < NG; ++q) {
                     const int rel = NH == NG ? q : 0;  // release group of these columns
@@ -526,6 +623,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     else if (q == 0) tc_fence_after();
                     const int c0 = q * (BM / NG) + half * GW;
                     uint32_t pk[GW / 2];  // P^T of this column group, packed
+                    float run = 0.f;  // kBias, near tile: running sum of a diagonal; else: this thread's sum of dS
                     // S^T / dP^T of the group in chunks of 16 columns.  With one group a thread (d = 128)
                     // the whole group is loaded at once and its TMEM columns released before P / dS are
                     // computed, so the next tile's S^T / dP^T GEMMs overlap this tile's element-wise work;
@@ -558,6 +656,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     }
                     if (ok) {
                         const bool any_mask = __any_sync(0xffffffffu, cmin > c0);
+                        // relative bias, near: entry r - c + BM - 1 of the window
+                        const float *wrow = win + (kind == kRelNear ? r + BM - 1 - c0 : 0);
+                        const float wfar = kBias ? win[0] : 0.f;
 #pragma unroll
                         for (int cc = 0; cc < NCH; ++cc) {
                             const int col0 = c0 + cc * 16, cur = cc & 1;
@@ -577,6 +678,44 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
 #pragma unroll
                                 for (int h2 = 0; h2 < 2; ++h2) {
                                     const int e = 4 * q4 + 2 * h2, c = col0 + e;
+                                    if (kBias) {
+                                        const int k = cc * 16 + e;  // column within the group of 32
+                                        float b0 = wfar, b1 = wfar;
+                                        if (kind == kRelNear) {
+                                            b0 = wrow[-k];
+                                            b1 = wrow[-k - 1];
+                                        }
+                                        float x0 = fmaf(__uint_as_float(sbuf[cur][e]), sc, b0) - lse4[2 * h2];
+                                        float x1 = fmaf(__uint_as_float(sbuf[cur][e + 1]), sc, b1) - lse4[2 * h2 + 1];
+                                        float g0 = __uint_as_float(dbuf[cur][e]) - dv4[2 * h2];
+                                        float g1 = __uint_as_float(dbuf[cur][e + 1]) - dv4[2 * h2 + 1];
+                                        if (any_mask) {  // a masked element's dP may be anything
+                                            x0 = c >= cmin ? x0 : -INFINITY;
+                                            x1 = c + 1 >= cmin ? x1 : -INFINITY;
+                                            g0 = c >= cmin ? g0 : 0.f;
+                                            g1 = c + 1 >= cmin ? g1 : 0.f;
+                                        }
+                                        const float p0 = ex2(x0), p1 = ex2(x1), ds0 = p0 * g0, ds1 = p1 * g1;
+                                        pk[cc * 8 + 2 * q4 + h2] = pack2<T>(p0, p1);
+                                        dk[2 * q4 + h2] = pack2<T>(ds0, ds1);
+                                        if (kind == kRelNear) {
+                                            // the sum of diagonal lane - column goes one lane up per column;
+                                            // lane 31's is complete
+                                            if (k > 0) {
+                                                if (lane == 31) diag[k - 1] = run;
+                                                const float up = __shfl_up_sync(0xffffffffu, run, 1);
+                                                run = lane == 0 ? ds0 : up + ds0;
+                                            } else {
+                                                run = ds0;
+                                            }
+                                            if (lane == 31) diag[k] = run;
+                                            const float up = __shfl_up_sync(0xffffffffu, run, 1);
+                                            run = lane == 0 ? ds1 : up + ds1;
+                                        } else {
+                                            run += ds0 + ds1;
+                                        }
+                                        continue;
+                                    }
                                     float x0 = fmaf(__uint_as_float(sbuf[cur][e]), sc, -lse4[2 * h2]);
                                     float x1 = fmaf(__uint_as_float(sbuf[cur][e + 1]), sc, -lse4[2 * h2 + 1]);
                                     if (any_mask) {
@@ -596,6 +735,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                         }
                     }
                     if (!kEarlyFree) release();
+                    if (kBias && ok) add_block(kind, run, wcode, c0);
                     // P^T into TMEM once the previous tile's dV GEMM has read it
                     if (q == 0) {
                         const uint32_t t_p = qi > 0 ? mbar_test_wait(p_free, (qi - 1) & 1) : 1u;
@@ -623,7 +763,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     st = 0;
                     st_par ^= 1;
                 }
-                if (++iq == nq) iq = 0;
+                if (++iq == nq) {
+                    iq = 0;
+                    if (kBias) flush(geo.kv_start(b) / 128 + b + jt, hq++);
+                }
             }
         }
         ATTN_END_UNITS
@@ -1213,7 +1356,7 @@ void plan_units(TcSched &S, const DenseArgs &a, const Geo &g, int64_t units, int
     last_key = key;
 }
 
-template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, const Geo &g, cudaStream_t s)
+template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
 {
     using Cfg = TcCfg<D>;
     constexpr bool packed = IsPacked<Geo>::value;
@@ -1221,6 +1364,7 @@ template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, cons
     if (ntiles == 0) return cudaSuccess;
     TcParams prm;
     prm.a = a;
+    if (rel) prm.rel = *rel;
     const int64_t nb = packed ? 1 : a.nseq;
     const int64_t sq = packed ? a.t_q : (a.t_q / (a.nseq ? a.nseq : 1));
     const int64_t skv = packed ? a.t_kv : (a.t_kv / (a.nseq ? a.nseq : 1));
@@ -1232,11 +1376,13 @@ template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, cons
         !map_view(&prm.tm_dk, a.dK, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
         !map_view(&prm.tm_dv, a.dV, a.dtype, D, skv, a.h_kv, nb, Cfg::BN))
         return cudaErrorInvalidValue;
-    if (!map_dqacc(&prm.tm_dq, a.dqacc, D, int64_t(a.n_part) * a.h * a.t_pad, Cfg::DQ_BOX_ROWS))
+    if (sq > 0 && !map_dqacc(&prm.tm_dq, a.dqacc, D, int64_t(a.n_part) * a.h * a.t_pad, Cfg::DQ_BOX_ROWS))
         return cudaErrorInvalidValue;
-    if (sq == 0) prm.tm_q = prm.tm_do = prm.tm_k;  // never read: no query tiles
-    auto k = a.ordered ? dense_bwd_tc_kernel<T, D, Geo, true> : dense_bwd_tc_kernel<T, D, Geo, false>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_ALLOC);
+    if (sq == 0) prm.tm_q = prm.tm_do = prm.tm_dq = prm.tm_k;  // never used: no query tiles
+    auto k = rel ? (a.ordered ? dense_bwd_tc_kernel<T, D, Geo, true, true> : dense_bwd_tc_kernel<T, D, Geo, false, true>)
+                 : (a.ordered ? dense_bwd_tc_kernel<T, D, Geo, true, false> : dense_bwd_tc_kernel<T, D, Geo, false, false>);
+    const int smem = rel ? Cfg::SMEM_ALLOC_BIAS : Cfg::SMEM_ALLOC;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     prm.a.tc_units = (a.deterministic ? a.n_part : ntiles) * a.nseq * a.h_kv;
     if (prm.a.tc_units > INT32_MAX) return cudaErrorInvalidValue;  // the kernel splits units in 32 bits
@@ -1244,20 +1390,26 @@ template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, cons
     plan_units<Cfg::BM, Cfg::BN>(prm.sched, prm.a, g, prm.a.tc_units, units);
     if (a.ordered && !prm.sched.on) return cudaErrorNotSupported;  // the waits need the planned order
     // ordered dQ mode waits across CTAs: a cooperative launch puts all of them on the GPU at once
-    return launch_kernel_ex(k, dim3(unsigned(units)), dim3(Cfg::THREADS + (a.ordered ? 32 : 0)), Cfg::SMEM_ALLOC, s,
-                            true, a.ordered != 0, prm, g);
+    return launch_kernel_ex(k, dim3(unsigned(units)), dim3(Cfg::THREADS + (a.ordered ? 32 : 0)), smem, s, true,
+                            a.ordered != 0, prm, g);
 }
 
-template <class Geo> cudaError_t dispatch(const DenseArgs &a, const Geo &g, cudaStream_t s)
+template <class Geo> cudaError_t dispatch(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
 {
     if (a.d == 64)
-        return a.dtype == ATTN_F16 ? run_tc<__half, 64>(a, g, s) : run_tc<__nv_bfloat16, 64>(a, g, s);
-    return a.dtype == ATTN_F16 ? run_tc<__half, 128>(a, g, s) : run_tc<__nv_bfloat16, 128>(a, g, s);
+        return a.dtype == ATTN_F16 ? run_tc<__half, 64>(a, rel, g, s) : run_tc<__nv_bfloat16, 64>(a, rel, g, s);
+    return a.dtype == ATTN_F16 ? run_tc<__half, 128>(a, rel, g, s) : run_tc<__nv_bfloat16, 128>(a, rel, g, s);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_bwd_main(const DenseArgs &a, const FixedGeo &g, cudaStream_t s) { return dispatch(a, g, s); }
-cudaError_t launch_dense_bwd_main(const DenseArgs &a, const PackedGeo &g, cudaStream_t s) { return dispatch(a, g, s); }
+cudaError_t launch_dense_bwd_main(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel)
+{
+    return dispatch(a, rel, g, s);
+}
+cudaError_t launch_dense_bwd_main(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel)
+{
+    return dispatch(a, rel, g, s);
+}
 
 }  // namespace attn

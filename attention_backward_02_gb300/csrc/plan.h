@@ -127,12 +127,13 @@ attn_status_t record_cuda_error(cudaError_t e);
 // Each returns cudaGetLastError() of its launches.
 cudaError_t launch_dense_preprocess(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
 cudaError_t launch_dense_preprocess(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
-cudaError_t launch_dense_bwd_main(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
-cudaError_t launch_dense_bwd_main(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
+struct RelArgs;  // relbias.h; NULL: no relative position bias
+cudaError_t launch_dense_bwd_main(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
+cudaError_t launch_dense_bwd_main(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
 cudaError_t launch_dq_finalize(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
 cudaError_t launch_dq_finalize(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
-cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
-cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
+cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
+cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
 
 cudaError_t launch_nsa_bwd(const NsaArgs &a, const PackedGeo &g, cudaStream_t s, cudaEvent_t before,
                            cudaEvent_t after);

@@ -11,6 +11,9 @@
  *   nsa_selected_attn_bwd   dQ, dK, dV of NSA selected attention, where every
  *                           query token attends to selectedBlockCount blocks of
  *                           selectedBlockSize keys chosen by int32 topkIndices.
+ *   sdpa_relbias_fwd_stats, the dense forward and backward with a learned relative
+ *   sdpa_relbias_bwd        position bias by buckets added to the scores, and the
+ *                           bias table's gradient.
  *   qk_norm_rope_fwd, _bwd  RMS norm of every query / key head with the rotary
  *                           position embedding in the same pass, and its gradient:
  *                           what makes Q and K for the calls above and takes their
@@ -294,6 +297,56 @@ attn_status_t nsa_selected_attn_bwd(const attn_nsa_desc_t *desc, const void *q, 
 attn_status_t nsa_block_lists(const attn_nsa_desc_t *desc, const int32_t *topk, int32_t *offsets,
                               int32_t *tokens, int64_t *nblk_max_out, void *workspace, size_t workspace_bytes,
                               void *stream);
+
+/* A learned relative position bias by buckets.  No counterpart on the pages: it
+ * is what a model whose positions enter the scores this way adds to the dense
+ * calls above.  The score of a query and a key becomes
+ *   s = scale q.k + table[bucket(delta)][query head],
+ *   delta = key position - query position,
+ * where key j stands at position j of its sequence and query i at i, or at
+ * i + s_kv - s_q under ATTN_CAUSAL_BOTTOM_RIGHT.
+ * The bucket of delta: with both directions, keys after the query (delta > 0)
+ * take the upper half of the buckets, n = num_buckets / 2 and x = |delta|; with
+ * one, n = num_buckets and x = max(-delta, 0).  With e = n / 2 (rounded down):
+ *   x < e: x;  else min(n - 1, e + floor(log(x / e) / log(max_distance / e) (n - e))),
+ * in real arithmetic (attn_relbias_bucket evaluates it).
+ * A table entry of -1e30 or less masks its bucket: keys in it are not visible to
+ * that head.                                                                */
+typedef struct {
+    const void *table;      /* device [num_buckets][h], contiguous              */
+    int table_type;         /* ATTN_F16, ATTN_BF16 or ATTN_F32                  */
+    int64_t num_buckets;    /* 2 .. 128; even and >= 4 with both directions     */
+    int64_t max_distance;   /* e < max_distance <= 65536                        */
+    int bidirectional;      /* 1: keys after the query have buckets of their own;
+                               0: they share bucket 0                           */
+} attn_relbias_t;
+
+#define ATTN_F32 2
+
+/* Bucket of a key delta positions after its query.  Host only; the table is not
+ * read.                                                                     */
+attn_status_t attn_relbias_bucket(const attn_relbias_t *bias, int64_t delta, int64_t *bucket);
+
+/* Workspace bytes of the two calls below.  Either output pointer may be NULL.
+ * Host only; no CUDA call.                                                  */
+attn_status_t sdpa_relbias_workspace_size(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, size_t *fwd_bytes,
+                                          size_t *bwd_bytes);
+
+/* sdpa_fwd_stats with the bias in the scores: everything but bias as there. */
+attn_status_t sdpa_relbias_fwd_stats(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q,
+                                     attn_view_t k, attn_view_t v, attn_view_t o, float *lse, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* sdpa_bwd with the bias in the scores, and the table's gradient
+ *   dtable[n][head] = sum of dS over the queries and keys with bucket n
+ * (fp32 [num_buckets][h], contiguous, overwritten): dS is summed in fp32 before
+ * it is rounded for the other gradients, in an order that does not change from
+ * run to run in any dQ mode.  P and dS are computed in fp32 for both types.
+ * Everything else as in sdpa_bwd.                                           */
+attn_status_t sdpa_relbias_bwd(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q, attn_view_t k,
+                               attn_view_t v, attn_view_t o, attn_view_t dO, const float *lse, attn_view_t dQ,
+                               attn_view_t dK, attn_view_t dV, float *dtable, void *workspace, size_t workspace_bytes,
+                               void *stream);
 
 /* Norm and rotation of the query and key heads.  Like the relative-bias calls,
  * these have no counterpart on the pages: they are what a model runs between

@@ -1,0 +1,374 @@
+"""GPU parity of sdpa_relbias_fwd_stats / _bwd with the fp64 definition, through the C ABI.
+
+Bounds.  h = eps(type) / 2 is the half step of the 16-bit type, u = 2^-23 covers an fp32 operation (rounded or
+truncated).  A score is d exact products summed in fp32, a fused product-sum and a difference, so the exponent
+is off by at most (d + 8) u (scale sum|q k| + |bias| + |LSE|), and the exponential adds 2^-21: call the relative
+error of P eP.  P and dS are rounded to 16 bits before they are multiplied on (h of the value, and for fp16
+2^-25, half its smallest step; in the forward P is relative to a reference at most 2^8 below the row's largest
+value).  With A = sum_j P_ij |v_j| and M_ij = P_ij (sum|dO v| + sum|dO O|):
+    |O err|  <= h |O| + sum_j (h + 2 max eP + n u) P_ij |v_j| + 2^-25 sum|v|
+    |LSE err| <= 2 max_j eP + n u + 2 u |LSE|
+    |dS err| <= h |dS| + (eP + (d + 8) u) M + 2^-25;   the gradients are sums of dS (P for dV) times the other
+    operand, in fp32 (n u of the sum of magnitudes), rounded once;  dtable sums dS before its rounding.
+The factor 2 of the row's largest eP covers the normalisation.  Padding of sequences, the row order of the
+sums and the 16-bit outputs' rounding are all within these."""
+import numpy as np
+import pytest
+
+from oracle import position as P
+from tests import harness as H
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+HALF = {"float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}
+STEP = {"float16": 2.0 ** -25, "bfloat16": 0.0}
+
+
+class Problem:
+    """lens: [(s_q, s_kv)]; packed when more than one or packed=True.  layout: 'bshd' or 'bhsd'."""
+
+    def __init__(self, dtype, lens, h, hk, d, mask, buckets=32, far=128, both=True, packed=None, b=1, layout="bshd",
+                 table="32", seed=0, mode=0, spread=1.5):
+        import torch
+        import attention_backward_02_gb300 as ab
+        self.ab, self.torch = ab, torch
+        self.dtype, self.dt = dtype, torch.float16 if dtype == "float16" else torch.bfloat16
+        self.packed = len(lens) > 1 if packed is None else packed
+        self.lens = list(lens) if self.packed else [lens[0]] * b
+        self.h, self.hk, self.d, self.mask, self.far, self.both = h, hk, d, mask, far, both
+        self.layout, self.scale = layout, d ** -0.5
+        g = torch.Generator().manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g)
+        self.tq, self.tk = sum(a for a, _ in self.lens), sum(a for _, a in self.lens)
+        self.q, self.k, self.v = rnd(self.tq, h, d).to(self.dt), rnd(self.tk, hk, d).to(self.dt), rnd(self.tk, hk, d).to(self.dt)
+        self.do = rnd(self.tq, h, d).to(self.dt)
+        tt = {"32": torch.float32, "16": self.dt}[table]
+        self.table = (rnd(buckets, h) * spread).to(tt).cuda()
+        self.bias = ab.relbias(self.table, max_distance=far, bidirectional=both)
+        kw = dict(dtype=ab.ATTN_F16 if dtype == "float16" else ab.ATTN_BF16, b=len(self.lens), h=h, h_kv=hk, d=d,
+                  scale=self.scale, mask=mask, deterministic=mode)
+        if self.packed:
+            kw.update(s_q=0, s_kv=0, cu_seqlens_q=list(np.cumsum([a for a, _ in self.lens])),
+                      cu_seqlens_kv=list(np.cumsum([a for _, a in self.lens])))
+        else:
+            kw.update(s_q=lens[0][0], s_kv=lens[0][1])
+        self.desc = ab.sdpa_desc(**kw)
+
+    def put(self, t):
+        """Token-major [T, n, d] onto the GPU in this problem's layout; returns the tensor that holds it."""
+        if self.packed:
+            return t.cuda().contiguous()
+        b = len(self.lens)
+        t = t.cuda().reshape(b, t.shape[0] // b, *t.shape[1:])
+        return t.permute(0, 2, 1, 3).contiguous() if self.layout == "bhsd" else t.contiguous()
+
+    def view(self, t):
+        if self.packed:
+            return self.ab.view_tnd(t)
+        return t if self.layout == "bhsd" else t.permute(0, 2, 1, 3)
+
+    def get(self, t):
+        """fp64 [T, n, d] of a tensor made by put."""
+        if not self.packed:
+            t = t.permute(0, 2, 1, 3) if self.layout == "bhsd" else t
+            t = t.reshape(-1, *t.shape[2:])
+        return t.double().cpu().numpy()
+
+    def nan(self, t):
+        return self.put(self.torch.full_like(t, float("nan")))
+
+    def get_lse(self, lse):
+        """[T, h] fp64 from the ABI layout."""
+        a = lse.double().cpu().numpy()
+        if self.packed:
+            return a.reshape(self.h, self.tq).T
+        b = len(self.lens)
+        return a.reshape(b, self.h, -1).transpose(0, 2, 1).reshape(-1, self.h)
+
+    def put_lse(self, a):
+        t = self.torch.from_numpy(np.ascontiguousarray(a)).float()
+        if self.packed:
+            return t.t().contiguous().cuda()
+        b = len(self.lens)
+        return t.reshape(b, -1, self.h).permute(0, 2, 1).contiguous().cuda()
+
+    def each(self):
+        """(query rows, key rows) slices of the sequences."""
+        a = c = 0
+        for sq, sk in self.lens:
+            yield slice(a, a + sq), slice(c, c + sk)
+            a, c = a + sq, c + sk
+
+    def f64(self):
+        return [x.double().numpy() for x in (self.q, self.k, self.v, self.do)] + [self.table.double().cpu().numpy()]
+
+    def kw(self):
+        return dict(scale=self.scale, mask=self.mask, max_distance=self.far, bidirectional=self.both)
+
+    def reference_fwd(self):
+        q, k, v, _, t = self.f64()
+        o, lse = np.zeros_like(q), np.full(q.shape[:2], np.inf)
+        for a, c in self.each():
+            o[a], lse[a] = P.relbias_fwd(q[a], k[c], v[c], t, **self.kw())
+        return o, lse
+
+    def fwd(self, **kw):
+        ten = [self.put(x) for x in (self.q, self.k, self.v)]
+        o = self.nan(self.q)
+        lse = self.torch.full((self.tq * self.h,), float("nan"), device="cuda")
+        ws = self.ab.sdpa_relbias_fwd_stats(self.desc, self.bias, *map(self.view, ten), self.view(o), lse, **kw)
+        assert self.ab.attn_query_status(ws, kw.get("stream")) == 0
+        return self.get(o), self.get_lse(lse)
+
+    def bwd(self, o, lse, **kw):
+        ten = [self.put(x) for x in (self.q, self.k, self.v, o, self.do)]
+        out = [self.nan(self.q), self.nan(self.k), self.nan(self.v)]
+        dt = self.torch.full(self.table.shape, float("nan"), device="cuda")
+        ws = self.ab.sdpa_relbias_bwd(self.desc, self.bias, *map(self.view, ten), self.put_lse(lse),
+                                      *map(self.view, out), dt, **kw)
+        assert self.ab.attn_query_status(ws, kw.get("stream")) == 0
+        return [self.get(x) for x in out] + [dt.double().cpu().numpy()]
+
+    def weights(self, a, c, x, lse):
+        """P, its relative error bound and bucket matrix of one sequence and head, from its LSE."""
+        q, k, _, _, t = self.f64()
+        g = x // (self.h // self.hk)
+        sq, sk = q[a].shape[0], k[c].shape[0]
+        sh = sk - sq if self.mask == 2 else 0
+        bk = P.bucket_matrix(sq, sk, sh, t.shape[0], self.far, self.both)
+        s = P._scores(q[a, x], k[c, g], t[:, x], bk, self.scale, self.mask, sh)
+        z = np.where(np.isinf(lse), 0.0, lse)[:, None]
+        p = np.where(np.isinf(lse)[:, None], 0.0, np.exp(s - z))
+        tb = np.where(t[:, x] <= P.MASKED, 0.0, t[:, x])
+        ep = (self.d + 8) * U * (self.scale * np.abs(q[a, x]) @ np.abs(k[c, g]).T + np.abs(tb)[bk] + np.abs(z)) + 2.0 ** -21
+        return p, ep, bk
+
+    def check_fwd(self, o, lse):
+        ro, rl = self.reference_fwd()
+        h_, st = HALF[self.dtype], STEP[self.dtype]
+        assert np.array_equal(np.isinf(lse), np.isinf(rl)) and not np.isnan(lse).any()
+        v = self.f64()[2]
+        for a, c in self.each():
+            n = c.stop - c.start
+            for x in range(self.h):
+                p, ep, _ = self.weights(a, c, x, rl[a, x])
+                e = ep.max(-1, initial=0.0)
+                av = np.abs(v[c, x // (self.h // self.hk)])
+                bound = h_ * np.abs(ro[a, x]) + (h_ + 2 * e + n * U)[:, None] * (p @ av) + st * av.sum(0) + 2 * st
+                err = np.abs(o[a, x] - ro[a, x])
+                assert np.all(err <= bound), ("O", x, float((err - bound).max()))
+                live = ~np.isinf(rl[a, x])
+                el = np.abs(lse[a, x][live] - rl[a, x][live])
+                assert np.all(el <= (2 * e + n * U)[live] + 2 * U * np.abs(rl[a, x][live])), ("LSE", float(el.max()))
+
+    def inputs_bwd(self):
+        """O as the type holds it and the fp32 LSE, from the definition."""
+        o, lse = self.reference_fwd()
+        return self.torch.from_numpy(o).to(self.dt), lse.astype(np.float32)
+
+    def check_bwd(self, got, o, lse):
+        q, k, v, do, t = self.f64()
+        o, lse = o.double().numpy(), lse.astype(np.float64)
+        h_, st = HALF[self.dtype], STEP[self.dtype]
+        ref = [np.zeros_like(x) for x in (q, k, v, t)]
+        bnd = [np.zeros_like(x) for x in (q, k, v, t)]
+        d, sc = self.d, self.scale
+        for a, c in self.each():
+            r = P.relbias_bwd(q[a], k[c], v[c], o[a], do[a], lse[a], t, **self.kw())
+            ref[0][a], ref[1][c], ref[2][c] = r[:3]
+            ref[3] += r[3]
+            nq, nk = a.stop - a.start, c.stop - c.start
+            for x in range(self.h):
+                g = x // (self.h // self.hk)
+                p, ep, bk = self.weights(a, c, x, lse[a, x])
+                ado, av = np.abs(do[a, x]), np.abs(v[c, g])
+                ds = np.abs(p * (do[a, x] @ v[c, g].T - (do[a, x] * o[a, x]).sum(-1, keepdims=True)))
+                m = p * (ado @ av.T + (ado * np.abs(o[a, x])).sum(-1, keepdims=True))
+                e = (ep + (d + 8) * U) * m
+                e16 = h_ * ds + e + np.where(p > 0, st, 0.0)
+                bnd[0][a, x] += sc * ((e16 + nk * U * ds) @ np.abs(k[c, g]))
+                bnd[1][c, g] += sc * ((e16 + nq * self.h * U * ds).T @ np.abs(q[a, x]))
+                bnd[2][c, g] += ((h_ + ep + nq * self.h * U) * p + np.where(p > 0, st, 0.0)).T @ ado
+                np.add.at(bnd[3][:, x], bk, e + (nq * nk) * 2.0 ** -24 * ds)
+        for name, y, r, w in zip(("dQ", "dK", "dV", "dtable"), got, ref, bnd):
+            assert np.all(np.isfinite(y)), name
+            w = w + (0 if name == "dtable" else h_ * np.abs(r) * (1 + h_) + h_ * w + 2 * st) + 1e-30
+            err = np.abs(y - r)
+            assert np.all(err <= w), (name, float((err - w).max()), float(err.max()))
+        return ref
+
+
+CASES = [
+    # dtype, lens, h, hk, d, mask, buckets, far, both, kw
+    ("float16", [(1, 1)], 1, 1, 64, 0, 32, 128, True, {}),
+    ("bfloat16", [(128, 128)], 2, 2, 128, 2, 32, 128, False, {}),
+    ("float16", [(300, 300)], 4, 2, 64, 0, 32, 128, True, dict(b=2)),
+    ("bfloat16", [(257, 511)], 4, 1, 128, 2, 32, 64, True, dict(layout="bhsd")),
+    ("float16", [(200, 77)], 2, 1, 64, 2, 16, 100, False, dict(b=2)),          # rows that see no key
+    ("bfloat16", [(130, 400)], 2, 2, 64, 1, 64, 256, False, dict(table="16")),
+    ("float16", [(640, 640)], 2, 2, 128, 0, 128, 1000, True, dict(table="16", layout="bhsd")),
+    ("bfloat16", [(700, 700)], 1, 1, 64, 1, 2, 2, False, {}),                  # the fewest buckets
+    ("bfloat16", [(650, 650)], 2, 1, 128, 0, 4, 9, True, {}),                  # far tiles on both sides
+    ("float16", [(5, 900)], 3, 3, 128, 2, 32, 128, False, {}),
+    ("float16", [(33, 65), (1, 1), (0, 17), (129, 129), (200, 0), (64, 300)], 4, 2, 64, 2, 32, 128, True, {}),
+    ("bfloat16", [(127, 127), (385, 384), (3, 250)], 6, 2, 128, 0, 64, 1024, True, {}),
+    ("bfloat16", [(140, 300)], 2, 2, 64, 0, 32, 128, True, dict(packed=True)),
+    ("bfloat16", [(100, 100)], 2, 2, 128, 2, 32, 65536, False, {}),            # borders past every key
+]
+ids = lambda c: "-".join(str(x) for x in c).replace(" ", "")
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_forward(case):
+    p = Problem(*case[:9], seed=len(str(case)), **case[9])
+    p.check_fwd(*p.fwd())
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_backward(case):
+    p = Problem(*case[:9], seed=len(str(case)), **case[9])
+    o, lse = p.inputs_bwd()
+    p.check_bwd(p.bwd(o, lse), o, lse)
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("case", [CASES[2], CASES[3], CASES[10]], ids=ids)
+def test_backward_deterministic_modes(case, mode):
+    p = Problem(*case[:9], seed=5, mode=mode, **case[9])
+    o, lse = p.inputs_bwd()
+    first = p.bwd(o, lse)
+    p.check_bwd(first, o, lse)
+    for a, b in zip(first, p.bwd(o, lse)):
+        np.testing.assert_array_equal(a, b)
+
+
+def test_table_gradient_is_reproducible_with_atomic_dq():
+    p = Problem("bfloat16", [(900, 900)], 4, 2, 128, 0, 32, 128, True, seed=6, b=2)
+    o, lse = p.inputs_bwd()
+    first = p.bwd(o, lse)
+    for _ in range(3):
+        again = p.bwd(o, lse)
+        for i in (1, 2, 3):
+            np.testing.assert_array_equal(first[i], again[i])
+
+
+@pytest.mark.parametrize("dtype,d,mask", [("float16", 64, 2), ("bfloat16", 128, 0)])
+def test_masked_buckets(dtype, d, mask):
+    """-inf, the type's lowest value and -1e30 mask a bucket; a row left without keys is empty, and nothing of
+    it reaches the gradients.  In head 0 everything is masked."""
+    p = Problem(dtype, [(150, 150)], 3, 3, d, mask, 8, 20, False, seed=7)
+    p.table[0, 1] = -float("inf")
+    p.table[7, 1] = p.torch.finfo(p.torch.float32).min
+    p.table[3, 2] = -1e30
+    p.table[:, 0] = -2e30
+    o, lse = p.fwd()
+    p.check_fwd(o, lse)
+    assert np.all(np.isinf(lse[:, 0])) and np.all(o[:, 0] == 0)
+    oi, li = p.inputs_bwd()
+    ref = p.check_bwd(p.bwd(oi, li), oi, li)
+    assert np.all(ref[3][:, 0] == 0) and ref[3][0, 1] == 0
+
+
+def test_zero_table_is_the_plain_call():
+    """With a zero table the biased forward adds 0.0 to every score: bit for bit the plain call's results (a
+    product and a product-sum with zero round alike)."""
+    import torch
+    p = Problem("bfloat16", [(300, 300)], 4, 2, 128, 2, 32, 128, True, seed=8)
+    p.table.zero_()
+    o, lse = p.fwd()
+    ten = [p.put(x) for x in (p.q, p.k, p.v)]
+    o2, l2 = p.nan(p.q), torch.empty(p.tq * p.h, device="cuda")
+    p.ab.sdpa_fwd_stats(p.desc, *map(p.view, ten), p.view(o2), l2)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(o, p.get(o2))
+    np.testing.assert_array_equal(lse, p.get_lse(l2))
+
+
+def test_no_queries_and_no_keys():
+    for lens in [(0, 40), (40, 0), (0, 0)]:
+        p = Problem("float16", [lens], 2, 1, 64, 0, 32, 128, True, seed=9)
+        o, lse = p.fwd()
+        assert np.all(o == 0) and np.all(np.isposinf(lse))
+        got = p.bwd(p.torch.from_numpy(o).to(p.dt), lse.astype(np.float32))
+        assert all(np.all(x == 0) for x in got)
+
+
+def test_graph_replay_and_side_stream():
+    """Forward and backward captured with workspaces of their own, replayed with another table and inputs; and
+    a direct call on a side stream that makes its own workspace."""
+    import torch
+    p = Problem("float16", [(260, 300)], 4, 2, 64, 2, 32, 128, True, seed=10, mode=1)
+    ab = p.ab
+    q, k, v, do = (p.put(x) for x in (p.q, p.k, p.v, p.do))
+    o, lse = p.nan(p.q), torch.empty(p.tq * p.h, device="cuda")
+    outs = [p.nan(x) for x in (p.q, p.k, p.v)]
+    dt = torch.empty(32, 4, device="cuda")
+    wf, wb = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in ab.sdpa_relbias_workspace_size(p.desc, p.bias))
+    V = p.view
+
+    def both(**kw):
+        ab.sdpa_relbias_fwd_stats(p.desc, p.bias, V(q), V(k), V(v), V(o), lse, workspace=kw.get("wf"), stream=kw.get("stream"))
+        ab.sdpa_relbias_bwd(p.desc, p.bias, V(q), V(k), V(v), V(o), V(do), lse, *map(V, outs), dt, workspace=kw.get("wb"),
+                            stream=kw.get("stream"))
+
+    both(wf=wf, wb=wb)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(wf=wf, wb=wb)
+    p.table.mul_(-0.5)
+    q.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [x.clone() for x in (o, lse, *outs, dt)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    both(stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(got, (o, lse, *outs, dt)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,d,rot", [("bfloat16", 128, 0), ("float16", 64, 32)])
+def test_layer(dtype, d, rot):
+    """The operators as a layer runs them: norm (and rotation) of the projections, biased attention, and both
+    backward, against the fp64 chain.  Each stage's 16-bit result feeds the next, so errors add up: relative
+    L2 of 4 half steps per stage, four stages, is the bound for the gradients that went through all of them."""
+    import torch
+    b, s, h, hk = 2, 190, 4, 2
+    p = Problem(dtype, [(s, s)], h, hk, d, 2, 32, 128, False, seed=11, b=b)
+    ab = p.ab
+    qk = ab.qk_norm_rope_desc(dtype=p.desc.dtype, b=b, s=s, h=h, h_kv=hk, d=d, rotary_dim=rot, max_pos=256 if rot else 0)
+    g = torch.Generator().manual_seed(1)
+    w = [(1 + 0.2 * torch.randn(d, generator=g)).to(p.dt).cuda() for _ in range(2)]
+    ang = torch.randn(256, max(rot // 2, 1), generator=g)
+    cos, sin = (ang.cos().cuda(), ang.sin().cuda()) if rot else (None, None)
+    x, y, v, do = (p.put(t) for t in (p.q, p.k, p.v, p.do))
+    V = p.view
+    q, k, o = torch.empty_like(x), torch.empty_like(y), torch.empty_like(x)
+    lse = torch.empty(b, h, s, device="cuda")
+    ab.qk_norm_rope_fwd(qk, V(x), V(y), *w, cos, sin, V(q), V(k))
+    ab.sdpa_relbias_fwd_stats(p.desc, p.bias, V(q), V(k), V(v), V(o), lse)
+    dq, dk, dv, dt = torch.empty_like(x), torch.empty_like(y), torch.empty_like(v), torch.empty_like(p.table)
+    ab.sdpa_relbias_bwd(p.desc, p.bias, V(q), V(k), V(v), V(o), V(do), lse, V(dq), V(dk), V(dv), dt)
+    dw = [torch.empty(d, device="cuda") for _ in range(2)]
+    ab.qk_norm_rope_bwd(qk, V(x), V(y), V(dq), V(dk), *w, cos, sin, V(dq), V(dk), *dw)  # in place
+    torch.cuda.synchronize()
+    f = lambda t: t.double().cpu().numpy()
+    xs = [f(t).reshape(b, s, -1, d) for t in (x, y)]
+    c, sn = [(None if t is None else np.broadcast_to(f(t)[:s], (b, s, rot // 2))) for t in (cos, sin)]
+    qn, kn = (P.norm_rope(a, f(wi), 1e-6, c, sn, rot, False) for a, wi in zip(xs, w))
+    tb, dts, grads = f(p.table), 0, [[], [], []]
+    for n in range(b):
+        on, ln = P.relbias_fwd(qn[n], kn[n], f(v)[n], tb, **p.kw())
+        r = P.relbias_bwd(qn[n], kn[n], f(v)[n], on, f(do)[n], ln, tb, **p.kw())
+        dts = dts + r[3]
+        for i in range(3):
+            grads[i].append(r[i])
+    ref = [P.norm_rope_bwd(a, np.stack(gr), f(wi), 1e-6, c, sn, rot, False) for a, gr, wi in zip(xs, grads, w)]
+    want = [ref[0][0], ref[1][0], np.stack(grads[2]), dts, ref[0][1], ref[1][1]]
+    got = [f(dq), f(dk), f(dv), f(dt), f(dw[0]), f(dw[1])]
+    for name, a, r in zip(("dx", "dy", "dv", "dtable", "dwq", "dwk"), got, want):
+        a = a.reshape(r.shape)
+        assert np.linalg.norm(a - r) <= 16 * HALF[dtype] * np.linalg.norm(r), name

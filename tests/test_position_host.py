@@ -89,3 +89,73 @@ def test_qk_calls(ab):
     assert _fwd(ab, d, ws=None) == WORKSPACE and _fwd(ab, d, ws=A + 128) == WORKSPACE and _fwd(ab, d, nbytes=8) == WORKSPACE
     need = ab.qk_norm_rope_workspace_size(d)[1]
     assert _bwd(ab, d, nbytes=need - 1) == WORKSPACE
+
+
+def _bias(ab, **kw):
+    base = dict(table=A, table_type=2, num_buckets=32, max_distance=128, bidirectional=1)
+    base.update(kw)
+    return ab.attn_relbias_t(*base.values())
+
+
+def _sdpa(ab, **kw):
+    base = dict(dtype=ab.ATTN_F16, b=2, h=4, h_kv=2, s_q=64, s_kv=96, d=64, scale=0.125)
+    base.update(kw)
+    return ab.sdpa_desc(**base)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), OK), (dict(num_buckets=2, max_distance=2, bidirectional=0), OK), (dict(num_buckets=128), OK),
+    (dict(num_buckets=4, max_distance=2), OK), (dict(max_distance=65536), OK), (dict(table_type=0), OK),
+    (dict(num_buckets=1, bidirectional=0), INVALID), (dict(num_buckets=2), INVALID), (dict(num_buckets=7), INVALID),
+    (dict(num_buckets=0), INVALID), (dict(num_buckets=-4), INVALID), (dict(max_distance=8), INVALID),
+    (dict(max_distance=16, bidirectional=0), INVALID), (dict(max_distance=-1), INVALID), (dict(table_type=3), INVALID),
+    (dict(table_type=-1), INVALID), (dict(bidirectional=2), INVALID), (dict(num_buckets=130), UNSUPPORTED),
+    (dict(max_distance=65537), UNSUPPORTED),
+])
+def test_relbias_descriptor(ab, kw, code):
+    f, b, n = C.c_size_t(), C.c_size_t(), C.c_int64()
+    lib, bias, desc = ab._lib.load(), _bias(ab, **kw), _sdpa(ab)
+    assert lib.sdpa_relbias_workspace_size(C.byref(desc), C.byref(bias), C.byref(f), C.byref(b)) == code
+    assert lib.attn_relbias_bucket(C.byref(bias), -5, C.byref(n)) == code
+    if code == OK:
+        plain = ab.sdpa_workspace_size(desc)
+        assert f.value > plain[0] and b.value > plain[1]
+
+
+def test_relbias_buckets(ab):
+    """Against the integer definition, over every border."""
+    from oracle import position as P
+    for nb, far, both in [(32, 128, 1), (32, 128, 0), (64, 1024, 0), (128, 1000, 1), (16, 100, 1), (2, 2, 0), (4, 9, 1),
+                          (3, 5, 0), (5, 77, 0), (128, 2000, 0)]:
+        bias = _bias(ab, num_buckets=nb, max_distance=far, bidirectional=both)
+        for delta in range(-far - 5, far + 6):
+            assert ab.relbias_bucket(bias, delta) == P.bucket(delta, nb, far, bool(both)), (nb, far, both, delta)
+        for delta in (-2 ** 63, 2 ** 63 - 1):
+            assert ab.relbias_bucket(bias, delta) == P.bucket(delta, nb, far, bool(both))
+    assert ab._lib.load().attn_relbias_bucket(None, 0, C.byref(C.c_int64())) == NULLPTR
+    assert ab._lib.load().attn_relbias_bucket(C.byref(_bias(ab)), 0, None) == NULLPTR
+
+
+def test_relbias_calls(ab):
+    lib, desc = ab._lib.load(), _sdpa(ab)
+    v = ab.attn_view_t(A, 4 * 96 * 64, 64, 256)
+    fwd = lambda b=None, d=desc, views=(v,) * 4, lse=A, ws=A, n=1 << 30: lib.sdpa_relbias_fwd_stats(
+        C.byref(d), None if b == 0 else C.byref(b or _bias(ab)), *views, lse, ws, n, None)
+    bwd = lambda b=None, d=desc, views=(v,) * 8, lse=A, dt=A, ws=A, n=1 << 30: lib.sdpa_relbias_bwd(
+        C.byref(d), None if b == 0 else C.byref(b or _bias(ab)), *views[:5], lse, *views[5:], dt, ws, n, None)
+    assert lib.sdpa_relbias_workspace_size(None, C.byref(_bias(ab)), None, None) == NULLPTR
+    assert lib.sdpa_relbias_workspace_size(C.byref(desc), None, None, None) == NULLPTR
+    for call, views in ((fwd, 4), (bwd, 8)):
+        assert call(0) == NULLPTR and call(_bias(ab, table=None)) == NULLPTR and call(lse=None) == NULLPTR
+        assert call(_bias(ab, table=A + 2)) == ALIGN and call(_bias(ab, table=A + 1, table_type=0)) == ALIGN
+        assert call(_bias(ab, num_buckets=7)) == INVALID
+        assert call(d=_sdpa(ab, d=96)) == UNSUPPORTED and call(d=_sdpa(ab, b=1, h=65536, h_kv=1)) == UNSUPPORTED
+        for i in range(views):
+            bad = [v] * views
+            bad[i] = ab.attn_view_t(None, 4 * 96 * 64, 64, 256)
+            assert call(views=bad) == NULLPTR
+            bad[i] = ab.attn_view_t(A + 8, 4 * 96 * 64, 64, 256)
+            assert call(views=bad) == ALIGN
+        need = ab.sdpa_relbias_workspace_size(desc, _bias(ab))[call is bwd]
+        assert call(ws=None) == WORKSPACE and call(ws=A + 16) == WORKSPACE and call(n=need - 1) == WORKSPACE
+    assert bwd(dt=None) == NULLPTR and bwd(dt=A + 2) == ALIGN
