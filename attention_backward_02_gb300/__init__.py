@@ -20,6 +20,7 @@ __all__ = ["sdpa_desc", "nsa_desc", "view_bhsd", "view_tnd", "sdpa_workspace_siz
            "sdpa_bwd", "nsa_workspace_size", "nsa_selected_attn_bwd", "nsa_block_lists",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd",
            "relbias", "relbias_bucket", "sdpa_relbias_workspace_size", "sdpa_relbias_fwd_stats", "sdpa_relbias_bwd",
+           "sdpa_relbias_decode_workspace_size", "sdpa_relbias_decode",
            "qk_norm_rope_desc", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
            "attn_query_status", "AttnError", "ATTN_F16", "ATTN_BF16", "ATTN_F32",
            "ATTN_MASK_NONE",
@@ -359,6 +360,33 @@ def sdpa_relbias_bwd(desc, bias, q, k, v, o, dO, lse, dQ, dK, dV, dtable, *, wor
     dt = call.ptr("dtable", dtable, torch.float32, tuple(bias.tensor.shape))
     call.run(_lib.load().sdpa_relbias_bwd, C.byref(desc), C.byref(bias), *views[:5], _lse_ptr(call, desc, lse, sl),
              *views[5:], dt, ws.data_ptr(), ws.numel())
+    return ws
+
+
+def sdpa_relbias_decode_workspace_size(desc, bias):
+    """Bytes of device workspace sdpa_relbias_decode needs (host only)."""
+    n = C.c_size_t()
+    check(_lib.load().sdpa_relbias_decode_workspace_size(C.byref(desc), C.byref(bias), C.byref(n)),
+          "sdpa_relbias_decode_workspace_size")
+    return n.value
+
+
+def sdpa_relbias_decode(desc, bias, q, k, v, lens, o, *, workspace=None, stream=None):
+    """Attention with a learned relative position bias for one new token per sequence: q, o [B, h, 1, D], the
+    cache k, v [B, h_kv, S_kv, D] (tensors or views), lens int32 CUDA [B] the keys cached, the new token's
+    among them (None: S_kv).  desc: s_q = 1 and ATTN_CAUSAL_BOTTOM_RIGHT.  Returns the workspace, for
+    attn_query_status (lengths out of range)."""
+    torch = _torch()
+    call = _Call("sdpa_relbias_decode", desc.dtype, bias.tensor.device, stream)
+    if bias.tensor.shape[1] != desc.h:
+        raise ValueError(f"sdpa_relbias_decode: bias table {tuple(bias.tensor.shape)}, {desc.h} heads")
+    ws = workspace
+    if ws is None:
+        ws = call.workspace(sdpa_relbias_decode_workspace_size(desc, bias), None)
+    sq, sk = (desc.b, desc.h, 1, desc.d), (desc.b, desc.h_kv, desc.s_kv, desc.d)
+    views = [call.view(n, x, s) for n, x, s in (("q", q, sq), ("k", k, sk), ("v", v, sk), ("o", o, sq))]
+    call.run(_lib.load().sdpa_relbias_decode, C.byref(desc), C.byref(bias), *views[:3],
+             call.ptr("lens", lens, torch.int32, (desc.b,)), views[3], ws.data_ptr(), ws.numel())
     return ws
 
 

@@ -27,7 +27,7 @@ EXPORTS = ("sdpa_workspace_size", "sdpa_fwd_stats", "sdpa_bwd", "nsa_workspace_s
            "attn_selftest_wait_timeout", "attn_selftest_occupy", "attn_last_error",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd",
            "qk_norm_rope_bwd", "attn_relbias_bucket", "sdpa_relbias_workspace_size", "sdpa_relbias_fwd_stats",
-           "sdpa_relbias_bwd")
+           "sdpa_relbias_bwd", "sdpa_relbias_decode_workspace_size", "sdpa_relbias_decode")
 
 
 class attn_view_t(C.Structure):
@@ -97,6 +97,8 @@ def load() -> C.CDLL:
         "sdpa_relbias_workspace_size": [D, R, P(S), P(S)],
         "sdpa_relbias_fwd_stats": [D, R, view, view, view, view, V, V, S, V],
         "sdpa_relbias_bwd": [D, R, view, view, view, view, view, V, view, view, view, V, V, S, V],
+        "sdpa_relbias_decode_workspace_size": [D, R, P(S)],
+        "sdpa_relbias_decode": [D, R, view, view, view, V, view, V, S, V],
         "qk_norm_rope_workspace_size": [K, P(S), P(S)],
         "qk_norm_rope_fwd": [K, view, view, V, V, V, V, V, view, view, V, S, V],
         "qk_norm_rope_bwd": [K, view, view, view, view, V, V, V, V, V, view, view, V, V, V, S, V],

@@ -12,6 +12,7 @@
 #include "plan.h"
 #include "qk_norm.h"
 #include "relbias.h"
+#include "relbias_decode.h"
 
 using namespace attn;
 
@@ -781,6 +782,78 @@ attn_status_t nsa_block_lists(const attn_nsa_desc_t *desc, const int32_t *topk, 
         pg.cu_kv[b + 1] = desc->cu_seqlens_kv[b];
     }
     return cuda_status(launch_nsa_block_lists(a, pg, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------- one token with the relative bias
+
+namespace {
+
+attn_status_t check_decode(const attn_sdpa_desc_t *d, const attn_relbias_t *bias, RelBias *r)
+{
+    DenseShape sh;
+    attn_status_t st = check_dense_desc(d, &sh);
+    if (st || (st = check_relbias(bias, r))) return st;
+    if (d->s_q != 1 || d->mask != ATTN_CAUSAL_BOTTOM_RIGHT) return ATTN_ERR_INVALID;
+    if (sh.packed) return ATTN_ERR_UNSUPPORTED;
+    if (d->h > 65535 || d->b > 65535 || d->s_kv > INT32_MAX) return ATTN_ERR_UNSUPPORTED;  // grid y and z, int32 lengths
+    return ATTN_OK;
+}
+
+struct DecodeLayout {
+    int64_t chunk;
+    size_t ml, o, total;
+};
+
+DecodeLayout decode_layout(const attn_sdpa_desc_t *d)
+{
+    DecodeLayout L;
+    L.chunk = decode_chunk(d->b, d->h_kv, d->s_kv);
+    const int64_t chunks = decode_chunks(d->s_kv, L.chunk);
+    const size_t rows = chunks > 1 ? size_t(d->b) * size_t(d->h) * size_t(chunks) : 0;
+    L.ml = Workspace::align(64 * sizeof(uint32_t));
+    L.o = L.ml + Workspace::align(rows * 2 * sizeof(float));
+    L.total = L.o + Workspace::align(rows * size_t(d->d) * sizeof(float));
+    return L;
+}
+
+}  // namespace
+
+attn_status_t sdpa_relbias_decode_workspace_size(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, size_t *bytes)
+{
+    RelBias r;
+    const attn_status_t st = check_decode(desc, bias, &r);
+    if (st) return st;
+    if (!bytes) return ATTN_ERR_NULLPTR;
+    *bytes = decode_layout(desc).total;
+    return ATTN_OK;
+}
+
+attn_status_t sdpa_relbias_decode(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q, attn_view_t k,
+                                  attn_view_t v, const int32_t *lens, attn_view_t o, void *workspace,
+                                  size_t workspace_bytes, void *stream)
+{
+    DecodeArgs a;
+    std::memset(&a, 0, sizeof a);
+    attn_status_t st = check_decode(desc, bias, &a.bias);
+    if (st || (st = check_rel_table(a.bias))) return st;
+    const int64_t keys = desc->b * desc->s_kv;
+    if ((st = check_view(q, desc->b)) || (st = check_view(o, desc->b)) || (st = check_view(k, keys)) ||
+        (st = check_view(v, keys)))
+        return st;
+    if (reinterpret_cast<uintptr_t>(lens) & 3) return ATTN_ERR_ALIGN;
+    const DecodeLayout L = decode_layout(desc);
+    if ((st = check_ws(workspace, workspace_bytes, L.total))) return st;
+    a.dtype = desc->dtype;
+    a.b = desc->b; a.h = desc->h; a.h_kv = desc->h_kv; a.d = desc->d; a.cap = desc->s_kv;
+    a.chunk = L.chunk;
+    a.scale = float(desc->scale);
+    a.q = to_view(q, false); a.k = to_view(k, false); a.v = to_view(v, false); a.o = to_view(o, false);
+    a.lens = lens;
+    char *ws = static_cast<char *>(workspace);
+    a.status = reinterpret_cast<uint32_t *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
+    a.part_o = reinterpret_cast<float *>(ws + L.o);
+    return cuda_status(launch_relbias_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
 // --------------------------------------------------- query / key norm and rotation

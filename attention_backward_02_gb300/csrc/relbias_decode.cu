@@ -1,0 +1,319 @@
+// relbias_decode.cu -- attention of one new token per sequence over a key / value
+// cache, with the learned relative position bias.
+//
+// For query head x of sequence b, whose L = lens[b] cached keys end with the new
+// token's own (delta of key j = j - (L - 1)):
+//   s_j = scale q.k_j + table[bucket(delta)][x],  O = sum_j exp(s_j) v_j / sum_j exp(s_j).
+//
+// Bound by HBM: every cached key and value is read once (4 d bytes a key and kv
+// head) against 4 d G operations for the G query heads that share it.  A block
+// takes one (sequence, kv head) and a chunk of its keys, four warps striding over
+// it 16 keys at a time; chunks past a sequence's length end at once, so sequences
+// of any mix of lengths load the GPU by their keys.  The query heads of a group
+// are the rows of mma.sync m16n8k16 products (more than 16: several blocks), which
+// keeps the operations off the critical path at every G: the tensor cores idle
+// either way, and the tcgen05 path would need the tile staged through shared
+// memory.  K and V go from global memory to registers as 16-byte loads that are
+// operand fragments as they stand: the order of the contraction over d is free, so
+// a lane's 16 bytes of a key serve two steps, and V's key pairs are joined by byte
+// permutes, output columns taken in the order that makes a lane's 16 bytes eight
+// column tiles.
+// Each warp keeps a running maximum and sum (log2 units); the warps of a block join
+// through shared memory, the chunks of a sequence through fp32 partial results in
+// the workspace and a second kernel that adds them in order.
+#include <cmath>
+#include <type_traits>
+
+#include "relbias_decode.h"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kKeys = 16;  // keys of a warp's step
+
+__device__ __forceinline__ float ex2f(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes of the cache: read once, not kept in L1
+__device__ __forceinline__ uint4 load_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// c += a b for a 16 x 16 a (rows lane / 4 and lane / 4 + 8) and a 16 x 8 b
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    if (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t part(const uint4 &u, int k) { return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w; }
+
+// Length of sequence b, brought into [0, cap].
+__device__ __forceinline__ int64_t cached_len(const DecodeArgs &a, int64_t b)
+{
+    if (!a.lens) return a.cap;
+    const int64_t n = a.lens[b];
+    return n < 0 ? 0 : (n > a.cap ? a.cap : n);
+}
+
+// grid (chunks, kv heads x row blocks of 16 query heads, sequences).  ROWS: query heads of a group handled, 8
+// (the second half of the product's rows is zero and never looked at) or 16.
+template <class T, int D, int ROWS>
+__global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __grid_constant__ DecodeArgs a)
+{
+    constexpr int NP = D / 32;   // 64-byte pieces of a key
+    constexpr int NJ = D / 64;   // 128-byte pieces of a value
+    constexpr int NR = ROWS / 8; // rows of a lane
+    __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
+    __shared__ float sm_o[kWarps][ROWS][D];
+
+    pdl_trigger();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) {  // the call's only status writer
+        bool bad = false;
+        if (a.lens)
+            for (int64_t n = lane; n < a.b; n += 32) bad |= a.lens[n] < 0 || a.lens[n] > a.cap;
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) *a.status = bad ? ATTN_DEV_INDEX_RANGE : 0u;
+    }
+    const int64_t b = blockIdx.z, G = a.h / a.h_kv;
+    const int64_t nrb = (G + ROWS - 1) / ROWS, kvh = blockIdx.y / nrb, rb = blockIdx.y - kvh * nrb;
+    const int64_t h0 = kvh * G + rb * ROWS;                 // first query head of the block
+    const int rows = int(G - rb * ROWS < ROWS ? G - rb * ROWS : ROWS);
+    const int64_t len = cached_len(a, b);
+    const int64_t k0 = int64_t(blockIdx.x) * a.chunk, k1 = k0 + a.chunk < len ? k0 + a.chunk : len;
+    const bool direct = gridDim.x == 1;                     // no second kernel behind
+    if (k0 >= len && !(direct && len == 0)) return;
+
+    // the query rows as the first operand, and each row's bias of the end bucket
+    uint4 qa[NR][NP];
+    float past[NR];
+    int64_t head[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const bool on = g + 8 * i < rows;
+        head[i] = h0 + (on ? g + 8 * i : 0);
+        const T *p = static_cast<const T *>(a.q.ptr) + b * a.q.sb + head[i] * a.q.sh;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            qa[i][n] = on ? *reinterpret_cast<const uint4 *>(p + 32 * n + 8 * q) : make_uint4(0, 0, 0, 0);
+        past[i] = rel_table_value(a.bias, int64_t(a.bias.n - 1) * a.h + head[i]);
+    }
+    const T *kp = static_cast<const T *>(a.k.ptr) + b * a.k.sb + kvh * a.k.sh;
+    const T *vp = static_cast<const T *>(a.v.ptr) + b * a.v.sb + kvh * a.v.sh;
+    const float sc = a.scale * kLog2e;
+
+    float m[NR], l[NR];
+    float acc[NJ][8][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][e][i] = 0.f;
+
+    for (int64_t base = k0 + warp * kKeys; base < k1; base += kWarps * kKeys) {
+        const int left = int(k1 - base < kKeys ? k1 - base : kKeys);
+        uint4 kr[2][NP], vr[4][NJ];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                kr[t][n] = 8 * t + g < left ? load_stream(kp + (base + 8 * t + g) * a.k.ss + 32 * n + 8 * q) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = 2 * q + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                vr[i][j] = key < left ? load_stream(vp + (base + key) * a.v.ss + 64 * j + 8 * g) : make_uint4(0, 0, 0, 0);
+        }
+        // scores: lane (g, q) gets rows g, g + 8 and keys 2q, 2q + 1 of both tiles
+        float s[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const uint4 x = qa[0][n], y = NR > 1 ? qa[NR - 1][n] : make_uint4(0, 0, 0, 0);
+                mma16816<T>(s[t], x.x, y.x, x.y, y.y, kr[t][n].x, kr[t][n].y);
+                mma16816<T>(s[t], x.z, y.z, x.w, y.w, kr[t][n].z, kr[t][n].w);
+            }
+        }
+        const bool far = base + kKeys - 1 - (len - 1) <= a.bias.lo;
+        float x[NR][4], mx[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            mx[i] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 8 * (e >> 1) + 2 * q + (e & 1);
+                float bias = past[i];
+                if (!far) bias = rel_table_value(a.bias, int64_t(a.bias.bucket(base + key - (len - 1))) * a.h + head[i]);
+                x[i][e] = key < left ? fmaf(s[e >> 1][2 * i + (e & 1)], sc, bias) : -INFINITY;
+                mx[i] = fmaxf(mx[i], x[i][e]);
+            }
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        }
+        bool raise = false;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) raise |= mx[i] > m[i];
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const float nm = fmaxf(m[i], mx[i]);
+                const float f = nm == -INFINITY ? 1.f : ex2f(m[i] - nm);
+                m[i] = nm;
+                l[i] *= f;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[j][e][2 * i] *= f;
+                        acc[j][e][2 * i + 1] *= f;
+                    }
+            }
+        }
+        // P, rounded to the 16-bit type for the product with V; its sum is taken before
+        uint32_t pa[2][2] = {{0u, 0u}, {0u, 0u}};  // [key tile][row]
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const float ref = m[i] == -INFINITY ? 0.f : m[i];
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[e] = ex2f(x[i][e] - ref);
+                l[i] += p[e];
+            }
+            pa[0][i] = pack2<T>(p[0], p[1]);
+            pa[1][i] = pack2<T>(p[2], p[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
+                const uint32_t b0 = __byte_perm(part(vr[0][j], e >> 1), part(vr[1][j], e >> 1), sel);
+                const uint32_t b1 = __byte_perm(part(vr[2][j], e >> 1), part(vr[3][j], e >> 1), sel);
+                mma16816<T>(acc[j][e], pa[0][0], pa[0][1], pa[1][0], pa[1][1], b0, b1);
+            }
+    }
+
+    // join the warps: lane (g, q) holds columns 64 j + 16 q + 8 (i & 1) + e of row g + 8 (i >> 1)
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if (q == 0) {
+            sm_m[warp][g + 8 * i] = m[i];
+            sm_l[warp][g + 8 * i] = l[i];
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sm_o[warp][g + 8 * i][64 * j + 16 * q + 8 * c + e] = acc[j][e][2 * i + c];
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < rows * (D / 8); t += 32 * kWarps) {
+        const int r = t / (D / 8), c = t % (D / 8) * 8;
+        float mm = -INFINITY, ll = 0.f, o[8] = {};
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][r]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2f(sm_m[w][r] - ref);
+            ll += f * sm_l[w][r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(f, sm_o[w][r][c + e], o[e]);
+        }
+        if (direct) {
+            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            T *dst = static_cast<T *>(a.o.ptr) + b * a.o.sb + (h0 + r) * a.o.sh + c;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                                         pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+        } else {
+            const int64_t row = (b * a.h + h0 + r) * gridDim.x + blockIdx.x;
+            if (c == 0) a.part_ml[row] = make_float2(mm, ll);
+            float4 *dst = reinterpret_cast<float4 *>(a.part_o + row * D + c);
+            dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+// O of a (sequence, head) from its chunks' results, in chunk order: D / 8 lanes a row.
+template <class T, int D>
+__global__ void __launch_bounds__(128) relbias_decode_join_kernel(const __grid_constant__ DecodeArgs a, int chunks)
+{
+    constexpr int LPR = D / 8;
+    const int64_t row = (int64_t(blockIdx.x) * 128 + threadIdx.x) / LPR;
+    const int c = threadIdx.x % LPR * 8;
+    pdl_wait();
+    if (row >= a.b * a.h) return;
+    const int64_t b = row / a.h, hq = row - b * a.h;
+    const int n = int((cached_len(a, b) + a.chunk - 1) / a.chunk);
+    const float2 *ml = a.part_ml + row * chunks;
+    float m = -INFINITY, l = 0.f, o[8] = {};
+    for (int k = 0; k < n; ++k) m = fmaxf(m, ml[k].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int k = 0; k < n; ++k) {
+        const float f = ex2f(ml[k].x - ref);
+        l = fmaf(f, ml[k].y, l);
+        const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (row * chunks + k) * D + c);
+        const float4 u = src[0], v = src[1];
+        o[0] = fmaf(f, u.x, o[0]); o[1] = fmaf(f, u.y, o[1]); o[2] = fmaf(f, u.z, o[2]); o[3] = fmaf(f, u.w, o[3]);
+        o[4] = fmaf(f, v.x, o[4]); o[5] = fmaf(f, v.y, o[5]); o[6] = fmaf(f, v.z, o[6]); o[7] = fmaf(f, v.w, o[7]);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    T *dst = static_cast<T *>(a.o.ptr) + b * a.o.sb + hq * a.o.sh + c;
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                                 pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+}
+
+template <class T, int D, int ROWS> cudaError_t run(const DecodeArgs &a, cudaStream_t s)
+{
+    const int64_t chunks = decode_chunks(a.cap, a.chunk), G = a.h / a.h_kv;
+    const dim3 grid(unsigned(chunks), unsigned(a.h_kv * ((G + ROWS - 1) / ROWS)), unsigned(a.b));
+    cudaError_t e = launch_kernel(relbias_decode_kernel<T, D, ROWS>, grid, dim3(32 * kWarps), 0, s, false, a);
+    if (e != cudaSuccess || chunks == 1) return e;
+    const int64_t lanes = a.b * a.h * (D / 8);
+    return launch_kernel(relbias_decode_join_kernel<T, D>, dim3(unsigned((lanes + 127) / 128)), dim3(128), 0, s, true, a,
+                         int(chunks));
+}
+
+template <class T> cudaError_t pick(const DecodeArgs &a, cudaStream_t s)
+{
+    const bool wide = a.h / a.h_kv > 8;
+    if (a.d == 64) return wide ? run<T, 64, 16>(a, s) : run<T, 64, 8>(a, s);
+    return wide ? run<T, 128, 16>(a, s) : run<T, 128, 8>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_relbias_decode(const DecodeArgs &a, cudaStream_t s)
+{
+    return a.dtype == ATTN_F16 ? pick<__half>(a, s) : pick<__nv_bfloat16>(a, s);
+}
+
+}  // namespace attn

@@ -14,6 +14,8 @@
  *   sdpa_relbias_fwd_stats, the dense forward and backward with a learned relative
  *   sdpa_relbias_bwd        position bias by buckets added to the scores, and the
  *                           bias table's gradient.
+ *   sdpa_relbias_decode     the same attention for one new token per sequence over
+ *                           a key / value cache.
  *   qk_norm_rope_fwd, _bwd  RMS norm of every query / key head with the rotary
  *                           position embedding in the same pass, and its gradient:
  *                           what makes Q and K for the calls above and takes their
@@ -78,7 +80,8 @@ typedef enum {
 /* Bits of the device status word (attn_query_status).                        */
 #define ATTN_DEV_TIMEOUT      0x1u  /* a bounded barrier wait ran out; the CTA quit */
 #define ATTN_DEV_INDEX_RANGE  0x2u  /* a topk index outside [0, S2_b / block_size), or a
-                                       position outside [0, max_pos)                 */
+                                       position outside [0, max_pos), or a cache
+                                       length outside [0, s_kv]                      */
 #define ATTN_DEV_INDEX_DUP    0x4u  /* a block listed twice for one (token, kv head) */
 
 typedef enum { ATTN_F16 = 0, ATTN_BF16 = 1 } attn_dtype_t;
@@ -347,6 +350,22 @@ attn_status_t sdpa_relbias_bwd(const attn_sdpa_desc_t *desc, const attn_relbias_
                                attn_view_t v, attn_view_t o, attn_view_t dO, const float *lse, attn_view_t dQ,
                                attn_view_t dK, attn_view_t dV, float *dtable, void *workspace, size_t workspace_bytes,
                                void *stream);
+
+/* One new token of every sequence over a key / value cache: O of the biased
+ * attention above, without stats.  desc: s_q = 1, s_kv = the keys a sequence's
+ * cache has room for, mask = ATTN_CAUSAL_BOTTOM_RIGHT (the new token is the last of
+ * its sequence), fixed-length mode; deterministic is ignored (the result is
+ * always bitwise reproducible).  q, o: [b,h,1,d]; k, v: [b,h_kv,s_kv,d] views.
+ * lens: device int32 [b], the keys cached for each sequence, the new token's own
+ * among them (NULL: s_kv for all); read on the device, so a captured call
+ * follows a growing cache.  Keys from lens[b] on are not read.  A sequence
+ * without keys gets O = 0; a length outside [0, s_kv] is brought into it and
+ * sets ATTN_DEV_INDEX_RANGE.                                                */
+attn_status_t sdpa_relbias_decode_workspace_size(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias,
+                                                 size_t *bytes);
+attn_status_t sdpa_relbias_decode(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q,
+                                  attn_view_t k, attn_view_t v, const int32_t *lens, attn_view_t o, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 /* Norm and rotation of the query and key heads.  Like the relative-bias calls,
  * these have no counterpart on the pages: they are what a model runs between

@@ -159,3 +159,26 @@ def test_relbias_calls(ab):
         need = ab.sdpa_relbias_workspace_size(desc, _bias(ab))[call is bwd]
         assert call(ws=None) == WORKSPACE and call(ws=A + 16) == WORKSPACE and call(n=need - 1) == WORKSPACE
     assert bwd(dt=None) == NULLPTR and bwd(dt=A + 2) == ALIGN
+
+
+def test_decode_refusals(ab):
+    lib = ab._lib.load()
+    size = lambda d, b=None: lib.sdpa_relbias_decode_workspace_size(C.byref(d), C.byref(b or _bias(ab)), C.byref(C.c_size_t()))
+    base = dict(s_q=1, s_kv=4096, mask=ab.ATTN_CAUSAL_BOTTOM_RIGHT)
+    ok = _sdpa(ab, **base)
+    assert size(ok) == OK and size(_sdpa(ab, **{**base, "s_kv": 0})) == OK
+    assert size(_sdpa(ab, **{**base, "s_q": 2})) == INVALID and size(_sdpa(ab, **{**base, "mask": 0})) == INVALID
+    assert size(_sdpa(ab, **{**base, "mask": 1})) == INVALID and size(ok, _bias(ab, num_buckets=3)) == INVALID
+    assert size(_sdpa(ab, **{**base, "d": 192})) == UNSUPPORTED
+    assert size(_sdpa(ab, **{**base, "s_kv": 1 << 31, "b": 1, "h_kv": 1})) == UNSUPPORTED
+    packed = _sdpa(ab, **base, cu_seqlens_q=[1, 2], cu_seqlens_kv=[10, 30])
+    assert size(packed) == UNSUPPORTED
+    assert lib.sdpa_relbias_decode_workspace_size(C.byref(ok), C.byref(_bias(ab)), None) == NULLPTR
+    v = ab.attn_view_t(A, 4096 * 128, 64, 128)
+    call = lambda i=None, x=None, lens=A, b=None, ws=A, n=1 << 30: lib.sdpa_relbias_decode(
+        C.byref(ok), C.byref(b or _bias(ab)), *[x if j == i else v for j in range(3)], lens, x if i == 3 else v, ws, n, None)
+    for i in range(4):
+        assert call(i, ab.attn_view_t(None, 0, 64, 128)) == NULLPTR
+        assert call(i, ab.attn_view_t(A + 8, 0, 64, 128)) == ALIGN and call(i, ab.attn_view_t(A, 4, 64, 128)) == ALIGN
+    assert call(lens=A + 2) == ALIGN and call(b=_bias(ab, table=None)) == NULLPTR
+    assert call(ws=None) == WORKSPACE and call(ws=A + 8) == WORKSPACE and call(n=300) == WORKSPACE
