@@ -66,9 +66,19 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_kernel(const QkNormArgs a
 {
     constexpr int D = NC * 64;
     __shared__ float xch[ROPE == kHalves ? kWarps * kItemHeads * D : 1];
-    const int sd = int(blockIdx.x) >= a.side[0].blocks;
+    if (blockIdx.x == 0) {  // the status word: one block looks over the positions beside the others' work
+        bool bad = false;
+        if (ROPE != kNoRope && a.pos)
+            for (int64_t t = threadIdx.x; t < a.b * a.s; t += 32 * kWarps) bad |= a.pos[t] < 0 || a.pos[t] >= a.max_pos;
+        if (ROPE != kNoRope && !a.pos) bad = a.s > a.max_pos;
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.status = bad ? ATTN_DEV_INDEX_RANGE : 0u;
+        return;
+    }
+    const int bid = int(blockIdx.x) - 1;
+    const int sd = bid >= a.side[0].blocks;
     const QkSide &s = a.side[sd];
-    const int cta = int(blockIdx.x) - (sd ? a.side[0].blocks : 0);
+    const int cta = bid - (sd ? a.side[0].blocks : 0);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, grp = lane / 8, l = lane % 8;
     float *const mine = xch + (ROPE == kHalves ? (warp * kItemHeads + grp) * D : 0);
 
@@ -117,7 +127,6 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_kernel(const QkNormArgs a
         if (ROPE != kNoRope) {
             const int32_t p = a.pos ? a.pos[t] : int32_t(i);
             valid = p >= 0 && p < a.max_pos;
-            if (!valid && lane == 0) raise_flag(a.status, ATTN_DEV_INDEX_RANGE);
             const float *cr = a.cos + int64_t(valid ? p : 0) * (a.rot / 2), *sr = a.sin + int64_t(valid ? p : 0) * (a.rot / 2);
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
@@ -275,15 +284,10 @@ template <class T, int NC, int ROPE, bool BWD> cudaError_t run(QkNormArgs a, cud
         }
         a.side[k].blocks = int(n);
     }
-    const int grid = a.side[0].blocks + a.side[1].blocks;
+    const int grid = 1 + a.side[0].blocks + a.side[1].blocks;
     if (BWD) a.side[1].part = a.side[0].part + int64_t(a.side[0].blocks) * a.d;
-    cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), st);
-    if (e != cudaSuccess) return e;
-    if (grid > 0) {
-        e = launch_kernel(qk_norm_kernel<T, NC, ROPE, BWD, U>, dim3(grid), dim3(32 * kWarps), 0, st, false, a);
-        if (e != cudaSuccess) return e;
-    }
-    if (BWD && (a.side[0].dw || a.side[1].dw))
+    cudaError_t e = launch_kernel(qk_norm_kernel<T, NC, ROPE, BWD, U>, dim3(grid), dim3(32 * kWarps), 0, st, false, a);
+    if (e == cudaSuccess && BWD && (a.side[0].dw || a.side[1].dw))
         e = launch_kernel(qk_norm_dw_kernel, dim3(unsigned(a.d / 32), 2), dim3(1024), 0, st, true, a);
     return e;
 }
