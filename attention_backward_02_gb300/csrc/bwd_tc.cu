@@ -659,6 +659,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                         // relative bias, near: entry r - c + BM - 1 of the window
                         const float *wrow = win + (kind == kRelNear ? r + BM - 1 - c0 : 0);
                         const float wfar = kBias ? win[0] : 0.f;
+                        // two copies of the loop with a bias: a test of the tile's kind per element pair, with
+                        // the shuffles behind it, cost more than the arithmetic
+                        auto compute = [&](auto near_tag) {
+                        constexpr bool kNear = decltype(near_tag)::value;
 #pragma unroll
                         for (int cc = 0; cc < NCH; ++cc) {
                             const int col0 = c0 + cc * 16, cur = cc & 1;
@@ -680,11 +684,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                     const int e = 4 * q4 + 2 * h2, c = col0 + e;
                                     if (kBias) {
                                         const int k = cc * 16 + e;  // column within the group of 32
-                                        float b0 = wfar, b1 = wfar;
-                                        if (kind == kRelNear) {
-                                            b0 = wrow[-k];
-                                            b1 = wrow[-k - 1];
-                                        }
+                                        const float b0 = kNear ? wrow[-k] : wfar, b1 = kNear ? wrow[-k - 1] : wfar;
                                         float x0 = fmaf(__uint_as_float(sbuf[cur][e]), sc, b0) - lse4[2 * h2];
                                         float x1 = fmaf(__uint_as_float(sbuf[cur][e + 1]), sc, b1) - lse4[2 * h2 + 1];
                                         float g0 = __uint_as_float(dbuf[cur][e]) - dv4[2 * h2];
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                         const float p0 = ex2(x0), p1 = ex2(x1), ds0 = p0 * g0, ds1 = p1 * g1;
                                         pk[cc * 8 + 2 * q4 + h2] = pack2<T>(p0, p1);
                                         dk[2 * q4 + h2] = pack2<T>(ds0, ds1);
-                                        if (kind == kRelNear) {
+                                        if (kNear) {
                                             // the sum of diagonal lane - column goes one lane up per column;
                                             // lane 31's is complete
                                             if (k > 0) {
@@ -733,6 +733,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                 st_shared_v4(adS + off, dk[4 * q2], dk[4 * q2 + 1], dk[4 * q2 + 2], dk[4 * q2 + 3]);
                             }
                         }
+                        };
+                        if (kBias && kind == kRelNear) compute(std::true_type{});
+                        else compute(std::false_type{});
                     }
                     if (!kEarlyFree) release();
                     if (kBias && ok) add_block(kind, run, wcode, c0);
