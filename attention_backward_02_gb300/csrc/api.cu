@@ -333,13 +333,11 @@ attn_status_t dense_fwd_call(const attn_sdpa_desc_t *desc, const RelBias *bias, 
     FixedGeo fg;
     static thread_local PackedGeo pg;
     fill_geo(desc, sh, &fg, &pg);
+    if (!bias) return cuda_status(sh.packed ? launch_dense_fwd(a, pg, s) : launch_dense_fwd(a, fg, s));
     RelArgs rel;
-    if (bias) {
-        fill_rel(&rel, desc, sh, *bias, RL, workspace, false, nullptr);
-        if ((st = cuda_status(launch_rel_expand(rel, s)))) return st;
-    }
-    const RelArgs *rp = bias ? &rel : nullptr;
-    return cuda_status(sh.packed ? launch_dense_fwd(a, pg, s, rp) : launch_dense_fwd(a, fg, s, rp));
+    fill_rel(&rel, desc, sh, *bias, RL, workspace, false, nullptr);
+    if ((st = cuda_status(launch_rel_expand(rel, s)))) return st;
+    return cuda_status(sh.packed ? launch_relbias_fwd(a, rel, pg, s) : launch_relbias_fwd(a, rel, fg, s));
 }
 
 // sdpa_bwd (bias NULL) and sdpa_relbias_bwd

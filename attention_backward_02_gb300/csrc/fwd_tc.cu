@@ -28,14 +28,6 @@
 // O / l and LSE = (m + log2 l) / log2 e come out at the end (the halves add
 // their sums first); a row that sees no key has O = 0 and LSE = +inf.
 //
-// Relative position bias (kBias): the scores of a tile take a window of the
-// head's expanded bias (log2 units), element (row r, column c) entry
-// c - r + 127.  The softmax threads load the next tile's 255 entries into one of
-// two shared buffers (one load and one store a thread, made visible by the
-// barrier that swaps the halves' maxima) and read them without bank conflicts,
-// consecutive rows consecutive entries.  A tile that lies in one end bucket
-// whole takes its bias from a register, folded into the scaling.
-//
 // Roles (11 warps): warp 0 issues the TMA loads of Q (once) and K (through an
 // NSK-stage ring), warp 10 those of V (an NSV-stage ring of its own: a K stage
 // is free once S has read it, a V stage only once O += P V has), warp 1 the
@@ -47,7 +39,6 @@
 #include <type_traits>
 
 #include "plan.h"
-#include "relbias.h"
 #include "sm103.cuh"
 #include "tc_util.cuh"
 #include "tmap.h"
@@ -69,8 +60,7 @@ struct FwdCfg {
     static constexpr int OFF_BAR = OFF_V + NSV * TILE_BYTES;
     static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
     static constexpr int OFF_XM = OFF_MISC + 64;        // [2 tile parities][2 halves][128 rows] floats
-    static constexpr int OFF_WIN = OFF_XM + 2 * 2 * 128 * 4;  // kBias: [2 tile parities][256] bias window floats
-    static constexpr int SMEM = OFF_WIN + 2 * 256 * 4;
+    static constexpr int SMEM = OFF_XM + 2 * 2 * 128 * 4;
     // room to align the base to 1024; at least half the SM's shared memory, so one CTA (holding all
     // 512 TMEM columns) runs per SM
     static constexpr int SMEM_ALLOC = SMEM + 1024 > 116 * 1024 ? SMEM + 1024 : 116 * 1024;
@@ -84,15 +74,12 @@ struct FwdCfg {
 struct FwdParams {
     CUtensorMap tm_q, tm_k, tm_v;
     DenseArgs a;
-    RelArgs rel;  // kBias
 };
 
 template <class Geo> struct FwdPacked : std::false_type {};
 template <> struct FwdPacked<PackedGeo> : std::true_type {};
 
-// kBias: a relative position bias is added to the scores.  A template parameter, so the plain forward carries
-// none of its code.
-template <class T, int D, class Geo, bool kBias>
+template <class T, int D, class Geo>
 __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     dense_fwd_tc_kernel(const __grid_constant__ FwdParams p, const Geo geo)
 {
@@ -272,27 +259,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        // relative bias: the window of key tile j starts at delta j BN - row0; this thread's entry of it
-        float *win = reinterpret_cast<float *>(smem + Cfg::OFF_WIN);
-        const int wt = int(threadIdx.x) - 64;
-        int64_t row0 = 0;
-        const float *rel = nullptr;
-        float past = 0.f, future = 0.f;
-        auto window = [&](int j) -> float {
-            const int64_t dmin = int64_t(j) * BN - row0;
-            return rel_tile(p.rel.b, dmin, 255) == kRelNear ? __ldcg(rel + (dmin + wt - (p.rel.b.lo - kRelPad))) : 0.f;
-        };
-        if (kBias) {
-            row0 = i0 + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0) + 127;
-            rel = p.rel.rel + hq * p.rel.stride;
-            pdl_wait();  // the bias has been expanded
-            past = __ldcg(rel);
-            future = __ldcg(rel + p.rel.stride - 1);
-            win[wt] = window(0);
-            named_bar_sync(1, 256);
-        }
         for (int j = 0; j < n_kt; ++j) {
-            const float next_win = kBias && j + 1 < n_kt ? window(j + 1) : 0.f;
             const int sb = j & 1;
             const uint32_t tS = tmem + lane_addr + Cfg::T_S + sb * 128;
             const int64_t lim64 = kmax - int64_t(j) * BN;  // columns <= lim are visible
@@ -310,29 +277,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                 tmem_ld32(tS + half * HC + 32, v1);
                 tmem_ld_wait_regs(v0);
                 tmem_ld_wait_regs(v1);
-                if (kBias) {
-                    const RelTile kind = rel_tile(p.rel.b, int64_t(j) * BN - row0, 255);
-                    if (kind == kRelNear) {
-                        const float *w = win + sb * 256 + half * HC - r + 127;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            x[e] = half * HC + e <= lim ? fmaf(__uint_as_float(v0[e]), c, w[e]) : -INFINITY;
-                            x[32 + e] = half * HC + 32 + e <= lim ? fmaf(__uint_as_float(v1[e]), c, w[32 + e]) : -INFINITY;
-                        }
-                    } else {
-                        const float w = kind == kRelPast ? past : future;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            x[e] = half * HC + e <= lim ? fmaf(__uint_as_float(v0[e]), c, w) : -INFINITY;
-                            x[32 + e] = half * HC + 32 + e <= lim ? fmaf(__uint_as_float(v1[e]), c, w) : -INFINITY;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        x[e] = half * HC + e <= lim ? __uint_as_float(v0[e]) * c : -INFINITY;
-                        x[32 + e] = half * HC + 32 + e <= lim ? __uint_as_float(v1[e]) * c : -INFINITY;
-                    }
+                for (int e = 0; e < 32; ++e) {
+                    x[e] = half * HC + e <= lim ? __uint_as_float(v0[e]) * c : -INFINITY;
+                    x[32 + e] = half * HC + 32 + e <= lim ? __uint_as_float(v1[e]) * c : -INFINITY;
                 }
 #pragma unroll
                 for (int e = 0; e < HC; ++e) mx = fmaxf(mx, x[e]);
@@ -343,7 +291,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             {
                 float *slot = xm + (j & 1) * 256;  // alternate by tile: the other half may still read the last
                 slot[half * 128 + r] = mx;
-                if (kBias) win[(sb ^ 1) * 256 + wt] = next_win;  // last read a tile ago, before that tile's barrier
                 named_bar_sync(1, 256);
                 mx = fmaxf(slot[r], slot[128 + r]);
             }
@@ -458,7 +405,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
 
 namespace {
 
-template <class T, int D, class Geo> cudaError_t run_fwd(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
+template <class T, int D, class Geo> cudaError_t run_fwd(const DenseArgs &a, const Geo &g, cudaStream_t s)
 {
     using Cfg = FwdCfg<D>;
     constexpr bool packed = FwdPacked<Geo>::value;
@@ -469,7 +416,6 @@ template <class T, int D, class Geo> cudaError_t run_fwd(const DenseArgs &a, con
     if (units > INT32_MAX) return cudaErrorInvalidValue;
     FwdParams prm;
     prm.a = a;
-    if (rel) prm.rel = *rel;
     const int64_t nb = packed ? 1 : a.nseq;
     const int64_t sq = packed ? a.t_q : g.q_len(0), skv = packed ? a.t_kv : g.kv_len(0);
     if (!tmap_view16(&prm.tm_q, a.q, a.dtype, D, sq, a.h, nb, Cfg::BM)) return cudaErrorInvalidValue;
@@ -480,30 +426,23 @@ template <class T, int D, class Geo> cudaError_t run_fwd(const DenseArgs &a, con
     } else {
         prm.tm_k = prm.tm_v = prm.tm_q;  // never read: no key tiles
     }
-    auto k = rel ? dense_fwd_tc_kernel<T, D, Geo, true> : dense_fwd_tc_kernel<T, D, Geo, false>;
+    auto k = dense_fwd_tc_kernel<T, D, Geo>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    // with a bias the expanding kernel ahead clears the status word, and this one starts beside it
-    if (!rel && (e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;
-    return launch_kernel(k, dim3(unsigned(units)), dim3(Cfg::THREADS), Cfg::SMEM_ALLOC, s, rel != nullptr, prm, g);
+    if ((e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;
+    return launch_kernel(k, dim3(unsigned(units)), dim3(Cfg::THREADS), Cfg::SMEM_ALLOC, s, false, prm, g);
 }
 
-template <class Geo> cudaError_t fwd(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
+template <class Geo> cudaError_t fwd(const DenseArgs &a, const Geo &g, cudaStream_t s)
 {
     if (a.d == 64)
-        return a.dtype == ATTN_F16 ? run_fwd<__half, 64>(a, rel, g, s) : run_fwd<__nv_bfloat16, 64>(a, rel, g, s);
-    return a.dtype == ATTN_F16 ? run_fwd<__half, 128>(a, rel, g, s) : run_fwd<__nv_bfloat16, 128>(a, rel, g, s);
+        return a.dtype == ATTN_F16 ? run_fwd<__half, 64>(a, g, s) : run_fwd<__nv_bfloat16, 64>(a, g, s);
+    return a.dtype == ATTN_F16 ? run_fwd<__half, 128>(a, g, s) : run_fwd<__nv_bfloat16, 128>(a, g, s);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel)
-{
-    return fwd(a, rel, g, s);
-}
-cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel)
-{
-    return fwd(a, rel, g, s);
-}
+cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s) { return fwd(a, g, s); }
+cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s) { return fwd(a, g, s); }
 
 }  // namespace attn

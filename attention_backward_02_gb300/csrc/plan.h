@@ -132,8 +132,10 @@ cudaError_t launch_dense_bwd_main(const DenseArgs &a, const FixedGeo &g, cudaStr
 cudaError_t launch_dense_bwd_main(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
 cudaError_t launch_dq_finalize(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
 cudaError_t launch_dq_finalize(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
-cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
-cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
+cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
+cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
+cudaError_t launch_relbias_fwd(const DenseArgs &a, const RelArgs &rel, const FixedGeo &g, cudaStream_t s);
+cudaError_t launch_relbias_fwd(const DenseArgs &a, const RelArgs &rel, const PackedGeo &g, cudaStream_t s);
 
 cudaError_t launch_nsa_bwd(const NsaArgs &a, const PackedGeo &g, cudaStream_t s, cudaEvent_t before,
                            cudaEvent_t after);
