@@ -51,15 +51,20 @@
 //
 // Relative position bias (kBias): the bias of a tile is a window of the head's
 // expanded bias (log2 units), element (key row r, query column c) entry r - c +
-// const; the window rides in the Q / dO ring stage.  The gradient of the bias
-// table is the sum of dS over each bucket, taken from the fp32 dS before it is
-// rounded (P and dS are computed in fp32 for both types here): a tile in one end
-// bucket whole adds its dS to one register; otherwise a warp sums its 32 x 32
-// blocks along their diagonals, passing one running sum from lane to lane per
-// column, then adds runs of diagonals of one bucket and the runs to its own row of
-// buckets in shared memory.  Each warp stores its row once per (key tile, head);
-// a kernel behind this one adds them up in a fixed order, so the table's gradient
-// is bitwise reproducible in every dQ mode.
+// const; the window rides in the Q / dO ring stage, and beside it a window of
+// bucket codes.  The gradient of the bias table is the sum of dS over each bucket,
+// taken from the fp32 dS before it is rounded (P and dS are computed in fp32 for
+// both types here, two columns an instruction).  A warp works on blocks of 32 key
+// rows x 32 query columns, whose 63 deltas are consecutive.  A block in one bucket
+// takes its bias from a register and adds its dS to one running sum a thread.
+// Otherwise the block is summed along its diagonals, one sum passed from lane to
+// lane per column; then runs of diagonals of one bucket are added up and the runs
+// added to the warp's row of buckets in shared memory, both behind the arrival that
+// lets the tile's GEMMs go.  Each warp stores its row once per (key tile, head); a
+// kernel behind this one adds them up in a fixed order, so the table's gradient is
+// bitwise reproducible in every dQ mode.  Packed sequences: rows of a tile that
+// belong to the next sequence are set to zero in shared memory before the GEMMs
+// that would multiply them by P = dS = 0, so that no infinity or NaN crosses over.
 //
 // Every barrier wait is bounded (about a second).  On a timeout the thread
 // sets ATTN_DEV_TIMEOUT in the status word and an abort flag in shared
@@ -124,7 +129,7 @@ struct TcCfg {
     static constexpr int OFF_WIN = SMEM;                      // NST x (bias, codes)
     static constexpr int OFF_HIST = OFF_WIN + NST * 2 * WIN_BYTES;
     static constexpr int OFF_DIAG = OFF_HIST + NSW * kRelMaxBuckets * 4;
-    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * 32 * 4 + 1024;
+    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * NG * 32 * 4 + 1024;
     static_assert(WIN_BYTES % 16 == 0 && SMEM % 16 == 0 && SMEM_ALLOC_BIAS <= 227 * 1024, "shared memory budget");
     static_assert(kRelPad >= BN + BM + 4, "a near tile's window lies within the expanded bias");
     static constexpr int T_S = 0, T_DP = BM, T_P = 2 * BM, T_DV = 2 * BM + BM / 2, T_DK = T_DV + D,
@@ -287,6 +292,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
 #define ATTN_END_UNITS }
 
     uint8_t *sK = smem + Cfg::OFF_K, *sV = smem + Cfg::OFF_V, *sX = smem + Cfg::OFF_X;
+    // kBias: entry of the expanded bias at which the window of a tile whose first delta is dmin starts; of a tile
+    // in one end bucket whole, a place in the pad where every entry is that bucket's
+    auto window_start = [&](int64_t dmin) -> int64_t {
+        const RelTile kind = rel_tile(p.rel.b, dmin, BN + BM - 1);
+        return kind == kRelNear ? dmin - (p.rel.b.lo - kRelPad) : (kind == kRelPast ? 0 : p.rel.stride - Cfg::WIN_BYTES / 4);
+    };
 
     if (warp == 0) {
         // ================================================= TMA producer
@@ -312,11 +323,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     if (x == 1 && ok && !(ok = mbar_wait(&q_full[0], 0, abort))) flag_abort(abort, a.status);
                     if (!ok) return;
                     const int64_t hq = g * G + it / nq, i0 = int64_t(qt0 + it % nq) * BM;
-                    // relative bias: the tile's window, from its first delta on; of a tile in one end bucket
-                    // the table's first or last entries alone
-                    const int64_t dmin = j0 - i0 - (BM - 1) - (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0);
-                    const RelTile kind = kBias ? rel_tile(p.rel.b, dmin, BN + BM - 1) : kRelPast;
-                    const uint32_t win_bytes = !kBias ? 0u : (kind == kRelNear ? 2u * Cfg::WIN_BYTES : 16u);
+                    const uint32_t win_bytes = kBias ? 2u * Cfg::WIN_BYTES : 0u;
                     uint8_t *sQ = smem + Cfg::OFF_Q + st * Cfg::Q_BYTES, *sdO = smem + Cfg::OFF_DO + st * Cfg::Q_BYTES;
                     q_armed = x + 1;
                     mbar_arrive_expect_tx(&q_full[st], 2 * Cfg::Q_BYTES + 2 * BM * 4 + win_bytes);
@@ -331,14 +338,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     }
                     bulk_load(smem + Cfg::OFF_LSE + st * BM * 4, a.lse2 + wrow, BM * 4, &q_full[st]);
                     bulk_load(smem + Cfg::OFF_DVEC + st * BM * 4, a.dvec + wrow, BM * 4, &q_full[st]);
-                    if (kBias) {
-                        const float *rel = p.rel.rel + hq * p.rel.stride;
+                    if (kBias) {  // the windows from the tile's first delta on, 16-byte aligned
                         uint8_t *win = smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES;
-                        const int64_t w0 = kind == kRelNear ? (dmin - (p.rel.b.lo - kRelPad)) & ~int64_t(3)
-                                                            : (kind == kRelPast ? 0 : p.rel.stride - 4);
-                        bulk_load(win, rel + w0, kind == kRelNear ? Cfg::WIN_BYTES : 16, &q_full[st]);
-                        if (kind == kRelNear)
-                            bulk_load(win + Cfg::WIN_BYTES, p.rel.code + w0, Cfg::WIN_BYTES, &q_full[st]);
+                        const int64_t w0 = window_start(j0 - i0 - (BM - 1) - (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0)) &
+                                           ~int64_t(3);
+                        bulk_load(win, p.rel.rel + hq * p.rel.stride + w0, Cfg::WIN_BYTES, &q_full[st]);
+                        bulk_load(win + Cfg::WIN_BYTES, p.rel.code + w0, Cfg::WIN_BYTES, &q_full[st]);
                     }
                 };
                 // the first query tile does not need the key tile: load it before waiting for K / V
@@ -528,10 +533,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             if (tc) tc_fence_after();
         };
 
-        // relative bias: this warp's bucket sums and finished diagonals, and the two end buckets' sums
+        // relative bias: this warp's bucket sums and finished diagonals; the bucket of the last block that lay in
+        // one, and each thread's sum since
         float *hist = reinterpret_cast<float *>(smem + Cfg::OFF_HIST) + (warp - 2) * kRelMaxBuckets;
-        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_DIAG) + (warp - 2) * 32;
-        float sum_past = 0.f, sum_future = 0.f;
+        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_DIAG) + (warp - 2) * NG * 32;
+        float one_sum = 0.f;
+        uint32_t one_bucket = 0;
         if (kBias) {
             for (int n = lane; n < kRelMaxBuckets; n += 32) hist[n] = 0.f;
             __syncwarp();
@@ -548,37 +555,22 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             if (lane == 0 || (code >> 16)) hist[code & 255u] += v;
             __syncwarp();
         };
-        // the dS of a 32 x 32 block: queries c0 .. c0 + 31 of the tile, this warp's key rows
-        auto add_block = [&](RelTile kind, float run, const uint32_t *wcode, int c0) {
-            if (kind == kRelPast) {
-                sum_past += run;
-            } else if (kind == kRelFuture) {
-                sum_future += run;
-            } else {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
-                __syncwarp();
-                const uint32_t *code = wcode + lg * 32 + BM - 1 - c0 + lane;  // of diagonal lane
-                add_runs(run, code[-31]);
-                add_runs(lane < 31 ? diag[30 - lane] : 0.f, code[1]);
-            }
+        auto add_one = [&]() {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) one_sum += __shfl_xor_sync(0xffffffffu, one_sum, o);
+            if (lane == 0) hist[one_bucket] += one_sum;
+            __syncwarp();
+            one_sum = 0.f;
         };
         // end of a (key tile, head): the sums go to their row of the workspace
         auto flush = [&](int64_t row, int64_t head) {
-            for (int o = 16; o > 0; o >>= 1) {
-                sum_past += __shfl_xor_sync(0xffffffffu, sum_past, o);
-                sum_future += __shfl_xor_sync(0xffffffffu, sum_future, o);
-            }
-            if (lane == 0) {
-                hist[p.rel.b.n - 1] += sum_past;
-                hist[p.rel.b.bidirectional ? p.rel.b.buckets - 1 : 0] += sum_future;
-            }
-            __syncwarp();
+            add_one();
             float *dst = p.rel.part + ((row * a.h + head) * 8 + (warp - 2)) * p.rel.b.buckets;
             for (int n = lane; n < p.rel.b.buckets; n += 32) {
                 dst[n] = hist[n];
                 hist[n] = 0.f;
             }
             __syncwarp();
-            sum_past = sum_future = 0.f;
         };
 
         ATTN_FOR_EACH_UNIT
@@ -611,11 +603,16 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                 // first visible query column of this key row; everything is masked past the sequence
                 const int64_t cmin64 = !row_ok ? INT64_MAX : (a.mask ? j - shift - i0 : INT64_MIN);
                 const int cmin = int(cmin64 < -1 ? -1 : (cmin64 > BM ? BM : cmin64));
-                const int64_t dmin = j0 - i0 - (BM - 1) - shift;  // kBias: the tile's first delta
-                const RelTile kind = kBias ? rel_tile(p.rel.b, dmin, BN + BM - 1) : kRelPast;
-                const float *win = reinterpret_cast<const float *>(smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES) +
-                                   (kind == kRelNear ? int(uint32_t(dmin - (p.rel.b.lo - kRelPad)) & 3u) : 0);
+                // kBias: the tile's windows; columns from cmax on lie past the sequence's queries; what is left of
+                // the tile's table gradient when its GEMMs are let go (per column group: two diagonal sums a lane
+                // and their codes)
+                const float *win = reinterpret_cast<const float *>(smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES);
+                if (kBias) win += uint32_t(window_start(j0 - i0 - (BM - 1) - shift)) & 3u;
                 const uint32_t *wcode = reinterpret_cast<const uint32_t *>(win) + Cfg::WIN_BYTES / 4;
+                const int cmax = kBias && lq - i0 < BM ? int(lq - i0) : BM;
+                float left_a[NG], left_b[NG];
+                uint32_t code_a[NG], code_b[NG];
+                bool several[NG];
 #pragma unroll
                 for (int q = 0; q < NG; ++q) {
                     const int rel = NH == NG ? q : 0;  // release group of these columns
@@ -623,14 +620,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     else if (q == 0) tc_fence_after();
                     const int c0 = q * (BM / NG) + half * GW;
                     uint32_t pk[GW / 2];  // P^T of this column group, packed
-                    float run = 0.f;  // kBias, near tile: running sum of a diagonal; else: this thread's sum of dS
                     // S^T / dP^T of the group in chunks of 16 columns.  With one group a thread (d = 128)
                     // the whole group is loaded at once and its TMEM columns released before P / dS are
                     // computed, so the next tile's S^T / dP^T GEMMs overlap this tile's element-wise work;
                     // with two (d = 64) chunk cc + 1 is loaded while chunk cc is computed and the columns
-                    // are released after the group (the early release measured slower there)
+                    // are released after the group (the early release measured slower there; so it does with a
+                    // bias at d = 128, whose arithmetic needs the registers: 816 us against 926 at b2 h32 s4096)
                     constexpr int NCH = GW / 16;
-                    constexpr bool kEarlyFree = NG == 1 && NCH == 2;
+                    constexpr bool kEarlyFree = NG == 1 && NCH == 2 && !kBias;
                     uint32_t sbuf[2][16], dbuf[2][16];
                     auto release = [&]() {
                         if (NH == NG || q == NG - 1) {
@@ -655,90 +652,132 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                         tmem_ld16(tmem + lane_addr + Cfg::T_DP + c0, dbuf[0]);
                     }
                     if (ok) {
-                        const bool any_mask = __any_sync(0xffffffffu, cmin > c0);
-                        // relative bias, near: entry r - c + BM - 1 of the window
-                        const float *wrow = win + (kind == kRelNear ? r + BM - 1 - c0 : 0);
-                        const float wfar = kBias ? win[0] : 0.f;
-                        // two copies of the loop with a bias: a test of the tile's kind per element pair, with
-                        // the shuffles behind it, cost more than the arithmetic
-                        auto compute = [&](auto near_tag) {
-                        constexpr bool kNear = decltype(near_tag)::value;
-#pragma unroll
-                        for (int cc = 0; cc < NCH; ++cc) {
-                            const int col0 = c0 + cc * 16, cur = cc & 1;
+                        const bool any_mask = __any_sync(0xffffffffu, cmin > c0) || (kBias && cmax < c0 + GW);
+                        // chunk cc's S^T / dP^T has arrived; the next chunk's loads go out
+                        auto fetch = [&](int cc) {
                             if (!kEarlyFree) {
-                                tmem_ld_wait_regs(sbuf[cur], dbuf[cur]);
+                                tmem_ld_wait_regs(sbuf[cc & 1], dbuf[cc & 1]);
                                 if (cc + 1 < NCH) {
-                                    tmem_ld16(tmem + lane_addr + Cfg::T_S + col0 + 16, sbuf[cur ^ 1]);
-                                    tmem_ld16(tmem + lane_addr + Cfg::T_DP + col0 + 16, dbuf[cur ^ 1]);
+                                    tmem_ld16(tmem + lane_addr + Cfg::T_S + c0 + cc * 16 + 16, sbuf[(cc & 1) ^ 1]);
+                                    tmem_ld16(tmem + lane_addr + Cfg::T_DP + c0 + cc * 16 + 16, dbuf[(cc & 1) ^ 1]);
                                 }
                             }
-                            uint32_t dk[8];
-#pragma unroll
-                            for (int q4 = 0; q4 < 4; ++q4) {
-                                const float4 l4 = ld_shared_f4(a_lse + uint32_t(col0 + 4 * q4) * 4);
-                                const float4 d4 = ld_shared_f4(a_dv + uint32_t(col0 + 4 * q4) * 4);
-                                const float lse4[4] = {l4.x, l4.y, l4.z, l4.w}, dv4[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                                for (int h2 = 0; h2 < 2; ++h2) {
-                                    const int e = 4 * q4 + 2 * h2, c = col0 + e;
-                                    if (kBias) {
-                                        const int k = cc * 16 + e;  // column within the group of 32
-                                        const float b0 = kNear ? wrow[-k] : wfar, b1 = kNear ? wrow[-k - 1] : wfar;
-                                        float x0 = fmaf(__uint_as_float(sbuf[cur][e]), sc, b0) - lse4[2 * h2];
-                                        float x1 = fmaf(__uint_as_float(sbuf[cur][e + 1]), sc, b1) - lse4[2 * h2 + 1];
-                                        float g0 = __uint_as_float(dbuf[cur][e]) - dv4[2 * h2];
-                                        float g1 = __uint_as_float(dbuf[cur][e + 1]) - dv4[2 * h2 + 1];
-                                        if (any_mask) {  // a masked element's dP may be anything
-                                            x0 = c >= cmin ? x0 : -INFINITY;
-                                            x1 = c + 1 >= cmin ? x1 : -INFINITY;
-                                            g0 = c >= cmin ? g0 : 0.f;
-                                            g1 = c + 1 >= cmin ? g1 : 0.f;
-                                        }
-                                        const float p0 = ex2(x0), p1 = ex2(x1), ds0 = p0 * g0, ds1 = p1 * g1;
-                                        pk[cc * 8 + 2 * q4 + h2] = pack2<T>(p0, p1);
-                                        dk[2 * q4 + h2] = pack2<T>(ds0, ds1);
-                                        if (kNear) {
-                                            // the sum of diagonal lane - column goes one lane up per column;
-                                            // lane 31's is complete
-                                            if (k > 0) {
-                                                if (lane == 31) diag[k - 1] = run;
-                                                const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                                                run = lane == 0 ? ds0 : up + ds0;
-                                            } else {
-                                                run = ds0;
-                                            }
-                                            if (lane == 31) diag[k] = run;
-                                            const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                                            run = lane == 0 ? ds1 : up + ds1;
-                                        } else {
-                                            run += ds0 + ds1;
-                                        }
-                                        continue;
-                                    }
-                                    float x0 = fmaf(__uint_as_float(sbuf[cur][e]), sc, -lse4[2 * h2]);
-                                    float x1 = fmaf(__uint_as_float(sbuf[cur][e + 1]), sc, -lse4[2 * h2 + 1]);
-                                    if (any_mask) {
-                                        x0 = c >= cmin ? x0 : -INFINITY;
-                                        x1 = c + 1 >= cmin ? x1 : -INFINITY;
-                                    }
-                                    const float g0 = __uint_as_float(dbuf[cur][e]) - dv4[2 * h2];
-                                    const float g1 = __uint_as_float(dbuf[cur][e + 1]) - dv4[2 * h2 + 1];
-                                    pk[cc * 8 + 2 * q4 + h2] = p_and_ds<T>(x0, x1, g0, g1, &dk[2 * q4 + h2]);
-                                }
-                            }
+                        };
+                        auto store_ds = [&](int cc, const uint32_t (&dk)[8]) {
 #pragma unroll
                             for (int q2 = 0; q2 < 2; ++q2) {
-                                const uint32_t off = sw128_offset(uint32_t(r), uint32_t(col0 + 8 * q2), BN);
+                                const uint32_t off = sw128_offset(uint32_t(r), uint32_t(c0 + cc * 16 + 8 * q2), BN);
                                 st_shared_v4(adS + off, dk[4 * q2], dk[4 * q2 + 1], dk[4 * q2 + 2], dk[4 * q2 + 3]);
                             }
-                        }
                         };
-                        if (kBias && kind == kRelNear) compute(std::true_type{});
-                        else compute(std::false_type{});
+                        if constexpr (kBias) {
+                            static_assert(GW == 32, "blocks of 32 x 32");
+                            const float *wrow = win + r + BM - 1 - c0;  // entry of column c0 + k: wrow[-k]
+                            const uint32_t *code = wcode + lg * 32 + BM - 1 - c0;  // of diagonal (row - column) 0
+                            several[q] = (code[-31] & 255u) != (code[31] & 255u);
+                            float2 sum2 = make_float2(0.f, 0.f);
+                            float run = 0.f;
+                            // kAny: several buckets, or masked elements
+                            auto block = [&](auto any_tag) {
+                                constexpr bool kAny = decltype(any_tag)::value;
+                                const float wone = wrow[0];
+                                const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(-1.f, -1.f);
+#pragma unroll
+                                for (int cc = 0; cc < NCH; ++cc) {
+                                    const int col0 = c0 + cc * 16, cur = cc & 1;
+                                    fetch(cc);
+                                    uint32_t dk[8];
+                                    float2 lse4[2], dv4[2];
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
+                                        const int k = cc * 16 + e, c = c0 + k;
+                                        if (e % 4 == 0) {
+                                            const float4 l4 = ld_shared_f4(a_lse + uint32_t(col0 + e) * 4);
+                                            const float4 d4 = ld_shared_f4(a_dv + uint32_t(col0 + e) * 4);
+                                            lse4[0] = make_float2(l4.x, l4.y);
+                                            lse4[1] = make_float2(l4.z, l4.w);
+                                            dv4[0] = make_float2(d4.x, d4.y);
+                                            dv4[1] = make_float2(d4.z, d4.w);
+                                        }
+                                        const float2 lse2 = lse4[e / 2 % 2], dv2 = dv4[e / 2 % 2];
+                                        const float2 b2 = kAny ? make_float2(wrow[-k], wrow[-k - 1]) : make_float2(wone, wone);
+                                        float2 x = fma2(make_float2(__uint_as_float(sbuf[cur][e]), __uint_as_float(sbuf[cur][e + 1])),
+                                                        sc2, fma2(lse2, neg2, b2));
+                                        float2 g = fma2(dv2, neg2,
+                                                        make_float2(__uint_as_float(dbuf[cur][e]), __uint_as_float(dbuf[cur][e + 1])));
+                                        if (kAny) {  // a masked element's dP may be anything
+                                            const bool v0 = c >= cmin && c < cmax, v1 = c + 1 >= cmin && c + 1 < cmax;
+                                            x.x = v0 ? x.x : -INFINITY;
+                                            x.y = v1 ? x.y : -INFINITY;
+                                            g.x = v0 ? g.x : 0.f;
+                                            g.y = v1 ? g.y : 0.f;
+                                        }
+                                        const float2 pp = make_float2(ex2(x.x), ex2(x.y)), ds = mul2(pp, g);
+                                        pk[k / 2] = pack2<T>(pp.x, pp.y);
+                                        dk[e / 2] = pack2<T>(ds.x, ds.y);
+                                        if (kAny) {
+                                            // the sum of diagonal lane - column goes one lane up per column; lane
+                                            // 31's is complete
+                                            if (k > 0) {
+                                                if (lane == 31) diag[q * 32 + k - 1] = run;
+                                                const float up = __shfl_up_sync(0xffffffffu, run, 1);
+                                                run = lane == 0 ? ds.x : up + ds.x;
+                                            } else {
+                                                run = ds.x;
+                                            }
+                                            if (lane == 31) diag[q * 32 + k] = run;
+                                            const float up = __shfl_up_sync(0xffffffffu, run, 1);
+                                            run = lane == 0 ? ds.y : up + ds.y;
+                                        } else {
+                                            sum2 = add2(sum2, ds);
+                                        }
+                                    }
+                                    store_ds(cc, dk);
+                                }
+                            };
+                            several[q] = several[q] || any_mask;
+                            if (several[q]) {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
+                                block(std::true_type{});
+                                __syncwarp();
+                                left_a[q] = run;
+                                code_a[q] = code[lane - 31];
+                                left_b[q] = lane < 31 ? diag[q * 32 + 30 - lane] : 0.f;
+                                code_b[q] = code[lane + 1];
+                            } else {
+                                block(std::false_type{});
+                                left_a[q] = sum2.x + sum2.y;
+                                code_a[q] = code[0] & 255u;
+                            }
+                        } else {
+#pragma unroll
+                            for (int cc = 0; cc < NCH; ++cc) {
+                                const int col0 = c0 + cc * 16, cur = cc & 1;
+                                fetch(cc);
+                                uint32_t dk[8];
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4) {
+                                    const float4 l4 = ld_shared_f4(a_lse + uint32_t(col0 + 4 * q4) * 4);
+                                    const float4 d4 = ld_shared_f4(a_dv + uint32_t(col0 + 4 * q4) * 4);
+                                    const float lse4[4] = {l4.x, l4.y, l4.z, l4.w}, dv4[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                                    for (int h2 = 0; h2 < 2; ++h2) {
+                                        const int e = 4 * q4 + 2 * h2, c = col0 + e;
+                                        float x0 = fmaf(__uint_as_float(sbuf[cur][e]), sc, -lse4[2 * h2]);
+                                        float x1 = fmaf(__uint_as_float(sbuf[cur][e + 1]), sc, -lse4[2 * h2 + 1]);
+                                        if (any_mask) {
+                                            x0 = c >= cmin ? x0 : -INFINITY;
+                                            x1 = c + 1 >= cmin ? x1 : -INFINITY;
+                                        }
+                                        const float g0 = __uint_as_float(dbuf[cur][e]) - dv4[2 * h2];
+                                        const float g1 = __uint_as_float(dbuf[cur][e + 1]) - dv4[2 * h2 + 1];
+                                        pk[cc * 8 + 2 * q4 + h2] = p_and_ds<T>(x0, x1, g0, g1, &dk[2 * q4 + h2]);
+                                    }
+                                }
+                                store_ds(cc, dk);
+                            }
+                        }
                     }
                     if (!kEarlyFree) release();
-                    if (kBias && ok) add_block(kind, run, wcode, c0);
                     // P^T into TMEM once the previous tile's dV GEMM has read it
                     if (q == 0) {
                         const uint32_t t_p = qi > 0 ? mbar_test_wait(p_free, (qi - 1) & 1) : 1u;
@@ -757,11 +796,40 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                         }
                     }
                 }
+                if (kBias && kPacked && ok) {  // rows of other sequences: zero before the GEMMs that read them by rows
+                    const int t = threadIdx.x - 64;
+                    auto zero_rows = [&](uint8_t *tile, int first, int rows) {
+                        for (int k = first * (D / 8) + t; k < rows * (D / 8); k += 32 * Cfg::NSW) {
+                            const int row = k / (D / 8), piece = k % (D / 8);
+                            st_shared_v4(smem_u32(tile) + uint32_t(piece / 8 * rows * 128 + row * 128 + piece % 8 * 16), 0, 0, 0, 0);
+                        }
+                    };
+                    if (cmax < BM) {
+                        zero_rows(smem + Cfg::OFF_Q + st * Cfg::Q_BYTES, cmax, BM);
+                        zero_rows(smem + Cfg::OFF_DO + st * Cfg::Q_BYTES, cmax, BM);
+                    }
+                    if (it == 0 && lkv - j0 < BN) zero_rows(sK, int(lkv - j0), BN);
+                }
                 if (ok) tmem_st_wait();
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready);
+                if (kBias && ok) {
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        if (several[q]) {
+                            add_runs(left_a[q], code_a[q]);
+                            add_runs(left_b[q], code_b[q]);
+                        } else {
+                            if (code_a[q] != one_bucket) {
+                                add_one();
+                                one_bucket = code_a[q];
+                            }
+                            one_sum += left_a[q];
+                        }
+                    }
+                }
                 if (++st == NST) {
                     st = 0;
                     st_par ^= 1;

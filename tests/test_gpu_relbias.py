@@ -371,3 +371,27 @@ def test_layer(dtype, d, rot):
     for name, a, r in zip(("dx", "dy", "dv", "dtable", "dwq", "dwk"), got, want):
         a = a.reshape(r.shape)
         assert np.linalg.norm(a - r) <= 16 * HALF[dtype] * np.linalg.norm(r), name
+
+
+@pytest.mark.parametrize("dtype,d,h,hk", [("float16", 64, 2, 2), ("bfloat16", 128, 4, 2)])
+def test_nan_stays_in_its_sequence(dtype, d, h, hk):
+    """Infinities and NaN in one packed sequence reach nothing of the others: their outputs and gradients are the
+    bits of the clean batch's (dQ in the ordered mode; the table's gradient is shared)."""
+    lens = [(70, 100), (45, 61), (130, 150)]
+    runs = []
+    for bad in (False, True):
+        p = Problem(dtype, lens, h, hk, d, 2, 32, 128, True, seed=12, mode=2)
+        o, lse = p.inputs_bwd()
+        if bad:
+            for t, v in ((p.q, float("nan")), (p.do, float("inf")), (o, float("nan"))):
+                t[70:115] = v
+            for t, v in ((p.k, float("inf")), (p.v, float("nan"))):
+                t[100:161] = v
+        ten = [p.put(x) for x in (p.q, p.k, p.v)]
+        of, lf = p.nan(p.q), p.torch.empty(p.tq * h, device="cuda")
+        p.ab.sdpa_relbias_fwd_stats(p.desc, p.bias, *map(p.view, ten), p.view(of), lf)
+        runs.append([p.get(of), p.get_lse(lf)] + p.bwd(o, lse)[:3])
+    for n, (a, b) in enumerate(zip(*runs)):
+        cut = (100, 161) if n in (3, 4) else (70, 115)
+        np.testing.assert_array_equal(a[:cut[0]], b[:cut[0]])
+        np.testing.assert_array_equal(a[cut[1]:], b[cut[1]:])
