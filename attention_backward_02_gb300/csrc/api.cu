@@ -411,22 +411,18 @@ attn_status_t dense_bwd_call(const attn_sdpa_desc_t *desc, const RelBias *bias, 
         fill_rel(&rel, desc, sh, *bias, RL, workspace, true, dtable);
         if ((e = launch_rel_expand(rel, s)) != cudaSuccess) return cuda_status(e);
     }
-    if (sh.t_q || sh.t_kv) {
-        if (sh.packed) {
-            if ((e = launch_dense_preprocess(a, pg, s)) != cudaSuccess) return cuda_status(e);
-            if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
-            if ((e = launch_dense_bwd_main(a, pg, s, rp)) != cudaSuccess) return cuda_status(e);
-            if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
-            if ((e = launch_dq_finalize(a, pg, s)) != cudaSuccess) return cuda_status(e);
-        } else {
-            if ((e = launch_dense_preprocess(a, fg, s)) != cudaSuccess) return cuda_status(e);
-            if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
-            if ((e = launch_dense_bwd_main(a, fg, s, rp)) != cudaSuccess) return cuda_status(e);
-            if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
-            if ((e = launch_dq_finalize(a, fg, s)) != cudaSuccess) return cuda_status(e);
-        }
+    if (sh.packed) {
+        if ((e = launch_dense_preprocess(a, pg, s, bias != nullptr)) != cudaSuccess) return cuda_status(e);
+        if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
+        if ((e = launch_dense_bwd_main(a, pg, s, rp)) != cudaSuccess) return cuda_status(e);
+        if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
+        return cuda_status(launch_dq_finalize(a, pg, s, rp));
     }
-    return bias ? cuda_status(launch_rel_dtable(rel, s)) : ATTN_OK;
+    if ((e = launch_dense_preprocess(a, fg, s, bias != nullptr)) != cudaSuccess) return cuda_status(e);
+    if ((e = mark(g_ev_before, s)) != cudaSuccess) return cuda_status(e);
+    if ((e = launch_dense_bwd_main(a, fg, s, rp)) != cudaSuccess) return cuda_status(e);
+    if ((e = mark(g_ev_after, s)) != cudaSuccess) return cuda_status(e);
+    return cuda_status(launch_dq_finalize(a, fg, s, rp));
 }
 
 }  // namespace

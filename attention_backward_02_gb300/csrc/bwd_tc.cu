@@ -129,7 +129,7 @@ struct TcCfg {
     static constexpr int OFF_WIN = SMEM;                      // NST x (bias, codes)
     static constexpr int OFF_HIST = OFF_WIN + NST * 2 * WIN_BYTES;
     static constexpr int OFF_DIAG = OFF_HIST + NSW * kRelMaxBuckets * 4;
-    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * NG * 32 * 4 + 1024;
+    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * 32 * 4 + 1024;
     static_assert(WIN_BYTES % 16 == 0 && SMEM % 16 == 0 && SMEM_ALLOC_BIAS <= 227 * 1024, "shared memory budget");
     static_assert(kRelPad >= BN + BM + 4, "a near tile's window lies within the expanded bias");
     static constexpr int T_S = 0, T_DP = BM, T_P = 2 * BM, T_DV = 2 * BM + BM / 2, T_DK = T_DV + D,
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
         // relative bias: this warp's bucket sums and finished diagonals; the bucket of the last block that lay in
         // one, and each thread's sum since
         float *hist = reinterpret_cast<float *>(smem + Cfg::OFF_HIST) + (warp - 2) * kRelMaxBuckets;
-        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_DIAG) + (warp - 2) * NG * 32;
+        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_DIAG) + (warp - 2) * 32;
         float one_sum = 0.f;
         uint32_t one_bucket = 0;
         if (kBias) {
@@ -603,17 +603,30 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                 // first visible query column of this key row; everything is masked past the sequence
                 const int64_t cmin64 = !row_ok ? INT64_MAX : (a.mask ? j - shift - i0 : INT64_MIN);
                 const int cmin = int(cmin64 < -1 ? -1 : (cmin64 > BM ? BM : cmin64));
-                // kBias: the tile's windows; columns from cmax on lie past the sequence's queries; what is left of
-                // the tile's table gradient when its GEMMs are let go (per column group: two diagonal sums a lane
-                // and their codes)
+                // kBias: the tile's windows; columns from cmax on lie past the sequence's queries; a block's share of
+                // the table's gradient: two diagonal sums a lane and their codes, or (one bucket) the thread's sum
                 const float *win = reinterpret_cast<const float *>(smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES);
                 if (kBias) win += uint32_t(window_start(j0 - i0 - (BM - 1) - shift)) & 3u;
                 const uint32_t *wcode = reinterpret_cast<const uint32_t *>(win) + Cfg::WIN_BYTES / 4;
                 const int cmax = kBias && lq - i0 < BM ? int(lq - i0) : BM;
-                float left_a[NG], left_b[NG];
-                uint32_t code_a[NG], code_b[NG];
-                bool several[NG];
-#pragma unroll
+                float left_a = 0.f, left_b = 0.f;
+                uint32_t code_a = 0, code_b = 0;
+                bool several = false;
+                auto add_block = [&]() {
+                    if (several) {
+                        add_runs(left_a, code_a);
+                        add_runs(left_b, code_b);
+                    } else {
+                        if (code_a != one_bucket) {
+                            add_one();
+                            one_bucket = code_a;
+                        }
+                        one_sum += left_a;
+                    }
+                };
+                // (with a bias the column groups share one copy of the code: unrolled, it does not fit the
+                // instruction cache)
+#pragma unroll (kBias ? 1 : NG)
                 for (int q = 0; q < NG; ++q) {
                     const int rel = NH == NG ? q : 0;  // release group of these columns
                     if (q == 0 ? !ready0 : (NH == NG && !ready1)) wait(&s_full[rel], qi & 1, true);
@@ -674,12 +687,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                             static_assert(GW == 32, "blocks of 32 x 32");
                             const float *wrow = win + r + BM - 1 - c0;  // entry of column c0 + k: wrow[-k]
                             const uint32_t *code = wcode + lg * 32 + BM - 1 - c0;  // of diagonal (row - column) 0
-                            several[q] = (code[-31] & 255u) != (code[31] & 255u);
+                            several = (code[-31] & 255u) != (code[31] & 255u) || any_mask;
                             float2 sum2 = make_float2(0.f, 0.f);
                             float run = 0.f;
-                            // kAny: several buckets, or masked elements
-                            auto block = [&](auto any_tag) {
-                                constexpr bool kAny = decltype(any_tag)::value;
+                            // kAny: several buckets, or masked elements (kMask)
+                            auto block = [&](auto any_tag, auto mask_tag) {
+                                constexpr bool kAny = decltype(any_tag)::value, kMask = decltype(mask_tag)::value;
                                 const float wone = wrow[0];
                                 const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(-1.f, -1.f);
 #pragma unroll
@@ -705,7 +718,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                                         sc2, fma2(lse2, neg2, b2));
                                         float2 g = fma2(dv2, neg2,
                                                         make_float2(__uint_as_float(dbuf[cur][e]), __uint_as_float(dbuf[cur][e + 1])));
-                                        if (kAny) {  // a masked element's dP may be anything
+                                        if (kMask) {  // a masked element's dP may be anything
                                             const bool v0 = c >= cmin && c < cmax, v1 = c + 1 >= cmin && c + 1 < cmax;
                                             x.x = v0 ? x.x : -INFINITY;
                                             x.y = v1 ? x.y : -INFINITY;
@@ -719,13 +732,13 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                             // the sum of diagonal lane - column goes one lane up per column; lane
                                             // 31's is complete
                                             if (k > 0) {
-                                                if (lane == 31) diag[q * 32 + k - 1] = run;
+                                                if (lane == 31) diag[k - 1] = run;
                                                 const float up = __shfl_up_sync(0xffffffffu, run, 1);
                                                 run = lane == 0 ? ds.x : up + ds.x;
                                             } else {
                                                 run = ds.x;
                                             }
-                                            if (lane == 31) diag[q * 32 + k] = run;
+                                            if (lane == 31) diag[k] = run;
                                             const float up = __shfl_up_sync(0xffffffffu, run, 1);
                                             run = lane == 0 ? ds.y : up + ds.y;
                                         } else {
@@ -735,19 +748,20 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                     store_ds(cc, dk);
                                 }
                             };
-                            several[q] = several[q] || any_mask;
-                            if (several[q]) {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
-                                block(std::true_type{});
+                            if (several) {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
+                                if (any_mask) block(std::true_type{}, std::true_type{});
+                                else block(std::true_type{}, std::false_type{});
                                 __syncwarp();
-                                left_a[q] = run;
-                                code_a[q] = code[lane - 31];
-                                left_b[q] = lane < 31 ? diag[q * 32 + 30 - lane] : 0.f;
-                                code_b[q] = code[lane + 1];
+                                left_a = run;
+                                code_a = code[lane - 31];
+                                left_b = lane < 31 ? diag[30 - lane] : 0.f;
+                                code_b = code[lane + 1];
                             } else {
-                                block(std::false_type{});
-                                left_a[q] = sum2.x + sum2.y;
-                                code_a[q] = code[0] & 255u;
+                                block(std::false_type{}, std::false_type{});
+                                left_a = sum2.x + sum2.y;
+                                code_a = code[0] & 255u;
                             }
+                            if (q < NG - 1) add_block();  // the last group's waits for the arrival below
                         } else {
 #pragma unroll
                             for (int cc = 0; cc < NCH; ++cc) {
@@ -815,21 +829,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready);
-                if (kBias && ok) {
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        if (several[q]) {
-                            add_runs(left_a[q], code_a[q]);
-                            add_runs(left_b[q], code_b[q]);
-                        } else {
-                            if (code_a[q] != one_bucket) {
-                                add_one();
-                                one_bucket = code_a[q];
-                            }
-                            one_sum += left_a[q];
-                        }
-                    }
-                }
+                if (kBias && ok) add_block();
                 if (++st == NST) {
                     st = 0;
                     st_par ^= 1;

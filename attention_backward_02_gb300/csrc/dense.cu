@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "plan.h"
+#include "relbias.h"
 
 namespace attn {
 
@@ -44,6 +45,8 @@ constexpr int kUnitRows = int(kWsRowAlign) / 2;
 // Then zeroes every partial dQ buffer (and, in ordered dQ mode, the per-tile
 // add counters).  Launched normally (it overwrites what
 // the previous call's last kernel reads); lets the main kernel launch behind it.
+// With a relative bias it runs beside the kernel that expands the bias table and
+// ends after it, so that waiting for this kernel is waiting for both.
 template <class T, class Geo, int D>
 __global__ void __launch_bounds__(256) dense_preprocess_kernel(DenseArgs a, Geo geo)
 {
@@ -101,21 +104,29 @@ __global__ void __launch_bounds__(256) dense_preprocess_kernel(DenseArgs a, Geo 
     if (a.ordered)  // no query tile has received an add yet
         for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < a.h * a.sem_stride; k += int64_t(gridDim.x) * 256)
             a.sem[k] = 0u;
+    pdl_wait();
 }
 
 // ------------------------------------------------------------ dq finalize
 // dQ = cast(scale * sum over the partial buffers, in index order).  Same
 // units as the preprocess; launched behind the main kernel and waits for it.
-template <class T, class Geo, int D>
-__global__ void __launch_bounds__(256) dq_finalize_kernel(DenseArgs a, Geo geo)
+// kBias: the first blocks sum the bias table's gradient instead.
+template <class T, class Geo, int D, bool kBias>
+__global__ void __launch_bounds__(256) dq_finalize_kernel(DenseArgs a, Geo geo, RelArgs rel, int rel_blocks)
 {
+    if (kBias && int(blockIdx.x) < rel_blocks) {
+        pdl_wait();
+        rel_dtable_block(rel, blockIdx.x);
+        return;
+    }
     constexpr int TPR = D / 8, RPP = 256 / TPR, RPT = kUnitRows / RPP;
     const int lane_in_row = threadIdx.x % TPR, k0 = threadIdx.x / TPR;
     const int ntile = int(a.t_pad / kUnitRows);
     const int nunit = int(a.h) * ntile;
     const int64_t part_stride = a.h * a.t_pad * D;
     pdl_wait();
-    for (int u = blockIdx.x; u < nunit; u += gridDim.x) {
+    const int first = kBias ? rel_blocks : 0;
+    for (int u = int(blockIdx.x) - first; u < nunit; u += int(gridDim.x) - first) {
         // heads fastest: blocks running together read the same tokens' rows (one DRAM page run)
         const int wt = u / int(a.h), h = u - wt * int(a.h);
         int64_t b = 0, i0 = 0;
@@ -169,33 +180,44 @@ unsigned row_grid(const DenseArgs &a)
     return unsigned(need < 1 ? 1 : (need < wave ? need : wave));
 }
 
-template <class Geo> cudaError_t preprocess(const DenseArgs &a, const Geo &g, cudaStream_t s)
+template <class Geo> cudaError_t preprocess(const DenseArgs &a, const Geo &g, cudaStream_t s, bool beside)
 {
     const dim3 grid(row_grid(a));
     if (a.d == 64)
         return a.dtype == ATTN_F16
-                   ? launch_kernel(dense_preprocess_kernel<__half, Geo, 64>, grid, 256, 0, s, false, a, g)
-                   : launch_kernel(dense_preprocess_kernel<__nv_bfloat16, Geo, 64>, grid, 256, 0, s, false, a, g);
-    return a.dtype == ATTN_F16 ? launch_kernel(dense_preprocess_kernel<__half, Geo, 128>, grid, 256, 0, s, false, a, g)
-                               : launch_kernel(dense_preprocess_kernel<__nv_bfloat16, Geo, 128>, grid, 256, 0, s, false, a, g);
+                   ? launch_kernel(dense_preprocess_kernel<__half, Geo, 64>, grid, 256, 0, s, beside, a, g)
+                   : launch_kernel(dense_preprocess_kernel<__nv_bfloat16, Geo, 64>, grid, 256, 0, s, beside, a, g);
+    return a.dtype == ATTN_F16 ? launch_kernel(dense_preprocess_kernel<__half, Geo, 128>, grid, 256, 0, s, beside, a, g)
+                               : launch_kernel(dense_preprocess_kernel<__nv_bfloat16, Geo, 128>, grid, 256, 0, s, beside, a, g);
 }
 
-template <class Geo> cudaError_t finalize(const DenseArgs &a, const Geo &g, cudaStream_t s)
+template <class T, int D, class Geo> cudaError_t run_finalize(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
 {
-    if (a.t_q == 0) return cudaSuccess;
-    const dim3 grid(row_grid(a));
+    const unsigned rows = a.t_q ? row_grid(a) : 0;
+    if (!rel) return launch_kernel(dq_finalize_kernel<T, Geo, D, false>, dim3(rows), 256, 0, s, true, a, g, RelArgs{}, 0);
+    const unsigned extra = unsigned(rel_dtable_blocks(*rel));
+    return launch_kernel(dq_finalize_kernel<T, Geo, D, true>, dim3(rows + extra), 256, 0, s, true, a, g, *rel, int(extra));
+}
+
+template <class Geo> cudaError_t finalize(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
+{
+    if (a.t_q == 0 && !rel) return cudaSuccess;
     if (a.d == 64)
-        return a.dtype == ATTN_F16 ? launch_kernel(dq_finalize_kernel<__half, Geo, 64>, grid, 256, 0, s, true, a, g)
-                                   : launch_kernel(dq_finalize_kernel<__nv_bfloat16, Geo, 64>, grid, 256, 0, s, true, a, g);
-    return a.dtype == ATTN_F16 ? launch_kernel(dq_finalize_kernel<__half, Geo, 128>, grid, 256, 0, s, true, a, g)
-                               : launch_kernel(dq_finalize_kernel<__nv_bfloat16, Geo, 128>, grid, 256, 0, s, true, a, g);
+        return a.dtype == ATTN_F16 ? run_finalize<__half, 64>(a, rel, g, s) : run_finalize<__nv_bfloat16, 64>(a, rel, g, s);
+    return a.dtype == ATTN_F16 ? run_finalize<__half, 128>(a, rel, g, s) : run_finalize<__nv_bfloat16, 128>(a, rel, g, s);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_preprocess(const DenseArgs &a, const FixedGeo &g, cudaStream_t s) { return preprocess(a, g, s); }
-cudaError_t launch_dense_preprocess(const DenseArgs &a, const PackedGeo &g, cudaStream_t s) { return preprocess(a, g, s); }
-cudaError_t launch_dq_finalize(const DenseArgs &a, const FixedGeo &g, cudaStream_t s) { return finalize(a, g, s); }
-cudaError_t launch_dq_finalize(const DenseArgs &a, const PackedGeo &g, cudaStream_t s) { return finalize(a, g, s); }
+cudaError_t launch_dense_preprocess(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, bool beside)
+{
+    return preprocess(a, g, s, beside);
+}
+cudaError_t launch_dense_preprocess(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, bool beside)
+{
+    return preprocess(a, g, s, beside);
+}
+cudaError_t launch_dq_finalize(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel) { return finalize(a, rel, g, s); }
+cudaError_t launch_dq_finalize(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel) { return finalize(a, rel, g, s); }
 
 }  // namespace attn

@@ -125,13 +125,14 @@ attn_status_t record_cuda_error(cudaError_t e);
 
 // ------------------------------------------------------------ launchers
 // Each returns cudaGetLastError() of its launches.
-cudaError_t launch_dense_preprocess(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
-cudaError_t launch_dense_preprocess(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
 struct RelArgs;  // relbias.h; NULL: no relative position bias
+// beside: may run beside the kernel launched before it (the expansion of the bias table), and ends after it
+cudaError_t launch_dense_preprocess(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, bool beside = false);
+cudaError_t launch_dense_preprocess(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, bool beside = false);
 cudaError_t launch_dense_bwd_main(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
 cudaError_t launch_dense_bwd_main(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
-cudaError_t launch_dq_finalize(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
-cudaError_t launch_dq_finalize(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
+cudaError_t launch_dq_finalize(const DenseArgs &a, const FixedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
+cudaError_t launch_dq_finalize(const DenseArgs &a, const PackedGeo &g, cudaStream_t s, const RelArgs *rel = nullptr);
 cudaError_t launch_dense_fwd(const DenseArgs &a, const FixedGeo &g, cudaStream_t s);
 cudaError_t launch_dense_fwd(const DenseArgs &a, const PackedGeo &g, cudaStream_t s);
 cudaError_t launch_relbias_fwd(const DenseArgs &a, const RelArgs &rel, const FixedGeo &g, cudaStream_t s);

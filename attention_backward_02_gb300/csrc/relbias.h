@@ -75,10 +75,31 @@ __device__ __forceinline__ float rel_table_value(const RelBias &b, int64_t at)
     return v <= kRelMasked ? -INFINITY : v * kLog2e;
 }
 
+// dtable[n][head] = the sum of the shares of 32 buckets of one head, in a fixed order: a block of 256 threads;
+// warp w sums every 8th share, the warps' sums are added in order.
+__device__ __forceinline__ void rel_dtable_block(const RelArgs &a, int unit)
+{
+    __shared__ float red[8][32];
+    const int nb = (a.b.buckets + 31) / 32, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t head = unit / nb;
+    const int n = unit % nb * 32 + lane;
+    float v = 0.f;
+    if (n < a.b.buckets) {
+        const float *p = a.part + (head * 8 + w) * a.b.buckets + n;
+#pragma unroll 4
+        for (int64_t row = 0; row < a.part_rows; ++row) v += p[row * a.h * 8 * a.b.buckets];
+    }
+    red[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && n < a.b.buckets) {
+        for (int k = 1; k < 8; ++k) v += red[k][lane];
+        a.dtable[int64_t(n) * a.h + head] = v;
+    }
+}
+inline int64_t rel_dtable_blocks(const RelArgs &a) { return a.h * ((a.b.buckets + 31) / 32); }
+
 // Expands the table (and zeroes the status word and the gradient shares, where there are any); dependents
 // may start at once and wait for it.
 cudaError_t launch_rel_expand(const RelArgs &a, cudaStream_t s);
-// dtable = sum of the shares, in a fixed order.  Chained behind the kernel before it.
-cudaError_t launch_rel_dtable(const RelArgs &a, cudaStream_t s);
 
 }  // namespace attn
