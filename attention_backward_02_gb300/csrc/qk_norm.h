@@ -24,6 +24,7 @@ struct QkNormArgs {
     const int32_t *pos;
     uint32_t *status;
     QkSide side[2];
+    int warp_smem;          // bytes of a warp's shared memory (set by the launcher)
 };
 
 // Most blocks the kernels are launched with on both sides together; each leaves one row of weight
