@@ -4,25 +4,29 @@
 //
 //   s_ij = scale q_i.k_j + table[bucket(j - i - shift)][head],  O = softmax(s) V
 //
-// One CTA per (sequence, query head, tile of 128 queries), longest tiles first.
-// Query rows are the MMA M dimension and the TMEM lanes:
-//   S = Q K^T      M=128 (queries) N=128 (keys) K=D   A=Q (smem, K-major) B=K (smem, K-major)
-//   O += P V       M=128           N=D          K=128 A=P (TMEM, 16-bit)  B=V (smem, MN-major)
+// One CTA per (sequence, query head, 256 queries), longest first.  Query rows are
+// the MMA M dimension and the TMEM lanes:
+//   S = Q K^T      M=128 (queries) N=64 (keys) K=D   A=Q (smem, K-major) B=K (smem, K-major)
+//   O += P V       M=128           N=D         K=64  A=P (TMEM, 16-bit)  B=V (smem, MN-major)
 //
-// Bound by the tensor pipe on paper, by the chain S -> softmax -> P -> O in
-// practice, so two softmax warpgroups work beside each other: one has the first
-// 64 keys of every key tile, the other the last 64, each with its own S, running
-// maximum, sum and O accumulator; they meet once, at the end, when the two O are
-// added (scaled to one maximum).  A thread owns a whole row of its 64 columns: no
-// exchange of row maxima between warps.  Each group has two S buffers of 64
-// columns, so S of the next key tile is ready when the softmax of this one ends
-// (S with 64 columns an MMA runs at two thirds of the tensor rate, which costs
-// less than the wait it removes: one buffer of 128 columns a group, tiles taken in
-// turn, took 306 us where this takes FWD_LONG at b2 h32 s4096 d128 causal bf16).
+// Two softmax warpgroups work beside each other, each on 128 query rows of its own
+// and 64 keys a step, with its own S, running maximum, sum and O accumulator; the
+// MMAs of one run under the softmax of the other.  A thread owns a row: no exchange
+// of row maxima between warps.  Each group has two S buffers of 64 columns, so S of
+// the next step is ready when the softmax of this one ends (S with 64 columns an MMA
+// runs at two thirds of the tensor rate, which costs less than the wait it removes).
 // P overwrites the S it came from (each thread its own row, after it has read it);
-// TMEM holds S 4 x 64 + O 2 x D columns.  The tensor pipe runs the MMAs in the
-// order they were issued, so S of tile j + 2 follows O += P V of tile j into the
-// same columns without a wait.
+// TMEM holds S 4 x 64 + O 2 x D columns.  The tensor pipe runs the MMAs in the order
+// they were issued, so S of step j + 2 follows O += P V of step j into the same
+// columns without a wait.
+//
+// Bound: the chain S -> softmax -> P -> O of a group.  256 rows a CTA because with
+// 128 the K / V tiles' reads from L2 bound it (8 TB/s; taking away the exponentials,
+// the MMAs or the maxima changed nothing): b2 h32 s4096 d128 causal bf16 279 us with
+// 128 rows, FWD_LONG with 256.  Where 128-row tiles do not fill the SMs once (kSplit),
+// a CTA has 128 rows and the groups take the first and last 64 keys of every key
+// tile; they meet at the end, when the two O are added, scaled to one maximum
+// (SPLIT_NOTE).
 //
 // The bias of a group's tile is a window of the head's expanded table (log2
 // units), element (row r, column c) entry c - r + 127.  A warpgroup loads its next
@@ -60,22 +64,22 @@ using namespace tc;
 
 template <int D> struct RelFwdCfg {
     static constexpr int BM = 128, BN = 128;
-    static constexpr int NSK = D == 64 ? 4 : 3;      // K ring stages
+    static constexpr int NSK = D == 64 ? 4 : 2;      // K ring stages
     static constexpr int NSV = D == 64 ? 4 : 2;      // V ring stages
     static constexpr int THREADS = 384;
-    static constexpr int TILE_BYTES = BN * D * 2;
+    static constexpr int TILE_BYTES = BN * D * 2;    // a K or V tile, and 128 query rows
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = OFF_Q + TILE_BYTES;
+    static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
     static constexpr int OFF_V = OFF_K + NSK * TILE_BYTES;
     static constexpr int OFF_BAR = OFF_V + NSV * TILE_BYTES;
     static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
     static constexpr int OFF_ML = OFF_MISC + 64;              // [2 groups][m, l][128 rows] floats
-    static constexpr int HN = BN / 2;                         // key columns of a group
+    static constexpr int HN = BN / 2;                         // key columns of a step
     static constexpr int OFF_WIN = OFF_ML + 2 * 2 * 128 * 4;  // [2 groups][2 tiles][256] floats
     static constexpr int SMEM = OFF_WIN + 2 * 2 * 256 * 4;
     // at least half the SM's shared memory: one CTA, which holds all of the TMEM, runs per SM
     static constexpr int SMEM_ALLOC = SMEM + 1024 > 116 * 1024 ? SMEM + 1024 : 116 * 1024;
-    static constexpr int T_S = 0, T_O = 256;  // S (and P) of group g, tile parity b at T_S + 128 g + 64 b, O at T_O + D g
+    static constexpr int T_S = 0, T_O = 256;  // S (and P) of group g, step parity b at T_S + 128 g + 64 b, O at T_O + D g
     static constexpr int T_COLS = 512;
     static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
     static_assert(2 + 2 * NSK + 2 * NSV + 10 <= 32, "barrier slots");
@@ -94,7 +98,7 @@ template <> struct IsPackedGeo<PackedGeo> : std::true_type {};
 
 }  // namespace
 
-template <class T, int D, class Geo>
+template <class T, int D, class Geo, bool kSplit>
 __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
     relbias_fwd_kernel(const __grid_constant__ RelFwdParams p, const Geo geo)
 {
@@ -116,13 +120,14 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
     const DenseArgs &a = p.a;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    // ---- the unit: (sequence b, query head hq, query tile qt), longest first
+    // ---- the unit: (sequence b, query head hq, query tile qt, or the two tiles qt and qt + 1), longest first
+    constexpr int ROWS = kSplit ? BM : 2 * BM;
     int64_t b, hq, qt;
     {
         const int64_t u = blockIdx.x;
         if (!kPacked) {
-            const int64_t nqt = (geo.q_len(0) + BM - 1) / BM, per = a.h * geo.nseq;
-            qt = nqt - 1 - u / per;
+            const int64_t nu = (geo.q_len(0) + ROWS - 1) / ROWS, per = a.h * geo.nseq;
+            qt = (nu - 1 - u / per) * (ROWS / BM);
             const int64_t rest = u - (u / per) * per;
             b = rest / a.h;
             hq = rest - b * a.h;
@@ -133,6 +138,7 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             geo.ws_locate(tile * BM, &b, &i0w);
             const int64_t nqt = (geo.q_len(b) + BM - 1) / BM;
             qt = nqt - 1 - i0w / BM;
+            if (!kSplit && (qt & 1)) return;  // the CTA of tile qt - 1 has it
         }
     }
     const int64_t G = a.h / a.h_kv, g = hq / G;
@@ -140,9 +146,20 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
     const int64_t q_row0 = kPacked ? geo.q_start(b) : 0, kv_row0 = kPacked ? geo.kv_start(b) : 0;
     const int q_b = kPacked ? 0 : int(b);
     const int64_t i0 = qt * BM;
-    const int64_t i_last = (i0 + BM - 1 < lq - 1) ? i0 + BM - 1 : lq - 1;
-    const int64_t key_last = lkv > 0 ? last_visible_key(a.mask, i_last, lq, lkv) : -1;
-    const int n_kt = key_last < 0 ? 0 : int(key_last / BN + 1);  // key tiles any row of the tile sees
+    // keys that any of the query rows first .. first + BM - 1 sees
+    auto keys_seen = [&](int64_t first) -> int64_t {
+        if (first >= lq || lkv <= 0) return 0;
+        const int64_t last = first + BM - 1 < lq - 1 ? first + BM - 1 : lq - 1;
+        return last_visible_key(a.mask, last, lq, lkv) + 1;
+    };
+    // steps of the two groups, and the key tiles they span (the second group's rows see at least the first's keys)
+    const int64_t seen0 = keys_seen(i0), seen1 = kSplit || i0 + BM >= lq ? seen0 : keys_seen(i0 + BM);
+    const int n_kt = seen1 <= 0 ? 0 : int((seen1 + BN - 1) / BN);
+    const int steps0 = kSplit ? n_kt : (seen0 <= 0 ? 0 : int((seen0 + HN - 1) / HN));
+    const int steps1 = kSplit ? n_kt : (i0 + BM >= lq || seen1 <= 0 ? 0 : int((seen1 + HN - 1) / HN));
+    const int n_steps = steps1 > steps0 ? steps1 : steps0;
+    auto tile_of = [](int j) { return kSplit ? j : j >> 1; };               // key tile of a step
+    auto half_of = [](int j, int grp) { return kSplit ? grp : j & 1; };     // and which half of it
 
     if (threadIdx.x == 0) {
         *abort = 0;
@@ -185,9 +202,11 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             int armed = 0;
             if (isk) {
                 prefetch_tmap(&p.tm_q);
-                mbar_arrive_expect_tx(q_full, Cfg::TILE_BYTES);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(sQ + c * BM * 128, &p.tm_q, q_full, c * 64, int(q_row0 + i0), int(hq), q_b);
+                mbar_arrive_expect_tx(q_full, (steps1 && !kSplit ? 2 : 1) * Cfg::TILE_BYTES);
+                for (int k = 0; k < (steps1 && !kSplit ? 2 : 1); ++k)
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(sQ + k * Cfg::TILE_BYTES + c * BM * 128, &p.tm_q, q_full, c * 64,
+                                    int(q_row0 + i0 + k * BM), int(hq), q_b);
             }
             for (int j = 0; j < n_kt; ++j) {
                 const int s = j % nst, use = j / nst;
@@ -214,43 +233,46 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                 if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, a.status);
                 tc_fence_after();
             };
-            const uint64_t kQ = desc_kmaj(smem_u32(sQ), BM, 0);
             wait(q_full, 0);
-            // S of tile j, then O += P V of tile j - 1.  S of tile j goes where P of tile j - 2 was, whose
+            // S of step j, then O += P V of step j - 1.  S of step j goes where P of step j - 2 was, whose
             // product was issued a round ago
-            for (int j = 0; j <= n_kt; ++j) {
-                if (j < n_kt) {
-                    const int s = j % NSK;
-                    wait(&k_full[s], uint32_t(j / NSK) & 1);
+            for (int j = 0; j <= n_steps; ++j) {
+                if (j < n_steps) {
+                    const int tl = tile_of(j), s = tl % NSK;
+                    if (kSplit || (j & 1) == 0) wait(&k_full[s], uint32_t(tl / NSK) & 1);
                     if (ok) {
                         const uint64_t kK = desc_kmaj(smem_u32(sK(s)), BN, 0);
 #pragma unroll
                         for (int grp = 0; grp < 2; ++grp) {
+                            if (j >= (grp ? steps1 : steps0)) continue;
+                            const uint64_t kQ = desc_kmaj(smem_u32(sQ + (kSplit ? 0 : grp * Cfg::TILE_BYTES)), BM, 0);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
                                 mma_f16_ss(tmem + Cfg::T_S + grp * 128 + (j & 1) * 64, kmaj_step(kQ, BM, kk),
-                                           kmaj_step(kK + uint64_t(grp * HN * 128 / 16), BN, kk), idS, kk > 0);
+                                           kmaj_step(kK + uint64_t(half_of(j, grp) * HN * 128 / 16), BN, kk), idS, kk > 0);
                             mma_commit(&s_full[grp * 2 + (j & 1)]);
                         }
-                        mma_commit(&k_empty[s]);  // S has read this K stage
+                        // the last S that reads this K stage
+                        if (kSplit || (j & 1) || j == n_steps - 1) mma_commit(&k_empty[s]);
                     }
                 }
                 if (j > 0) {
-                    const int x = j - 1, s = x % NSV, sb = x & 1;
-                    wait(&v_full[s], uint32_t(x / NSV) & 1);
+                    const int x = j - 1, tl = tile_of(x), s = tl % NSV, sb = x & 1;
+                    if (kSplit || (x & 1) == 0) wait(&v_full[s], uint32_t(tl / NSV) & 1);
                     const uint64_t mV = desc_mn(smem_u32(sV(s)), BN, 0);
 #pragma unroll
                     for (int grp = 0; grp < 2; ++grp) {
+                        if (x >= (grp ? steps1 : steps0)) continue;
                         wait(&p_full[grp * 2 + sb], uint32_t(x >> 1) & 1);
                         if (ok) {
 #pragma unroll
                             for (int kk = 0; kk < HN / 16; ++kk)
                                 mma_f16_ts(tmem + Cfg::T_O + grp * D, tmem + Cfg::T_S + grp * 128 + sb * 64 + kk * 8,
-                                           mn_step(mV, grp * (HN / 16) + kk), idO, x > 0 || kk > 0);
+                                           mn_step(mV, half_of(x, grp) * (HN / 16) + kk), idO, x > 0 || kk > 0);
                             mma_commit(&o_done[grp]);
                         }
                     }
-                    if (ok) mma_commit(&v_empty[s]);
+                    if (ok && (kSplit || (x & 1) || x == n_steps - 1)) mma_commit(&v_empty[s]);
                 }
             }
             volatile int never = 0;
@@ -259,10 +281,12 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
         }
     } else {
         // ================================================= softmax and epilogue (warps 4..11)
-        const int grp = (warp >> 2) - 1, qd = warp & 3;  // the half of the key columns; TMEM lane quadrant
+        const int grp = (warp >> 2) - 1, qd = warp & 3;  // the group; TMEM lane quadrant
         const uint32_t lane_addr = uint32_t(qd * 32) << 16;
         const int r = qd * 32 + lane, wt = threadIdx.x & 127;
-        const int64_t i = i0 + r;  // query position in the sequence
+        const int steps = grp ? steps1 : steps0;
+        const int64_t first_row = i0 + (kSplit ? 0 : grp * BM);
+        const int64_t i = first_row + r;  // query position in the sequence
         const float c = a.scale * kLog2e;
         const int64_t kmax = lkv > 0 && i < lq ? last_visible_key(a.mask, i, lq, lkv) : -1;  // last key it sees
         const uint32_t tO = tmem + lane_addr + Cfg::T_O + grp * D;
@@ -274,32 +298,34 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        // the window of this half of key tile j starts at delta j BN - row0; this thread's two entries of it
+        // the window of step j, whose first key is key0(j), starts at delta key0(j) - row0; this thread's two
+        // entries of it
         float *win = reinterpret_cast<float *>(smem + Cfg::OFF_WIN) + grp * 512;
-        const int64_t row0 = i0 + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0) + 127 - grp * HN;
-        auto kind_of = [&](int j) { return rel_tile(p.rel.b, int64_t(j) * BN - row0, HN + 127); };
+        auto key0 = [&](int j) { return int64_t(tile_of(j)) * BN + half_of(j, grp) * HN; };
+        const int64_t row0 = first_row + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0) + 127;
+        auto kind_of = [&](int j) { return rel_tile(p.rel.b, key0(j) - row0, HN + 127); };
         const float *rel = p.rel.rel + hq * p.rel.stride;
         auto window = [&](int j) -> float2 {
             if (kind_of(j) != kRelNear) return make_float2(0.f, 0.f);
-            const float *w = rel + (int64_t(j) * BN - row0 - (p.rel.b.lo - kRelPad)) + wt;
+            const float *w = rel + (key0(j) - row0 - (p.rel.b.lo - kRelPad)) + wt;
             return make_float2(__ldcg(w), __ldcg(w + 128));
         };
         pdl_wait();  // the bias has been expanded
         const float past = __ldcg(rel), future = __ldcg(rel + p.rel.stride - 1);
-        if (n_kt > 0) {
+        if (steps > 0) {
             const float2 w = window(0);
             win[wt] = w.x;
             win[wt + 128] = w.y;
         }
         named_bar_sync(1 + grp, 128);
 
-        for (int j = 0; j < n_kt; ++j) {
+        for (int j = 0; j < steps; ++j) {
             const int sb = j & 1;
             const uint32_t tS = tmem + lane_addr + Cfg::T_S + grp * 128 + sb * 64;
             const RelTile kind = kind_of(j);
-            const bool next_near = j + 1 < n_kt && kind_of(j + 1) == kRelNear;
+            const bool next_near = j + 1 < steps && kind_of(j + 1) == kRelNear;
             const float2 next_win = next_near ? window(j + 1) : make_float2(0.f, 0.f);
-            const int64_t lim64 = kmax - int64_t(j) * BN - grp * HN;  // columns <= lim are visible
+            const int64_t lim64 = kmax - key0(j);  // columns <= lim are visible
             const int lim = int(lim64 < -1 ? -1 : (lim64 > HN ? HN : lim64));
             const bool whole = __all_sync(0xffffffffu, lim >= HN - 1);
             wait(&s_full[grp * 2 + sb], uint32_t(j >> 1) & 1);
@@ -395,11 +421,11 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                     tmem_st8(tS + e0 / 2, w);
                 }
                 tmem_st_wait();
-                if (kPacked && int64_t(j + 1) * BN > lkv) {  // values of the next sequence
-                    const int s = j % NSV;
-                    wait(&v_full[s], uint32_t(j / NSV) & 1);
-                    const int row = grp * HN + r;  // of the group's half of the tile
-                    if (r < HN && int64_t(j) * BN + row >= lkv)
+                if (kPacked && key0(j) + HN > lkv) {  // values of the next sequence
+                    const int tl = tile_of(j), s = tl % NSV;
+                    wait(&v_full[s], uint32_t(tl / NSV) & 1);
+                    const int row = half_of(j, grp) * HN + r;  // of the tile
+                    if (r < HN && key0(j) + r >= lkv)
                         for (int q = 0; q < D / 64; ++q)
                             for (int e = 0; e < 8; ++e)
                                 st_shared_v4(smem_u32(sV(s)) + q * BN * 128 + row * 128 + e * 16, 0, 0, 0, 0);
@@ -410,31 +436,38 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[grp * 2 + sb]);
         }
-        // ---- epilogue: the groups' maxima and sums, then O / l (16 bit, row per thread, half of the columns) and LSE
-        float *ml = reinterpret_cast<float *>(smem + Cfg::OFF_ML);
-        ml[grp * 256 + r] = m_ref;
-        ml[grp * 256 + 128 + r] = l2.x + l2.y;
-        named_bar_sync(3, 256);
-        const float ma = ml[r], mb = ml[256 + r], m = fmaxf(ma, mb);
-        const float fa = ma == -INFINITY ? 0.f : ex2(ma - m), fb = mb == -INFINITY ? 0.f : ex2(mb - m);
-        const float l = fa * ml[128 + r] + fb * ml[256 + 128 + r];
-        if (n_kt > 0) {
-            wait(&o_done[0], uint32_t(n_kt - 1) & 1);
-            wait(&o_done[1], uint32_t(n_kt - 1) & 1);
+        // ---- epilogue: O / l (16 bit, row per thread) and LSE; kSplit: the groups' maxima and sums first, and each
+        // group writes half of the columns of both
+        float m = m_ref, l = l2.x + l2.y, fa = 1.f, fb = 0.f;
+        if (kSplit) {
+            float *ml = reinterpret_cast<float *>(smem + Cfg::OFF_ML);
+            ml[grp * 256 + r] = m_ref;
+            ml[grp * 256 + 128 + r] = l;
+            named_bar_sync(3, 256);
+            const float ma = ml[r], mb = ml[256 + r];
+            m = fmaxf(ma, mb);
+            fa = ma == -INFINITY ? 0.f : ex2(ma - m);
+            fb = mb == -INFINITY ? 0.f : ex2(mb - m);
+            l = fa * ml[128 + r] + fb * ml[256 + 128 + r];
+        }
+        if (n_kt > 0 && (kSplit || steps > 0)) {
+            wait(&o_done[grp], uint32_t(steps - 1) & 1);
+            if (kSplit) wait(&o_done[grp ^ 1], uint32_t(steps - 1) & 1);
         }
         const bool row_ok = i < lq;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         T *O = static_cast<T *>(a.o.ptr) + (kPacked ? 0 : int64_t(q_b) * a.o.sb) + hq * a.o.sh + (q_row0 + i) * a.o.ss;
+        const uint32_t tOa = tmem + lane_addr + Cfg::T_O + (kSplit ? 0 : grp * D);
 #pragma unroll 1
-        for (int o0 = grp * (D / 2); o0 < (grp + 1) * (D / 2); o0 += 32) {
+        for (int o0 = kSplit ? grp * (D / 2) : 0; o0 < (kSplit ? (grp + 1) * (D / 2) : D); o0 += 32) {
             uint32_t va[32], vb[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) va[e] = vb[e] = 0u;
-            if (ok && n_kt > 0) {
-                tmem_ld32(tmem + lane_addr + Cfg::T_O + o0, va);
-                tmem_ld32(tmem + lane_addr + Cfg::T_O + D + o0, vb);
+            if (ok && steps > 0) {
+                tmem_ld32(tOa + o0, va);
+                if (kSplit) tmem_ld32(tOa + D + o0, vb);
                 tmem_ld_wait_regs(va);
-                tmem_ld_wait_regs(vb);
+                if (kSplit) tmem_ld_wait_regs(vb);
             }
             if (row_ok) {
                 const float ga = fa * inv, gb = fb * inv;
@@ -442,14 +475,16 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                 for (int e = 0; e < 32; e += 8) {
                     float y[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        y[k] = fmaf(__uint_as_float(va[e + k]), ga, __uint_as_float(vb[e + k]) * gb);
+                    for (int k = 0; k < 8; ++k) {
+                        y[k] = __uint_as_float(va[e + k]) * ga;
+                        if (kSplit) y[k] = fmaf(__uint_as_float(vb[e + k]), gb, y[k]);
+                    }
                     *reinterpret_cast<uint4 *>(O + o0 + e) =
                         make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
                 }
             }
         }
-        if (row_ok && grp == 0) {
+        if (row_ok && (!kSplit || grp == 0)) {
             const float lse = l > 0.f ? (m + __log2f(l)) / kLog2e : INFINITY;
             const int64_t idx = kPacked ? hq * a.t_q + q_row0 + i : (int64_t(q_b) * a.h + hq) * lq + i;
             a.lse_out[idx] = lse;
@@ -468,11 +503,22 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
 
 namespace {
 
+int64_t sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 1;
+    return n > 0 ? n : 1;
+}
+
 template <class T, int D, class Geo> cudaError_t run(const DenseArgs &a, const RelArgs &rel, const Geo &g, cudaStream_t s)
 {
     using Cfg = RelFwdCfg<D>;
     constexpr bool packed = IsPackedGeo<Geo>::value;
-    const int64_t units = packed ? (g.ws_rows() / Cfg::BM) * a.h : (g.q_len(0) + Cfg::BM - 1) / Cfg::BM * a.h * a.nseq;
+    const int64_t tiles = packed ? (g.ws_rows() / Cfg::BM) * a.h : (g.q_len(0) + Cfg::BM - 1) / Cfg::BM * a.h * a.nseq;
+    const bool split = tiles <= sm_count();
+    // packed: a CTA for every 128-row tile, of which every other one ends at once
+    const int64_t units = split || packed ? tiles : (g.q_len(0) + 2 * Cfg::BM - 1) / (2 * Cfg::BM) * a.h * a.nseq;
     if (units == 0) return cudaSuccess;
     if (units > INT32_MAX) return cudaErrorInvalidValue;
     RelFwdParams prm;
@@ -488,7 +534,7 @@ template <class T, int D, class Geo> cudaError_t run(const DenseArgs &a, const R
     } else {
         prm.tm_k = prm.tm_v = prm.tm_q;  // never read: no key tiles
     }
-    auto k = relbias_fwd_kernel<T, D, Geo>;
+    auto k = split ? relbias_fwd_kernel<T, D, Geo, true> : relbias_fwd_kernel<T, D, Geo, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     // starts beside the kernel that expands the table (and clears the status word); the softmax warps wait for it
