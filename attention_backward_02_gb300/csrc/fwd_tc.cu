@@ -359,8 +359,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             named_bar_sync(1, 256);
             l = slot[r] + slot[128 + r];
         }
-        // the last two phases in turn: a parity tells neighbours apart only, and p_free vouches for the phases before
-        if (n_kt > 1) wait(o_done, uint32_t(n_kt - 2) & 1);
+        // o_done's last phase, once the one before it has completed (a parity tells neighbours apart only): the
+        // product of the last tile but one has read its P then, and nothing completes that barrier again
+        if (n_kt > 1) wait(&p_free[n_kt & 1], uint32_t((n_kt - 2) >> 1) & 1);
         if (n_kt > 0) wait(o_done, uint32_t(n_kt - 1) & 1);
         const bool row_ok = i < lq;
         const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -4,8 +4,9 @@
 //
 //   s_ij = scale q_i.k_j + table[bucket(j - i - shift)][head],  O = softmax(s) V
 //
-// One CTA per (sequence, query head, 256 queries), longest first.  Query rows are
-// the MMA M dimension and the TMEM lanes:
+// Persistent, one CTA an SM; a unit is (sequence, query head, 256 queries), dealt
+// longest first, in alternating direction.  Query rows are the MMA M dimension and
+// the TMEM lanes:
 //   S = Q K^T      M=128 (queries) N=64 (keys) K=D   A=Q (smem, K-major) B=K (smem, K-major)
 //   O += P V       M=128           N=D         K=64  A=P (TMEM, 16-bit)  B=V (smem, MN-major)
 //
@@ -20,13 +21,15 @@
 // they were issued, so S of step j + 2 follows O += P V of step j into the same
 // columns without a wait.
 //
-// Bound: the chain S -> softmax -> P -> O of a group.  256 rows a CTA because with
-// 128 the K / V tiles' reads from L2 bound it (8 TB/s; taking away the exponentials,
-// the MMAs or the maxima changed nothing): b2 h32 s4096 d128 causal bf16 279 us with
-// 128 rows, FWD_LONG with 256.  Where 128-row tiles do not fill the SMs once (kSplit),
-// a CTA has 128 rows and the groups take the first and last 64 keys of every key
-// tile; they meet at the end, when the two O are added, scaled to one maximum
-// (SPLIT_NOTE).
+// Bound: the chain S -> softmax -> P -> O of a group, about 1700 cycles for 64 keys
+// and 256 rows against 1280 of MMAs.  Persistent because a CTA's start, first loads,
+// last products and the gap to the next one took 15 000 cycles (of 75 000 a unit at
+// b2 h32 s4096 d128 causal): the loads and first S of the next unit now run under the
+// end of this one (251 us a CTA a unit, FWD_LONG persistent).  256 rows a unit
+// because K / V tiles read for 128 rows came near what L2 delivers (279 us).  Where
+// that leaves SMs idle (kSplit; split_rule below), a unit is 128 queries and the
+// groups take the first and last 64 keys of every key tile; they meet at its end,
+// when the two O are added, scaled to one maximum.
 //
 // The bias of a group's tile is a window of the head's expanded table (log2
 // units), element (row r, column c) entry c - r + 127.  A warpgroup loads its next
@@ -82,13 +85,14 @@ template <int D> struct RelFwdCfg {
     static constexpr int T_S = 0, T_O = 256;  // S (and P) of group g, step parity b at T_S + 128 g + 64 b, O at T_O + D g
     static constexpr int T_COLS = 512;
     static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
-    static_assert(2 + 2 * NSK + 2 * NSV + 10 <= 32, "barrier slots");
+    static_assert(3 + 2 * NSK + 2 * NSV + 10 <= 32, "barrier slots");
 };
 
 struct RelFwdParams {
     CUtensorMap tm_q, tm_k, tm_v;
     DenseArgs a;
     RelArgs rel;
+    int64_t units;
 };
 
 namespace {
@@ -110,60 +114,76 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
-    uint64_t *q_full = bars + 0, *drain = bars + 1;
-    uint64_t *k_full = bars + 2, *k_empty = k_full + NSK, *v_full = k_empty + NSK, *v_empty = v_full + NSV;
+    uint64_t *q_full = bars + 0, *q_empty = bars + 1, *drain = bars + 2;
+    uint64_t *k_full = bars + 3, *k_empty = k_full + NSK, *v_full = k_empty + NSK, *v_empty = v_full + NSV;
     uint64_t *s_full = v_empty + NSV;      // [2 groups][2 buffers] S is written
     uint64_t *p_full = s_full + 4;         // [2 groups][2 buffers] P is written (and O rescaled if needed)
-    uint64_t *o_done = s_full + 8;         // [2 groups] O += P V has completed
+    uint64_t *o_done = s_full + 8;         // [2 groups] O += P V of the last but one step, and of the last
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC + 8);
     const DenseArgs &a = p.a;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    // ---- the unit: (sequence b, query head hq, query tile qt, or the two tiles qt and qt + 1), longest first
+    // ---- a unit: (sequence b, query head hq, queries i0 .. i0 + ROWS - 1)
     constexpr int ROWS = kSplit ? BM : 2 * BM;
-    int64_t b, hq, qt;
-    {
-        const int64_t u = blockIdx.x;
-        if (!kPacked) {
-            const int64_t nu = (geo.q_len(0) + ROWS - 1) / ROWS, per = a.h * geo.nseq;
-            qt = (nu - 1 - u / per) * (ROWS / BM);
-            const int64_t rest = u - (u / per) * per;
-            b = rest / a.h;
-            hq = rest - b * a.h;
-        } else {  // 128-row tiles of the packed workspace rows, each sequence's last tile first
-            const int64_t tile = u / a.h;
-            hq = u - tile * a.h;
-            int64_t i0w = 0;
-            geo.ws_locate(tile * BM, &b, &i0w);
-            const int64_t nqt = (geo.q_len(b) + BM - 1) / BM;
-            qt = nqt - 1 - i0w / BM;
-            if (!kSplit && (qt & 1)) return;  // the CTA of tile qt - 1 has it
-        }
-    }
-    const int64_t G = a.h / a.h_kv, g = hq / G;
-    const int64_t lq = geo.q_len(b), lkv = geo.kv_len(b);
-    const int64_t q_row0 = kPacked ? geo.q_start(b) : 0, kv_row0 = kPacked ? geo.kv_start(b) : 0;
-    const int q_b = kPacked ? 0 : int(b);
-    const int64_t i0 = qt * BM;
-    // keys that any of the query rows first .. first + BM - 1 sees
-    auto keys_seen = [&](int64_t first) -> int64_t {
-        if (first >= lq || lkv <= 0) return 0;
-        const int64_t last = first + BM - 1 < lq - 1 ? first + BM - 1 : lq - 1;
-        return last_visible_key(a.mask, last, lq, lkv) + 1;
+    const int64_t G = a.h / a.h_kv;
+    struct Unit {
+        int64_t b, hq, g, lq, lkv, q_row0, kv_row0, i0;
+        int q_b;
+        int steps0, steps1;  // steps of the groups
+        int n_steps, n_kt;   // the longer of the two, and the key tiles they span
     };
-    // steps of the two groups, and the key tiles they span (the second group's rows see at least the first's keys)
-    const int64_t seen0 = keys_seen(i0), seen1 = kSplit || i0 + BM >= lq ? seen0 : keys_seen(i0 + BM);
-    const int n_kt = seen1 <= 0 ? 0 : int((seen1 + BN - 1) / BN);
-    const int steps0 = kSplit ? n_kt : (seen0 <= 0 ? 0 : int((seen0 + HN - 1) / HN));
-    const int steps1 = kSplit ? n_kt : (i0 + BM >= lq || seen1 <= 0 ? 0 : int((seen1 + HN - 1) / HN));
-    const int n_steps = steps1 > steps0 ? steps1 : steps0;
+    // this CTA's unit of round r into u; false behind the last one
+    auto next_unit = [&](int64_t &r, Unit &u) -> bool {
+        for (;; ++r) {
+            const int64_t k = r * gridDim.x + ((r & 1) ? int64_t(gridDim.x) - 1 - blockIdx.x : int64_t(blockIdx.x));
+            if (r * gridDim.x >= p.units) return false;
+            if (k >= p.units) continue;
+            int64_t qt;
+            if (!kPacked) {
+                const int64_t nu = (geo.q_len(0) + ROWS - 1) / ROWS, per = a.h * geo.nseq;
+                qt = (nu - 1 - k / per) * (ROWS / BM);
+                const int64_t rest = k - (k / per) * per;
+                u.b = rest / a.h;
+                u.hq = rest - u.b * a.h;
+            } else {  // 128-row tiles of the packed workspace rows, each sequence's last tile first
+                const int64_t tile = k / a.h;
+                u.hq = k - tile * a.h;
+                int64_t i0w = 0;
+                geo.ws_locate(tile * BM, &u.b, &i0w);
+                const int64_t nqt = (geo.q_len(u.b) + BM - 1) / BM;
+                qt = nqt - 1 - i0w / BM;
+                if (!kSplit && (qt & 1)) continue;  // goes with tile qt - 1
+            }
+            u.g = u.hq / G;
+            u.lq = geo.q_len(u.b);
+            u.lkv = geo.kv_len(u.b);
+            u.q_row0 = kPacked ? geo.q_start(u.b) : 0;
+            u.kv_row0 = kPacked ? geo.kv_start(u.b) : 0;
+            u.q_b = kPacked ? 0 : int(u.b);
+            u.i0 = qt * BM;
+            // keys that any of the query rows first .. first + BM - 1 sees
+            auto keys_seen = [&](int64_t first) -> int64_t {
+                if (first >= u.lq || u.lkv <= 0) return 0;
+                const int64_t last = first + BM - 1 < u.lq - 1 ? first + BM - 1 : u.lq - 1;
+                const int64_t n = last_visible_key(a.mask, last, u.lq, u.lkv) + 1;
+                return n > 0 ? n : 0;
+            };
+            const int64_t seen0 = keys_seen(u.i0), seen1 = kSplit ? seen0 : keys_seen(u.i0 + BM);
+            u.steps0 = int((seen0 + (kSplit ? BN : HN) - 1) / (kSplit ? BN : HN));
+            u.steps1 = int((seen1 + (kSplit ? BN : HN) - 1) / (kSplit ? BN : HN));
+            u.n_steps = u.steps1 > u.steps0 ? u.steps1 : u.steps0;
+            u.n_kt = kSplit ? u.n_steps : (u.n_steps + 1) / 2;
+            return true;
+        }
+    };
     auto tile_of = [](int j) { return kSplit ? j : j >> 1; };               // key tile of a step
     auto half_of = [](int j, int grp) { return kSplit ? grp : j & 1; };     // and which half of it
 
     if (threadIdx.x == 0) {
         *abort = 0;
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         mbar_init(drain, 1);
         for (int s = 0; s < NSK; ++s) {
             mbar_init(&k_full[s], 1);
@@ -191,40 +211,51 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
     auto sV = [&](int s) { return smem + Cfg::OFF_V + s * Cfg::TILE_BYTES; };
 
     if (warp < 4) {
-        if ((warp == 0 || warp == 2) && elect_one() && n_kt > 0) {
+        if ((warp == 0 || warp == 2) && elect_one()) {
             // ============================================= TMA producers: Q and K (warp 0), V (warp 2)
             const bool isk = warp == 0;
             const int nst = isk ? NSK : NSV;
             uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
             const CUtensorMap *tm = isk ? &p.tm_k : &p.tm_v;
             prefetch_tmap(tm);
+            if (isk) prefetch_tmap(&p.tm_q);
             bool ok = true;
-            int armed = 0;
-            if (isk) {
-                prefetch_tmap(&p.tm_q);
-                mbar_arrive_expect_tx(q_full, (steps1 && !kSplit ? 2 : 1) * Cfg::TILE_BYTES);
-                for (int k = 0; k < (steps1 && !kSplit ? 2 : 1); ++k)
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, a.status);
+            };
+            uint32_t n_tile = 0, n_unit = 0;  // key tiles and units with keys so far
+            Unit u;
+            for (int64_t r = 0; ok && next_unit(r, u); ++r) {
+                if (u.n_steps == 0) continue;
+                if (isk) {
+                    if (n_unit > 0) wait(q_empty, (n_unit - 1) & 1);
+                    if (!ok) break;
+                    const int n = !kSplit && u.steps1 ? 2 : 1;
+                    ++n_unit;
+                    mbar_arrive_expect_tx(q_full, n * Cfg::TILE_BYTES);
+                    for (int k = 0; k < n; ++k)
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_4d(sQ + k * Cfg::TILE_BYTES + c * BM * 128, &p.tm_q, q_full, c * 64,
+                                        int(u.q_row0 + u.i0 + k * BM), int(u.hq), u.q_b);
+                }
+                for (int j = 0; j < u.n_kt; ++j) {
+                    const uint32_t s = n_tile % nst, use = n_tile / nst;
+                    if (use > 0) wait(&empty[s], (use - 1) & 1);
+                    if (!ok) break;
+                    ++n_tile;
+                    mbar_arrive_expect_tx(&full[s], Cfg::TILE_BYTES);
+                    uint8_t *dst = isk ? sK(s) : sV(s);
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(sQ + k * Cfg::TILE_BYTES + c * BM * 128, &p.tm_q, q_full, c * 64,
-                                    int(q_row0 + i0 + k * BM), int(hq), q_b);
+                        tma_load_4d(dst + c * BN * 128, tm, &full[s], c * 64, int(u.kv_row0 + j * BN), int(u.g), u.q_b);
+                }
             }
-            for (int j = 0; j < n_kt; ++j) {
-                const int s = j % nst, use = j / nst;
-                if (use > 0 && ok && !(ok = mbar_wait(&empty[s], uint32_t(use - 1) & 1, abort)))
-                    flag_abort(abort, a.status);
-                if (!ok) break;
-                armed = j + 1;
-                mbar_arrive_expect_tx(&full[s], Cfg::TILE_BYTES);
-                uint8_t *dst = isk ? sK(s) : sV(s);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(dst + c * BN * 128, tm, &full[s], c * 64, int(kv_row0 + j * BN), int(g), q_b);
+            if (!ok) {  // let every copy this thread started land before the CTA exits
+                volatile int never = 0;
+                if (isk && n_unit > 0) mbar_wait(q_full, (n_unit - 1) & 1, &never, 100000000ull);
+                for (uint32_t j = n_tile > uint32_t(nst) ? n_tile - nst : 0; j < n_tile; ++j)
+                    mbar_wait(&full[j % nst], (j / nst) & 1, &never, 100000000ull);
             }
-            // let every copy this thread started land before the CTA exits
-            volatile int never = 0;
-            if (isk) mbar_wait(q_full, 0, &never, 100000000ull);
-            for (int j = armed - nst; j < armed; ++j)
-                if (j >= 0) mbar_wait(&full[j % nst], uint32_t(j / nst) & 1, &never, 100000000ull);
-        } else if (warp == 1 && elect_one() && n_kt > 0) {
+        } else if (warp == 1 && elect_one()) {
             // ============================================= MMA issuer
             constexpr uint32_t idS = idesc_f16(128, HN, kType, 0, 0);
             constexpr uint32_t idO = idesc_f16(128, D, kType, 0, 1);
@@ -233,47 +264,69 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                 if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, a.status);
                 tc_fence_after();
             };
-            wait(q_full, 0);
-            // S of step j, then O += P V of step j - 1.  S of step j goes where P of step j - 2 was, whose
-            // product was issued a round ago
-            for (int j = 0; j <= n_steps; ++j) {
-                if (j < n_steps) {
-                    const int tl = tile_of(j), s = tl % NSK;
-                    if (kSplit || (j & 1) == 0) wait(&k_full[s], uint32_t(tl / NSK) & 1);
-                    if (ok) {
-                        const uint64_t kK = desc_kmaj(smem_u32(sK(s)), BN, 0);
-#pragma unroll
-                        for (int grp = 0; grp < 2; ++grp) {
-                            if (j >= (grp ? steps1 : steps0)) continue;
-                            const uint64_t kQ = desc_kmaj(smem_u32(sQ + (kSplit ? 0 : grp * Cfg::TILE_BYTES)), BM, 0);
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                mma_f16_ss(tmem + Cfg::T_S + grp * 128 + (j & 1) * 64, kmaj_step(kQ, BM, kk),
-                                           kmaj_step(kK + uint64_t(half_of(j, grp) * HN * 128 / 16), BN, kk), idS, kk > 0);
-                            mma_commit(&s_full[grp * 2 + (j & 1)]);
-                        }
-                        // the last S that reads this K stage
-                        if (kSplit || (j & 1) || j == n_steps - 1) mma_commit(&k_empty[s]);
+            uint32_t k_base = 0, n_unit = 0, base0 = 0, base1 = 0;  // key tiles, units, steps of the groups before this unit
+            Unit u;
+            for (int64_t r = 0; next_unit(r, u); ++r) {
+                if (u.n_steps == 0) continue;
+                wait(q_full, n_unit & 1);
+                ++n_unit;
+                // S of group grp's step j; the wait is for the key tile's first use
+                int k_tiles = 0;  // key tiles of the unit waited for
+                auto s_gemm = [&](int grp, int j) {
+                    const uint32_t tl = k_base + tile_of(j), s = tl % NSK, sb = ((grp ? base1 : base0) + j) & 1;
+                    if (tile_of(j) == k_tiles) {
+                        wait(&k_full[s], (tl / NSK) & 1);
+                        ++k_tiles;
                     }
+                    if (ok) {
+                        const uint64_t kQ = desc_kmaj(smem_u32(sQ + (kSplit ? 0 : grp * Cfg::TILE_BYTES)), BM, 0);
+                        const uint64_t kK = desc_kmaj(smem_u32(sK(s)), BN, 0) + uint64_t(half_of(j, grp) * HN * 128 / 16);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_f16_ss(tmem + Cfg::T_S + grp * 128 + sb * 64, kmaj_step(kQ, BM, kk), kmaj_step(kK, BN, kk), idS,
+                                       kk > 0);
+                        mma_commit(&s_full[grp * 2 + sb]);
+                    }
+                };
+                // the last S of step j reads its K stage for the last time; the last of the unit, Q too
+                auto k_done = [&](int j) {
+                    if (ok && j < u.n_steps && (kSplit || (j & 1) || j == u.n_steps - 1)) {
+                        mma_commit(&k_empty[(k_base + tile_of(j)) % NSK]);
+                        if (j == u.n_steps - 1) mma_commit(q_empty);
+                    }
+                };
+                for (int j = 0; j < 2; ++j) {
+                    for (int grp = 0; grp < 2; ++grp)
+                        if (j < (grp ? u.steps1 : u.steps0)) s_gemm(grp, j);
+                    k_done(j);
                 }
-                if (j > 0) {
-                    const int x = j - 1, tl = tile_of(x), s = tl % NSV, sb = x & 1;
-                    if (kSplit || (x & 1) == 0) wait(&v_full[s], uint32_t(tl / NSV) & 1);
+                // for each group in turn, O += P V of step x and S of step x + 2 into the columns of that P: the
+                // groups' MMAs alternate, and each group has its next S before its softmax asks for it
+                for (int x = 0; x < u.n_steps; ++x) {
+                    const uint32_t tl = k_base + tile_of(x), s = tl % NSV;
+                    if (kSplit || (x & 1) == 0) wait(&v_full[s], (tl / NSV) & 1);
                     const uint64_t mV = desc_mn(smem_u32(sV(s)), BN, 0);
 #pragma unroll
                     for (int grp = 0; grp < 2; ++grp) {
-                        if (x >= (grp ? steps1 : steps0)) continue;
-                        wait(&p_full[grp * 2 + sb], uint32_t(x >> 1) & 1);
+                        const int steps = grp ? u.steps1 : u.steps0;
+                        if (x >= steps) continue;
+                        const uint32_t n = (grp ? base1 : base0) + x, sb = n & 1;
+                        wait(&p_full[grp * 2 + sb], (n >> 1) & 1);
                         if (ok) {
 #pragma unroll
                             for (int kk = 0; kk < HN / 16; ++kk)
                                 mma_f16_ts(tmem + Cfg::T_O + grp * D, tmem + Cfg::T_S + grp * 128 + sb * 64 + kk * 8,
                                            mn_step(mV, half_of(x, grp) * (HN / 16) + kk), idO, x > 0 || kk > 0);
-                            mma_commit(&o_done[grp]);
+                            if (x >= steps - 2) mma_commit(&o_done[grp]);  // earlier ones are behind S of step x + 2
                         }
+                        if (x + 2 < steps) s_gemm(grp, x + 2);
                     }
-                    if (ok && (kSplit || (x & 1) || x == n_steps - 1)) mma_commit(&v_empty[s]);
+                    k_done(x + 2);
+                    if (ok && (kSplit || (x & 1) || x == u.n_steps - 1)) mma_commit(&v_empty[s]);
                 }
+                k_base += u.n_kt;
+                base0 += u.steps0;
+                base1 += u.steps1;
             }
             volatile int never = 0;
             mma_commit(drain);
@@ -284,43 +337,51 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
         const int grp = (warp >> 2) - 1, qd = warp & 3;  // the group; TMEM lane quadrant
         const uint32_t lane_addr = uint32_t(qd * 32) << 16;
         const int r = qd * 32 + lane, wt = threadIdx.x & 127;
-        const int steps = grp ? steps1 : steps0;
-        const int64_t first_row = i0 + (kSplit ? 0 : grp * BM);
-        const int64_t i = first_row + r;  // query position in the sequence
         const float c = a.scale * kLog2e;
-        const int64_t kmax = lkv > 0 && i < lq ? last_visible_key(a.mask, i, lq, lkv) : -1;  // last key it sees
         const uint32_t tO = tmem + lane_addr + Cfg::T_O + grp * D;
-        float m_ref = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
+        float *win = reinterpret_cast<float *>(smem + Cfg::OFF_WIN) + grp * 512;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, a.status);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
+        uint32_t base = 0, k_base = 0, n_done = 0;  // steps of this group, key tiles, o_done phases before this unit
+        pdl_wait();  // the bias has been expanded
+
+        Unit u;
+        for (int64_t round = 0; next_unit(round, u); ++round) {
+        const int steps = grp ? u.steps1 : u.steps0;
+        const int64_t first_row = u.i0 + (kSplit ? 0 : grp * BM);
+        const int64_t i = first_row + r;  // query position in the sequence
+        const int64_t kmax = u.lkv > 0 && i < u.lq ? last_visible_key(a.mask, i, u.lq, u.lkv) : -1;  // last key it sees
+        float m_ref = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
         // the window of step j, whose first key is key0(j), starts at delta key0(j) - row0; this thread's two
         // entries of it
-        float *win = reinterpret_cast<float *>(smem + Cfg::OFF_WIN) + grp * 512;
         auto key0 = [&](int j) { return int64_t(tile_of(j)) * BN + half_of(j, grp) * HN; };
-        const int64_t row0 = first_row + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0) + 127;
+        const int64_t row0 = first_row + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? u.lkv - u.lq : 0) + 127;
         auto kind_of = [&](int j) { return rel_tile(p.rel.b, key0(j) - row0, HN + 127); };
-        const float *rel = p.rel.rel + hq * p.rel.stride;
+        const float *rel = p.rel.rel + u.hq * p.rel.stride;
         auto window = [&](int j) -> float2 {
             if (kind_of(j) != kRelNear) return make_float2(0.f, 0.f);
             const float *w = rel + (key0(j) - row0 - (p.rel.b.lo - kRelPad)) + wt;
             return make_float2(__ldcg(w), __ldcg(w + 128));
         };
-        pdl_wait();  // the bias has been expanded
         const float past = __ldcg(rel), future = __ldcg(rel + p.rel.stride - 1);
+        // the windows alternate by this group's running step number; all reads of the last unit's are behind its
+        // last barrier here
+        named_bar_sync(1 + grp, 128);
         if (steps > 0) {
             const float2 w = window(0);
-            win[wt] = w.x;
-            win[wt + 128] = w.y;
+            win[(base & 1) * 256 + wt] = w.x;
+            win[(base & 1) * 256 + wt + 128] = w.y;
         }
         named_bar_sync(1 + grp, 128);
 
         for (int j = 0; j < steps; ++j) {
-            const int sb = j & 1;
+            const uint32_t n = base + j;  // running step number
+            const int sb = n & 1;
             const uint32_t tS = tmem + lane_addr + Cfg::T_S + grp * 128 + sb * 64;
             const RelTile kind = kind_of(j);
             const bool next_near = j + 1 < steps && kind_of(j + 1) == kRelNear;
@@ -328,7 +389,7 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             const int64_t lim64 = kmax - key0(j);  // columns <= lim are visible
             const int lim = int(lim64 < -1 ? -1 : (lim64 > HN ? HN : lim64));
             const bool whole = __all_sync(0xffffffffu, lim >= HN - 1);
-            wait(&s_full[grp * 2 + sb], uint32_t(j >> 1) & 1);
+            wait(&s_full[grp * 2 + sb], (n >> 1) & 1);
             // the row of S in log2 units, with its bias and masked, and its maximum
             float x[HN];
             float mx = -INFINITY;
@@ -379,8 +440,10 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             const bool need = m_new > m_ref + 8.f;  // also the first finite max
             if (__any_sync(0xffffffffu, need)) {
                 const float f = need ? ex2(m_ref - m_new) : 1.f;  // exp2(-inf) = 0 on the first raise
-                if (j > 0) {  // O holds earlier tiles: scale this row once their GEMMs have completed
-                    wait(&o_done[grp], uint32_t(j - 1) & 1);
+                if (j > 0) {  // O holds earlier tiles: scale this row once their GEMMs have completed, which S of
+                              // the next step, issued behind the last of them, shows
+                    if (j + 1 < steps) wait(&s_full[grp * 2 + (sb ^ 1)], ((n + 1) >> 1) & 1);
+                    else wait(&o_done[grp], n_done & 1);
                     if (ok) {
 #pragma unroll 1
                         for (int o0 = 0; o0 < D; o0 += 32) {
@@ -421,11 +484,11 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                     tmem_st8(tS + e0 / 2, w);
                 }
                 tmem_st_wait();
-                if (kPacked && key0(j) + HN > lkv) {  // values of the next sequence
-                    const int tl = tile_of(j), s = tl % NSV;
-                    wait(&v_full[s], uint32_t(tl / NSV) & 1);
+                if (kPacked && key0(j) + HN > u.lkv) {  // values of the next sequence
+                    const uint32_t tl = k_base + tile_of(j), s = tl % NSV;
+                    wait(&v_full[s], (tl / NSV) & 1);
                     const int row = half_of(j, grp) * HN + r;  // of the tile
-                    if (r < HN && key0(j) + r >= lkv)
+                    if (r < HN && key0(j) + r >= u.lkv)
                         for (int q = 0; q < D / 64; ++q)
                             for (int e = 0; e < 8; ++e)
                                 st_shared_v4(smem_u32(sV(s)) + q * BN * 128 + row * 128 + e * 16, 0, 0, 0, 0);
@@ -450,13 +513,14 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             fb = mb == -INFINITY ? 0.f : ex2(mb - m);
             l = fa * ml[128 + r] + fb * ml[256 + 128 + r];
         }
-        if (n_kt > 0 && (kSplit || steps > 0)) {
-            wait(&o_done[grp], uint32_t(steps - 1) & 1);
-            if (kSplit) wait(&o_done[grp ^ 1], uint32_t(steps - 1) & 1);
+        for (int k = 0; k < 2 && k < steps; ++k, ++n_done) {  // each phase in turn: a parity tells neighbours apart only
+            wait(&o_done[grp], n_done & 1);
+            if (kSplit) wait(&o_done[grp ^ 1], n_done & 1);
         }
-        const bool row_ok = i < lq;
+        const bool row_ok = i < u.lq;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        T *O = static_cast<T *>(a.o.ptr) + (kPacked ? 0 : int64_t(q_b) * a.o.sb) + hq * a.o.sh + (q_row0 + i) * a.o.ss;
+        T *O = static_cast<T *>(a.o.ptr) + (kPacked ? 0 : int64_t(u.q_b) * a.o.sb) + u.hq * a.o.sh +
+               (u.q_row0 + i) * a.o.ss;
         const uint32_t tOa = tmem + lane_addr + Cfg::T_O + (kSplit ? 0 : grp * D);
 #pragma unroll 1
         for (int o0 = kSplit ? grp * (D / 2) : 0; o0 < (kSplit ? (grp + 1) * (D / 2) : D); o0 += 32) {
@@ -486,8 +550,14 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
         }
         if (row_ok && (!kSplit || grp == 0)) {
             const float lse = l > 0.f ? (m + __log2f(l)) / kLog2e : INFINITY;
-            const int64_t idx = kPacked ? hq * a.t_q + q_row0 + i : (int64_t(q_b) * a.h + hq) * lq + i;
+            const int64_t idx = kPacked ? u.hq * a.t_q + u.q_row0 + i : (int64_t(u.q_b) * a.h + u.hq) * u.lq + i;
             a.lse_out[idx] = lse;
+        }
+        base += steps;
+        k_base += u.n_kt;
+        // the next unit's first product overwrites O once this group's P of it is there, which is behind these
+        // reads; with kSplit the other group's reads too
+        if (kSplit) named_bar_sync(3, 256);
         }
     }
 
@@ -511,19 +581,49 @@ int64_t sm_count()
     return n > 0 ? n : 1;
 }
 
+// Units of 128 queries, the keys of a tile split between the groups, or of 256?  Both take about a step's time for
+// 128 x 128 scores and about three steps around a unit, so the estimate of each is the work shared out over the SMs
+// plus one of the smallest units (the last to be dealt), or the longest unit if that is more.  Measured (us, split /
+// whole, d = 64 unless noted): b1 h12 s1024 13.1 / 21.1; b2 h12 s1024 23.6 / 21.3, causal 15.2 / 21.1; b4 h12 s1024
+// 34.9 / 39.4; b8 h12 s1024 causal 47.7 / 40.5; b2 h32 s4096 d128 causal 276 / 251.  Packed batches: whole where
+// there are tiles for every SM four times over.
+template <int BM, int BN, class Geo> bool split_rule(const DenseArgs &a, const Geo &g, int64_t tiles)
+{
+    const double sms = double(sm_count());
+    if (IsPackedGeo<Geo>::value) return double(tiles) < 4 * sms;
+    const int64_t lq = g.q_len(0), lkv = g.kv_len(0);
+    double est[2];
+    for (int whole = 0; whole < 2; ++whole) {
+        const int64_t rows = whole ? 2 * BM : BM, n = (lq + rows - 1) / rows;
+        double sum = 0, longest = 0, shortest = 0;
+        for (int64_t k = 0; k < n; ++k) {
+            const int64_t last = (k + 1) * rows - 1 < lq - 1 ? (k + 1) * rows - 1 : lq - 1;
+            const int64_t seen = lkv > 0 ? last_visible_key(a.mask, last, lq, lkv) + 1 : 0;
+            const double c = 3 + (seen > 0 ? double((seen + BN / (whole ? 2 : 1) - 1) / (BN / (whole ? 2 : 1))) : 0);
+            sum += c;
+            longest = c > longest ? c : longest;
+            shortest = k == 0 || c < shortest ? c : shortest;
+        }
+        const double per = double(a.h * a.nseq), units = per * double(n), shared = per * sum / sms + shortest;
+        est[whole] = units <= sms || longest > shared ? longest : shared;
+    }
+    return est[0] < est[1];
+}
+
 template <class T, int D, class Geo> cudaError_t run(const DenseArgs &a, const RelArgs &rel, const Geo &g, cudaStream_t s)
 {
     using Cfg = RelFwdCfg<D>;
     constexpr bool packed = IsPackedGeo<Geo>::value;
     const int64_t tiles = packed ? (g.ws_rows() / Cfg::BM) * a.h : (g.q_len(0) + Cfg::BM - 1) / Cfg::BM * a.h * a.nseq;
-    const bool split = tiles <= sm_count();
-    // packed: a CTA for every 128-row tile, of which every other one ends at once
+    const bool split = split_rule<Cfg::BM, Cfg::BN>(a, g, tiles);
+    // packed: a unit for every 128-row tile, of which every other one is passed over
     const int64_t units = split || packed ? tiles : (g.q_len(0) + 2 * Cfg::BM - 1) / (2 * Cfg::BM) * a.h * a.nseq;
     if (units == 0) return cudaSuccess;
     if (units > INT32_MAX) return cudaErrorInvalidValue;
     RelFwdParams prm;
     prm.a = a;
     prm.rel = rel;
+    prm.units = units;
     const int64_t nb = packed ? 1 : a.nseq;
     const int64_t sq = packed ? a.t_q : g.q_len(0), skv = packed ? a.t_kv : g.kv_len(0);
     if (!tmap_view16(&prm.tm_q, a.q, a.dtype, D, sq, a.h, nb, Cfg::BM)) return cudaErrorInvalidValue;
@@ -538,7 +638,8 @@ template <class T, int D, class Geo> cudaError_t run(const DenseArgs &a, const R
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     // starts beside the kernel that expands the table (and clears the status word); the softmax warps wait for it
-    return launch_kernel(k, dim3(unsigned(units)), dim3(Cfg::THREADS), Cfg::SMEM_ALLOC, s, true, prm, g);
+    const int64_t ctas = units < sm_count() ? units : sm_count();
+    return launch_kernel(k, dim3(unsigned(ctas)), dim3(Cfg::THREADS), Cfg::SMEM_ALLOC, s, true, prm, g);
 }
 
 template <class Geo> cudaError_t pick(const DenseArgs &a, const RelArgs &rel, const Geo &g, cudaStream_t s)
