@@ -85,7 +85,7 @@ template <int D> struct RelFwdCfg {
     static constexpr int T_S = 0, T_O = 256;  // S (and P) of group g, step parity b at T_S + 128 g + 64 b, O at T_O + D g
     static constexpr int T_COLS = 512;
     static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
-    static_assert(3 + 2 * NSK + 2 * NSV + 10 <= 32, "barrier slots");
+    static_assert(3 + 2 * NSK + 2 * NSV + 12 <= 32, "barrier slots");
 };
 
 struct RelFwdParams {
@@ -99,6 +99,19 @@ namespace {
 
 template <class Geo> struct IsPackedGeo : std::false_type {};
 template <> struct IsPackedGeo<PackedGeo> : std::true_type {};
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// mbar_wait out of line, for the MMA thread: its waits are nearly always over when it comes.
+__device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    return mbar_wait(bar, parity, abort);
+}
 
 }  // namespace
 
@@ -118,7 +131,8 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
     uint64_t *k_full = bars + 3, *k_empty = k_full + NSK, *v_full = k_empty + NSK, *v_empty = v_full + NSV;
     uint64_t *s_full = v_empty + NSV;      // [2 groups][2 buffers] S is written
     uint64_t *p_full = s_full + 4;         // [2 groups][2 buffers] P is written (and O rescaled if needed)
-    uint64_t *o_done = s_full + 8;         // [2 groups] O += P V of the last but one step, and of the last
+    uint64_t *o_prev = s_full + 8;         // [2 groups] O += P V of a unit's last step but one has completed ...
+    uint64_t *o_last = s_full + 10;        // [2 groups] ... and of its last step
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC + 8);
     const DenseArgs &a = p.a;
@@ -197,8 +211,10 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             mbar_init(&s_full[k], 1);
             mbar_init(&p_full[k], 4);
         }
-        mbar_init(&o_done[0], 1);
-        mbar_init(&o_done[1], 1);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&o_prev[k], 1);
+            mbar_init(&o_last[k], 1);
+        }
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, Cfg::T_COLS);
@@ -257,76 +273,86 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             }
         } else if (warp == 1 && elect_one()) {
             // ============================================= MMA issuer
+            // One thread, and the time it takes between two MMAs is the tensor pipe's to lose: descriptors are
+            // one add from values kept in registers, a unit starts at buffer 0 so that buffers and halves are
+            // constants of the (two-step) loop body, and phases are bits that flip with each wait.
             constexpr uint32_t idS = idesc_f16(128, HN, kType, 0, 0);
             constexpr uint32_t idO = idesc_f16(128, D, kType, 0, 1);
+            constexpr uint32_t STAGE = Cfg::TILE_BYTES / 16;  // a ring stage, in descriptor units
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, a.status);
+                if (ok && !mbar_test_wait(bar, parity) && !(ok = mbar_wait_slow(bar, parity, abort))) flag_abort(abort, a.status);
                 tc_fence_after();
             };
-            uint32_t k_base = 0, n_unit = 0, base0 = 0, base1 = 0;  // key tiles, units, steps of the groups before this unit
+            const uint64_t kQ = desc_kmaj(smem_u32(sQ), BM, 0), kK = desc_kmaj(smem_u32(sK(0)), BN, 0);
+            const uint64_t mV = desc_mn(smem_u32(sV(0)), BN, 0);
+            uint32_t ks = 0, vs = 0, k_par = 0, v_par = 0, q_par = 0, p_par = 0;  // p_par: bit 2 group + buffer
             Unit u;
             for (int64_t r = 0; next_unit(r, u); ++r) {
                 if (u.n_steps == 0) continue;
-                wait(q_full, n_unit & 1);
-                ++n_unit;
-                // S of group grp's step j; the wait is for the key tile's first use
-                int k_tiles = 0;  // key tiles of the unit waited for
-                auto s_gemm = [&](int grp, int j) {
-                    const uint32_t tl = k_base + tile_of(j), s = tl % NSK, sb = ((grp ? base1 : base0) + j) & 1;
-                    if (tile_of(j) == k_tiles) {
-                        wait(&k_full[s], (tl / NSK) & 1);
-                        ++k_tiles;
-                    }
-                    if (ok) {
-                        const uint64_t kQ = desc_kmaj(smem_u32(sQ + (kSplit ? 0 : grp * Cfg::TILE_BYTES)), BM, 0);
-                        const uint64_t kK = desc_kmaj(smem_u32(sK(s)), BN, 0) + uint64_t(half_of(j, grp) * HN * 128 / 16);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            mma_f16_ss(tmem + Cfg::T_S + grp * 128 + sb * 64, kmaj_step(kQ, BM, kk), kmaj_step(kK, BN, kk), idS,
-                                       kk > 0);
-                        mma_commit(&s_full[grp * 2 + sb]);
-                    }
-                };
-                // the last S of step j reads its K stage for the last time; the last of the unit, Q too
-                auto k_done = [&](int j) {
-                    if (ok && j < u.n_steps && (kSplit || (j & 1) || j == u.n_steps - 1)) {
-                        mma_commit(&k_empty[(k_base + tile_of(j)) % NSK]);
-                        if (j == u.n_steps - 1) mma_commit(q_empty);
-                    }
-                };
-                for (int j = 0; j < 2; ++j) {
-                    for (int grp = 0; grp < 2; ++grp)
-                        if (j < (grp ? u.steps1 : u.steps0)) s_gemm(grp, j);
-                    k_done(j);
-                }
-                // for each group in turn, O += P V of step x and S of step x + 2 into the columns of that P: the
-                // groups' MMAs alternate, and each group has its next S before its softmax asks for it
-                for (int x = 0; x < u.n_steps; ++x) {
-                    const uint32_t tl = k_base + tile_of(x), s = tl % NSV;
-                    if (kSplit || (x & 1) == 0) wait(&v_full[s], (tl / NSV) & 1);
-                    const uint64_t mV = desc_mn(smem_u32(sV(s)), BN, 0);
-#pragma unroll
-                    for (int grp = 0; grp < 2; ++grp) {
-                        const int steps = grp ? u.steps1 : u.steps0;
-                        if (x >= steps) continue;
-                        const uint32_t n = (grp ? base1 : base0) + x, sb = n & 1;
-                        wait(&p_full[grp * 2 + sb], (n >> 1) & 1);
+                wait(q_full, q_par);
+                q_par ^= 1;
+                const int n_steps = u.n_steps, steps0 = u.steps0, steps1 = u.steps1;
+                // S of step j, then O += P V of step j - 1 (buffer sb ^ 1).  S of step j goes where P of step
+                // j - 2 was, whose product was issued a round ago
+                auto round = [&](int j, auto sb_tag) {
+                    constexpr int sb = decltype(sb_tag)::value, xb = sb ^ 1;
+                    if (j < n_steps) {
+                        if (kSplit || sb == 0) wait(&k_full[ks], k_par);
                         if (ok) {
 #pragma unroll
-                            for (int kk = 0; kk < HN / 16; ++kk)
-                                mma_f16_ts(tmem + Cfg::T_O + grp * D, tmem + Cfg::T_S + grp * 128 + sb * 64 + kk * 8,
-                                           mn_step(mV, half_of(x, grp) * (HN / 16) + kk), idO, x > 0 || kk > 0);
-                            if (x >= steps - 2) mma_commit(&o_done[grp]);  // earlier ones are behind S of step x + 2
+                            for (int grp = 0; grp < 2; ++grp) {
+                                if (j >= (grp ? steps1 : steps0)) continue;
+                                const uint64_t dk = kK + ks * STAGE + (kSplit ? grp : sb) * (HN * 128 / 16);
+                                const uint64_t dq = kQ + (kSplit ? 0 : grp * STAGE);
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    mma_f16_ss(tmem + Cfg::T_S + grp * 128 + sb * 64, kmaj_step(dq, BM, kk), kmaj_step(dk, BN, kk), idS,
+                                               kk > 0);
+                                mma_commit(&s_full[grp * 2 + sb]);
+                            }
                         }
-                        if (x + 2 < steps) s_gemm(grp, x + 2);
+                        if (kSplit || sb || j == n_steps - 1) {  // the last S that reads this K stage
+                            if (ok) mma_commit(&k_empty[ks]);
+                            if (++ks == NSK) {
+                                ks = 0;
+                                k_par ^= 1;
+                            }
+                            if (ok && j == n_steps - 1) mma_commit(q_empty);
+                        }
                     }
-                    k_done(x + 2);
-                    if (ok && (kSplit || (x & 1) || x == u.n_steps - 1)) mma_commit(&v_empty[s]);
+                    if (j > 0) {
+                        const int x = j - 1;
+                        if (kSplit || xb == 0) wait(&v_full[vs], v_par);
+#pragma unroll
+                        for (int grp = 0; grp < 2; ++grp) {
+                            const int steps = grp ? steps1 : steps0;
+                            if (x >= steps) continue;
+                            wait(&p_full[grp * 2 + xb], p_par >> (grp * 2 + xb) & 1);
+                            p_par ^= 1u << (grp * 2 + xb);
+                            if (ok) {
+                                const uint64_t dv = mV + vs * STAGE + (kSplit ? grp : xb) * (HN / 16) * 128;
+#pragma unroll
+                                for (int kk = 0; kk < HN / 16; ++kk)
+                                    mma_f16_ts(tmem + Cfg::T_O + grp * D, tmem + Cfg::T_S + grp * 128 + xb * 64 + kk * 8,
+                                               mn_step(dv, kk), idO, x > 0 || kk > 0);
+                                // (earlier ones are behind S of step x + 2)
+                                if (x >= steps - 2) mma_commit(x == steps - 1 ? &o_last[grp] : &o_prev[grp]);
+                            }
+                        }
+                        if (kSplit || xb || x == n_steps - 1) {
+                            if (ok) mma_commit(&v_empty[vs]);
+                            if (++vs == NSV) {
+                                vs = 0;
+                                v_par ^= 1;
+                            }
+                        }
+                    }
+                };
+                for (int j = 0; j <= n_steps; j += 2) {
+                    round(j, std::integral_constant<int, 0>{});
+                    if (j < n_steps) round(j + 1, std::integral_constant<int, 1>{});
                 }
-                k_base += u.n_kt;
-                base0 += u.steps0;
-                base1 += u.steps1;
             }
             volatile int never = 0;
             mma_commit(drain);
@@ -346,7 +372,8 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        uint32_t base = 0, k_base = 0, n_done = 0;  // steps of this group, key tiles, o_done phases before this unit
+        // key tiles, and phases of o_prev and o_last before this unit; phase parity of the S buffers
+        uint32_t k_base = 0, n_prev = 0, n_last = 0, s_par = 0;
         pdl_wait();  // the bias has been expanded
 
         Unit u;
@@ -354,42 +381,40 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
         const int steps = grp ? u.steps1 : u.steps0;
         const int64_t first_row = u.i0 + (kSplit ? 0 : grp * BM);
         const int64_t i = first_row + r;  // query position in the sequence
-        const int64_t kmax = u.lkv > 0 && i < u.lq ? last_visible_key(a.mask, i, u.lq, u.lkv) : -1;  // last key it sees
+        // Positions in 32 bits, relative to the unit (sequence lengths fit): step j's first key is kfirst + j kstep, of
+        // which this row sees those up to kmax; its window starts at delta dfirst + j kstep.
+        constexpr int kstep = kSplit ? BN : HN;
+        const int kfirst = kSplit ? grp * HN : 0;
+        const int kmax = u.lkv > 0 && i < u.lq ? int(last_visible_key(a.mask, i, u.lq, u.lkv)) : -1;
+        const int dfirst = kfirst - int(first_row + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? u.lkv - u.lq : 0)) - 127;
+        const int dlo = p.rel.b.lo - (HN + 126), dhi = p.rel.b.hi;  // near: dlo < first delta < dhi
         float m_ref = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
-        // the window of step j, whose first key is key0(j), starts at delta key0(j) - row0; this thread's two
-        // entries of it
-        auto key0 = [&](int j) { return int64_t(tile_of(j)) * BN + half_of(j, grp) * HN; };
-        const int64_t row0 = first_row + (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? u.lkv - u.lq : 0) + 127;
-        auto kind_of = [&](int j) { return rel_tile(p.rel.b, key0(j) - row0, HN + 127); };
         const float *rel = p.rel.rel + u.hq * p.rel.stride;
-        auto window = [&](int j) -> float2 {
-            if (kind_of(j) != kRelNear) return make_float2(0.f, 0.f);
-            const float *w = rel + (key0(j) - row0 - (p.rel.b.lo - kRelPad)) + wt;
-            return make_float2(__ldcg(w), __ldcg(w + 128));
+        const float *rel_wt = rel + (kRelPad - p.rel.b.lo) + wt;  // this thread's entry of the window at delta 0
+        auto window = [&](int d) -> float2 {  // its two entries of the window at delta d
+            return d > dlo && d < dhi ? make_float2(__ldcg(rel_wt + d), __ldcg(rel_wt + d + 128)) : make_float2(0.f, 0.f);
         };
         const float past = __ldcg(rel), future = __ldcg(rel + p.rel.stride - 1);
-        // the windows alternate by this group's running step number; all reads of the last unit's are behind its
-        // last barrier here
-        named_bar_sync(1 + grp, 128);
+        named_bar_sync(1 + grp, 128);  // the last unit's windows have been read
         if (steps > 0) {
-            const float2 w = window(0);
-            win[(base & 1) * 256 + wt] = w.x;
-            win[(base & 1) * 256 + wt + 128] = w.y;
+            const float2 w = window(dfirst);
+            win[wt] = w.x;
+            win[wt + 128] = w.y;
         }
         named_bar_sync(1 + grp, 128);
 
         for (int j = 0; j < steps; ++j) {
-            const uint32_t n = base + j;  // running step number
-            const int sb = n & 1;
+            const int sb = j & 1;
             const uint32_t tS = tmem + lane_addr + Cfg::T_S + grp * 128 + sb * 64;
-            const RelTile kind = kind_of(j);
-            const bool next_near = j + 1 < steps && kind_of(j + 1) == kRelNear;
-            const float2 next_win = next_near ? window(j + 1) : make_float2(0.f, 0.f);
-            const int64_t lim64 = kmax - key0(j);  // columns <= lim are visible
-            const int lim = int(lim64 < -1 ? -1 : (lim64 > HN ? HN : lim64));
+            const int d = dfirst + j * kstep;
+            const bool near = d > dlo && d < dhi;
+            const bool next_near = j + 1 < steps && d + kstep > dlo && d + kstep < dhi;
+            const float2 next_win = next_near ? window(d + kstep) : make_float2(0.f, 0.f);
+            const int lim = kmax - kfirst - j * kstep;  // columns <= lim are visible
             const bool whole = __all_sync(0xffffffffu, lim >= HN - 1);
-            wait(&s_full[grp * 2 + sb], (n >> 1) & 1);
+            wait(&s_full[grp * 2 + sb], s_par >> sb & 1);
+            s_par ^= 1u << sb;
             // the row of S in log2 units, with its bias and masked, and its maximum
             float x[HN];
             float mx = -INFINITY;
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                 tmem_ld_wait_regs(v[0]);
                 tmem_ld_wait_regs(v[1]);
                 const float2 c2 = make_float2(c, c);
-                if (kind == kRelNear) {
+                if (near) {
                     const float *w = win + sb * 256 - r + 127;
 #pragma unroll
                     for (int e = 0; e < HN; e += 2) {
@@ -410,7 +435,7 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                         x[e + 1] = y.y;
                     }
                 } else {
-                    const float b1 = kind == kRelPast ? past : future;
+                    const float b1 = d <= dlo ? past : future;
                     const float2 b2 = make_float2(b1, b1);
 #pragma unroll
                     for (int e = 0; e < HN; e += 2) {
@@ -428,8 +453,8 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < HN; e += 8)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mq[k] = fmaxf(mq[k], fmaxf(x[e + 2 * k], x[e + 2 * k + 1]));
-                mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                    for (int k = 0; k < 4; ++k) mq[k] = max3(mq[k], x[e + 2 * k], x[e + 2 * k + 1]);
+                mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
             }
             if (next_near) {  // the other buffer was last read a tile ago, before that tile's barrier
                 win[(sb ^ 1) * 256 + wt] = next_win.x;
@@ -442,8 +467,8 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                 const float f = need ? ex2(m_ref - m_new) : 1.f;  // exp2(-inf) = 0 on the first raise
                 if (j > 0) {  // O holds earlier tiles: scale this row once their GEMMs have completed, which S of
                               // the next step, issued behind the last of them, shows
-                    if (j + 1 < steps) wait(&s_full[grp * 2 + (sb ^ 1)], ((n + 1) >> 1) & 1);
-                    else wait(&o_done[grp], n_done & 1);
+                    if (j + 1 < steps) wait(&s_full[grp * 2 + (sb ^ 1)], s_par >> (sb ^ 1) & 1);
+                    else wait(&o_prev[grp], n_prev & 1);
                     if (ok) {
 #pragma unroll 1
                         for (int o0 = 0; o0 < D; o0 += 32) {
@@ -484,11 +509,11 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
                     tmem_st8(tS + e0 / 2, w);
                 }
                 tmem_st_wait();
-                if (kPacked && key0(j) + HN > u.lkv) {  // values of the next sequence
+                if (kPacked && kfirst + j * kstep + HN > int(u.lkv)) {  // values of the next sequence
                     const uint32_t tl = k_base + tile_of(j), s = tl % NSV;
                     wait(&v_full[s], (tl / NSV) & 1);
                     const int row = half_of(j, grp) * HN + r;  // of the tile
-                    if (r < HN && key0(j) + r >= u.lkv)
+                    if (r < HN && kfirst + j * kstep + r >= int(u.lkv))
                         for (int q = 0; q < D / 64; ++q)
                             for (int e = 0; e < 8; ++e)
                                 st_shared_v4(smem_u32(sV(s)) + q * BN * 128 + row * 128 + e * 16, 0, 0, 0, 0);
@@ -513,10 +538,14 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             fb = mb == -INFINITY ? 0.f : ex2(mb - m);
             l = fa * ml[128 + r] + fb * ml[256 + 128 + r];
         }
-        for (int k = 0; k < 2 && k < steps; ++k, ++n_done) {  // each phase in turn: a parity tells neighbours apart only
-            wait(&o_done[grp], n_done & 1);
-            if (kSplit) wait(&o_done[grp ^ 1], n_done & 1);
+        // (neither barrier gets to its next phase before every warp that waits here is through: the next unit's
+        // products wait for their P)
+        if (steps > 0) {
+            wait(&o_last[grp], n_last & 1);
+            if (kSplit) wait(&o_last[grp ^ 1], n_last & 1);
+            ++n_last;
         }
+        if (steps > 1) ++n_prev;
         const bool row_ok = i < u.lq;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         T *O = static_cast<T *>(a.o.ptr) + (kPacked ? 0 : int64_t(u.q_b) * a.o.sb) + u.hq * a.o.sh +
@@ -553,7 +582,6 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             const int64_t idx = kPacked ? u.hq * a.t_q + u.q_row0 + i : (int64_t(u.q_b) * a.h + u.hq) * u.lq + i;
             a.lse_out[idx] = lse;
         }
-        base += steps;
         k_base += u.n_kt;
         // the next unit's first product overwrites O once this group's P of it is there, which is behind these
         // reads; with kSplit the other group's reads too
