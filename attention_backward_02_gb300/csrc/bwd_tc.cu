@@ -294,9 +294,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
     uint8_t *sK = smem + Cfg::OFF_K, *sV = smem + Cfg::OFF_V, *sX = smem + Cfg::OFF_X;
     // kBias: entry of the expanded bias at which the window of a tile whose first delta is dmin starts; of a tile
     // in one end bucket whole, a place in the pad where every entry is that bucket's
-    auto window_start = [&](int64_t dmin) -> int64_t {
-        const RelTile kind = rel_tile(p.rel.b, dmin, BN + BM - 1);
-        return kind == kRelNear ? dmin - (p.rel.b.lo - kRelPad) : (kind == kRelPast ? 0 : p.rel.stride - Cfg::WIN_BYTES / 4);
+    // (32 bits: sequence lengths fit)
+    auto window_start = [&](int dmin) -> int {
+        const int lo = p.rel.b.lo;
+        return dmin <= lo - (BN + BM - 2) ? 0 : dmin >= p.rel.b.hi ? int(p.rel.stride) - Cfg::WIN_BYTES / 4 : dmin - lo + kRelPad;
     };
 
     if (warp == 0) {
@@ -340,8 +341,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     bulk_load(smem + Cfg::OFF_DVEC + st * BM * 4, a.dvec + wrow, BM * 4, &q_full[st]);
                     if (kBias) {  // the windows from the tile's first delta on, 16-byte aligned
                         uint8_t *win = smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES;
-                        const int64_t w0 = window_start(j0 - i0 - (BM - 1) - (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0)) &
-                                           ~int64_t(3);
+                        const int w0 = window_start(int(j0 - i0 - (BM - 1) - (a.mask == ATTN_CAUSAL_BOTTOM_RIGHT ? lkv - lq : 0))) & ~3;
                         bulk_load(win, p.rel.rel + hq * p.rel.stride + w0, Cfg::WIN_BYTES, &q_full[st]);
                         bulk_load(win + Cfg::WIN_BYTES, p.rel.code + w0, Cfg::WIN_BYTES, &q_full[st]);
                     }
@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             query_tiles<BM>(a.mask, j0, lq, lkv, &qt0, &nq);
             const int n_iter = G * nq;
             int iq = 0;  // query tile within the head
-            int64_t hq = g * G;  // kBias: the head
+            int64_t hq = g * G;                 // kBias: the head
+            const int jrel = int(j - shift);    // kBias: the key's position as the queries' are counted
             for (int it = 0; it < n_iter; ++it, ++qi) {
                 const int64_t i0 = int64_t(qt0 + iq) * BM;
                 // Usually LSE / D of this tile have landed (q_full), the GEMMs of tile qi - 2 that read
@@ -601,14 +602,19 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                 const uint32_t a_lse = smem_u32(smem + Cfg::OFF_LSE + st * BM * 4);
                 const uint32_t a_dv = smem_u32(smem + Cfg::OFF_DVEC + st * BM * 4);
                 // first visible query column of this key row; everything is masked past the sequence
-                const int64_t cmin64 = !row_ok ? INT64_MAX : (a.mask ? j - shift - i0 : INT64_MIN);
-                const int cmin = int(cmin64 < -1 ? -1 : (cmin64 > BM ? BM : cmin64));
+                int cmin;
+                if (kBias) {
+                    cmin = !row_ok ? BM : (a.mask ? jrel - int(i0) : -1);
+                } else {
+                    const int64_t cmin64 = !row_ok ? INT64_MAX : (a.mask ? j - shift - i0 : INT64_MIN);
+                    cmin = int(cmin64 < -1 ? -1 : (cmin64 > BM ? BM : cmin64));
+                }
                 // kBias: the tile's windows; columns from cmax on lie past the sequence's queries; a block's share of
                 // the table's gradient: two diagonal sums a lane and their codes, or (one bucket) the thread's sum
                 const float *win = reinterpret_cast<const float *>(smem + Cfg::OFF_WIN + st * 2 * Cfg::WIN_BYTES);
-                if (kBias) win += uint32_t(window_start(j0 - i0 - (BM - 1) - shift)) & 3u;
+                if (kBias) win += window_start(jrel - r - (BM - 1) - int(i0)) & 3;
                 const uint32_t *wcode = reinterpret_cast<const uint32_t *>(win) + Cfg::WIN_BYTES / 4;
-                const int cmax = kBias && lq - i0 < BM ? int(lq - i0) : BM;
+                const int cmax = kBias ? min(BM, int(lq) - int(i0)) : BM;
                 float left_a = 0.f, left_b = 0.f;
                 uint32_t code_a = 0, code_b = 0;
                 bool several = false;
