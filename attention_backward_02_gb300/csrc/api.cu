@@ -801,7 +801,7 @@ struct DecodeLayout {
 DecodeLayout decode_layout(const attn_sdpa_desc_t *d)
 {
     DecodeLayout L;
-    L.chunk = decode_chunk(d->b, d->h_kv, d->s_kv);
+    L.chunk = decode_chunk(d->b, d->h, d->h_kv, d->s_kv, d->d);
     const int64_t chunks = decode_chunks(d->s_kv, L.chunk);
     const size_t rows = chunks > 1 ? size_t(d->b) * size_t(d->h) * size_t(chunks) : 0;
     L.ml = Workspace::align(64 * sizeof(uint32_t));
