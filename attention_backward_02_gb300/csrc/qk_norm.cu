@@ -17,8 +17,9 @@
 // warp takes a run of items.  The rows of the next items, and the cos and sin rows of
 // their tokens, come through a ring of asynchronous copies in shared memory that is
 // the warp's own: HBM needs about 40 KB of loads in flight an SM, more than the
-// registers hold (one item ahead in registers: 104 us where this takes QK_FWD at
-// 20442 tokens x 40 heads x 128).  A lane reads back its own 16 bytes.  Blocks work
+// registers hold (one item ahead in registers: 104 us where this takes 75 at
+// 20442 tokens x 40 heads x 128, 0.84 of the measured copy rate; the backward there
+// 107 us, 0.88).  A lane reads back its own 16 bytes.  Blocks work
 // on one side (query or key heads) each, so weights and weight-gradient sums stay in
 // registers.
 #include <cstdint>
@@ -75,8 +76,9 @@ enum { kNoRope = 0, kHalves = 1, kHalves128 = 2, kPairs = 3 };
 // Blocks an SM holds: set so that the registers of a lane (its row, weights, cos and sin, backward the
 // weight-gradient sums) fit without spills.
 template <int NC, bool BWD> constexpr int kBlocksPerSm = BWD ? (NC == 1 ? 4 : NC == 2 ? 3 : 2) : (NC == 1 ? 6 : NC == 2 ? 4 : 3);
-// Items a warp has in flight: 8 KB of rows or so.
-template <int NC, bool BWD> constexpr int kDepth = (NC == 1 ? 8 : 4) / (BWD ? 2 : 1) + (BWD ? 1 : 0);
+// Items a warp has in flight.  More is worse where the copies bound it (forward, 20442 tokens x 40 heads x 128: 2
+// items 73 us, 3 75, 4 82; 8192 tokens: 31.8, 30.6, 30.8), and makes no difference at d = 64 and 192.
+template <int NC, bool BWD> constexpr int kDepth = NC == 2 ? 3 : 4;
 
 // Shared memory of a warp: rows [depth][x, dy][chunk][lane] of 16 bytes; cos and sin rows [depth + 1][rot]
 // floats; the exchange of the turn [4 rows][D] floats.

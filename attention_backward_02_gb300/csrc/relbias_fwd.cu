@@ -25,7 +25,8 @@
 // and 256 rows against 1280 of MMAs.  Persistent because a CTA's start, first loads,
 // last products and the gap to the next one took 15 000 cycles (of 75 000 a unit at
 // b2 h32 s4096 d128 causal): the loads and first S of the next unit now run under the
-// end of this one (251 us a CTA a unit, FWD_LONG persistent).  256 rows a unit
+// end of this one (251 -> 239 us, with the MMA thread's and the rows' integer work
+// cut down; 0.60 of the measured tensor peak).  256 rows a unit
 // because K / V tiles read for 128 rows came near what L2 delivers (279 us).  Where
 // that leaves SMs idle (kSplit; split_rule below), a unit is 128 queries and the
 // groups take the first and last 64 keys of every key tile; they meet at its end,
@@ -53,6 +54,7 @@
 // idle: a warp reads the TMEM lanes of its place in its warpgroup).  Every
 // barrier wait is bounded; a wait that runs out sets ATTN_DEV_TIMEOUT and the CTA
 // skips the rest of its work, drains its copies and MMAs, and frees its TMEM.
+#include <algorithm>
 #include <climits>
 #include <type_traits>
 
@@ -609,31 +611,32 @@ int64_t sm_count()
     return n > 0 ? n : 1;
 }
 
-// Units of 128 queries, the keys of a tile split between the groups, or of 256?  Both take about a step's time for
-// 128 x 128 scores and about three steps around a unit, so the estimate of each is the work shared out over the SMs
-// plus one of the smallest units (the last to be dealt), or the longest unit if that is more.  Measured (us, split /
-// whole, d = 64 unless noted): b1 h12 s1024 13.1 / 21.1; b2 h12 s1024 23.6 / 21.3, causal 15.2 / 21.1; b4 h12 s1024
-// 34.9 / 39.4; b8 h12 s1024 causal 47.7 / 40.5; b2 h32 s4096 d128 causal 276 / 251.  Packed batches: whole where
-// there are tiles for every SM four times over.
-template <int BM, int BN, class Geo> bool split_rule(const DenseArgs &a, const Geo &g, int64_t tiles)
+// Units of 128 queries, the keys of a tile split between the groups, or of 256?  A step of either takes about the
+// same time (split a little more), and what lies around a unit that of 3 to 5 steps, so the estimate of each is the
+// longest sum of a CTA's units as they are dealt.  Measured (us, split / whole, causal: c): d = 64, h12: b1 s1024 14.0
+// / 20.7; b2 s1024 25.5 / 20.9, c 15.4 / 20.9; b4 s1024 35.4 / 39.3; b8 s1024 c 45.6 / 38.2; b1 h5 s4096 c 34.7 / 59.9.
+// d = 128: b1 h16 s1024 c 16.3 / 22.9; b4 h12 s1024 c 32.1 / 27.0; b8 h32 s333 50.8 / 42.5; b2 h32 s4096 c 297 / 239.
+// Packed batches, and batches of more units than are worth adding up: whole where there are tiles for every SM four
+// times over.
+template <int D, int BM, int BN, class Geo> bool split_rule(const DenseArgs &a, const Geo &g, int64_t tiles, int64_t sms)
 {
-    const double sms = double(sm_count());
-    if (IsPackedGeo<Geo>::value) return double(tiles) < 4 * sms;
-    const int64_t lq = g.q_len(0), lkv = g.kv_len(0);
-    double est[2];
+    constexpr int64_t kMaxCtas = 512;
+    if (IsPackedGeo<Geo>::value || tiles > 4096 || sms > kMaxCtas) return tiles < 4 * sms;
+    const int64_t lq = g.q_len(0), lkv = g.kv_len(0), per = a.h * a.nseq;
+    float est[2];
     for (int whole = 0; whole < 2; ++whole) {
-        const int64_t rows = whole ? 2 * BM : BM, n = (lq + rows - 1) / rows;
-        double sum = 0, longest = 0, shortest = 0;
-        for (int64_t k = 0; k < n; ++k) {
+        const int64_t rows = whole ? 2 * BM : BM, keys = whole ? BN / 2 : BN, n = (lq + rows - 1) / rows;
+        const int64_t ctas = n * per < sms ? n * per : sms;
+        float load[kMaxCtas] = {};
+        int64_t u = 0;
+        for (int64_t k = n - 1; k >= 0; --k) {
             const int64_t last = (k + 1) * rows - 1 < lq - 1 ? (k + 1) * rows - 1 : lq - 1;
             const int64_t seen = lkv > 0 ? last_visible_key(a.mask, last, lq, lkv) + 1 : 0;
-            const double c = 3 + (seen > 0 ? double((seen + BN / (whole ? 2 : 1) - 1) / (BN / (whole ? 2 : 1))) : 0);
-            sum += c;
-            longest = c > longest ? c : longest;
-            shortest = k == 0 || c < shortest ? c : shortest;
+            const float steps = seen > 0 ? float((seen + keys - 1) / keys) : 0.f;
+            const float cost = whole ? steps + (D == 64 ? 3.f : 4.f) : 1.05f * steps + (D == 64 ? 3.5f : 5.f);
+            for (int64_t x = 0; x < per; ++x, ++u) load[(u / ctas) & 1 ? ctas - 1 - u % ctas : u % ctas] += cost;
         }
-        const double per = double(a.h * a.nseq), units = per * double(n), shared = per * sum / sms + shortest;
-        est[whole] = units <= sms || longest > shared ? longest : shared;
+        est[whole] = *std::max_element(load, load + ctas);
     }
     return est[0] < est[1];
 }
@@ -643,7 +646,8 @@ template <class T, int D, class Geo> cudaError_t run(const DenseArgs &a, const R
     using Cfg = RelFwdCfg<D>;
     constexpr bool packed = IsPackedGeo<Geo>::value;
     const int64_t tiles = packed ? (g.ws_rows() / Cfg::BM) * a.h : (g.q_len(0) + Cfg::BM - 1) / Cfg::BM * a.h * a.nseq;
-    const bool split = split_rule<Cfg::BM, Cfg::BN>(a, g, tiles);
+    const int64_t sms = sm_count();
+    const bool split = split_rule<D, Cfg::BM, Cfg::BN>(a, g, tiles, sms);
     // packed: a unit for every 128-row tile, of which every other one is passed over
     const int64_t units = split || packed ? tiles : (g.q_len(0) + 2 * Cfg::BM - 1) / (2 * Cfg::BM) * a.h * a.nseq;
     if (units == 0) return cudaSuccess;
@@ -666,7 +670,7 @@ template <class T, int D, class Geo> cudaError_t run(const DenseArgs &a, const R
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     // starts beside the kernel that expands the table (and clears the status word); the softmax warps wait for it
-    const int64_t ctas = units < sm_count() ? units : sm_count();
+    const int64_t ctas = units < sms ? units : sms;
     return launch_kernel(k, dim3(unsigned(ctas)), dim3(Cfg::THREADS), Cfg::SMEM_ALLOC, s, true, prm, g);
 }
 
