@@ -228,9 +228,16 @@ attn_status_t check_relbias(const attn_relbias_t *b, RelBias *r)
     const int64_t n = b->bidirectional ? b->num_buckets / 2 : b->num_buckets;
     if (b->max_distance <= n / 2) return ATTN_ERR_INVALID;
     if (b->num_buckets > kRelMaxBuckets || b->max_distance > kRelMaxDistance) return ATTN_ERR_UNSUPPORTED;
+    // the borders of the last bucket layout (a hundred logarithms, several microseconds of a small call)
+    static thread_local RelBias last;
+    static thread_local int64_t last_distance = 0;
+    if (last.buckets == b->num_buckets && last_distance == b->max_distance && last.bidirectional == b->bidirectional) {
+        *r = last;
+        r->table = b->table;
+        r->table_type = b->table_type;
+        return ATTN_OK;
+    }
     std::memset(r, 0, sizeof *r);
-    r->table = b->table;
-    r->table_type = b->table_type;
     r->buckets = int(b->num_buckets);
     r->n = int(n);
     r->e = int(n / 2);
@@ -247,6 +254,10 @@ attn_status_t check_relbias(const attn_relbias_t *b, RelBias *r)
     const int w = r->nthr ? r->thr[r->nthr - 1] : r->e;
     r->lo = -w;
     r->hi = r->bidirectional ? w : 0;
+    last = *r;
+    last_distance = b->max_distance;
+    r->table = b->table;
+    r->table_type = b->table_type;
     return ATTN_OK;
 }
 

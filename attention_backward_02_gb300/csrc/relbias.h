@@ -57,15 +57,6 @@ struct RelArgs {
 
 inline int64_t rel_stride(const RelBias &b) { return (int64_t(b.hi) - b.lo + 1 + 2 * kRelPad + 3) / 4 * 4; }
 
-// Window of the tile with key rows j0 .. j0 + BN - 1 and query rows i0 .. i0 + BM - 1 of a sequence whose
-// query i stands at position i + shift: its deltas are dmin .. dmin + BN + BM - 2.
-enum RelTile { kRelNear, kRelPast, kRelFuture };  // several buckets; all of the lo bucket; all of the hi bucket
-__host__ __device__ __forceinline__ RelTile rel_tile(const RelBias &b, int64_t dmin, int span)
-{
-    if (dmin + span - 1 <= b.lo) return kRelPast;
-    return dmin >= b.hi ? kRelFuture : kRelNear;
-}
-
 __device__ __forceinline__ float rel_table_value(const RelBias &b, int64_t at)
 {
     float v;

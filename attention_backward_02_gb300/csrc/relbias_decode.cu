@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __gri
             for (int e = 0; e < 8; ++e) o[e] = fmaf(f, sm_o[w][r][c + e], o[e]);
         }
         if (direct) {
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
             T *dst = static_cast<T *>(a.o.ptr) + b * a.o.sb + (h0 + r) * a.o.sh + c;
             *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
                                                          pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(128) relbias_decode_join_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += sm_o[k][c + e];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     T *dst = static_cast<T *>(a.o.ptr) + b * a.o.sb + hq * a.o.sh + c;
     *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
                                                  pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));

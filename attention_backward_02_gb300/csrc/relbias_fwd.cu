@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
         }
         if (steps > 1) ++n_prev;
         const bool row_ok = i < u.lq;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // (NaN stays NaN)
         T *O = static_cast<T *>(a.o.ptr) + (kPacked ? 0 : int64_t(u.q_b) * a.o.sb) + u.hq * a.o.sh +
                (u.q_row0 + i) * a.o.ss;
         const uint32_t tOa = tmem + lane_addr + Cfg::T_O + (kSplit ? 0 : grp * D);
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(RelFwdCfg<D>::THREADS, 1)
             }
         }
         if (row_ok && (!kSplit || grp == 0)) {
-            const float lse = l > 0.f ? (m + __log2f(l)) / kLog2e : INFINITY;
+            const float lse = l == 0.f ? INFINITY : (m + __log2f(l)) / kLog2e;
             const int64_t idx = kPacked ? u.hq * a.t_q + u.q_row0 + i : (int64_t(u.q_b) * a.h + u.hq) * u.lq + i;
             a.lse_out[idx] = lse;
         }

@@ -280,3 +280,19 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     p.check_fwd(out)
     p.check_bwd(gout, dw)
+
+
+def test_offsets_past_32_bits():
+    """Sequences 2.2e9 elements apart."""
+    import torch
+    p = Problem("bfloat16", 2, 9, 3, 2, 128, 64, seed=10)
+    gap = 2_200_000_000
+    buf = torch.zeros(gap + 9 * 3 * 128, dtype=p.dt, device="cuda")
+    far = buf.as_strided((2, 3, 9, 128), (gap, 128, 3 * 128, 1))
+    far.copy_(p.x[0])
+    p.x[0] = far
+    out, _ = p.fwd()
+    p.check_fwd(out)
+    want, _ = p.fwd()
+    p.fwd(out=[far, out[1]])  # in place
+    assert torch.equal(far, want[0])

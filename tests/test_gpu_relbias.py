@@ -284,6 +284,19 @@ def test_zero_table_agrees_with_the_plain_call():
     p.check_fwd(p.get(o2), p.get_lse(l2))
 
 
+def test_a_query_with_nan_has_nan_results():
+    """Not those of an empty row, and no other row's change."""
+    p = Problem("bfloat16", [(140, 140)], 2, 2, 64, 2, 32, 128, True, seed=13)
+    o, lse = p.fwd()
+    p.q[77, 1, 5] = float("nan")
+    o2, lse2 = p.fwd()
+    assert np.all(np.isnan(o2[77, 1])) and np.isnan(lse2[77, 1])
+    keep = np.ones(o.shape[:2], bool)
+    keep[77, 1] = False
+    np.testing.assert_array_equal(o[keep], o2[keep])
+    np.testing.assert_array_equal(lse[keep], lse2[keep])
+
+
 def test_no_queries_and_no_keys():
     for lens in [(0, 40), (40, 0), (0, 0)]:
         p = Problem("float16", [lens], 2, 1, 64, 0, 32, 128, True, seed=9)
@@ -293,11 +306,12 @@ def test_no_queries_and_no_keys():
         assert all(np.all(x == 0) for x in got)
 
 
-def test_graph_replay_and_side_stream():
+@pytest.mark.parametrize("mode", [1, 2])
+def test_graph_replay_and_side_stream(mode):
     """Forward and backward captured with workspaces of their own, replayed with another table and inputs; and
     a direct call on a side stream that makes its own workspace."""
     import torch
-    p = Problem("float16", [(260, 300)], 4, 2, 64, 2, 32, 128, True, seed=10, mode=1)
+    p = Problem("float16", [(260, 300)], 4, 2, 64, 2, 32, 128, True, seed=10, mode=mode)
     ab = p.ab
     q, k, v, do = (p.put(x) for x in (p.q, p.k, p.v, p.do))
     o, lse = p.nan(p.q), torch.empty(p.tq * p.h, device="cuda")
@@ -327,6 +341,28 @@ def test_graph_replay_and_side_stream():
     torch.cuda.synchronize()
     for a, b in zip(got, (o, lse, *outs, dt)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,d,h,lens", [
+    ("bfloat16", 128, 12, [(1024, 1024)]),                       # units of 256 queries, several a CTA
+    ("float16", 64, 20, [(513, 700)]),                           # ... the second 128 past the end
+    ("bfloat16", 64, 160, [(200, 130)]),                         # more units than SMs, rows without keys
+    ("float16", 128, 40, [(300, 300), (90, 700), (1030, 513), (5, 5), (640, 640)]),  # packed, whole units
+])
+@pytest.mark.parametrize("mask", [0, 2])
+def test_forward_with_many_units(dtype, d, h, lens, mask):
+    """Enough units for every CTA to have several, so that what one leaves in shared memory, TMEM and barriers
+    meets the next.  The reference takes a few of the heads."""
+    p = Problem(dtype, lens, h, h, d, mask, 32, 128, True, seed=h, b=2 if len(lens) == 1 else 1)
+    o, lse = p.fwd()
+    again, lse2 = p.fwd()
+    np.testing.assert_array_equal(o, again)
+    np.testing.assert_array_equal(lse, lse2)
+    pick = sorted({0, 1, h // 2, h - 1})
+    small = Problem(dtype, lens, len(pick), len(pick), d, mask, 32, 128, True, seed=0, b=2 if len(lens) == 1 else 1)
+    small.q, small.k, small.v = p.q[:, pick], p.k[:, pick], p.v[:, pick]
+    small.table = p.table[:, pick].contiguous()
+    small.check_fwd(o[:, pick], lse[:, pick])
 
 
 @pytest.mark.parametrize("dtype,d,rot", [("bfloat16", 128, 0), ("float16", 64, 32)])

@@ -159,3 +159,39 @@ def test_the_training_forward_agrees():
     p.ab.sdpa_relbias_fwd_stats(desc, p.bias, p.q, p.k, p.v, o, lse)
     p.check(o)
     p.check(p.run())
+
+
+def test_offsets_past_32_bits():
+    """A cache of 2.3e9 elements: the last sequence's keys lie beyond 2^31 elements.  First a few of its keys, then
+    a length that spans all of it: zeros but for the last 64 keys.  (Bound there: the P rounding 2^-8 of the
+    magnitude and of the output, and half of it again for 380000 fp32 terms of equal sign.)"""
+    import torch
+    import attention_backward_02_gb300 as ab
+    b, cap, h, d = 3, 380000, 16, 128
+    p = Problem("bfloat16", [0, 0, 64], 64, h, h, d, seed=8)
+    big = [torch.zeros(b, cap, h, d, dtype=p.dt, device="cuda") for _ in range(2)]
+    assert big[0].numel() > 2 ** 31
+    for t, x in zip(big, (p.k, p.v)):
+        t[2, :64] = x[2].permute(1, 0, 2)
+    k, v = (t.permute(0, 2, 1, 3) for t in big)
+    desc = ab.sdpa_desc(dtype=p.desc.dtype, b=b, h=h, h_kv=h, s_q=1, s_kv=cap, d=d, scale=d ** -0.5,
+                        mask=ab.ATTN_CAUSAL_BOTTOM_RIGHT)
+    o = torch.full_like(p.q, float("nan"))
+    ws = ab.sdpa_relbias_decode(desc, p.bias, p.q, k, v, p.dlens, o)
+    assert ab.attn_query_status(ws) == 0
+    p.check(o)
+    p.dlens[2] = cap
+    for t, x in zip(big, (p.k, p.v)):
+        t[2, :64] = 0
+        t[2, cap - 64:] = x[2].permute(1, 0, 2)
+    ab.sdpa_relbias_decode(desc, p.bias, p.q, k, v, p.dlens, o)
+    table = p.table.double()
+    bucket = torch.full((cap,), 31, device="cuda")
+    bucket[cap - 200:] = torch.tensor([P.bucket(x, 32, 128, False) for x in range(-199, 1)], device="cuda")
+    want, mag = torch.empty(h, d, device="cuda", dtype=torch.float64), torch.empty(h, d, device="cuda", dtype=torch.float64)
+    for x in range(h):
+        kk, vv = big[0][2, :, x].double(), big[1][2, :, x].double()
+        w = torch.softmax(kk @ p.q[2, x, 0].double() * d ** -0.5 + table[bucket, x], -1)
+        want[x], mag[x] = w @ vv, w @ vv.abs()
+    bound = 2.0 ** -8 * (want.abs() + 1.5 * mag) + 1e-6
+    assert bool(((o[2, :, 0].double() - want).abs() <= bound).all())
