@@ -253,7 +253,7 @@ attn_status_t check_relbias(const attn_relbias_t *b, RelBias *r)
     }
     const int w = r->nthr ? r->thr[r->nthr - 1] : r->e;
     r->lo = -w;
-    r->hi = r->bidirectional ? w : 0;
+    r->hi = r->bidirectional ? w : 1;  // (1: a causal mask may part it from 0)
     last = *r;
     last_distance = b->max_distance;
     r->table = b->table;
@@ -297,6 +297,7 @@ void fill_rel(RelArgs *a, const attn_sdpa_desc_t *d, const DenseShape &sh, const
     a->stride = rel_stride(r);
     a->status = reinterpret_cast<uint32_t *>(ws);
     if (backward) {
+        a->causal = d->mask != ATTN_MASK_NONE;
         a->code = reinterpret_cast<uint32_t *>(ws + L.code);
         a->part = reinterpret_cast<float *>(ws + L.part);
         a->part_rows = sh.t_kv / 128 + d->b + 1;

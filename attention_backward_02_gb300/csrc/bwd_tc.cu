@@ -57,10 +57,17 @@
 // both types here, two columns an instruction).  A warp works on blocks of 32 key
 // rows x 32 query columns, whose 63 deltas are consecutive.  A block in one bucket
 // takes its bias from a register and adds its dS to one running sum a thread.
-// Otherwise the block is summed along its diagonals, one sum passed from lane to
-// lane per column; then runs of diagonals of one bucket are added up and the runs
+// Otherwise the block is summed along its diagonals, the sums of even and of odd
+// columns each passed two lanes up per pair of columns (one packed add for both;
+// one lane up per column took 797 us where this takes 790 at b2 h32 s4096 d128
+// causal); then runs of diagonals of one bucket are added up and the runs
 // added to the warp's row of buckets in shared memory, both behind the arrival that
-// lets the tile's GEMMs go.  Each warp stores its row once per (key tile, head); a
+// lets the tile's GEMMs go.  The causal mask is in the expanded bias (-inf), so a
+// tile on the diagonal runs the same code as its neighbours: the P / dS loop's copies
+// compete for the instruction cache (790 -> 758 us; a third copy for blocks of two
+// buckets, without shuffles, cost 50).  Element masks remain where a tile passes the
+// end of a sequence.  At those sizes 758 us against 748 without a bias; 74 / 54 at b4
+// h12 s1024 d64 without a mask.  Each warp stores its row once per (key tile, head); a
 // kernel behind this one adds them up in a fixed order, so the table's gradient is
 // bitwise reproducible in every dQ mode.  Packed sequences: rows of a tile that
 // belong to the next sequence are set to zero in shared memory before the GEMMs
@@ -128,8 +135,8 @@ struct TcCfg {
     static constexpr int WIN_BYTES = (BN + BM + 4) * 4;
     static constexpr int OFF_WIN = SMEM;                      // NST x (bias, codes)
     static constexpr int OFF_HIST = OFF_WIN + NST * 2 * WIN_BYTES;
-    static constexpr int OFF_DIAG = OFF_HIST + NSW * kRelMaxBuckets * 4;
-    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * 32 * 4 + 1024;
+    static constexpr int OFF_DIAG = OFF_HIST + NSW * kRelCodes * 4;
+    static constexpr int SMEM_ALLOC_BIAS = OFF_DIAG + NSW * 32 * 8 + 1024;
     static_assert(WIN_BYTES % 16 == 0 && SMEM % 16 == 0 && SMEM_ALLOC_BIAS <= 227 * 1024, "shared memory budget");
     static_assert(kRelPad >= BN + BM + 4, "a near tile's window lies within the expanded bias");
     static constexpr int T_S = 0, T_DP = BM, T_P = 2 * BM, T_DV = 2 * BM + BM / 2, T_DK = T_DV + D,
@@ -535,12 +542,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
 
         // relative bias: this warp's bucket sums and finished diagonals; the bucket of the last block that lay in
         // one, and each thread's sum since
-        float *hist = reinterpret_cast<float *>(smem + Cfg::OFF_HIST) + (warp - 2) * kRelMaxBuckets;
-        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_DIAG) + (warp - 2) * 32;
+        float *hist = reinterpret_cast<float *>(smem + Cfg::OFF_HIST) + (warp - 2) * kRelCodes;
+        float2 *diag = reinterpret_cast<float2 *>(smem + Cfg::OFF_DIAG) + (warp - 2) * 32;
         float one_sum = 0.f;
         uint32_t one_bucket = 0;
         if (kBias) {
-            for (int n = lane; n < kRelMaxBuckets; n += 32) hist[n] = 0.f;
+            for (int n = lane; n < kRelCodes; n += 32) hist[n] = 0.f;
             __syncwarp();
         }
         // adds v, the sum of one diagonal a lane (consecutive deltas), to the bucket sums: runs of one bucket are
@@ -601,10 +608,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                 const uint32_t adS = aX + uint32_t(qi & 1) * Cfg::X_BYTES;
                 const uint32_t a_lse = smem_u32(smem + Cfg::OFF_LSE + st * BM * 4);
                 const uint32_t a_dv = smem_u32(smem + Cfg::OFF_DVEC + st * BM * 4);
-                // first visible query column of this key row; everything is masked past the sequence
+                // first visible query column of this key row; everything is masked past the sequence (kBias: the
+                // causal mask is in the bias)
                 int cmin;
                 if (kBias) {
-                    cmin = !row_ok ? BM : (a.mask ? jrel - int(i0) : -1);
+                    cmin = !row_ok ? BM : -1;
                 } else {
                     const int64_t cmin64 = !row_ok ? INT64_MAX : (a.mask ? j - shift - i0 : INT64_MIN);
                     cmin = int(cmin64 < -1 ? -1 : (cmin64 > BM ? BM : cmin64));
@@ -695,7 +703,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                             const uint32_t *code = wcode + lg * 32 + BM - 1 - c0;  // of diagonal (row - column) 0
                             several = (code[-31] & 255u) != (code[31] & 255u) || any_mask;
                             float2 sum2 = make_float2(0.f, 0.f);
-                            float run = 0.f;
+                            float2 run = make_float2(0.f, 0.f);
+                            const float2 up1 = lane < 2 ? make_float2(0.f, 0.f) : make_float2(1.f, 1.f);
                             // kAny: several buckets, or masked elements (kMask)
                             auto block = [&](auto any_tag, auto mask_tag) {
                                 constexpr bool kAny = decltype(any_tag)::value, kMask = decltype(mask_tag)::value;
@@ -735,18 +744,16 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                         pk[k / 2] = pack2<T>(pp.x, pp.y);
                                         dk[e / 2] = pack2<T>(ds.x, ds.y);
                                         if (kAny) {
-                                            // the sum of diagonal lane - column goes one lane up per column; lane
-                                            // 31's is complete
+                                            // the sums of diagonals lane - k (even columns) and lane - k - 1 (odd
+                                            // ones) go two lanes up a pair; those of lanes 30 and 31 are complete
                                             if (k > 0) {
-                                                if (lane == 31) diag[k - 1] = run;
-                                                const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                                                run = lane == 0 ? ds.x : up + ds.x;
+                                                if (lane >= 30) diag[lane - k + 2] = run;
+                                                const float2 up = make_float2(__shfl_up_sync(0xffffffffu, run.x, 2),
+                                                                              __shfl_up_sync(0xffffffffu, run.y, 2));
+                                                run = fma2(up, up1, ds);
                                             } else {
-                                                run = ds.x;
+                                                run = ds;
                                             }
-                                            if (lane == 31) diag[k] = run;
-                                            const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                                            run = lane == 0 ? ds.y : up + ds.y;
                                         } else {
                                             sum2 = add2(sum2, ds);
                                         }
@@ -757,10 +764,13 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                             if (several) {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
                                 if (any_mask) block(std::true_type{}, std::true_type{});
                                 else block(std::true_type{}, std::false_type{});
+                                const float up = __shfl_up_sync(0xffffffffu, run.x, 1);
+                                if (lane == 31) diag[1] = run;
                                 __syncwarp();
-                                left_a = run;
+                                left_a = lane == 0 ? run.y : up + run.y;
                                 code_a = code[lane - 31];
-                                left_b = lane < 31 ? diag[30 - lane] : 0.f;
+                                // diagonal lane + 1: its even columns' sum is in that entry, its odd ones' in the next
+                                left_b = (lane < 31 ? diag[lane + 1].x : 0.f) + (lane < 30 ? diag[lane + 2].y : 0.f);
                                 code_b = code[lane + 1];
                             } else {
                                 block(std::false_type{}, std::false_type{});

@@ -5,6 +5,8 @@
 // and every delta <= lo, and every delta >= hi, has one bucket.  Expanded over
 // lo .. hi a head's table is a line of floats, and the bias of a tile of scores is
 // a window of it: element (key row r, query column c) reads window[r - c + const].
+// For the backward under a causal mask the entries of keys after their query are
+// -inf, which is the mask.
 #include <cmath>
 
 #include "relbias.h"
@@ -19,15 +21,17 @@ __global__ void __launch_bounds__(256) rel_expand_kernel(const RelArgs a)
     pdl_trigger();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0u;
     const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x, delta = t + a.b.lo - kRelPad;
-    const int n = a.b.bucket(delta);
+    // keys after their query are masked like a bucket, of their own where they share one with their query's key
+    auto bucket = [&](int64_t x) { return a.causal && !a.b.bidirectional && x > 0 ? kRelMaxBuckets : a.b.bucket(x); };
+    const int n = bucket(delta);
     if (t < a.stride)
         for (int64_t h = blockIdx.y; h < a.h; h += gridDim.y)
-            a.rel[h * a.stride + t] = rel_table_value(a.b, int64_t(n) * a.h + h);
+            a.rel[h * a.stride + t] = a.causal && delta > 0 ? -INFINITY : rel_table_value(a.b, int64_t(n) * a.h + h);
     if (a.code && blockIdx.y == 0) {
         __shared__ int16_t near[256 + 32];  // buckets of delta - 1 .. delta + 31 of the block's deltas
         near[threadIdx.x + 1] = int16_t(n);
-        if (threadIdx.x < 31) near[threadIdx.x + 257] = int16_t(a.b.bucket(delta + 256));
-        if (threadIdx.x == 0) near[0] = int16_t(a.b.bucket(delta - 1));
+        if (threadIdx.x < 31) near[threadIdx.x + 257] = int16_t(bucket(delta + 256));
+        if (threadIdx.x == 0) near[0] = int16_t(bucket(delta - 1));
         __syncthreads();
         uint32_t rem = 0;
         while (rem < 31 && near[threadIdx.x + rem + 2] == n) ++rem;

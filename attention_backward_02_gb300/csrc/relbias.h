@@ -9,6 +9,7 @@ namespace attn {
 
 constexpr int kRelMaxBuckets = 128;
 constexpr int64_t kRelMaxDistance = 65536;
+constexpr int kRelCodes = kRelMaxBuckets + 4;  // bucket codes: kRelMaxBuckets is that of causally masked deltas
 constexpr float kRelMasked = -1e30f;  // a table entry at or below this masks its bucket
 
 // The caller's bias.  A key delta positions after its query has distance |delta| (both directions) or
@@ -47,6 +48,7 @@ struct RelArgs {
     RelBias b;
     int64_t h;
     float *rel;               // [h][stride]
+    int causal;               // backward under a causal mask: entries of delta > 0 are -inf
     uint32_t *code;           // [stride] bucket | min(31, deltas after this one in its bucket) << 8 | first of it << 16
     int64_t stride;           // hi - lo + 1 + 2 kRelPad, rounded up to 4
     float *part;              // backward: [part_rows][h][8 warps][buckets] shares of the table's gradient
