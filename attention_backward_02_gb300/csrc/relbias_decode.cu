@@ -21,6 +21,10 @@
 // Each warp keeps a running maximum and sum (log2 units); the warps of a block join
 // through shared memory, the chunks of a sequence through fp32 partial results in
 // the workspace and a second kernel that adds them in order.
+// 32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 102 us for 537 MB, 0.79 of the
+// measured copy rate (K and V through a ring of asynchronous copies in shared memory:
+// 112 against 107 as loads at the time; kv heads as the grid's fastest index: 111); one
+// sequence of 1000 keys, 12 heads of 64: 7 us, two launches' latency.
 #include <cmath>
 #include <type_traits>
 

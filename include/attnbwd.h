@@ -314,7 +314,9 @@ attn_status_t nsa_block_lists(const attn_nsa_desc_t *desc, const int32_t *topk, 
  *   x < e: x;  else min(n - 1, e + floor(log(x / e) / log(max_distance / e) (n - e))),
  * in real arithmetic (attn_relbias_bucket evaluates it).
  * A table entry of -1e30 or less masks its bucket: keys in it are not visible to
- * that head.                                                                */
+ * that head.  A masked key of the same sequence still meets the products with
+ * weight 0, so its k and v have to be finite (0 times infinity is NaN); keys of
+ * other sequences, and a cache's from its length on, may hold anything.     */
 typedef struct {
     const void *table;      /* device [num_buckets][h], contiguous              */
     int table_type;         /* ATTN_F16, ATTN_BF16 or ATTN_F32                  */
@@ -394,7 +396,8 @@ attn_status_t qk_norm_rope_workspace_size(const attn_qk_norm_desc_t *desc, size_
  *   z = weight * x * r,  r = 1 / sqrt(mean(x^2) + eps),
  *   y = z with each pair (a, b) of its first rotary_dim elements turned by the
  *       token's angle: (a cos - b sin, b cos + a sin),
- * computed in fp32 and rounded once.  q, q_out: [b,h,s,d] views; k, k_out:
+ * computed in fp32 and rounded once (the squares' sum too: elements of bf16 from
+ * about 1e18 on pass its range).  q, q_out: [b,h,s,d] views; k, k_out:
  * [b,h_kv,s,d]; an output view may be its input view (in place), and must not
  * overlap it otherwise.  q_weight, k_weight: [d], shared by the heads (NULL:
  * ones).  cos, sin: fp32 [max_pos][rotary_dim / 2], 16-byte aligned;
