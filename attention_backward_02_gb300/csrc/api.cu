@@ -4,7 +4,9 @@
 // returns an error has launched nothing.  Launch order on the caller's
 // stream: preprocess -> main backward -> dQ finalize (dense), and
 // preprocess -> block lists -> main -> finalizes (NSA); each kernel is
-// chained to its predecessor with programmatic dependent launch.
+// chained to its predecessor with programmatic dependent launch.  With a relative
+// bias the expansion of its table goes first (forward: then the main kernel), and the
+// dQ finalize sums the table's gradient too.
 #include <cmath>
 #include <cstring>
 

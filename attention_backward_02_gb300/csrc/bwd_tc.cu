@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                                     store_ds(cc, dk);
                                 }
                             };
-                            if (several) {  // run: diagonal lane - 31; diag[k]: diagonal 31 - k
+                            if (several) {  // diag[d]: diagonal d's even columns and diagonal d - 1's odd ones
                                 if (any_mask) block(std::true_type{}, std::true_type{});
                                 else block(std::true_type{}, std::false_type{});
                                 const float up = __shfl_up_sync(0xffffffffu, run.x, 1);
