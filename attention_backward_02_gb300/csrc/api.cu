@@ -7,6 +7,7 @@
 // chained to its predecessor with programmatic dependent launch.  With a relative
 // bias the expansion of its table goes first (forward: then the main kernel), and the
 // dQ finalize sums the table's gradient too.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -271,10 +272,59 @@ attn_status_t check_rel_table(const RelBias &r)
 }
 
 // Workspace of the calls with a bias, behind `base` bytes of the call without one: the expanded table and, for
-// the backward, its bucket codes and the shares of the table's gradient.
+// the backward, its bucket codes, the shares of the table's gradient and those of dK and dV.
 struct RelLayout {
-    size_t rel, code, part, total;
+    size_t rel, code, part, kv, total;
+    int shares;
 };
+
+// Units that share the query heads of a (key tile, kv head) in the backward: more than one where the units are few
+// and large, so that some SMs would wait for others.  The estimate: the longest sum of a CTA's units, taken as
+// the largest of the mean and, for each k, k + 1 units of the k * 152 + 1st size (half a query tile takes 0.85 us
+// at d = 128, 1.2 at d = 64; a unit's start is one of them), and the shares' way through the workspace at 2.2 TB/s.
+// The split and ordered dQ modes keep one unit: their order of adds is by key tiles.  A constant 152 SMs: the
+// workspace size must not depend on a CUDA call.  Measured (us, whole call, causal but for the last; 1, 2, 4, 8 shares,
+// the choice in brackets): b1 h32/8 s2048 d128 205 [131] 152; b1 h32/8 s4096 [395] 497 434; b2 h32/4 s1024 213 128 [98]
+// 116; b1 h16/1 s1024 d64 276 148 82 [51]; b1 h8/1 s512, 4096 keys 115 68 [46] 51; b4 h32/8 s1024 [158] 187 219; b1
+// h32/8 s1301, 2285 keys [145] 155 153; b2 h12/4 s777 d64 [85], 3 shares 61: here the estimate errs.
+int rel_shares(const attn_sdpa_desc_t *d, const DenseShape &sh)
+{
+    const int64_t G = d->h / d->h_kv, sms = 152;
+    constexpr int kTiles = 1024;
+    if (G == 1 || d->deterministic || sh.t_q == 0 || sh.t_kv == 0) return 1;
+    const int64_t BM = d->d == 64 ? 128 : 64, copies = sh.packed ? d->h_kv : d->h_kv * d->b;
+    int32_t nq[kTiles];  // query tiles of each key tile
+    int n = 0;
+    for (int64_t b = 0; b < (sh.packed ? d->b : 1); ++b) {
+        const int64_t lq = sh.packed ? d->cu_seqlens_q[b] - (b ? d->cu_seqlens_q[b - 1] : 0) : d->s_q;
+        const int64_t lkv = sh.packed ? d->cu_seqlens_kv[b] - (b ? d->cu_seqlens_kv[b - 1] : 0) : d->s_kv;
+        for (int64_t j0 = 0; j0 < lkv; j0 += 128) {
+            if (n == kTiles) return 1;
+            const int64_t lo = first_query_seeing(d->mask, j0, lq, lkv);
+            nq[n++] = int32_t(lq <= 0 || lo >= lq ? 0 : (lq + BM - 1) / BM - lo / BM);
+        }
+    }
+    if (n * copies > 8 * sms) return 1;
+    std::sort(nq, nq + n, [](int32_t x, int32_t y) { return x > y; });
+    int best = 1;
+    double best_us = 0;
+    for (int64_t s = 1; s <= G && s <= 8; ++s) {
+        if (G % s) continue;
+        double total = 0, most = 0;
+        for (int k = 0; k < n; ++k) total += double(2 * (G / s) * nq[k] + 2) * double(copies * s);
+        for (int64_t k = 0; k * sms < n * copies * s; ++k) {
+            const double sum = double(k + 1) * double(2 * (G / s) * nq[k * sms / (copies * s)] + 2);
+            most = sum > most ? sum : most;
+        }
+        if (most < total / double(sms)) most = total / double(sms);
+        const double us = most * (d->d == 64 ? 1.2 : 0.85) + (s > 1 ? double(s * 2 * sh.t_kv * d->h_kv * d->d * 8) / 2.2e6 + 4 : 0.);
+        if (s == 1 || us < 0.95 * best_us) {
+            best = int(s);
+            best_us = us;
+        }
+    }
+    return best;
+}
 
 RelLayout rel_layout(const attn_sdpa_desc_t *d, const DenseShape &sh, const RelBias &r, size_t base, bool backward)
 {
@@ -284,7 +334,9 @@ RelLayout rel_layout(const attn_sdpa_desc_t *d, const DenseShape &sh, const RelB
     L.code = L.rel + Workspace::align(size_t(d->h) * line * sizeof(float));
     L.part = L.code + (backward ? Workspace::align(line * sizeof(uint32_t)) : 0);
     const size_t rows = size_t(sh.t_kv / 128 + d->b + 1);
-    L.total = L.part + (backward ? Workspace::align(rows * size_t(d->h) * 8 * size_t(r.buckets) * sizeof(float)) : 0);
+    L.kv = L.part + (backward ? Workspace::align(rows * size_t(d->h) * 8 * size_t(r.buckets) * sizeof(float)) : 0);
+    L.shares = backward ? rel_shares(d, sh) : 1;
+    L.total = L.kv + (L.shares > 1 ? Workspace::align(size_t(2 * L.shares) * size_t(sh.t_kv * d->h_kv * d->d) * sizeof(float)) : 0);
     return L;
 }
 
@@ -304,6 +356,8 @@ void fill_rel(RelArgs *a, const attn_sdpa_desc_t *d, const DenseShape &sh, const
         a->part = reinterpret_cast<float *>(ws + L.part);
         a->part_rows = sh.t_kv / 128 + d->b + 1;
         a->dtable = dtable;
+        a->shares = L.shares;
+        a->kv_part = reinterpret_cast<float *>(ws + L.kv);
     }
 }
 

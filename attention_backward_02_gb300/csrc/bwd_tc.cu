@@ -73,6 +73,11 @@
 // belong to the next sequence are set to zero in shared memory before the GEMMs
 // that would multiply them by P = dS = 0, so that no infinity or NaN crosses over.
 //
+// With few kv heads and many queries each the units are too large to spread evenly:
+// the query heads of a group are then shared out among several units (kBias, shares;
+// to the kernel, shares x h_kv kv heads), whose dK and dV go as fp32 into the
+// workspace and are added in order by the kernel behind this one.
+//
 // Every barrier wait is bounded (about a second).  On a timeout the thread
 // sets ATTN_DEV_TIMEOUT in the status word and an abort flag in shared
 // memory; from then on every wait of the CTA fails fast and all work is
@@ -276,6 +281,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
     const int64_t nheads = a.nseq * a.h_kv;
     const int64_t tile_step = a.deterministic ? a.n_part : INT64_MAX / 2;
     const int G = int(a.h / a.h_kv);
+    const int shares = kBias ? p.rel.shares : 1;  // units of a (key tile, kv head); a.h_kv counts them
 #define ATTN_FOR_EACH_UNIT                                                                                    \
     for (int64_t round_ = 0;; ++round_) {                                                                     \
         const int64_t unit = cta_unit(p, round_);                                                             \
@@ -362,8 +368,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                         kv_armed = kt + 1;
                         mbar_arrive_expect_tx(kv_full, 2 * Cfg::KV_BYTES);
                         for (int c = 0; c < D / 64; ++c) {
-                            tma_load_4d(sK + c * BN * 128, &p.tm_k, kv_full, c * 64, int(kv_row0 + j0), int(g), kv_b);
-                            tma_load_4d(sV + c * BN * 128, &p.tm_v, kv_full, c * 64, int(kv_row0 + j0), int(g), kv_b);
+                            tma_load_4d(sK + c * BN * 128, &p.tm_k, kv_full, c * 64, int(kv_row0 + j0), int(g) / shares, kv_b);
+                            tma_load_4d(sV + c * BN * 128, &p.tm_v, kv_full, c * 64, int(kv_row0 + j0), int(g) / shares, kv_b);
                         }
                     }
                 };
@@ -391,8 +397,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                     }
                     if (has)
                         for (int c = 0; c < D / 64; ++c) {
-                            tma_prefetch_4d(&p.tm_k, c * 64, int(nrow0 + njt * BN), int(ng), nkv_b);
-                            tma_prefetch_4d(&p.tm_v, c * 64, int(nrow0 + njt * BN), int(ng), nkv_b);
+                            tma_prefetch_4d(&p.tm_k, c * 64, int(nrow0 + njt * BN), int(ng) / shares, nkv_b);
+                            tma_prefetch_4d(&p.tm_v, c * 64, int(nrow0 + njt * BN), int(ng) / shares, nkv_b);
                         }
                 };
                 if (kt > 0 || n_iter == 1) prefetch_next();
@@ -911,8 +917,20 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             int qt0, nq;
             query_tiles<BM>(a.mask, j0, lq, lkv, &qt0, &nq);
             const int n_iter = G * nq;
+            // shares > 1: this thread's row of its unit's fp32 dK, and how far behind that of dV lies
+            const int64_t share_size = (a.h_kv / shares) * a.t_kv * D;
+            auto share_row = [&]() {
+                return p.rel.kv_part + (g % shares) * share_size +
+                       ((g / shares) * a.t_kv + (kPacked ? kv_row0 : int64_t(kv_b) * lkv) + j) * D;
+            };
             if (n_iter == 0) {  // no query sees these keys: dK = dV = 0
-                if (row_ok)
+                if (kBias && shares > 1) {
+                    if (row_ok)
+                        for (int x = 0; x < D; x += 4) {
+                            *reinterpret_cast<float4 *>(share_row() + x) = make_float4(0.f, 0.f, 0.f, 0.f);
+                            *reinterpret_cast<float4 *>(share_row() + shares * share_size + x) = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                } else if (row_ok)
                     for (int x = 0; x < D; x += 8) {
                         *reinterpret_cast<uint4 *>(dK + offk() + x) = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4 *>(dV + offv() + x) = make_uint4(0, 0, 0, 0);
@@ -925,7 +943,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
             // and written by a TMA store
             // (d = 64 only: at d = 128 the 64 KB of dK / dV would pass through the 16 KB buffer in four
             // serial rounds, slower than the row stores)
-            const bool tma_epi = D == 64 && (!kPacked || j0 + BN <= lkv);
+            const bool tma_epi = D == 64 && (!kPacked || j0 + BN <= lkv) && !(kBias && shares > 1);
             auto epilogue_tma = [&]() {
                 constexpr int NBOX = D / 64;
 #pragma unroll 1
@@ -983,7 +1001,16 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(acc_free);
                     }
-                    if (ok && row_ok) {
+                    if (kBias && shares > 1) {
+                        if (ok && row_ok) {
+                            uint4 *pk = reinterpret_cast<uint4 *>(share_row() + cc * 8);
+                            uint4 *pv = reinterpret_cast<uint4 *>(share_row() + shares * share_size + cc * 8);
+                            pk[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                            pk[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                            pv[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            pv[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    } else if (ok && row_ok) {
                         uint4 ov, ok4;
                         ov.x = pack2<T>(__uint_as_float(w[0]), __uint_as_float(w[1]));
                         ov.y = pack2<T>(__uint_as_float(w[2]), __uint_as_float(w[3]));
@@ -1471,7 +1498,8 @@ template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, cons
     const int smem = rel ? Cfg::SMEM_ALLOC_BIAS : Cfg::SMEM_ALLOC;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    prm.a.tc_units = (a.deterministic ? a.n_part : ntiles) * a.nseq * a.h_kv;
+    if (rel) prm.a.h_kv *= rel->shares;  // (the tensor maps have the real ones)
+    prm.a.tc_units = (a.deterministic ? a.n_part : ntiles) * a.nseq * prm.a.h_kv;
     if (prm.a.tc_units > INT32_MAX) return cudaErrorInvalidValue;  // the kernel splits units in 32 bits
     const int64_t units = prm.a.tc_units < sm_count() ? prm.a.tc_units : sm_count();
     plan_units<Cfg::BM, Cfg::BN>(prm.sched, prm.a, g, prm.a.tc_units, units);

@@ -110,13 +110,18 @@ __global__ void __launch_bounds__(256) dense_preprocess_kernel(DenseArgs a, Geo 
 // ------------------------------------------------------------ dq finalize
 // dQ = cast(scale * sum over the partial buffers, in index order).  Same
 // units as the preprocess; launched behind the main kernel and waits for it.
-// kBias: the first blocks sum the bias table's gradient instead.
+// kBias: the first blocks sum the bias table's gradient instead, and kv_blocks behind them the shares of dK, dV.
 template <class T, class Geo, int D, bool kBias>
-__global__ void __launch_bounds__(256) dq_finalize_kernel(DenseArgs a, Geo geo, RelArgs rel, int rel_blocks)
+__global__ void __launch_bounds__(256) dq_finalize_kernel(DenseArgs a, Geo geo, RelArgs rel, int rel_blocks, int kv_blocks)
 {
     if (kBias && int(blockIdx.x) < rel_blocks) {
         pdl_wait();
         rel_dtable_block(rel, blockIdx.x);
+        return;
+    }
+    if (kBias && int(blockIdx.x) < rel_blocks + kv_blocks) {
+        pdl_wait();
+        rel_sum_shares<T>(rel, a, geo.kv_len(0), blockIdx.x - rel_blocks, kv_blocks);
         return;
     }
     constexpr int TPR = D / 8, RPP = 256 / TPR, RPT = kUnitRows / RPP;
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(256) dq_finalize_kernel(DenseArgs a, Geo geo, 
     const int nunit = int(a.h) * ntile;
     const int64_t part_stride = a.h * a.t_pad * D;
     pdl_wait();
-    const int first = kBias ? rel_blocks : 0;
+    const int first = kBias ? rel_blocks + kv_blocks : 0;
     for (int u = int(blockIdx.x) - first; u < nunit; u += int(gridDim.x) - first) {
         // heads fastest: blocks running together read the same tokens' rows (one DRAM page run)
         const int wt = u / int(a.h), h = u - wt * int(a.h);
@@ -194,9 +199,12 @@ template <class Geo> cudaError_t preprocess(const DenseArgs &a, const Geo &g, cu
 template <class T, int D, class Geo> cudaError_t run_finalize(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)
 {
     const unsigned rows = a.t_q ? row_grid(a) : 0;
-    if (!rel) return launch_kernel(dq_finalize_kernel<T, Geo, D, false>, dim3(rows), 256, 0, s, true, a, g, RelArgs{}, 0);
+    if (!rel) return launch_kernel(dq_finalize_kernel<T, Geo, D, false>, dim3(rows), 256, 0, s, true, a, g, RelArgs{}, 0, 0);
     const unsigned extra = unsigned(rel_dtable_blocks(*rel));
-    return launch_kernel(dq_finalize_kernel<T, Geo, D, true>, dim3(rows + extra), 256, 0, s, true, a, g, *rel, int(extra));
+    const int64_t pieces = rel->shares > 1 ? (2 * a.t_kv * a.h_kv * (D / 8) + 255) / 256 : 0;
+    const unsigned kv = unsigned(pieces < 1024 ? pieces : 1024);
+    return launch_kernel(dq_finalize_kernel<T, Geo, D, true>, dim3(rows + extra + kv), 256, 0, s, true, a, g, *rel, int(extra),
+                         int(kv));
 }
 
 template <class Geo> cudaError_t finalize(const DenseArgs &a, const RelArgs *rel, const Geo &g, cudaStream_t s)

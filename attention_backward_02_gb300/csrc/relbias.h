@@ -54,6 +54,8 @@ struct RelArgs {
     float *part;              // backward: [part_rows][h][8 warps][buckets] shares of the table's gradient
     int64_t part_rows;        // one per key tile: row of tile jt of sequence b = kv_start(b) / 128 + b + jt
     float *dtable;            // [buckets][h]
+    int shares;               // backward: CTAs that share the query heads of a (key tile, kv head); more than one:
+    float *kv_part;           // [dK, dV][shares][h_kv][t_kv][d] their sums, which the dQ finalize adds up
     uint32_t *status;
 };
 
@@ -87,6 +89,31 @@ __device__ __forceinline__ void rel_dtable_block(const RelArgs &a, int unit)
     if (w == 0 && n < a.b.buckets) {
         for (int k = 1; k < 8; ++k) v += red[k][lane];
         a.dtable[int64_t(n) * a.h + head] = v;
+    }
+}
+// dK (scaled) and dV = the sums of the shares, in order: 8 elements a thread, tokens' heads side by side.
+template <class T>
+__device__ __forceinline__ void rel_sum_shares(const RelArgs &a, const DenseArgs &d, int64_t s_kv, int block, int blocks)
+{
+    const uint32_t per = uint32_t(d.d / 8), hk = uint32_t(d.h_kv), n = uint32_t(2 * d.t_kv) * hk * per;
+    const int64_t share = d.h_kv * d.t_kv * d.d;
+    for (uint32_t k = uint32_t(block) * 256 + threadIdx.x; k < n; k += uint32_t(blocks) * 256) {
+        const uint32_t c = k % per, x = k / per, head = x % hk, y = x / hk;
+        const bool isv = y >= uint32_t(d.t_kv);
+        const uint32_t t = isv ? y - uint32_t(d.t_kv) : y;
+        const float *p = a.kv_part + (isv ? a.shares * share : 0) + (head * d.t_kv + t) * d.d + c * 8;
+        float v[8] = {};
+        for (int s = 0; s < a.shares; ++s) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + s * share), w = *reinterpret_cast<const float4 *>(p + s * share + 4);
+            v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+            v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+        }
+        const float m = isv ? 1.f : d.scale;
+        const View &o = isv ? d.dV : d.dK;
+        const uint32_t b = d.packed ? 0 : t / uint32_t(s_kv);
+        T *dst = static_cast<T *>(o.ptr) + b * o.sb + head * o.sh + int64_t(d.packed ? t : t - b * uint32_t(s_kv)) * o.ss + c * 8;
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(v[0] * m, v[1] * m), pack2<T>(v[2] * m, v[3] * m),
+                                                     pack2<T>(v[4] * m, v[5] * m), pack2<T>(v[6] * m, v[7] * m));
     }
 }
 inline int64_t rel_dtable_blocks(const RelArgs &a) { return a.h * ((a.b.buckets + 31) / 32); }
