@@ -329,6 +329,22 @@ def test_no_queries_and_no_keys():
         assert all(np.all(x == 0) for x in got)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_plain_backward_without_queries(d):
+    """sdpa_bwd with keys that no query sees: zero dK and dV."""
+    import torch
+    import attention_backward_02_gb300 as ab
+    desc = ab.sdpa_desc(dtype=ab.ATTN_F16, b=2, h=4, h_kv=2, s_q=0, s_kv=150, d=d, scale=d ** -0.5)
+    k = torch.randn(2, 2, 150, d, device="cuda").half()
+    v, none = torch.randn_like(k), torch.empty(2, 4, 0, d, device="cuda", dtype=torch.half)
+    dk, dv = torch.full_like(k, float("nan")), torch.full_like(k, float("nan"))
+    empty = torch.empty(2, 4, 0, 1, device="cuda")
+    ws = torch.empty(max(ab.sdpa_workspace_size(desc)[1], 256), dtype=torch.uint8, device="cuda")
+    ab.sdpa_bwd(desc, none, k, v, none, none, empty, none, dk, dv, workspace=ws)
+    assert ab.attn_query_status(ws) == 0
+    assert bool((dk == 0).all()) and bool((dv == 0).all())
+
+
 @pytest.mark.parametrize("mode", [1, 2])
 def test_graph_replay_and_side_stream(mode):
     """Forward and backward captured with workspaces of their own, replayed with another table and inputs; and
@@ -386,6 +402,52 @@ def test_forward_with_many_units(dtype, d, h, lens, mask):
     small.q, small.k, small.v = p.q[:, pick], p.k[:, pick], p.v[:, pick]
     small.table = p.table[:, pick].contiguous()
     small.check_fwd(o[:, pick], lse[:, pick])
+
+
+def test_two_threads_two_streams():
+    """Two threads with a stream, a shape and a workspace each, at once: the results of each alone."""
+    import threading
+    import torch
+    runs, errors = [], []
+
+    def work(p, ten, stream, n):
+        ab = p.ab
+        q, k, v, do = ten
+        outs = []
+        for _ in range(n):
+            o, lse = torch.empty_like(q), torch.empty(p.tq * p.h, device="cuda")
+            g = [torch.empty_like(x) for x in (q, k, v)]
+            dt = torch.empty(p.table.shape, device="cuda")
+            V = p.view
+            ab.sdpa_relbias_fwd_stats(p.desc, p.bias, V(q), V(k), V(v), V(o), lse, stream=stream)
+            ab.sdpa_relbias_bwd(p.desc, p.bias, V(q), V(k), V(v), V(o), V(do), lse, *map(V, g), dt, stream=stream)
+            outs.append((o, lse, *g, dt))
+        return outs
+
+    def guarded(i, *a):
+        try:
+            runs[i] = work(*a)
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+
+    ps = [Problem("float16", [(300, 333)], 4, 2, 64, 2, 32, 128, True, seed=15, mode=2),
+          Problem("bfloat16", [(190, 200), (64, 257)], 4, 4, 128, 0, 64, 400, False, seed=16, mode=1)]
+    tens = [[p.put(x) for x in (p.q, p.k, p.v, p.do)] for p in ps]
+    alone = [work(p, t, None, 1)[0] for p, t in zip(ps, tens)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    runs[:] = [None, None]
+    threads = [threading.Thread(target=guarded, args=(i, ps[i], tens[i], streams[i], 8)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for want, got in zip(alone, runs):
+        for one in got:
+            for a, b in zip(want, one):
+                assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("dtype,d,rot", [("bfloat16", 128, 0), ("float16", 64, 32)])
