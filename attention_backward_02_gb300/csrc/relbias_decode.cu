@@ -9,22 +9,27 @@
 // head) against 4 d G operations for the G query heads that share it.  A block
 // takes one (sequence, kv head) and a chunk of its keys, four warps striding over
 // it 16 keys at a time; chunks past a sequence's length end at once, so sequences
-// of any mix of lengths load the GPU by their keys.  The query heads of a group
-// are the rows of mma.sync m16n8k16 products (more than 16: several blocks), which
-// keeps the operations off the critical path at every G: the tensor cores idle
-// either way, and the tcgen05 path would need the tile staged through shared
-// memory.  K and V go from global memory to registers as 16-byte loads that are
-// operand fragments as they stand: the order of the contraction over d is free, so
-// a lane's 16 bytes of a key serve two steps, and V's key pairs are joined by byte
-// permutes, output columns taken in the order that makes a lane's 16 bytes eight
-// column tiles.
+// of any mix of lengths load the GPU by their keys.  Both products are mma.sync
+// m16n8k16, which keeps the operations off the critical path at every G: the tensor
+// cores idle either way, and the tcgen05 path would need the tile staged through
+// shared memory.  S = Q K^T has the query heads of a group as its rows (8 of 16 used
+// up to G = 8; more than 16: several blocks); its accumulator is, as it stands, the
+// second operand of O^T = V^T P^T, whose rows are head dims and whose eight columns
+// are heads, so O takes D / 4 registers a lane for eight heads (with O = P V, half
+// of whose rows were empty, a lane held 212 registers, two blocks an SM, and 32
+// sequences took 104 us where three blocks take 93).  K and V go from global memory
+// to registers as 16-byte loads that are operand fragments as they stand: the order
+// of the contraction over d is free, so a lane's 16 bytes of a key serve two steps,
+// and V's key pairs are joined by byte permutes, head dims taken in the order that
+// makes a lane's 16 bytes four row pairs.
 // Each warp keeps a running maximum and sum (log2 units); the warps of a block join
 // through shared memory, the chunks of a sequence through fp32 partial results in
 // the workspace and a second kernel that adds them in order.
-// 32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 102 us for 537 MB, 0.79 of the
-// measured copy rate (K and V through a ring of asynchronous copies in shared memory:
-// 112 against 107 as loads at the time; kv heads as the grid's fastest index: 111); one
-// sequence of 1000 keys, 12 heads of 64: 7 us, two launches' latency.
+// 32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 93 us for 537 MB, 0.87 of the
+// measured copy rate, and 0.97 with all of 8192 (K and V through a ring of asynchronous
+// copies in shared memory: 112 against 107 as loads at the time; kv heads as the
+// grid's fastest index: 111; K a step ahead in registers: no gain); one sequence of 1000
+// keys, 12 heads of 64: 7 us, two launches' latency.
 #include <cmath>
 #include <type_traits>
 
@@ -75,10 +80,10 @@ __device__ __forceinline__ int64_t cached_len(const DecodeArgs &a, int64_t b)
     return n < 0 ? 0 : (n > a.cap ? a.cap : n);
 }
 
-// grid (chunks, kv heads x row blocks of 16 query heads, sequences).  ROWS: query heads of a group handled, 8
-// (the second half of the product's rows is zero and never looked at) or 16.
+// grid (chunks, kv heads x row blocks of ROWS query heads, sequences).  ROWS: query heads of a group handled, 8
+// (the second half of S's rows is zero and never looked at) or 16.
 template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __grid_constant__ DecodeArgs a)
+__global__ void __launch_bounds__(32 * kWarps, decode_blocks(D, ROWS)) relbias_decode_kernel(const __grid_constant__ DecodeArgs a)
 {
     constexpr int NP = D / 32;   // 64-byte pieces of a key
     constexpr int NJ = D / 64;   // 128-byte pieces of a value
@@ -123,18 +128,18 @@ __global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __gri
     const float sc = a.scale * kLog2e;
 
     float m[NR], l[NR];
-    float acc[NJ][8][4];
+    float acc[NR][NJ][4][4];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][e][i] = 0.f;
+            for (int e = 0; e < 4; ++e) acc[i][j][e][0] = acc[i][j][e][1] = acc[i][j][e][2] = acc[i][j][e][3] = 0.f;
 
     for (int64_t base = k0 + warp * kKeys; base < k1; base += kWarps * kKeys) {
         const int left = int(k1 - base < kKeys ? k1 - base : kKeys);
@@ -189,12 +194,16 @@ __global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __gri
                 const float f = nm == -INFINITY ? 1.f : ex2f(m[i] - nm);
                 m[i] = nm;
                 l[i] *= f;
+                // (the accumulator holds heads 2 q and 2 q + 1 of the eight)
+                const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[j][e][2 * i] *= f;
-                        acc[j][e][2 * i + 1] *= f;
+                    for (int e = 0; e < 4; ++e) {
+                        acc[i][j][e][0] *= f0;
+                        acc[i][j][e][1] *= f1;
+                        acc[i][j][e][2] *= f0;
+                        acc[i][j][e][3] *= f1;
                     }
             }
         }
@@ -215,15 +224,16 @@ __global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-                const uint32_t b0 = __byte_perm(part(vr[0][j], e >> 1), part(vr[1][j], e >> 1), sel);
-                const uint32_t b1 = __byte_perm(part(vr[2][j], e >> 1), part(vr[3][j], e >> 1), sel);
-                mma16816<T>(acc[j][e], pa[0][0], pa[0][1], pa[1][0], pa[1][1], b0, b1);
+            for (int e = 0; e < 4; ++e) {  // columns 64 j + 8 g + 2 e (and + 1), keys 2 q, 2 q + 1 (and + 8)
+                const uint32_t u0 = part(vr[0][j], e), u1 = part(vr[1][j], e), u2 = part(vr[2][j], e), u3 = part(vr[3][j], e);
+                const uint32_t a0 = __byte_perm(u0, u1, 0x5410), a1 = __byte_perm(u0, u1, 0x7632);
+                const uint32_t a2 = __byte_perm(u2, u3, 0x5410), a3 = __byte_perm(u2, u3, 0x7632);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) mma16816<T>(acc[i][j][e], a0, a1, a2, a3, pa[0][i], pa[1][i]);
             }
     }
 
-    // join the warps: lane (g, q) holds columns 64 j + 16 q + 8 (i & 1) + e of row g + 8 (i >> 1)
+    // join the warps: lane (g, q) holds the sums of head g (+ 8 i), and columns 64 j + 8 g + .. of heads 2 q and 2 q + 1
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -237,7 +247,9 @@ __global__ void __launch_bounds__(32 * kWarps) relbias_decode_kernel(const __gri
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sm_o[warp][g + 8 * i][64 * j + 16 * q + 8 * c + e] = acc[j][e][2 * i + c];
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<float2 *>(&sm_o[warp][2 * q + c + 8 * i][64 * j + 8 * g + 2 * e]) =
+                        make_float2(acc[i][j][e][c], acc[i][j][e][2 + c]);
     }
     __syncthreads();
     for (int t = threadIdx.x; t < rows * (D / 8); t += 32 * kWarps) {

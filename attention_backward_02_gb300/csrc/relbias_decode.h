@@ -24,15 +24,20 @@ struct DecodeArgs {
 // Query heads a block handles: the rows of its products.
 inline int64_t decode_rows(int64_t h, int64_t h_kv) { return h / h_kv > 8 ? 16 : 8; }
 
-// Keys of a block.  Two blocks fit an SM at d = 128, four at d = 64; a block's start and end take about the time of
-// 128 keys.  Of the chunk counts that fill one, two, .. sixteen waves of blocks when the cache is full, the one with
-// the least waves x (keys + 128); a multiple of the 64 keys of a block's step.  (At 32 sequences of 8192 keys, 8 kv
-// heads of 128: chunks of 1024 take 188 us, of 2048 196, of 1216, this choice, 183.)  A constant 152 SMs: the
-// workspace size must not depend on a CUDA call.
+// Blocks an SM holds: set by the registers of a lane's K, V, Q and sums.
+constexpr int decode_blocks(int64_t d, int64_t rows) { return d == 64 ? 4 : rows == 8 ? 3 : 2; }
+
+// Keys of a block.  A block's start and end take about the time of 128 keys.  Of the chunk counts that fill one, two,
+// .. sixteen waves of blocks when the cache is full, the one with the least time of two caches: a full one, whole
+// waves x (keys + 128), and one half full with sequences of all lengths, whose blocks spread evenly but for half a block
+// at the end; a multiple of the 64 keys of a block's step.  (us, lengths of 1 to 8192 / all 8192, 32 / 8 heads of
+// 128; the choice in brackets: 32 sequences, chunks of 640 91 / 176, [1216 93 / 165], 1664 97 / 165, 2048 106 / 186; 8
+// sequences, [640 26 / 47], 1216 34 / 43, 2048 44 / 51.)  A constant 152 SMs: the workspace size must not depend on a
+// CUDA call.
 inline int64_t decode_chunk(int64_t b, int64_t h, int64_t h_kv, int64_t cap, int64_t d)
 {
     const int64_t rows = decode_rows(h, h_kv), units = b * h_kv * ((h / h_kv + rows - 1) / rows);
-    const int64_t slots = 152 * (d == 64 ? 4 : 2);
+    const int64_t slots = 152 * decode_blocks(d, rows);
     int64_t best = cap, best_cost = -1;
     for (int64_t waves = 1; waves <= 16; ++waves) {
         int64_t n = waves * slots / units;
@@ -40,7 +45,8 @@ inline int64_t decode_chunk(int64_t b, int64_t h, int64_t h_kv, int64_t cap, int
         int64_t chunk = ((cap + n - 1) / n + 63) / 64 * 64;
         if (chunk < 64) chunk = 64;
         n = (cap + chunk - 1) / chunk;
-        const int64_t cost = (units * n + slots - 1) / slots * (chunk + 128);
+        const int64_t cost = (units * n + slots - 1) / slots * (chunk + 128) +
+                             (units * n + slots) * (chunk + 128) / (2 * slots);
         if (best_cost < 0 || cost < best_cost) {
             best = chunk;
             best_cost = cost;
