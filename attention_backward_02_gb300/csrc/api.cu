@@ -214,11 +214,36 @@ namespace {
 
 // -------------------------------------------------- relative position bias
 
-// Whether distance x has reached step m of the buckets past the exact ones.  Borders that are whole numbers
-// belong to the bucket above: the logarithms' rounding is far below the 1e-9 that is allowed for it.
-bool rel_reached(const RelBias &r, double max_distance, int64_t x, int m)
+// base^power (base at most 65536, power at most 64: 1025 bits) times what is in w, in words of 32 bits.
+constexpr int kRelWords = 34;
+void rel_multiply(uint32_t (&w)[kRelWords], uint64_t base, int power)
 {
-    return std::log(double(x) / r.e) / std::log(max_distance / r.e) * (r.n - r.e) + 1e-9 >= double(m);
+    for (; power > 0; --power) {
+        uint64_t carry = 0;
+        for (uint32_t &x : w) {
+            carry += x * base;
+            x = uint32_t(carry);
+            carry >>= 32;
+        }
+    }
+}
+
+// Whether distance x (e .. max_distance) has reached step m < k of the k = n - e buckets past the exact ones:
+// log(x / e) / log(max_distance / e) k >= m.  By logarithms where the two sides are further apart than their
+// rounding (below 1e-12; whole distances come much closer than 1e-9 to a border without reaching it), else by
+// x^k >= max_distance^m e^(k - m) in integers, each side below 2^1025.
+bool rel_reached(const RelBias &r, int64_t max_distance, int64_t x, int m)
+{
+    const int k = r.n - r.e;
+    const double step = std::log(double(x) / r.e) / std::log(double(max_distance) / r.e) * k;
+    if (std::fabs(step - m) > 1e-9) return step > m;
+    uint32_t left[kRelWords] = {1}, right[kRelWords] = {1};
+    rel_multiply(left, uint64_t(x), k);
+    rel_multiply(right, uint64_t(max_distance), m);
+    rel_multiply(right, uint64_t(r.e), k - m);
+    for (int i = kRelWords - 1; i >= 0; --i)
+        if (left[i] != right[i]) return left[i] > right[i];
+    return true;
 }
 
 attn_status_t check_relbias(const attn_relbias_t *b, RelBias *r)
@@ -250,8 +275,8 @@ attn_status_t check_relbias(const attn_relbias_t *b, RelBias *r)
     for (int m = 1; m <= r->nthr; ++m) {  // the first distance of step m: a guess, then by the definition
         int64_t x = int64_t(r->e * std::pow(far / r->e, double(m) / (r->n - r->e)));
         if (x < r->e) x = r->e;
-        while (x > r->e && rel_reached(*r, far, x - 1, m)) --x;
-        while (!rel_reached(*r, far, x, m)) ++x;
+        while (x > r->e && rel_reached(*r, b->max_distance, x - 1, m)) --x;
+        while (!rel_reached(*r, b->max_distance, x, m)) ++x;
         r->thr[m - 1] = int32_t(x);
     }
     const int w = r->nthr ? r->thr[r->nthr - 1] : r->e;

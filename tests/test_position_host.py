@@ -182,3 +182,44 @@ def test_decode_refusals(ab):
         assert call(i, ab.attn_view_t(A + 8, 0, 64, 128)) == ALIGN and call(i, ab.attn_view_t(A, 4, 64, 128)) == ALIGN
     assert call(lens=A + 2) == ALIGN and call(b=_bias(ab, table=None)) == NULLPTR
     assert call(ws=None) == WORKSPACE and call(ws=A + 8) == WORKSPACE and call(n=300) == WORKSPACE
+
+
+def test_relbias_buckets_next_to_a_border(ab):
+    """Distances that come within 1e-9 of a border (as the logarithms count) without reaching it, and their
+    neighbours; and borders that are whole numbers."""
+    from oracle import position as P
+    near = [(32, 43921, 16325), (64, 23785, 10409), (32, 61179, 36534), (64, 16463, 13545), (73, 905, 347),
+            (99, 5217, 1067), (126, 58181, 42031), (127, 32736, 22146), (128, 65536, 65535)]
+    for nb, far, x in near:
+        for both in ([0, 1] if 2 * nb <= 128 else [0]):
+            n = 2 * nb if both else nb
+            bias = _bias(ab, num_buckets=n, max_distance=far, bidirectional=both)
+            for delta in (-x - 1, -x, 1 - x, x - 1, x, x + 1):
+                assert ab.relbias_bucket(bias, delta) == P.bucket(delta, n, far, bool(both)), (n, far, both, delta)
+    for nb, far, whole in [(128, 65536, 2048), (64, 65536, 1 << 12), (8, 65536, 1 << 9)]:
+        e = nb // 2
+        bias = _bias(ab, num_buckets=nb, max_distance=far, bidirectional=0)
+        for delta in (-whole, 1 - whole, -e, -far, 1 - far):
+            assert ab.relbias_bucket(bias, delta) == P.bucket(delta, nb, far, False), (nb, far, delta)
+
+
+def test_relbias_buckets_at_drawn_borders(ab):
+    """Every border of drawn layouts up to the largest: the last distance below it and the first at it, found by
+    bisection of the integer definition."""
+    import random
+    from oracle import position as P
+    rng = random.Random(17)
+    for _ in range(60):
+        nb = rng.randint(2, 128)
+        far = rng.randint(nb // 2 + 1, 65536)
+        bias = _bias(ab, num_buckets=nb, max_distance=far, bidirectional=0)
+        for n in range(nb // 2 + 1, nb):
+            lo, hi = nb // 2, far  # bucket(lo) < n or lo is the border; bucket(hi) >= n
+            while lo < hi:
+                mid = (lo + hi) // 2
+                if P.bucket(-mid, nb, far, False) >= n:
+                    hi = mid
+                else:
+                    lo = mid + 1
+            for x in (lo - 1, lo):
+                assert ab.relbias_bucket(bias, -x) == P.bucket(-x, nb, far, False), (nb, far, x)
