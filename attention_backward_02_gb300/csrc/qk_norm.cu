@@ -279,10 +279,6 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm<NC, BWD>) qk_norm_ke
             }
         }
         issue(item + DEPTH);
-        if (ROPE != kNoRope && !valid) {  // a token out of range: zeros in, zeros out, nothing for the weights
-#pragma unroll
-            for (int k = 0; k < NC; ++k) xr[k] = yr[k] = make_uint4(0, 0, 0, 0);
-        }
         float2 x[NC][4], z[NC][4];
         float2 sq = both(0.f);
 #pragma unroll
@@ -292,7 +288,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm<NC, BWD>) qk_norm_ke
             for (int e = 0; e < 4; ++e) sq = fma2(x[k][e], x[k][e], sq);
         }
         const float r = rsqrtf(fmaf(row_sum(sq.x + sq.y), 1.f / D, a.eps));
-        if (!BWD) {  // the norm's factor is common to a row: it goes on last
+        if (ROPE != kNoRope && !valid) {  // a token out of range: zeros whatever its row, the weights and the tables
+                                          // hold, and nothing for the weights' gradient
+#pragma unroll
+            for (int k = 0; k < NC; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[k][e] = both(0.f);
+        } else if (!BWD) {  // the norm's factor is common to a row: it goes on last
 #pragma unroll
             for (int k = 0; k < NC; ++k)
 #pragma unroll

@@ -296,3 +296,34 @@ def test_offsets_past_32_bits():
     want, _ = p.fwd()
     p.fwd(out=[far, out[1]])  # in place
     assert torch.equal(far, want[0])
+
+
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 64, False), (64, 32, True), (192, 192, False)])
+def test_tokens_out_of_range_beside_values_that_are_not_finite(d, rot, inter):
+    """Tokens without a position get zeros, and add nothing to the weights' gradients, whatever their rows, the
+    norm weights and the tables hold; row 0 of cos and sin, which no token has, is NaN."""
+    p = Problem("bfloat16", 2, 9, 5, 2, d, rot, inter, weights="32", seed=21)
+    torch = p.torch
+    p.pos.clamp_(min=1)
+    for n, i, v in [(0, 0, -1), (0, 5, 97), (1, 8, -7)]:
+        p.pos[n, i] = v
+    live = (p.pos >= 0) & (p.pos < 97)
+    clean, _ = p.fwd()
+    clean_b, clean_w, _ = p.bwd()
+    p.cos[0] = p.sin[0] = float("nan")
+    for t in p.x + p.dy:
+        t.permute(0, 2, 1, 3)[~live] = float("nan")
+    out, ws = p.fwd()
+    assert p.ab.attn_query_status(ws) == 2
+    got, dw, _ = p.bwd()
+    for a, b in zip(out + got + dw, clean + clean_b + clean_w):
+        assert torch.equal(a, b)
+    for w in p.w:
+        w[3] = float("inf")
+        w[d - 1] = float("nan")
+    out, _ = p.fwd()
+    got, dw, _ = p.bwd()
+    for t in out + got:
+        assert bool((t.permute(0, 2, 1, 3)[~live] == 0).all())
+    for a, b in zip(dw, clean_w):  # the weights' gradients do not depend on the weights
+        assert torch.equal(a, b)
