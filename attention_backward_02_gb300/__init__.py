@@ -341,19 +341,27 @@ def _relbias_call(where, desc, bias, lse, stream):
     return call
 
 
+def _same_order(got, want):
+    """Whether a contiguous tensor of shape `got` is one of shape `want` with neighbouring dimensions merged or
+    dimensions of 1 added; of other shapes the order of the elements is not known."""
+    ends = [{math.prod(s[i:]) for i in range(len(s) + 1)} for s in (got, want)]
+    return math.prod(got) == math.prod(want) and ends[0] <= ends[1]
+
+
 def _lse_ptr(call, desc, lse, shape):
     torch = _torch()
     if shape is None:
         shape = (desc.h, int(desc.cu_seqlens_q[desc.b - 1]))
-    if (lse.dtype is not torch.float32 or lse.numel() != math.prod(shape) or lse.get_device() != call.device or
-            not lse.is_contiguous()):
-        raise ValueError(f"{call.where}: lse must be contiguous fp32 of {shape}")
+    if (lse.dtype is not torch.float32 or lse.get_device() != call.device or not lse.is_contiguous() or
+            (lse.shape != shape and not _same_order(lse.shape, shape))):
+        call.refuse("lse", lse, torch.float32, shape)
     return lse.data_ptr()
 
 
 def sdpa_relbias_fwd_stats(desc, bias, q, k, v, o, lse, *, workspace=None, stream=None):
     """sdpa_fwd_stats with a learned relative position bias (see relbias) in the scores.  q, k, v, o: views or
-    [B, H, S, D] tensors; lse: fp32 [B, h, S_q] (packed: [h, T_q]).  Returns the workspace."""
+    [B, H, S, D] tensors; lse: fp32 [B, h, S_q] (packed: [h, T_q]), or the same elements in a shape that merges
+    neighbouring dimensions.  Returns the workspace."""
     call = _relbias_call("sdpa_relbias_fwd_stats", desc, bias, lse, stream)
     ws = call.workspace(sdpa_relbias_workspace_size(desc, bias)[0] if workspace is None else 0, workspace)
     sq, sk, sl = _dense_shapes(desc)
@@ -365,7 +373,7 @@ def sdpa_relbias_fwd_stats(desc, bias, q, k, v, o, lse, *, workspace=None, strea
 
 def sdpa_relbias_bwd(desc, bias, q, k, v, o, dO, lse, dQ, dK, dV, dtable, *, workspace=None, stream=None):
     """sdpa_bwd with a learned relative position bias in the scores; also the gradient of the bias table,
-    dtable: fp32 [num_buckets, h], bitwise reproducible.  Returns the workspace."""
+    dtable: fp32 [num_buckets, h], bitwise reproducible.  lse as in the forward.  Returns the workspace."""
     torch = _torch()
     call = _relbias_call("sdpa_relbias_bwd", desc, bias, lse, stream)
     ws = call.workspace(sdpa_relbias_workspace_size(desc, bias)[1] if workspace is None else 0, workspace)

@@ -223,3 +223,33 @@ def test_relbias_buckets_at_drawn_borders(ab):
                     lo = mid + 1
             for x in (lo - 1, lo):
                 assert ab.relbias_bucket(bias, -x) == P.bucket(-x, nb, far, False), (nb, far, x)
+
+
+def test_lse_shape(ab):
+    """lse is taken in the documented order of its elements alone: [B, h, S_q] (packed: [h, T_q]), its neighbouring
+    dimensions merged or not, and refused where another order has the same number of elements."""
+    import types
+    import torch
+    call = types.SimpleNamespace(where="call", device=-1, refuse=ab._Call.refuse.__get__(
+        types.SimpleNamespace(where="call", device=-1)))
+    take = lambda d, shape, t: ab._lse_ptr(call, d, t, shape)
+    fixed, want = _sdpa(ab), (2, 4, 64)
+    for shape in [(2, 4, 64), (2, 4, 64, 1), (512,), (8, 64), (2, 256), (1, 2, 4, 64)]:
+        t = torch.zeros(shape)
+        assert take(fixed, want, t) == t.data_ptr()
+    for shape in [(2, 64, 4), (4, 2, 64), (64, 8), (2, 64, 4, 1), (2, 4, 32), (2, 4, 65), (511,), (2, 4, 8, 8)]:
+        with pytest.raises(ValueError, match="lse"):
+            take(fixed, want, torch.zeros(shape))
+    for t in (torch.zeros(2, 64, 4).permute(0, 2, 1), torch.zeros(2, 4, 64, dtype=torch.float64)):
+        with pytest.raises(ValueError, match="lse"):
+            take(fixed, want, t)
+    packed = _sdpa(ab, cu_seqlens_q=[30, 50], cu_seqlens_kv=[30, 50])
+    for shape in [(4, 50), (200,), (4, 50, 1)]:
+        t = torch.zeros(shape)
+        assert take(packed, None, t) == t.data_ptr()
+    for shape in [(50, 4), (2, 4, 25), (4, 51)]:
+        with pytest.raises(ValueError, match="lse"):
+            take(packed, None, torch.zeros(shape))
+    empty = _sdpa(ab, s_q=0)
+    for shape in [(2, 4, 0), (0,)]:
+        take(empty, (2, 4, 0), torch.zeros(shape))
