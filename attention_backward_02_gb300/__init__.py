@@ -292,17 +292,23 @@ class _Call:
 
 def relbias(table, *, max_distance=128, bidirectional=True):
     """An attn_relbias_t: a learned relative position bias.  table [num_buckets, h] (fp32, fp16 or bf16; held by
-    the result): table[bucket(key position - query position), head] is added to the score.  Half of a
-    direction's buckets are exact distances, the rest grow to max_distance; bidirectional: keys after the
-    query have buckets of their own."""
-    torch = _torch()
-    types = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}
-    if table.dtype not in types or table.dim() != 2 or not table.is_contiguous():
-        raise ValueError("relbias: a contiguous [num_buckets, h] table of fp32, fp16 or bf16")
-    bias = attn_relbias_t(table.data_ptr(), types[table.dtype], int(table.shape[0]), int(max_distance),
-                          int(bool(bidirectional)))
+    the result, and read anew by every call): table[bucket(key position - query position), head] is added to
+    the score.  Half of a direction's buckets are exact distances, the rest grow to max_distance;
+    bidirectional: keys after the query have buckets of their own."""
+    bias = attn_relbias_t(None, 0, 0, int(max_distance), int(bool(bidirectional)))
     bias.tensor = table
+    _read_table(bias)
     return bias
+
+
+def _read_table(bias):
+    """The table's address, type and number of buckets, as its tensor is now: its memory may have been replaced
+    (tensor.data = ...) since the last call."""
+    torch, t = _torch(), bias.tensor
+    code = ATTN_F32 if t.dtype is torch.float32 else {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16}.get(t.dtype)
+    if code is None or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("relbias: a contiguous [num_buckets, h] table of fp32, fp16 or bf16")
+    bias.table, bias.table_type, bias.num_buckets = t.data_ptr(), code, t.shape[0]
 
 
 def relbias_bucket(bias, delta):
@@ -333,11 +339,13 @@ def _packed_or(call, name, x, shape):
     return call.view(name, x, shape)
 
 
-def _relbias_call(where, desc, bias, lse, stream):
-    call = _Call(where, desc.dtype, lse.get_device(), stream)
+def _relbias_call(where, desc, bias, on, stream):
+    """The call on the device of the tensor `on`."""
+    call = _Call(where, desc.dtype, on.get_device(), stream)
+    _read_table(bias)
     if bias.tensor.shape[1] != desc.h or bias.tensor.get_device() != call.device:
         raise ValueError(f"{where}: bias table {tuple(bias.tensor.shape)} on {bias.tensor.device}, {desc.h} heads on "
-                         f"{lse.device}")
+                         f"{on.device}")
     return call
 
 
@@ -401,9 +409,7 @@ def sdpa_relbias_decode(desc, bias, q, k, v, lens, o, *, workspace=None, stream=
     among them (None: S_kv).  desc: s_q = 1 and ATTN_CAUSAL_BOTTOM_RIGHT.  Returns the workspace, for
     attn_query_status (lengths out of range)."""
     torch = _torch()
-    call = _Call("sdpa_relbias_decode", desc.dtype, bias.tensor.get_device(), stream)
-    if bias.tensor.shape[1] != desc.h:
-        raise ValueError(f"sdpa_relbias_decode: bias table {tuple(bias.tensor.shape)}, {desc.h} heads")
+    call = _relbias_call("sdpa_relbias_decode", desc, bias, bias.tensor, stream)
     ws = call.workspace(sdpa_relbias_decode_workspace_size(desc, bias) if workspace is None else 0, workspace)
     sq, sk = (desc.b, desc.h, 1, desc.d), (desc.b, desc.h_kv, desc.s_kv, desc.d)
     views = [call.view(n, x, s) for n, x, s in (("q", q, sq), ("k", k, sk), ("v", v, sk), ("o", o, sq))]

@@ -516,3 +516,24 @@ def test_nan_stays_in_its_sequence(dtype, d, h, hk):
         cut = (100, 161) if n in (3, 4) else (70, 115)
         np.testing.assert_array_equal(a[:cut[0]], b[:cut[0]])
         np.testing.assert_array_equal(a[cut[1]:], b[cut[1]:])
+
+
+def test_table_with_other_memory():
+    """The table's tensor given other memory of another type between calls with one bias: as a bias made anew."""
+    import torch
+    p = Problem("bfloat16", [(150, 170)], 4, 2, 64, 2, 32, 128, True, seed=17)
+    o, lse = p.inputs_bwd()
+    old = p.table.data
+    p.table.data = (torch.randn(32, 4, generator=torch.Generator().manual_seed(3)) * 1.5).bfloat16().cuda()
+    old.fill_(float("nan"))
+    p.check_fwd(*p.fwd())
+    o, lse = p.inputs_bwd()
+    p.check_bwd(p.bwd(o, lse), o, lse)
+    ab, V = p.ab, p.view
+    desc = ab.sdpa_desc(dtype=ab.ATTN_BF16, b=1, h=4, h_kv=2, s_q=1, s_kv=170, d=64, scale=p.scale,
+                        mask=ab.ATTN_CAUSAL_BOTTOM_RIGHT)
+    q, k, v = (p.put(x) for x in (p.q[:1], p.k, p.v))
+    outs = [torch.empty_like(q) for _ in range(2)]
+    for bias, out in zip((p.bias, ab.relbias(p.table, max_distance=128)), outs):
+        ab.sdpa_relbias_decode(desc, bias, V(q), V(k), V(v), None, V(out))
+    assert bool(torch.isfinite(outs[0]).all()) and torch.equal(*outs)

@@ -253,3 +253,46 @@ def test_lse_shape(ab):
     empty = _sdpa(ab, s_q=0)
     for shape in [(2, 4, 0), (0,)]:
         take(empty, (2, 4, 0), torch.zeros(shape))
+
+
+class _Memory:
+    """A CUDA tensor as the argument checks see it."""
+
+    def __init__(self, ptr, dtype, shape, contiguous=True, device=0):
+        self.ptr, self.dtype, self.shape, self.contiguous, self.index = ptr, dtype, shape, contiguous, device
+        self.device = f"cuda:{device}"
+
+    def data_ptr(self):
+        return self.ptr
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def get_device(self):
+        return self.index
+
+
+def test_a_table_whose_memory_was_replaced(ab):
+    """tensor.data = ... gives a table other memory and another type: a call reads what the tensor is then."""
+    import types
+    import torch
+    stream = types.SimpleNamespace(cuda_stream=0, device=types.SimpleNamespace(index=0))
+    table = _Memory(A, torch.float32, (32, 4))
+    bias = ab.relbias(table)
+    assert (bias.table, bias.table_type, bias.num_buckets) == (A, 2, 32)
+    table.ptr, table.dtype, table.shape = 3 * A, torch.bfloat16, (16, 4)
+    ab._relbias_call("call", _sdpa(ab), bias, table, stream)
+    assert (bias.table, bias.table_type, bias.num_buckets) == (3 * A, 1, 16)
+    for bad in (dict(dtype=torch.float64), dict(shape=(16, 5)), dict(shape=(64,)), dict(contiguous=False)):
+        table = _Memory(A, torch.float32, (32, 4))
+        bias = ab.relbias(table)
+        for k, v in bad.items():
+            setattr(table, k, v)
+        with pytest.raises(ValueError, match="table"):
+            ab._relbias_call("call", _sdpa(ab), bias, _Memory(A, torch.float32, (2, 4, 64)), stream)
+    with pytest.raises(ValueError, match="table"):
+        ab._relbias_call("call", _sdpa(ab), ab.relbias(_Memory(A, torch.float32, (32, 4), device=1)),
+                         _Memory(A, torch.float32, (2, 4, 64)), stream)
