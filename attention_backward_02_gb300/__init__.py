@@ -134,17 +134,22 @@ def sdpa_workspace_size(desc):
     return fwd.value, bwd.value
 
 
-def _workspace(nbytes, device, workspace):
+def _workspace(nbytes, device, workspace, stream):
+    """The caller's workspace, or memory of the stream that the call runs on: that of the current stream might
+    still be in use by earlier work there, and would go back to it before the call is done."""
     torch = _torch()
     if workspace is not None:
         return workspace
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def sdpa_fwd_stats(desc, q, k, v, o, lse, *, workspace=None, stream=None):
     """q, k, v, o: views (attn_view_t) or tensors; lse: fp32 CUDA tensor."""
     fwd, _ = sdpa_workspace_size(desc)
-    ws = _workspace(fwd, lse.device, workspace)
+    ws = _workspace(fwd, lse.device, workspace, stream)
     vq, vk, vv, vo = (x if isinstance(x, attn_view_t) else view_bhsd(x) for x in (q, k, v, o))
     st = _lib.load().sdpa_fwd_stats(C.byref(desc), vq, vk, vv, vo,
                                     C.cast(C.c_void_p(lse.data_ptr()), C.POINTER(C.c_float)),
@@ -159,7 +164,7 @@ def sdpa_bwd(desc, q, k, v, o, dO, lse, dQ, dK, dV, *, workspace=None, stream=No
     asynchronous on `stream` (default: the current stream).  A workspace of the size
     sdpa_workspace_size gives is allocated when none is passed; it is returned, for attn_query_status."""
     _, bwd = sdpa_workspace_size(desc)
-    ws = _workspace(bwd, lse.device, workspace)
+    ws = _workspace(bwd, lse.device, workspace, stream)
     views = [x if isinstance(x, attn_view_t) else view_bhsd(x) for x in (q, k, v, o, dO, dQ, dK, dV)]
     st = _lib.load().sdpa_bwd(C.byref(desc), *views[:5],
                               C.cast(C.c_void_p(lse.data_ptr()), C.POINTER(C.c_float)), *views[5:],
@@ -181,7 +186,7 @@ def nsa_selected_attn_bwd(desc, q, k, v, o, dO, softmax_max, softmax_sum, topk, 
     dk, dv [T2, n2, d]; softmax_max / softmax_sum [T1, n1, 8] fp32; topk [T1, n2, block_count] int32.
     Asynchronous on `stream`; returns the workspace (allocated when none is passed) for
     attn_query_status, which reports indices that were out of range or repeated."""
-    ws = _workspace(nsa_workspace_size(desc), q.device, workspace)
+    ws = _workspace(nsa_workspace_size(desc), q.device, workspace, stream)
     fp = lambda t: C.cast(C.c_void_p(t.data_ptr()), C.POINTER(C.c_float))
     st = _lib.load().nsa_selected_attn_bwd(
         C.byref(desc), *(C.c_void_p(t.data_ptr()) for t in (q, k, v, o, dO)), fp(softmax_max), fp(softmax_sum),
@@ -204,7 +209,7 @@ def nsa_selected_attn_fwd(desc, q, k, v, topk, o, softmax_max, softmax_sum, *, w
     v [T2, n2, d_v], topk [T1, n2, block_count] int32 -> o [T1, n1, d_v] (input dtype), softmax_max /
     softmax_sum [T1, n1, 8] fp32.  Asynchronous on `stream`; returns the workspace (its first word is the
     device status)."""
-    ws = _workspace(nsa_fwd_workspace_size(desc), q.device, workspace)
+    ws = _workspace(nsa_fwd_workspace_size(desc), q.device, workspace, stream)
     fp = lambda t: C.cast(C.c_void_p(t.data_ptr()), C.POINTER(C.c_float))
     st = _lib.load().nsa_selected_attn_fwd(
         C.byref(desc), *(C.c_void_p(t.data_ptr()) for t in (q, k, v)),
@@ -216,7 +221,7 @@ def nsa_selected_attn_fwd(desc, q, k, v, topk, o, softmax_max, softmax_sum, *, w
 
 def nsa_block_lists(desc, topk, offsets, tokens, *, workspace=None, stream=None):
     """Fills device int32 tensors offsets / tokens; returns nblk_max."""
-    ws = _workspace(nsa_workspace_size(desc), topk.device, workspace)
+    ws = _workspace(nsa_workspace_size(desc), topk.device, workspace, stream)
     ip = lambda t: C.cast(C.c_void_p(t.data_ptr()), C.POINTER(C.c_int32))
     nblk = C.c_int64()
     st = _lib.load().nsa_block_lists(C.byref(desc), ip(topk), ip(offsets), ip(tokens), C.byref(nblk),
@@ -228,10 +233,9 @@ def nsa_block_lists(desc, topk, offsets, tokens, *, workspace=None, stream=None)
 
 class _Call:
     """One call on CUDA tensors that all live on one device: checks them, makes that device current for
-    the call, and holds the stream and workspace it runs with.  A workspace made here for a stream other
-    than the current one is recorded on it, so its memory is not reused before the call is done.  These
-    checks are most of a small call's time, so they read each property of a tensor once (the raw stream
-    and device queries are the ones torch's own generated code uses: 0.1 us instead of 1.5)."""
+    the call, and holds the stream and workspace it runs with.  These checks are most of a small call's
+    time, so they read each property of a tensor once (the raw stream and device queries are the ones
+    torch's own generated code uses: 0.1 us instead of 1.5)."""
 
     __slots__ = ("where", "dtype", "device", "stream", "given")
 
@@ -270,12 +274,9 @@ class _Call:
         return attn_view_t(x.data_ptr(), st[0], st[1], st[2])
 
     def workspace(self, nbytes, workspace):
-        torch = _torch()
         if workspace is None:
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", self.device))
-            if self.given is not None:
-                workspace.record_stream(self.given)
-        elif workspace.get_device() != self.device or not workspace.is_contiguous():
+            return _workspace(nbytes, _torch().device("cuda", self.device), None, self.given)
+        if workspace.get_device() != self.device or not workspace.is_contiguous():
             raise ValueError(f"{self.where}: workspace on {workspace.device}, tensors on cuda:{self.device}")
         return workspace
 

@@ -537,3 +537,26 @@ def test_table_with_other_memory():
     for bias, out in zip((p.bias, ab.relbias(p.table, max_distance=128)), outs):
         ab.sdpa_relbias_decode(desc, bias, V(q), V(k), V(v), None, V(out))
     assert bool(torch.isfinite(outs[0]).all()) and torch.equal(*outs)
+
+
+def test_workspace_on_a_side_stream():
+    """A workspace made by a call on a side stream is none of the memory that was freed on the current stream, whose
+    work on it may still be queued; and it goes back to the side stream."""
+    import torch
+    p = Problem("float16", [(200, 200)], 4, 2, 64, 2, 32, 128, True, seed=18)
+    q, k, v = (p.put(x) for x in (p.q, p.k, p.v))
+    o, lse = p.nan(p.q), torch.empty(p.tq * p.h, device="cuda")
+    V, s = p.view, torch.cuda.Stream()
+    for call, need in ((lambda **kw: p.ab.sdpa_relbias_fwd_stats(p.desc, p.bias, V(q), V(k), V(v), V(o), lse, **kw),
+                        p.ab.sdpa_relbias_workspace_size(p.desc, p.bias)[0]),
+                       (lambda **kw: p.ab.sdpa_fwd_stats(p.desc, V(q), V(k), V(v), V(o), lse, **kw),
+                        max(256, p.ab.sdpa_workspace_size(p.desc)[0]))):
+        torch.cuda.synchronize()
+        block = torch.empty(need, dtype=torch.uint8, device="cuda")
+        freed = block.data_ptr()
+        del block
+        first = call(stream=s).data_ptr()
+        again = call(stream=s).data_ptr()
+        own = call().data_ptr()
+        torch.cuda.synchronize()
+        assert first != freed and again == first and own == freed

@@ -296,3 +296,57 @@ def test_a_table_whose_memory_was_replaced(ab):
     with pytest.raises(ValueError, match="table"):
         ab._relbias_call("call", _sdpa(ab), ab.relbias(_Memory(A, torch.float32, (32, 4), device=1)),
                          _Memory(A, torch.float32, (2, 4, 64)), stream)
+
+
+def test_a_workspace_made_by_a_call_is_memory_of_its_stream(ab, monkeypatch):
+    """Every call that makes its own workspace takes it from the stream it is given: the current stream's free
+    memory may still be in use by work queued there.  torch and the library's launches are stood in for."""
+    import contextlib
+    import types
+    import torch
+    made, at = [], [None]
+
+    @contextlib.contextmanager
+    def use(stream):
+        before, at[0] = at[0], stream
+        yield
+        at[0] = before
+
+    def empty(n, dtype, device):
+        made.append(at[0])
+        return types.SimpleNamespace(data_ptr=lambda: A, numel=lambda: n, record_stream=lambda s: None)
+
+    raw = types.SimpleNamespace(_cuda_getDevice=lambda: 0, _cuda_getCurrentRawStream=lambda d: 0)
+    names = ("float16", "bfloat16", "float32", "int32", "uint8", "device")
+    now = types.SimpleNamespace(cuda_stream=0)
+    fake = types.SimpleNamespace(empty=empty, _C=raw, **{n: getattr(torch, n) for n in names}, cuda=types.SimpleNamespace(
+        stream=use, current_stream=lambda *a: now, current_device=lambda: 0))
+    real = ab._lib.load()
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(real, name) if name.endswith("_size") else lambda *a: 0
+
+    d, bias = _sdpa(ab), ab.relbias(_Memory(A, torch.float32, (32, 4)))
+    one = _sdpa(ab, s_q=1, s_kv=4096, mask=ab.ATTN_CAUSAL_BOTTOM_RIGHT)
+    n = ab.nsa_desc(dtype=ab.ATTN_BF16, cu_seqlens_q=[64], cu_seqlens_kv=[128], n1=4, n2=1, d=128, scale=0.1,
+                    block_size=64, block_count=2, sparse_mode=0)
+    v, x, lse = ab.attn_view_t(A, 4 * 96 * 64, 64, 256), _Memory(A, torch.float32, (8,)), _Memory(A, torch.float32, (2, 4, 64))
+    dt = _Memory(A, torch.float32, (32, 4))
+    calls = [lambda **k: ab.sdpa_fwd_stats(d, v, v, v, v, lse, **k),
+             lambda **k: ab.sdpa_bwd(d, v, v, v, v, v, lse, v, v, v, **k),
+             lambda **k: ab.nsa_selected_attn_fwd(n, *[x] * 7, **k),
+             lambda **k: ab.nsa_selected_attn_bwd(n, *[x] * 11, **k),
+             lambda **k: ab.nsa_block_lists(n, x, x, x, **k),
+             lambda **k: ab.sdpa_relbias_fwd_stats(d, bias, v, v, v, v, lse, **k),
+             lambda **k: ab.sdpa_relbias_bwd(d, bias, v, v, v, v, v, lse, v, v, v, dt, **k),
+             lambda **k: ab.sdpa_relbias_decode(one, bias, v, v, v, None, v, **k),
+             lambda **k: ab.qk_norm_rope_fwd(_qk(ab, rotary_dim=0), v, v, None, None, None, None, v, v, **k),
+             lambda **k: ab.qk_norm_rope_bwd(_qk(ab, rotary_dim=0), v, v, v, v, None, None, None, None, v, v, **k)]
+    monkeypatch.setattr(ab, "_torch_module", fake)
+    monkeypatch.setattr(ab._lib, "load", Lib)
+    stream = types.SimpleNamespace(cuda_stream=5, device=types.SimpleNamespace(index=0))
+    for i, call in enumerate(calls):
+        call()
+        call(stream=stream)
+        assert len(made) == 2 * i + 2 and made[-2] is None and made[-1] is stream, i
