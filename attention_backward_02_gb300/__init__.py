@@ -502,10 +502,13 @@ def qk_norm_rope_bwd(desc, q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, d
 
 
 def attn_query_status(workspace, stream=None):
-    """Synchronises the stream; returns the device status bits (0 = clean)."""
+    """Synchronises the stream (default: the current stream of the workspace's device); returns the device status
+    bits (0 = clean)."""
+    torch = _torch()
     flags = C.c_uint32()
-    st = _lib.load().attn_query_status(C.c_void_p(workspace.data_ptr()), C.c_void_p(_stream_ptr(stream)),
-                                       C.byref(flags))
+    with torch.cuda.device(workspace.get_device()):  # a default stream is that of the device that is current
+        st = _lib.load().attn_query_status(C.c_void_p(workspace.data_ptr()), C.c_void_p(_stream_ptr(stream)),
+                                           C.byref(flags))
     if st not in (_lib.ATTN_OK, _lib.ATTN_ERR_DEVICE):
         check(st, "attn_query_status")
     return flags.value

@@ -350,3 +350,33 @@ def test_a_workspace_made_by_a_call_is_memory_of_its_stream(ab, monkeypatch):
         call()
         call(stream=stream)
         assert len(made) == 2 * i + 2 and made[-2] is None and made[-1] is stream, i
+
+
+def test_status_of_a_workspace_on_another_device(ab, monkeypatch):
+    """The status is read behind the current stream of the workspace's device, with that device current.  torch and the
+    library are stood in for."""
+    import contextlib
+    import types
+    import torch
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    fake = types.SimpleNamespace(cuda=types.SimpleNamespace(
+        device=device, current_stream=lambda d=None: types.SimpleNamespace(cuda_stream=100 + (current[0] if d is None else d))))
+
+    def query(ws, stream, flags):
+        seen.append((current[0], ws.value, stream.value))
+        flags._obj.value = 2
+        return 7
+
+    monkeypatch.setattr(ab, "_torch_module", fake)
+    monkeypatch.setattr(ab._lib, "load", lambda: types.SimpleNamespace(attn_query_status=query))
+    for index in (0, 1):
+        assert ab.attn_query_status(_Memory(A, torch.uint8, (256,), device=index)) == 2
+        assert ab.attn_query_status(_Memory(A, torch.uint8, (256,), device=index), types.SimpleNamespace(cuda_stream=7)) == 2
+    assert seen == [(0, A, 100), (0, A, 7), (1, A, 101), (1, A, 7)] and current == [0]
