@@ -83,8 +83,6 @@
 // memory; from then on every wait of the CTA fails fast and all work is
 // skipped while the control flow (and so every named barrier) stays the same;
 // the CTA drains its in-flight copies and MMAs, frees its TMEM and exits.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <climits>
 #include <queue>
@@ -96,6 +94,7 @@
 #include "relbias.h"
 #include "sm103.cuh"
 #include "tc_util.cuh"
+#include "tmap.h"
 
 namespace attn {
 using namespace sm103;
@@ -1142,40 +1141,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS + (kOrdered ? 32 : 0), 1)
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-    return fn;
-}
-
-// 16-bit [B][H][S][D] view (element strides) as a 4-D map (d, s, h, b), box (64, rows, 1, 1).
-bool map_view(CUtensorMap *m, const View &v, int dtype, int64_t d, int64_t s, int64_t h, int64_t b, uint32_t rows)
-{
-    auto enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(s), cuuint64_t(h), cuuint64_t(b)};
-    const int64_t sb = b > 1 ? v.sb : s * v.ss;  // unused extent-1 dim: any legal stride
-    cuuint64_t strides[3] = {cuuint64_t(v.ss * 2), cuuint64_t(v.sh * 2), cuuint64_t((sb > 0 ? sb : 8) * 2)};
-    cuuint32_t box[4] = {64, rows, 1, 1};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    CUresult r = enc(m, dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                     v.ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 bool map_dqacc(CUtensorMap *m, float *base, int64_t d, int64_t rows, uint32_t box_rows)
 {
-    auto enc = encode_fn();
+    auto enc = tmap_encoder();
     if (!enc) return false;
     cuuint64_t dims[2] = {cuuint64_t(d), cuuint64_t(rows)};
     cuuint64_t strides[1] = {cuuint64_t(d * 4)};
@@ -1482,13 +1450,13 @@ template <class T, int D, class Geo> cudaError_t run_tc(const DenseArgs &a, cons
     const int64_t nb = packed ? 1 : a.nseq;
     const int64_t sq = packed ? a.t_q : (a.t_q / (a.nseq ? a.nseq : 1));
     const int64_t skv = packed ? a.t_kv : (a.t_kv / (a.nseq ? a.nseq : 1));
-    if (sq > 0 && (!map_view(&prm.tm_q, a.q, a.dtype, D, sq, a.h, nb, Cfg::BM) ||
-                   !map_view(&prm.tm_do, a.dO, a.dtype, D, sq, a.h, nb, Cfg::BM)))
+    if (sq > 0 && (!tmap_view16(&prm.tm_q, a.q, a.dtype, D, sq, a.h, nb, Cfg::BM) ||
+                   !tmap_view16(&prm.tm_do, a.dO, a.dtype, D, sq, a.h, nb, Cfg::BM)))
         return cudaErrorInvalidValue;
-    if (!map_view(&prm.tm_k, a.k, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
-        !map_view(&prm.tm_v, a.v, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
-        !map_view(&prm.tm_dk, a.dK, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
-        !map_view(&prm.tm_dv, a.dV, a.dtype, D, skv, a.h_kv, nb, Cfg::BN))
+    if (!tmap_view16(&prm.tm_k, a.k, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
+        !tmap_view16(&prm.tm_v, a.v, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
+        !tmap_view16(&prm.tm_dk, a.dK, a.dtype, D, skv, a.h_kv, nb, Cfg::BN) ||
+        !tmap_view16(&prm.tm_dv, a.dV, a.dtype, D, skv, a.h_kv, nb, Cfg::BN))
         return cudaErrorInvalidValue;
     if (sq > 0 && !map_dqacc(&prm.tm_dq, a.dqacc, D, int64_t(a.n_part) * a.h * a.t_pad, Cfg::DQ_BOX_ROWS))
         return cudaErrorInvalidValue;

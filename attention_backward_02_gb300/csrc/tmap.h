@@ -27,15 +27,16 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder()
 }
 
 // A 16-bit [B][H][S][D] view (element strides) as a 4-D map (d, s, h, b) with
-// boxes of 64 elements x `rows` rows and the 128-byte swizzle.
+// boxes of 64 elements x `rows` rows and the 128-byte swizzle.  A stride of 0 (an
+// input that is one and the same for all sequences, heads or tokens) is one the map takes.
 inline bool tmap_view16(CUtensorMap *m, const View &v, int dtype, int64_t d, int64_t s, int64_t h, int64_t b,
                         uint32_t rows)
 {
     auto enc = tmap_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(s), cuuint64_t(h), cuuint64_t(b)};
-    const int64_t sb = b > 1 ? v.sb : s * v.ss;  // unused extent-1 dim: any legal stride
-    cuuint64_t strides[3] = {cuuint64_t(v.ss * 2), cuuint64_t(v.sh * 2), cuuint64_t((sb > 0 ? sb : 8) * 2)};
+    const int64_t sb = b > 1 ? v.sb : 0;  // (packed: the dimension is not used)
+    cuuint64_t strides[3] = {cuuint64_t(v.ss * 2), cuuint64_t(v.sh * 2), cuuint64_t(sb * 2)};
     cuuint32_t box[4] = {64, rows, 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     CUresult r = enc(m, dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,

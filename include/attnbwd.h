@@ -97,7 +97,8 @@ typedef enum {
 /* A 16-bit tensor seen as logical [B, H, S, D] with element strides
  * (sb, sh, ss, 1).  The sample's BSHD storage viewed as BHSD has
  * (S*H*D, D, H*D, 1).  In packed (varlen, TND) mode token t of head h is at
- * ptr + t*ss + h*sh and sb is ignored.                                       */
+ * ptr + t*ss + h*sh and sb is ignored.  An input's stride may be 0 (the same for
+ * all sequences, heads or tokens); the elements of an output are apart.      */
 typedef struct {
     void *ptr;
     int64_t sb, sh, ss;
