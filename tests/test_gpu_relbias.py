@@ -560,3 +560,25 @@ def test_workspace_on_a_side_stream():
         own = call().data_ptr()
         torch.cuda.synchronize()
         assert first != freed and again == first and own == freed
+
+
+@pytest.mark.parametrize("dtype,d,mask,mode", [("float16", 64, 2, 0), ("bfloat16", 128, 0, 2), ("bfloat16", 64, 1, 1)])
+def test_rows_behind_the_last_sequence(dtype, d, mask, mode):
+    """Packed tensors with more rows than the sequences have: those of the inputs (NaN here) are not looked at, those of
+    the outputs stay as they were."""
+    import torch
+    lens, h, hk = [(70, 100), (45, 61), (130, 150)], 4, 2
+    p = Problem(dtype, lens, h, hk, d, mask, 32, 128, True, seed=19, mode=mode)
+    o, lse = p.inputs_bwd()
+    ab, V = p.ab, p.view
+    longer = lambda t: torch.cat([t, torch.full((133, *t.shape[1:]), float("nan"), dtype=t.dtype)]).cuda()
+    q, k, v, do, oin = (longer(t) for t in (p.q, p.k, p.v, p.do, o))
+    out = [torch.full_like(t, 3.0) for t in (q, q, k, v)]
+    l2, dt = torch.full((h * p.tq,), float("nan"), device="cuda"), torch.empty_like(p.table)
+    ab.sdpa_relbias_fwd_stats(p.desc, p.bias, V(q), V(k), V(v), V(out[0]), l2)
+    ws = ab.sdpa_relbias_bwd(p.desc, p.bias, V(q), V(k), V(v), V(oin), V(do), p.put_lse(lse), *map(V, out[1:]), dt)
+    assert ab.attn_query_status(ws) == 0
+    for t, n in zip(out, (p.tq, p.tq, p.tk, p.tk)):
+        assert bool((t[n:] == 3.0).all())
+    p.check_fwd(p.get(out[0][:p.tq]), p.get_lse(l2))
+    p.check_bwd([p.get(t[:n]) for t, n in zip(out[1:], (p.tq, p.tk, p.tk))] + [dt.double().cpu().numpy()], o, lse)
