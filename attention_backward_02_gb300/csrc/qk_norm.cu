@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm<NC, BWD>) qk_norm_ke
                     const float *cr = a.cos + int64_t(ok ? p : 0) * (a.rot / 2), *sr = a.sin + int64_t(ok ? p : 0) * (a.rot / 2);
                     const uint32_t dst = tc::smem_u32(angles + (begun % (DEPTH + 1)) * a.rot);
                     const int half = int(a.rot) / 8;  // 16-byte pieces of a cos or sin row
-                    for (int k = lane; k < 2 * half; k += 32) copy16(dst + k * 16, k < half ? cr + 4 * k : sr + 4 * (k - half), true);
+                    for (int k = lane; k < 2 * half; k += 32) copy16(dst + k * 16, k < half ? cr + 4 * k : sr + 4 * (k - half), ok);
                 }
                 ++begun;
             }
@@ -279,6 +279,11 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm<NC, BWD>) qk_norm_ke
             }
         }
         issue(item + DEPTH);
+        if (ROPE != kNoRope && !valid) {  // a token out of range: with a row and angles of zeros it adds nothing to the
+                                          // weights' gradient, and its outputs are zeros whatever the weights hold
+#pragma unroll
+            for (int k = 0; k < NC; ++k) xr[k] = yr[k] = make_uint4(0, 0, 0, 0);
+        }
         float2 x[NC][4], z[NC][4];
         float2 sq = both(0.f);
 #pragma unroll
@@ -288,13 +293,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm<NC, BWD>) qk_norm_ke
             for (int e = 0; e < 4; ++e) sq = fma2(x[k][e], x[k][e], sq);
         }
         const float r = rsqrtf(fmaf(row_sum(sq.x + sq.y), 1.f / D, a.eps));
-        if (ROPE != kNoRope && !valid) {  // a token out of range: zeros whatever its row, the weights and the tables
-                                          // hold, and nothing for the weights' gradient
-#pragma unroll
-            for (int k = 0; k < NC; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[k][e] = both(0.f);
-        } else if (!BWD) {  // the norm's factor is common to a row: it goes on last
+        if (!BWD) {  // the norm's factor is common to a row: it goes on last
 #pragma unroll
             for (int k = 0; k < NC; ++k)
 #pragma unroll
@@ -326,7 +325,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm<NC, BWD>) qk_norm_ke
         }
         if (int64_t(c_hb) * kItemHeads + grp < s.h) {
 #pragma unroll
-            for (int k = 0; k < NC; ++k) *reinterpret_cast<uint4 *>(yp + 64 * k) = pack8<T>(z[k]);
+            for (int k = 0; k < NC; ++k)
+                *reinterpret_cast<uint4 *>(yp + 64 * k) = ROPE == kNoRope || valid ? pack8<T>(z[k]) : make_uint4(0, 0, 0, 0);
         }
         yp += kItemHeads * s.y.sh;
         if (++c_hb == nhb) {
