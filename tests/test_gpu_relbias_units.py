@@ -65,3 +65,26 @@ def test_several_units_a_cta_in_the_reproducible_modes(dtype, lens, h, d, mask, 
     p.check_bwd(first, o, lse)
     for a, b in zip(first, p.bwd(o, lse)):
         np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,lens,h,hk,d,mask,kw", [
+    ("float16", [(1 + 7 * n % 40, 1 + 11 * n % 37) for n in range(256)], 18, 18, 64, 2, {}),  # the most packed sequences
+    ("bfloat16", [(33, 20)], 18, 18, 128, 0, dict(b=256)),
+])
+def test_more_units_than_the_host_plans(dtype, lens, h, hk, d, mask, kw):
+    """More units than a plan holds: they are taken in turn.  Forward and backward, the forward's units past its estimate's
+    reach too."""
+    import torch
+    p = Problem(dtype, lens, h, hk, d, mask, 32, 128, True, seed=d, **kw)
+    assert sum((n + 127) // 128 for _, n in p.lens) * hk > 4096
+    o, lse = p.fwd()
+    ot, lt = torch.from_numpy(o).to(p.dt), lse.astype(np.float32)
+    first, again = p.bwd(ot, lt), p.bwd(ot, lt)
+    for i in (1, 2, 3):
+        np.testing.assert_array_equal(first[i], again[i])
+    pick = [0, h - 1]  # the definition takes a few of the heads
+    few = Problem(dtype, lens, 2, 2, d, mask, 32, 128, True, **kw)
+    few.q, few.k, few.v, few.do = (t[:, pick] for t in (p.q, p.k, p.v, p.do))
+    few.table = p.table[:, pick].contiguous()
+    few.check_fwd(o[:, pick], lse[:, pick])
+    few.check_bwd([x[:, pick] for x in first], ot[:, pick], lt[:, pick])
