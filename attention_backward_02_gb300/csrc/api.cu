@@ -308,10 +308,12 @@ struct RelLayout {
 // the largest of the mean and, for each k, k + 1 units of the k * 152 + 1st size (half a query tile takes 0.85 us
 // at d = 128, 1.2 at d = 64; a unit's start is one of them), and the shares' way through the workspace at 2.2 TB/s.
 // The split and ordered dQ modes keep one unit: their order of adds is by key tiles.  A constant 152 SMs: the
-// workspace size must not depend on a CUDA call.  Measured (us, whole call, causal but for the last; 1, 2, 4, 8 shares,
-// the choice in brackets): b1 h32/8 s2048 d128 205 [131] 152; b1 h32/8 s4096 [395] 497 434; b2 h32/4 s1024 213 128 [98]
-// 116; b1 h16/1 s1024 d64 276 148 82 [51]; b1 h8/1 s512, 4096 keys 115 68 [46] 51; b4 h32/8 s1024 [158] 187 219; b1
-// h32/8 s1301, 2285 keys [145] 155 153; b2 h12/4 s777 d64 [85], 3 shares 61: here the estimate errs.
+// workspace size must not depend on a CUDA call.  Measured (us, whole call, causal, 32 buckets to 128 unless said; 1, 2,
+// 4, 8 shares, the choice in brackets): b1 h32/8 s2048 d128 209 [135] 155; b1 h32/8 s4096 [398] 502 438; b2 h32/4 s1024
+// 216 131 [101] 120; b1 h16/1 s1024 d64 283 152 84 [53]; b1 h8/1 s512, 4096 keys 117 71 [49] 53; b4 h32/8 s1024 [161]
+// 190 222; b1 h32/8 s1301, 2285 keys [148] 159 157, and with 64 buckets to 1024 [177] 188 174; b2 h12/4 s777 d64
+// without a mask [88], 3 shares 64.  The estimate counts all blocks of scores alike, though one that crosses a bucket's
+// border costs more (half of them do with 64 buckets to 1024, a tenth with 32 to 128), and it errs in the last two.
 int rel_shares(const attn_sdpa_desc_t *d, const DenseShape &sh)
 {
     const int64_t G = d->h / d->h_kv, sms = 152;

@@ -66,7 +66,7 @@
 // tile on the diagonal runs the same code as its neighbours: the P / dS loop's copies
 // compete for the instruction cache (790 -> 758 us; a third copy for blocks of two
 // buckets, without shuffles, cost 50).  Element masks remain where a tile passes the
-// end of a sequence.  At those sizes 758 us against 748 without a bias; 74 / 54 at b4
+// end of a sequence.  At those sizes 767 us against 751 without a bias; 75 / 53 at b4
 // h12 s1024 d64 without a mask.  Each warp stores its row once per (key tile, head); a
 // kernel behind this one adds them up in a fixed order, so the table's gradient is
 // bitwise reproducible in every dQ mode.  Packed sequences: rows of a tile that

@@ -71,7 +71,10 @@ __device__ __forceinline__ float rel_table_value(const RelBias &b, int64_t at)
 }
 
 // dtable[n][head] = the sum of the shares of 32 buckets of one head, in a fixed order: a block of 256 threads;
-// warp w sums every 8th share, the warps' sums are added in order.
+// warp w sums every 8th share, the warps' sums are added in order.  A warp takes the rows one after the other, four
+// loads in flight, which shows where the rows are many and the heads few: the finalize takes 81 us where it takes 18
+// without a bias at 16 sequences of 4096 keys, 5 heads of 64 (529 rows), and 110 where 48 at 256 packed sequences of 50
+// to 350, 12 heads of 64 (667 rows).
 __device__ __forceinline__ void rel_dtable_block(const RelArgs &a, int unit)
 {
     __shared__ float red[8][32];

@@ -25,7 +25,11 @@
 // Each warp keeps a running maximum and sum (log2 units); the warps of a block join
 // through shared memory, the chunks of a sequence through fp32 partial results in
 // the workspace and a second kernel that adds them in order.
-// 32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 93 us for 537 MB, 0.87 of the
+// The weights P are rounded to the 16-bit type for the product with V, after their sum
+// is taken: the operands of that product are 16-bit, and a weight is off by half a step of V's own
+// type, as in the training forward (against the 64-bit form 0.00073 of the largest output for
+// bf16, where fp32 weights give 0.00065: O's own rounding is most of both).
+// 32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 93 us for 537 MB, 0.86 of the
 // measured copy rate, and 0.97 with all of 8192 (K and V through a ring of asynchronous
 // copies in shared memory: 112 against 107 as loads at the time; kv heads as the
 // grid's fastest index: 111; K a step ahead in registers: no gain); one sequence of 1000
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps, decode_blocks(D, ROWS)) relbias_d
                     }
             }
         }
-        // P, rounded to the 16-bit type for the product with V; its sum is taken before
+        // P, rounded to the 16-bit type (see above) for the product with V; its sum is taken before
         uint32_t pa[2][2] = {{0u, 0u}, {0u, 0u}};  // [key tile][row]
 #pragma unroll
         for (int i = 0; i < NR; ++i) {

@@ -42,8 +42,8 @@
 // A row's reference maximum m is raised only when a tile's maximum exceeds it by
 // more than 8 (log2 units), and then l and the row of O in TMEM are scaled by
 // exp2(m_old - m_new): P = exp2(x - m) <= 2^8 fits both 16-bit types.  P is
-// rounded to the 16-bit type for the second product, after its sum l is taken.  A
-// row that sees no key has O = 0 and LSE = +inf.
+// rounded to the 16-bit type for the second product, whose operands are of that type,
+// after its sum l is taken.  A row that sees no key has O = 0 and LSE = +inf.
 //
 // Packed sequences: the last key tile may run into the next sequence, whose values
 // meet P = 0; they are set to zero in shared memory first, so that an infinity or
