@@ -1059,7 +1059,8 @@ attn_status_t attn_query_status(void *workspace, void *stream, uint32_t *device_
     if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_status(e);
     uint32_t flags = 0;
     if ((e = cudaMemcpy(&flags, workspace, sizeof flags, cudaMemcpyDeviceToHost)) != cudaSuccess) return cuda_status(e);
-    if (flags && (e = cudaMemset(workspace, 0, sizeof flags)) != cudaSuccess) return cuda_status(e);
+    // on the stream: cudaMemset may return first, and would then race with the next call's status on this stream
+    if (flags && (e = cudaMemsetAsync(workspace, 0, sizeof flags, s)) != cudaSuccess) return cuda_status(e);
     *device_flags = flags;
     return flags ? ATTN_ERR_DEVICE : ATTN_OK;
 }

@@ -327,3 +327,17 @@ def test_tokens_out_of_range_beside_values_that_are_not_finite(d, rot, inter):
         assert bool((t.permute(0, 2, 1, 3)[~live] == 0).all())
     for a, b in zip(dw, clean_w):  # the weights' gradients do not depend on the weights
         assert torch.equal(a, b)
+
+
+def test_status_of_one_call_after_another_on_a_side_stream():
+    """Reading a status clears it ahead of the next call on that stream, whose own status is not lost."""
+    p = Problem("bfloat16", 1, 6, 2, 1, 64, 64, seed=22)
+    torch = p.torch
+    p.pos[0, 2] = -1
+    s = torch.cuda.Stream()
+    out, ws = p.fwd()
+    torch.cuda.synchronize()
+    for _ in range(200):
+        p.fwd(out=out, workspace=ws, stream=s)
+        assert p.ab.attn_query_status(ws, s) == 2
+    assert p.ab.attn_query_status(ws, s) == 0
