@@ -13,16 +13,19 @@ import math
 
 from . import _lib
 from ._lib import (ATTN_BF16, ATTN_CAUSAL_BOTTOM_RIGHT, ATTN_CAUSAL_TOP_LEFT, ATTN_DQ_ATOMIC, ATTN_DQ_ORDERED,
-                   ATTN_DQ_SPLIT, ATTN_F16, ATTN_F32, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t, attn_qk_norm_desc_t,
-                   attn_relbias_t, attn_sdpa_desc_t, attn_view_t, check)
+                   ATTN_DQ_SPLIT, ATTN_E4M3, ATTN_F16, ATTN_F32, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t,
+                   attn_paged_cache_t, attn_paged_seqs_t, attn_qk_norm_desc_t, attn_relbias_t, attn_sdpa_desc_t,
+                   attn_view_t, check)
 
 __all__ = ["sdpa_desc", "nsa_desc", "view_bhsd", "view_tnd", "sdpa_workspace_size", "sdpa_fwd_stats",
            "sdpa_bwd", "nsa_workspace_size", "nsa_selected_attn_bwd", "nsa_block_lists",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd",
            "relbias", "relbias_bucket", "sdpa_relbias_workspace_size", "sdpa_relbias_fwd_stats", "sdpa_relbias_bwd",
            "sdpa_relbias_decode_workspace_size", "sdpa_relbias_decode",
+           "paged_cache", "paged_cache_workspace_size", "paged_cache_write", "paged_cache_read",
+           "sdpa_paged_workspace_size", "sdpa_paged_fwd",
            "qk_norm_rope_desc", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
-           "attn_query_status", "AttnError", "ATTN_F16", "ATTN_BF16", "ATTN_F32",
+           "attn_query_status", "AttnError", "ATTN_F16", "ATTN_BF16", "ATTN_F32", "ATTN_E4M3",
            "ATTN_MASK_NONE",
            "ATTN_CAUSAL_TOP_LEFT", "ATTN_CAUSAL_BOTTOM_RIGHT"]
 
@@ -416,6 +419,128 @@ def sdpa_relbias_decode(desc, bias, q, k, v, lens, o, *, workspace=None, stream=
     views = [call.view(n, x, s) for n, x, s in (("q", q, sq), ("k", k, sk), ("v", v, sk), ("o", o, sq))]
     call.run(_lib.load().sdpa_relbias_decode, C.byref(desc), C.byref(bias), *views[:3],
              call.ptr("lens", lens, torch.int32, (desc.b,)), views[3], ws.data_ptr(), ws.numel())
+    return ws
+
+
+def paged_cache(k, v, *, k_scale=None, v_scale=None):
+    """An attn_paged_cache_t: a key / value cache in pages.  k, v: [n_pages, page_size, h_kv, d] of the calls' dtype
+    or float8_e4m3fn, any strides with a unit innermost one, alike in both (a cache stored by heads is passed
+    transposed); float8: k_scale, v_scale fp32 [n_pages, page_size, h_kv], strides alike in both.  The tensors
+    are held by the result, and read anew by every call."""
+    cache = attn_paged_cache_t()
+    cache.tensors = (k, v, k_scale, v_scale)
+    _read_cache(cache)
+    return cache
+
+
+def _read_cache(cache):
+    """The pages' addresses, type and strides, as their tensors are now."""
+    torch = _torch()
+    k, v, ks, vs = cache.tensors
+    code = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16, torch.float8_e4m3fn: ATTN_E4M3}.get(k.dtype)
+    st, dev = k.stride(), k.get_device()
+    if (code is None or k.dim() != 4 or v.dtype is not k.dtype or v.shape != k.shape or v.stride() != st or
+            v.get_device() != dev or (st[3] != 1 and k.shape[3] > 1)):
+        raise ValueError("paged_cache: k, v [n_pages, page_size, h_kv, d] of fp16, bf16 or float8_e4m3fn with the same "
+                         f"strides on one device, got {k.dtype} {tuple(k.shape)} {st} and {v.dtype} {tuple(v.shape)} "
+                         f"{v.stride()}")
+    cache.k, cache.v, cache.type = k.data_ptr(), v.data_ptr(), code
+    cache.n_pages, cache.page_size = k.shape[0], k.shape[1]
+    cache.sp, cache.ss, cache.sh = st[0], st[1], st[2]
+    if code == ATTN_E4M3:
+        if (ks is None or vs is None or ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or
+                ks.shape != k.shape[:3] or vs.shape != ks.shape or vs.stride() != ks.stride() or
+                ks.get_device() != dev or vs.get_device() != dev):
+            raise ValueError("paged_cache: float8 pages need k_scale, v_scale fp32 [n_pages, page_size, h_kv] with the "
+                             "same strides on the pages' device")
+        cache.k_scale, cache.v_scale = ks.data_ptr(), vs.data_ptr()
+        cache.scale_sp, cache.scale_ss, cache.scale_sh = ks.stride()
+    return dev
+
+
+def _paged_call(where, desc, cache, page_table, lens, cu_new, tokens, stream):
+    """The call on the device of the pages, and its attn_paged_seqs_t."""
+    torch = _torch()
+    call = _Call(where, desc.dtype, _read_cache(cache), stream)
+    k = cache.tensors[0]
+    if k.shape[2] != desc.h_kv or k.shape[3] != desc.d:
+        raise ValueError(f"{where}: pages {tuple(k.shape)}, {desc.h_kv} kv heads of {desc.d}")
+    b = desc.b
+    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != b or
+            page_table.get_device() != call.device or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        call.refuse("page_table", page_table, torch.int32, (b, -1))
+    seqs = attn_paged_seqs_t(page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+                             call.ptr("lens", lens, torch.int32, (b,)), call.ptr("cu_new", cu_new, torch.int32, (b + 1,)),
+                             tokens)
+    return call, seqs
+
+
+def _paged_rows(call, desc, name, x, heads, packed, tokens):
+    """View of the new tokens' rows: [B, heads, S_q, D], packed [tokens, heads, D]."""
+    if not packed:
+        return call.view(name, x, (desc.b, heads, desc.s_q, desc.d))
+    if x.dtype is not call.dtype or x.shape != (tokens, heads, desc.d) or x.get_device() != call.device or x.stride(2) != 1:
+        call.refuse(name, x, call.dtype, (tokens, heads, desc.d))
+    return attn_view_t(x.data_ptr(), 0, x.stride(1), x.stride(0))
+
+
+def paged_cache_workspace_size(desc, cache):
+    """Bytes of device workspace paged_cache_write and paged_cache_read need (host only)."""
+    n = C.c_size_t()
+    check(_lib.load().paged_cache_workspace_size(C.byref(desc), C.byref(cache), C.byref(n)), "paged_cache_workspace_size")
+    return n.value
+
+
+def _paged_copy(where, fn, desc, cache, page_table, lens, k, v, cu_new, workspace, stream):
+    packed = cu_new is not None
+    tokens = k.shape[0] if packed else 0
+    call, seqs = _paged_call(where, desc, cache, page_table, lens, cu_new, tokens, stream)
+    ws = call.workspace(256, workspace)
+    views = [_paged_rows(call, desc, n, x, desc.h_kv, packed, tokens) for n, x in (("k", k), ("v", v))]
+    call.run(fn, C.byref(desc), C.byref(cache), C.byref(seqs), *views, ws.data_ptr(), ws.numel())
+    return ws
+
+
+def paged_cache_write(desc, cache, page_table, lens, k, v, *, cu_new=None, workspace=None, stream=None):
+    """The new tokens' keys and values into their places of a paged_cache: the last tokens of each sequence, whose
+    lens [B] (int32 CUDA) cached tokens they are counted in, page_table [B, pages] (int32 CUDA) naming its pages
+    in order.  desc: an sdpa_desc with s_kv = the most tokens a sequence may have cached, s_q = the new tokens
+    of each.  k, v: [B, h_kv, S_q, D] tensors or views; with cu_new (int32 CUDA [B + 1], first rows) packed
+    [T, h_kv, D] tensors.  float8 pages: each row rounded to e4m3 with a scale of its own.  Returns the
+    workspace, for attn_query_status (lengths, counts or page ids out of range)."""
+    return _paged_copy("paged_cache_write", _lib.load().paged_cache_write, desc, cache, page_table, lens, k, v, cu_new,
+                       workspace, stream)
+
+
+def paged_cache_read(desc, cache, page_table, lens, k, v, *, cu_new=None, workspace=None, stream=None):
+    """The inverse of paged_cache_write: the last tokens of each sequence from the cache into k, v (float8 pages:
+    number times scale, rounded).  Returns the workspace, for attn_query_status."""
+    return _paged_copy("paged_cache_read", _lib.load().paged_cache_read, desc, cache, page_table, lens, k, v, cu_new,
+                       workspace, stream)
+
+
+def sdpa_paged_workspace_size(desc, cache):
+    """Bytes of device workspace sdpa_paged_fwd needs (host only)."""
+    n = C.c_size_t()
+    check(_lib.load().sdpa_paged_workspace_size(C.byref(desc), C.byref(cache), C.byref(n)), "sdpa_paged_workspace_size")
+    return n.value
+
+
+def sdpa_paged_fwd(desc, cache, page_table, lens, q, o, *, lse=None, cu_new=None, workspace=None, stream=None):
+    """Attention of each sequence's new tokens over everything it has in a paged_cache (their own keys and values
+    included: paged_cache_write comes first).  desc, page_table, lens, cu_new as there, mask
+    ATTN_CAUSAL_BOTTOM_RIGHT (up to a token's own position) or ATTN_MASK_NONE; q, o: [B, h, S_q, D] tensors or
+    views, packed [T, h, D]; lse: fp32 [B, h, S_q], packed [h, T], or None.  Returns the workspace, for
+    attn_query_status."""
+    torch = _torch()
+    packed = cu_new is not None
+    tokens = q.shape[0] if packed else 0
+    call, seqs = _paged_call("sdpa_paged_fwd", desc, cache, page_table, lens, cu_new, tokens, stream)
+    ws = call.workspace(sdpa_paged_workspace_size(desc, cache) if workspace is None else 0, workspace)
+    views = [_paged_rows(call, desc, n, x, desc.h, packed, tokens) for n, x in (("q", q), ("o", o))]
+    stats = call.ptr("lse", lse, torch.float32, (desc.h, tokens) if packed else (desc.b, desc.h, desc.s_q))
+    call.run(_lib.load().sdpa_paged_fwd, C.byref(desc), C.byref(cache), C.byref(seqs), *views, stats, ws.data_ptr(),
+             ws.numel())
     return ws
 
 

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libattnbwd.so")
 ATTN_OK, ATTN_ERR_NULLPTR, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED = 0, 1, 2, 3
 ATTN_ERR_WORKSPACE, ATTN_ERR_ALIGN, ATTN_ERR_CUDA, ATTN_ERR_DEVICE = 4, 5, 6, 7
 ATTN_DEV_TIMEOUT, ATTN_DEV_INDEX_RANGE, ATTN_DEV_INDEX_DUP = 0x1, 0x2, 0x4
-ATTN_F16, ATTN_BF16, ATTN_F32 = 0, 1, 2
+ATTN_F16, ATTN_BF16, ATTN_F32, ATTN_E4M3 = 0, 1, 2, 3
 ATTN_MASK_NONE, ATTN_CAUSAL_TOP_LEFT, ATTN_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
 ATTN_DQ_ATOMIC, ATTN_DQ_SPLIT, ATTN_DQ_ORDERED = 0, 1, 2
 
@@ -27,7 +27,9 @@ EXPORTS = ("sdpa_workspace_size", "sdpa_fwd_stats", "sdpa_bwd", "nsa_workspace_s
            "attn_selftest_wait_timeout", "attn_selftest_occupy", "attn_last_error",
            "nsa_fwd_workspace_size", "nsa_selected_attn_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_fwd",
            "qk_norm_rope_bwd", "attn_relbias_bucket", "sdpa_relbias_workspace_size", "sdpa_relbias_fwd_stats",
-           "sdpa_relbias_bwd", "sdpa_relbias_decode_workspace_size", "sdpa_relbias_decode")
+           "sdpa_relbias_bwd", "sdpa_relbias_decode_workspace_size", "sdpa_relbias_decode",
+           "paged_cache_workspace_size", "paged_cache_write", "paged_cache_read", "sdpa_paged_workspace_size",
+           "sdpa_paged_fwd")
 
 
 class attn_view_t(C.Structure):
@@ -61,6 +63,18 @@ class attn_relbias_t(C.Structure):
                 ("max_distance", C.c_int64), ("bidirectional", C.c_int)]
 
 
+class attn_paged_cache_t(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("type", C.c_int), ("n_pages", C.c_int64), ("page_size", C.c_int64), ("sp", C.c_int64),
+                ("sh", C.c_int64), ("ss", C.c_int64), ("scale_sp", C.c_int64), ("scale_sh", C.c_int64),
+                ("scale_ss", C.c_int64)]
+
+
+class attn_paged_seqs_t(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("table_stride", C.c_int64), ("table_pages", C.c_int64),
+                ("lens", C.c_void_p), ("cu_new", C.c_void_p), ("tokens", C.c_int64)]
+
+
 _lib = None
 
 
@@ -76,6 +90,7 @@ def load() -> C.CDLL:
     P, V, S, I = C.POINTER, C.c_void_p, C.c_size_t, C.c_int
     D, N, view = P(attn_sdpa_desc_t), P(attn_nsa_desc_t), attn_view_t
     K, R = P(attn_qk_norm_desc_t), P(attn_relbias_t)
+    G, Q = P(attn_paged_cache_t), P(attn_paged_seqs_t)
     sig = {
         "sdpa_workspace_size": [D, P(S), P(S)],
         "sdpa_fwd_stats": [D, view, view, view, view, P(C.c_float), V, S, V],
@@ -99,6 +114,11 @@ def load() -> C.CDLL:
         "sdpa_relbias_bwd": [D, R, view, view, view, view, view, V, view, view, view, V, V, S, V],
         "sdpa_relbias_decode_workspace_size": [D, R, P(S)],
         "sdpa_relbias_decode": [D, R, view, view, view, V, view, V, S, V],
+        "paged_cache_workspace_size": [D, G, P(S)],
+        "paged_cache_write": [D, G, Q, view, view, V, S, V],
+        "paged_cache_read": [D, G, Q, view, view, V, S, V],
+        "sdpa_paged_workspace_size": [D, G, P(S)],
+        "sdpa_paged_fwd": [D, G, Q, view, view, V, V, S, V],
         "qk_norm_rope_workspace_size": [K, P(S), P(S)],
         "qk_norm_rope_fwd": [K, view, view, V, V, V, V, V, view, view, V, S, V],
         "qk_norm_rope_bwd": [K, view, view, view, view, V, V, V, V, V, view, view, V, V, V, S, V],

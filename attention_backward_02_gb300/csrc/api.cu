@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include "attnbwd.h"
+#include "paged.h"
 #include "plan.h"
 #include "qk_norm.h"
 #include "relbias.h"
@@ -943,6 +944,178 @@ attn_status_t sdpa_relbias_decode(const attn_sdpa_desc_t *desc, const attn_relbi
     a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.part_o = reinterpret_cast<float *>(ws + L.o);
     return cuda_status(launch_relbias_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ paged cache
+
+namespace {
+
+constexpr int64_t kPagedMost = int64_t(1) << 30;  // cached tokens of a sequence
+
+bool offset_fits(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t d)
+{
+    const int64_t lim = int64_t(1) << 31;
+    return s1 < lim && s2 < lim && (n1 - 1) * s1 + (n2 - 1) * s2 + d < lim;
+}
+
+attn_status_t check_paged(const attn_sdpa_desc_t *d, const attn_paged_cache_t *c, PagedCache *out)
+{
+    if (!d || !c) return ATTN_ERR_NULLPTR;
+    if (d->dtype != ATTN_F16 && d->dtype != ATTN_BF16) return ATTN_ERR_INVALID;
+    if (d->b < 1 || d->h < 1 || d->h_kv < 1 || d->h % d->h_kv != 0 || d->d < 1) return ATTN_ERR_INVALID;
+    if (d->s_q < 0 || d->s_kv < 0 || !std::isfinite(d->scale)) return ATTN_ERR_INVALID;
+    if (d->mask != ATTN_MASK_NONE && d->mask != ATTN_CAUSAL_TOP_LEFT && d->mask != ATTN_CAUSAL_BOTTOM_RIGHT)
+        return ATTN_ERR_INVALID;
+    if (c->type != int(d->dtype) && c->type != ATTN_E4M3) return ATTN_ERR_INVALID;
+    if (c->n_pages < 0 || c->page_size < 1) return ATTN_ERR_INVALID;
+    const bool eight = c->type == ATTN_E4M3;
+    if (c->sp < 0 || c->sh < 0 || c->ss < 0) return ATTN_ERR_INVALID;
+    if (eight && (c->scale_sp < 0 || c->scale_sh < 0 || c->scale_ss < 0)) return ATTN_ERR_INVALID;
+    if (d->mask == ATTN_CAUSAL_TOP_LEFT || d->cu_seqlens_q || d->cu_seqlens_kv) return ATTN_ERR_UNSUPPORTED;
+    if ((d->d != 64 && d->d != 128) || d->h / d->h_kv > kPagedMaxGroup) return ATTN_ERR_UNSUPPORTED;
+    if (d->b > 65535 || d->h > 65535 || d->s_q > kPagedMost || d->s_kv > kPagedMost) return ATTN_ERR_UNSUPPORTED;
+    int shift = 4;
+    while (shift < 9 && (int64_t(1) << shift) != c->page_size) ++shift;
+    if (shift == 9 || c->n_pages > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (c->sp >= int64_t(1) << 38 || !offset_fits(c->page_size, c->ss, d->h_kv, c->sh, d->d)) return ATTN_ERR_UNSUPPORTED;
+    if (eight && !offset_fits(c->page_size, c->scale_ss, d->h_kv, c->scale_sh, 1)) return ATTN_ERR_UNSUPPORTED;
+    const int64_t unit = eight ? 16 : 8;
+    if (c->sp % unit || c->sh % unit || c->ss % unit) return ATTN_ERR_ALIGN;
+    out->k = c->k; out->v = c->v;
+    out->k_scale = c->k_scale; out->v_scale = c->v_scale;
+    out->type = c->type;
+    out->n_pages = int(c->n_pages);
+    out->shift = shift;
+    out->sp = c->sp; out->sh = int(c->sh); out->ss = int(c->ss);
+    out->sc_sp = eight ? c->scale_sp : 0; out->sc_sh = eight ? int(c->scale_sh) : 0; out->sc_ss = eight ? int(c->scale_ss) : 0;
+    return ATTN_OK;
+}
+
+// The cache's memory and the sequences, of a call.
+attn_status_t check_paged_call(const attn_sdpa_desc_t *d, const attn_paged_cache_t *c, const attn_paged_seqs_t *s, PagedSeqs *out)
+{
+    if (c->n_pages > 0) {
+        if (!c->k || !c->v || (c->type == ATTN_E4M3 && (!c->k_scale || !c->v_scale))) return ATTN_ERR_NULLPTR;
+        if (!aligned16(c->k) || !aligned16(c->v)) return ATTN_ERR_ALIGN;
+        if (c->type == ATTN_E4M3 && ((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) & 3))
+            return ATTN_ERR_ALIGN;
+    }
+    if (!s || !s->lens) return ATTN_ERR_NULLPTR;
+    if (d->s_kv > 0 && !s->page_table) return ATTN_ERR_NULLPTR;
+    if (s->table_stride < 0 || s->table_pages < (d->s_kv + c->page_size - 1) / c->page_size) return ATTN_ERR_INVALID;
+    if (s->cu_new && s->tokens < 0) return ATTN_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(s->page_table) | reinterpret_cast<uintptr_t>(s->lens) |
+         reinterpret_cast<uintptr_t>(s->cu_new)) & 3)
+        return ATTN_ERR_ALIGN;
+    const int64_t tokens = s->cu_new ? s->tokens : d->b * d->s_q, lim = int64_t(1) << 31;
+    // 32-bit row indices inside the kernels
+    if (tokens >= lim || tokens * (d->h > 2 * d->h_kv ? d->h : 2 * d->h_kv) >= lim) return ATTN_ERR_UNSUPPORTED;
+    out->table = s->page_table;
+    out->table_stride = s->table_stride;
+    out->lens = s->lens;
+    out->cu = s->cu_new;
+    out->b = int(d->b); out->s_q = int(d->s_q); out->tokens = int(tokens);
+    out->cap = int(d->s_kv);
+    return ATTN_OK;
+}
+
+constexpr size_t kPagedCopyBytes = 256;
+
+attn_status_t paged_copy_call(bool write, const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                              const attn_paged_seqs_t *seqs, attn_view_t k, attn_view_t v, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    PagedCopyArgs a;
+    std::memset(&a, 0, sizeof a);
+    attn_status_t st = check_paged(desc, cache, &a.cache);
+    if (st || (st = check_paged_call(desc, cache, seqs, &a.seqs))) return st;
+    if ((st = check_view(k, a.seqs.tokens)) || (st = check_view(v, a.seqs.tokens))) return st;
+    if ((st = check_ws(workspace, workspace_bytes, kPagedCopyBytes))) return st;
+    a.dtype = desc->dtype;
+    a.h_kv = int(desc->h_kv); a.d = int(desc->d);
+    a.k = to_view(k, a.seqs.cu != nullptr); a.v = to_view(v, a.seqs.cu != nullptr);
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_status(launch_paged_copy(a, write, static_cast<cudaStream_t>(stream)));
+}
+
+struct PagedLayout {
+    size_t flags, rec, ml, o, total;
+};
+
+PagedLayout paged_layout(const attn_sdpa_desc_t *d)
+{
+    const PagedShape p = paged_shape(d->h, d->h_kv, d->d, d->s_q);
+    const size_t parts = size_t(p.shares) * 2;
+    PagedLayout L;
+    L.flags = Workspace::align(64 * sizeof(uint32_t));
+    L.rec = L.flags + Workspace::align(size_t(p.shares) * sizeof(uint32_t));
+    L.ml = L.rec + Workspace::align(parts * sizeof(int4));
+    L.o = L.ml + Workspace::align(parts * size_t(p.rows) * sizeof(float2));
+    L.total = L.o + Workspace::align(parts * size_t(p.rows) * size_t(d->d) * sizeof(float));
+    return L;
+}
+
+}  // namespace
+
+attn_status_t paged_cache_workspace_size(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache, size_t *bytes)
+{
+    PagedCache c;
+    const attn_status_t st = check_paged(desc, cache, &c);
+    if (st) return st;
+    if (!bytes) return ATTN_ERR_NULLPTR;
+    *bytes = kPagedCopyBytes;
+    return ATTN_OK;
+}
+
+attn_status_t paged_cache_write(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                                const attn_paged_seqs_t *seqs, attn_view_t k, attn_view_t v, void *workspace,
+                                size_t workspace_bytes, void *stream)
+{
+    return paged_copy_call(true, desc, cache, seqs, k, v, workspace, workspace_bytes, stream);
+}
+
+attn_status_t paged_cache_read(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                               const attn_paged_seqs_t *seqs, attn_view_t k, attn_view_t v, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    return paged_copy_call(false, desc, cache, seqs, k, v, workspace, workspace_bytes, stream);
+}
+
+attn_status_t sdpa_paged_workspace_size(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache, size_t *bytes)
+{
+    PagedCache c;
+    const attn_status_t st = check_paged(desc, cache, &c);
+    if (st) return st;
+    if (!bytes) return ATTN_ERR_NULLPTR;
+    *bytes = paged_layout(desc).total;
+    return ATTN_OK;
+}
+
+attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                             const attn_paged_seqs_t *seqs, attn_view_t q, attn_view_t o, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    PagedAttnArgs a;
+    std::memset(&a, 0, sizeof a);
+    attn_status_t st = check_paged(desc, cache, &a.cache);
+    if (st || (st = check_paged_call(desc, cache, seqs, &a.seqs))) return st;
+    if ((st = check_view(q, a.seqs.tokens)) || (st = check_view(o, a.seqs.tokens))) return st;
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return ATTN_ERR_ALIGN;
+    const PagedLayout L = paged_layout(desc);
+    if ((st = check_ws(workspace, workspace_bytes, L.total))) return st;
+    a.dtype = desc->dtype;
+    a.h = int(desc->h); a.h_kv = int(desc->h_kv); a.d = int(desc->d);
+    a.causal = desc->mask == ATTN_CAUSAL_BOTTOM_RIGHT;
+    a.scale = float(desc->scale);
+    a.q = to_view(q, a.seqs.cu != nullptr); a.o = to_view(o, a.seqs.cu != nullptr);
+    a.lse = lse;
+    char *ws = static_cast<char *>(workspace);
+    a.status = reinterpret_cast<uint32_t *>(ws);
+    a.flags = reinterpret_cast<uint32_t *>(ws + L.flags);
+    a.rec = reinterpret_cast<int4 *>(ws + L.rec);
+    a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
+    a.part_o = reinterpret_cast<float *>(ws + L.o);
+    return cuda_status(launch_paged_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
 // --------------------------------------------------- query / key norm and rotation

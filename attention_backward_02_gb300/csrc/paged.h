@@ -1,0 +1,91 @@
+// paged.h -- argument bundles of the paged key / value cache: its write and read
+// kernels and the attention of new tokens over it.
+#pragma once
+
+#include "plan.h"
+
+namespace attn {
+
+constexpr int kPagedMaxGroup = 128;  // query heads that may share a key / value head
+constexpr int kPagedCtas = 152;      // SMs: a constant, as the workspace size must not depend on a CUDA call
+
+// Pages of k and v (same strides, in elements) and, for e4m3, the fp32 scales of their rows.
+struct PagedCache {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int type;                     // ATTN_F16, ATTN_BF16 or ATTN_E4M3
+    int n_pages, shift;           // page size: 1 << shift tokens
+    int64_t sp, sc_sp;            // stride of a page; within one, offsets fit 32 bits:
+    int sh, ss, sc_sh, sc_ss;     // strides of a head and a token
+};
+
+// Where the sequences and their new tokens lie.
+struct PagedSeqs {
+    const int32_t *table;         // [b] rows of page ids
+    int64_t table_stride;
+    const int32_t *lens;          // [b] tokens cached, the new ones among them
+    const int32_t *cu;            // [b + 1] first rows of the sequences' new tokens (NULL: s_q each)
+    int b, s_q, tokens;           // tokens: rows of all new tokens
+    int cap;                      // most tokens a sequence may have cached
+
+    // First row and number of new tokens of sequence n, in bounds whatever cu holds; *bad is set where that changed them.
+    __host__ __device__ __forceinline__ void rows(int n, int *first, int *m, bool *bad) const
+    {
+        if (!cu) {
+            *first = n * s_q;
+            *m = s_q;
+            return;
+        }
+        const int a = cu[n], e = cu[n + 1];
+        *first = a < 0 ? 0 : (a > tokens ? tokens : a);
+        const int end = e < *first ? *first : (e > tokens ? tokens : e);
+        *m = end - *first;
+        if (*first != a || end != e) *bad = true;
+    }
+    // Its cached tokens, in [0, cap].
+    __host__ __device__ __forceinline__ int len(int n, bool *bad) const
+    {
+        const int l = lens[n], c = l < 0 ? 0 : (l > cap ? cap : l);
+        if (c != l) *bad = true;
+        return c;
+    }
+};
+
+struct PagedCopyArgs {
+    int dtype;
+    int h_kv, d;
+    View k, v;                    // rows of the new tokens
+    PagedCache cache;
+    PagedSeqs seqs;
+    uint32_t *status;
+};
+
+// Workspace of the attention (all offsets 256-byte aligned), for C work shares of R rows:
+//   status uint32[64];  flags uint32[C]   what a share found wrong
+//   rec    int32 [C][8]                   its two partial results' units
+//   ml     f32   [C][2][R][2]             their maxima (log2 units) and sums
+//   o      f32   [C][2][R][d]             their unnormalised outputs
+struct PagedAttnArgs {
+    int dtype;
+    int h, h_kv, d, causal;
+    float scale;
+    View q, o;
+    float *lse;                   // [b][h][s_q], packed [h][tokens]; NULL: not wanted
+    PagedCache cache;
+    PagedSeqs seqs;
+    uint32_t *status, *flags;
+    int4 *rec;
+    float2 *part_ml;
+    float *part_o;
+};
+
+// Rows of a share's partial result and shares, of the kernel that a call with these sizes takes.
+struct PagedShape {
+    int rows, shares;
+};
+PagedShape paged_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q);
+
+cudaError_t launch_paged_copy(const PagedCopyArgs &a, bool write, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedAttnArgs &a, cudaStream_t s);
+
+}  // namespace attn

@@ -16,6 +16,10 @@
  *                           bias table's gradient.
  *   sdpa_relbias_decode     the same attention for one new token per sequence over
  *                           a key / value cache.
+ *   paged_cache_write,      keys and values of new tokens into a paged cache, as they
+ *   paged_cache_read        are or as e4m3 numbers with a scale a row, and back.
+ *   sdpa_paged_fwd          attention of every sequence's new tokens (one, a few, or
+ *                           a long chunk) over what it has in such a cache.
  *   qk_norm_rope_fwd, _bwd  RMS norm of every query / key head with the rotary
  *                           position embedding in the same pass, and its gradient:
  *                           what makes Q and K for the calls above and takes their
@@ -81,7 +85,9 @@ typedef enum {
 #define ATTN_DEV_TIMEOUT      0x1u  /* a bounded barrier wait ran out; the CTA quit */
 #define ATTN_DEV_INDEX_RANGE  0x2u  /* a topk index outside [0, S2_b / block_size), or a
                                        position outside [0, max_pos), or a cache
-                                       length outside [0, s_kv]                      */
+                                       length outside [0, s_kv], or a page id outside
+                                       [0, n_pages), or new tokens' counts that are
+                                       not ascending                                 */
 #define ATTN_DEV_INDEX_DUP    0x4u  /* a block listed twice for one (token, kv head) */
 
 typedef enum { ATTN_F16 = 0, ATTN_BF16 = 1 } attn_dtype_t;
@@ -369,6 +375,80 @@ attn_status_t sdpa_relbias_decode_workspace_size(const attn_sdpa_desc_t *desc, c
 attn_status_t sdpa_relbias_decode(const attn_sdpa_desc_t *desc, const attn_relbias_t *bias, attn_view_t q,
                                   attn_view_t k, attn_view_t v, const int32_t *lens, attn_view_t o, void *workspace,
                                   size_t workspace_bytes, void *stream);
+
+/* A paged key / value cache: pages of page_size tokens in any order, found through
+ * a table.  No counterpart on the pages: it is what a program that serves a model
+ * keeps its keys and values in.  Element (page p, token t, kv head g, i) of k and v
+ * is at p*sp + t*ss + g*sh + i (elements of `type`), its row's scale at p*scale_sp +
+ * t*scale_ss + g*scale_sh.  Strides are not negative; those of k and v are
+ * multiples of 16 bytes, both start on a 16-byte boundary, and a page spans less
+ * than 2^31 elements of each.                                                */
+#define ATTN_E4M3 3
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;  /* ATTN_E4M3: a scale for each row; else ignored  */
+    int type;                  /* the descriptor's dtype, or ATTN_E4M3            */
+    int64_t n_pages;
+    int64_t page_size;         /* 16, 32, 64, 128 or 256                          */
+    int64_t sp, sh, ss;
+    int64_t scale_sp, scale_sh, scale_ss;
+} attn_paged_cache_t;
+
+/* Where the sequences and their new tokens lie, all of it read on the device, so
+ * that a captured call follows a growing cache.  Sequence n has lens[n] tokens
+ * in the cache, its m new ones (the last) among them: new token i stands at position
+ * lens[n] - m + i, and position x lies in page page_table[n*table_stride + x /
+ * page_size].  The new tokens' rows: cu_new NULL: s_q of each sequence, in [b,h,s_q,d]
+ * views.  Else packed views, token row t at t*ss: rows cu_new[n] .. cu_new[n+1] - 1,
+ * of `tokens` in all; rows that belong to no sequence are neither read nor
+ * written.  A new token at a position below 0 (a sequence with more new tokens than
+ * cached ones, padded in front) is not written to the cache, is read back as zeros
+ * and sees no key.  Table entries of pages that hold no needed position are not
+ * read.  Lengths outside [0, s_kv] and counts out of order or range are brought
+ * into range, and they and page ids outside [0, n_pages) set ATTN_DEV_INDEX_RANGE; a
+ * token of such a page is not written, and read as zeros.                    */
+typedef struct {
+    const int32_t *page_table;  /* device [b] rows of table_pages ids             */
+    int64_t table_stride, table_pages;  /* table_pages*page_size >= s_kv          */
+    const int32_t *lens;        /* device [b]                                     */
+    const int32_t *cu_new;      /* device [b + 1], or NULL                        */
+    int64_t tokens;             /* rows of the packed views; ignored without cu_new */
+} attn_paged_seqs_t;
+
+/* The three calls take an attn_sdpa_desc_t in fixed-length mode (its host arrays
+ * NULL): s_kv = the most tokens a sequence may have cached (up to 2^30), s_q = the new
+ * tokens of every sequence or, with cu_new, the most that a sequence is expected to
+ * have (a longer one is computed all the same: it chooses the kernel); h / h_kv <= 128;
+ * mask ATTN_MASK_NONE (a new token sees all of its sequence) or
+ * ATTN_CAUSAL_BOTTOM_RIGHT (up to its own position); deterministic is ignored: the
+ * results are always bitwise reproducible.
+ *
+ * The new tokens' rows of k and v ([b,h_kv,s_q,d] or packed views) into their places of
+ * the cache.  Into ATTN_E4M3, a row x of d elements goes as
+ *   a = max(max |x|, 2^-110), scale = a / 448, code = e4m3(x (448 / a)),
+ * in fp32, codes rounded to nearest even, the maximum over the finite elements (an
+ * infinity becomes the largest code of its sign, a NaN stays one): the row stands for
+ * code * scale.  No two of the call's tokens may have one place.
+ * paged_cache_read: the same rows from the cache, code * scale rounded to dtype.
+ * Workspace of both: paged_cache_workspace_size bytes.                       */
+attn_status_t paged_cache_workspace_size(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache, size_t *bytes);
+attn_status_t paged_cache_write(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                                const attn_paged_seqs_t *seqs, attn_view_t k, attn_view_t v, void *workspace,
+                                size_t workspace_bytes, void *stream);
+attn_status_t paged_cache_read(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                               const attn_paged_seqs_t *seqs, attn_view_t k, attn_view_t v, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Attention of the new tokens over everything their sequences have cached (which
+ * includes their own keys and values: write them first).  q, o: [b,h,s_q,d] or packed
+ * views; lse (fp32, natural log, contiguous): [b][h][s_q] or [h][tokens], or NULL when
+ * it is not wanted.  A new token without a visible key has O = 0, LSE = +inf.  Cached
+ * rows from lens[n] on may hold anything; those of a sequence that a new token does not
+ * see still meet it with weight 0, so they have to be finite.               */
+attn_status_t sdpa_paged_workspace_size(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache, size_t *bytes);
+attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
+                             const attn_paged_seqs_t *seqs, attn_view_t q, attn_view_t o, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /* Norm and rotation of the query and key heads.  Like the relative-bias calls,
  * these have no counterpart on the pages: they are what a model runs between
