@@ -1042,9 +1042,15 @@ struct PagedLayout {
     size_t flags, rec, ml, o, total;
 };
 
-PagedLayout paged_layout(const attn_sdpa_desc_t *d)
+// The kernel a call takes: from 17 rows (new tokens x query heads of a kv head) on the tensor-core one.
+PagedShape paged_shape(const attn_sdpa_desc_t *d)
 {
-    const PagedShape p = paged_shape(d->h, d->h_kv, d->d, d->s_q);
+    if (d->s_q * (d->h / d->h_kv) > 16) return paged_chunk_shape(d->h, d->h_kv, d->s_q);
+    return paged_decode_shape(d->h, d->h_kv, d->d, d->s_q);
+}
+
+PagedLayout paged_layout(const attn_sdpa_desc_t *d, const PagedShape &p)
+{
     const size_t parts = size_t(p.shares) * 2;
     PagedLayout L;
     L.flags = Workspace::align(64 * sizeof(uint32_t));
@@ -1087,7 +1093,8 @@ attn_status_t sdpa_paged_workspace_size(const attn_sdpa_desc_t *desc, const attn
     const attn_status_t st = check_paged(desc, cache, &c);
     if (st) return st;
     if (!bytes) return ATTN_ERR_NULLPTR;
-    *bytes = paged_layout(desc).total;
+    // (a call without tokens or pages takes the other kernel; one of its shares' rows are always fewer)
+    *bytes = paged_layout(desc, paged_shape(desc)).total;
     return ATTN_OK;
 }
 
@@ -1101,8 +1108,11 @@ attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cach
     if (st || (st = check_paged_call(desc, cache, seqs, &a.seqs))) return st;
     if ((st = check_view(q, a.seqs.tokens)) || (st = check_view(o, a.seqs.tokens))) return st;
     if (reinterpret_cast<uintptr_t>(lse) & 3) return ATTN_ERR_ALIGN;
-    const PagedLayout L = paged_layout(desc);
-    if ((st = check_ws(workspace, workspace_bytes, L.total))) return st;
+    PagedShape shape = paged_shape(desc);
+    if ((st = check_ws(workspace, workspace_bytes, paged_layout(desc, shape).total))) return st;
+    // nothing to make a tensor map of: the other kernel writes the status, and reads no page
+    if (shape.chunk && (a.seqs.tokens == 0 || a.cache.n_pages == 0)) shape = paged_decode_shape(desc->h, desc->h_kv, desc->d, 1);
+    const PagedLayout L = paged_layout(desc, shape);
     a.dtype = desc->dtype;
     a.h = int(desc->h); a.h_kv = int(desc->h_kv); a.d = int(desc->d);
     a.causal = desc->mask == ATTN_CAUSAL_BOTTOM_RIGHT;
@@ -1115,7 +1125,9 @@ attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cach
     a.rec = reinterpret_cast<int4 *>(ws + L.rec);
     a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.part_o = reinterpret_cast<float *>(ws + L.o);
-    return cuda_status(launch_paged_decode(a, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = shape.chunk ? launch_paged_chunk(a, shape, s) : launch_paged_decode(a, shape, s);
+    return cuda_status(e != cudaSuccess ? e : launch_paged_join(a, shape, s));
 }
 
 // --------------------------------------------------- query / key norm and rotation

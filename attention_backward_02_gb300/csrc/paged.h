@@ -79,13 +79,20 @@ struct PagedAttnArgs {
     float *part_o;
 };
 
-// Rows of a share's partial result and shares, of the kernel that a call with these sizes takes.
+// The kernel that a call takes: rows of a share's partial result, shares, and how a unit's rows name new tokens and
+// query heads.  A unit has `row_blocks` head blocks to a kv head and `groups` groups of rows; row r of a group is token
+// r / heads and head r % heads of the block, for `tokens` tokens.
 struct PagedShape {
+    bool chunk;                   // paged_chunk.cu (else paged_decode.cu)
     int rows, shares;
+    int groups, tokens, heads, row_blocks;
 };
-PagedShape paged_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q);
+PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q);
+PagedShape paged_chunk_shape(int64_t h, int64_t h_kv, int64_t s_q);
 
 cudaError_t launch_paged_copy(const PagedCopyArgs &a, bool write, cudaStream_t s);
-cudaError_t launch_paged_decode(const PagedAttnArgs &a, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedAttnArgs &a, const PagedShape &shape, cudaStream_t s);
+cudaError_t launch_paged_chunk(const PagedAttnArgs &a, const PagedShape &shape, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedAttnArgs &a, const PagedShape &shape, cudaStream_t s);
 
 }  // namespace attn

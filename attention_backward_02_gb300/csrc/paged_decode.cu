@@ -412,43 +412,44 @@ __global__ void __launch_bounds__(kThreads, decode_blocks(D, ROWS)) paged_decode
     }
 }
 
-// Outputs of the units that several shares hold, a block for every share that holds a unit's first piece: the pieces'
-// maxima, then their sums in order of the shares, groups of D / 8 lanes taking every NG-th row.  The block of share 0
-// gathers the call's status.
-template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int shares)
+// Outputs of the units that several shares hold, a block for every share that holds a unit's first piece and every 16
+// rows: the pieces' maxima, then their sums in order of the shares, D / 8 lanes a row.  The first block gathers the
+// call's status.
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, const PagedShape shape)
 {
     constexpr int LPR = D / 8, NG = kThreads / LPR;
-    const int c0 = blockIdx.x;
+    const int c0 = blockIdx.x, shares = shape.shares, rows = shape.rows;
     pdl_wait();
-    if (c0 == 0) {
+    if (c0 == 0 && blockIdx.y == 0) {
         uint32_t flags = 0;
         for (int k = threadIdx.x; k < shares; k += kThreads) flags |= a.flags[k];
-        flags = __syncthreads_or(flags != 0) ? ATTN_DEV_INDEX_RANGE : 0u;
-        if (threadIdx.x == 0) *a.status = flags;
+        const int range = __syncthreads_or(flags & ATTN_DEV_INDEX_RANGE), timeout = __syncthreads_or(flags & ATTN_DEV_TIMEOUT);
+        if (threadIdx.x == 0) *a.status = (range ? ATTN_DEV_INDEX_RANGE : 0u) | (timeout ? ATTN_DEV_TIMEOUT : 0u);
     }
     const int4 name = a.rec[2 * c0 + 1];
     if (name.w == kNone) return;
     // the shares that hold the rest: up to the one whose first piece ends the unit
     int end = c0 + 1;
     while (end < shares && a.rec[2 * end].w != kEnds) ++end;
-    const int G = a.h / a.h_kv, hb = G < ROWS ? G : ROWS, nrb = (G + ROWS - 1) / ROWS, tokens = ROWS / hb;
-    const int kvh = name.y / nrb, rb = name.y - kvh * nrb;
+    const int G = a.h / a.h_kv, kvh = name.y / shape.row_blocks, block = name.y - kvh * shape.row_blocks;
     bool none = false;
     int first, m;
     a.seqs.rows(name.x, &first, &m, &none);
-    const int g = threadIdx.x / LPR, c = threadIdx.x % LPR * 8;
-    for (int r = g; r < ROWS; r += NG) {
-        const int tok = r / hb, ti = name.z * tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
-        if (tok >= tokens || ti >= m || rb * ROWS + r - tok * hb >= G) continue;
+    const int g = threadIdx.x / LPR, c = threadIdx.x % LPR * 8, group_rows = rows / shape.groups;
+    for (int r = blockIdx.y * 16 + g; r < int(blockIdx.y) * 16 + 16 && r < rows; r += NG) {
+        const int grp = r / group_rows, in = r - grp * group_rows, tok = in / shape.heads;
+        const int x = block * shape.heads + in - tok * shape.heads, head = kvh * G + x;
+        const int ti = (name.z * shape.groups + grp) * shape.tokens + tok;
+        if (tok >= shape.tokens || ti >= m || x >= G) continue;
         float mm = -INFINITY;
         for (int k = c0; k <= end && k < shares; ++k)
-            if (k == c0 || a.rec[2 * k].w != kNone) mm = fmaxf(mm, a.part_ml[(int64_t(k) * 2 + (k == c0)) * ROWS + r].x);
+            if (k == c0 || a.rec[2 * k].w != kNone) mm = fmaxf(mm, a.part_ml[(int64_t(k) * 2 + (k == c0)) * rows + r].x);
         const float ref = mm == -INFINITY ? 0.f : mm;
         float ll = 0.f, o[8] = {};
         for (int k = c0; k <= end && k < shares; ++k) {
             if (k != c0 && a.rec[2 * k].w == kNone) continue;
-            const int64_t row = (int64_t(k) * 2 + (k == c0)) * ROWS + r;
+            const int64_t row = (int64_t(k) * 2 + (k == c0)) * rows + r;
             const float2 x = a.part_ml[row];
             const float4 *src = reinterpret_cast<const float4 *>(a.part_o + row * D + c);
             const float4 u = src[0], v = src[1];
@@ -468,37 +469,44 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     }
 }
 
-constexpr int shares_of(int d, int rows) { return kPagedCtas * decode_blocks(d, rows); }
-
-template <class T, bool kEight, int D, int ROWS> cudaError_t run(const PagedAttnArgs &a, cudaStream_t s)
+template <class T, bool kEight, int D, int ROWS> cudaError_t run(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    constexpr int kShares = shares_of(D, ROWS);
-    const cudaError_t e = launch_kernel(paged_decode_kernel<T, kEight, D, ROWS>, dim3(kShares), dim3(kThreads), 0, s, false, a);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(paged_join_kernel<T, D, ROWS>, dim3(kShares), dim3(kThreads), 0, s, true, a, kShares);
+    return launch_kernel(paged_decode_kernel<T, kEight, D, ROWS>, dim3(unsigned(p.shares)), dim3(kThreads), 0, s, false, a);
 }
 
-template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, int rows, cudaStream_t s)
+template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    if (a.d == 64) return rows == 16 ? run<T, kEight, 64, 16>(a, s) : run<T, kEight, 64, 8>(a, s);
-    return rows == 16 ? run<T, kEight, 128, 16>(a, s) : run<T, kEight, 128, 8>(a, s);
+    if (a.d == 64) return p.rows == 16 ? run<T, kEight, 64, 16>(a, p, s) : run<T, kEight, 64, 8>(a, p, s);
+    return p.rows == 16 ? run<T, kEight, 128, 16>(a, p, s) : run<T, kEight, 128, 8>(a, p, s);
 }
 
 }  // namespace
 
-PagedShape paged_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q)
+PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q)
 {
+    const int group = int(h / h_kv);
     PagedShape p;
-    p.rows = h / h_kv * (s_q < 16 ? s_q : 16) > 8 ? 16 : 8;
-    p.shares = shares_of(int(d), p.rows);
+    p.chunk = false;
+    p.rows = group * (s_q < 16 ? s_q : 16) > 8 ? 16 : 8;
+    p.shares = kPagedCtas * decode_blocks(int(d), p.rows);
+    p.groups = 1;
+    p.heads = group < p.rows ? group : p.rows;
+    p.tokens = p.rows / p.heads;
+    p.row_blocks = (group + p.rows - 1) / p.rows;
     return p;
 }
 
-cudaError_t launch_paged_decode(const PagedAttnArgs &a, cudaStream_t s)
+cudaError_t launch_paged_decode(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    const int rows = paged_shape(a.h, a.h_kv, a.d, a.seqs.s_q).rows;
-    if (a.cache.type == ATTN_E4M3) return a.dtype == ATTN_F16 ? pick<__half, true>(a, rows, s) : pick<__nv_bfloat16, true>(a, rows, s);
-    return a.dtype == ATTN_F16 ? pick<__half, false>(a, rows, s) : pick<__nv_bfloat16, false>(a, rows, s);
+    if (a.cache.type == ATTN_E4M3) return a.dtype == ATTN_F16 ? pick<__half, true>(a, p, s) : pick<__nv_bfloat16, true>(a, p, s);
+    return a.dtype == ATTN_F16 ? pick<__half, false>(a, p, s) : pick<__nv_bfloat16, false>(a, p, s);
+}
+
+cudaError_t launch_paged_join(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
+{
+    auto k = a.d == 64 ? (a.dtype == ATTN_F16 ? paged_join_kernel<__half, 64> : paged_join_kernel<__nv_bfloat16, 64>)
+                       : (a.dtype == ATTN_F16 ? paged_join_kernel<__half, 128> : paged_join_kernel<__nv_bfloat16, 128>);
+    return launch_kernel(k, dim3(unsigned(p.shares), unsigned((p.rows + 15) / 16)), dim3(kThreads), 0, s, true, a, p);
 }
 
 }  // namespace attn

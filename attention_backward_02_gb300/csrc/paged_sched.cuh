@@ -156,7 +156,7 @@ template <int kUnitCost> struct Sched {
 // One CTA's walk over its pieces.
 template <int kUnitCost> struct Walk {
     const Sched<kUnitCost> &sc;
-    Range r;
+    const Range &r;
     int n, x, t;     // the unit at hand
     SeqUnits u;
     int k0, k1, all; // keys of it that are this CTA's, and all
