@@ -658,8 +658,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
     } else if (kEight) {
         // ================================================= e4m3 -> 16 bit (warps 12..15)
         regs_decrease<kRegsConvert>();
-        constexpr int LPR = D / 16, PASS = 128 / LPR, N = HN / PASS;  // lanes of a row, rows of a pass, passes
-        const int wt = threadIdx.x - 384, row = wt / LPR, col = wt % LPR;
+        // a thread's row k of the stage, of which it takes every other 16 bytes from col on: eight lanes eight rows, whose
+        // swizzled 16-byte pieces lie in different banks on both sides
+        constexpr int N = D / 32;
+        const int wt = threadIdx.x - 384, k = wt & 63, col = wt >> 6;
         const float c = a.scale * kLog2e;
         float *scales = reinterpret_cast<float *>(smem + Cfg::OFF_KS);
         bool ok = true;
@@ -679,31 +681,29 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                     const uint8_t *src = smem + Cfg::OFF_E + (2 * es + side) * Cfg::E_BYTES;
                     const float *sizes = reinterpret_cast<const float *>(smem + Cfg::OFF_ES) + (2 * es + side) * HN;
                     uint4 x[N];
-                    float size[N];
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const int k = i * PASS + row;
-                        x[i] = *reinterpret_cast<const uint4 *>(src + k * D + col * 16);
+                        const int c16 = col + 2 * i, at = D == 128 ? c16 ^ (k & 7) : c16 ^ (k >> 1 & 3);
+                        x[i] = *reinterpret_cast<const uint4 *>(src + k * D + at * 16);
                         if (k >= left) x[i] = make_uint4(0, 0, 0, 0);
-                        if (side) size[i] = sizes[k];
                     }
-                    if (!side && wt < HN) scales[n % NKS * HN + wt] = sizes[wt] * c;
+                    const float2 f = make_float2(sizes[k], sizes[k]);
+                    if (!side && wt < HN) scales[n % NKS * HN + wt] = f.x * c;
                     if (n >= uint32_t(NS)) wait(side ? &v_empty[s] : &k_empty[s], par);
                     if (ok) {
-                        const uint32_t dst = smem_u32(side ? sV(s) : sK(s)) + (col >> 2) * HN * 128;
-                        const uint32_t c0 = (col & 3) * 2;  // 16-byte chunk of the 128-byte row
+                        const uint32_t dst = smem_u32(side ? sV(s) : sK(s)) + k * 128;
 #pragma unroll
                         for (int i = 0; i < N; ++i) {
-                            const int k = i * PASS + row;
-                            const float2 f = make_float2(size[i], size[i]);
+                            const int c16 = col + 2 * i;
+                            const uint32_t to = dst + (c16 >> 2) * HN * 128, c0 = (c16 & 3) * 2;  // 16-byte piece of 128 bytes
                             uint32_t y[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const uint32_t u = (e / 2 == 0 ? x[i].x : e / 2 == 1 ? x[i].y : e / 2 == 2 ? x[i].z : x[i].w) >> (16 * (e & 1));
                                 y[e] = side ? widen<T>(u, f) : widen<T>(u);
                             }
-                            st_shared_v4(dst + k * 128 + ((c0 ^ (k & 7)) << 4), y[0], y[1], y[2], y[3]);
-                            st_shared_v4(dst + k * 128 + (((c0 + 1) ^ (k & 7)) << 4), y[4], y[5], y[6], y[7]);
+                            st_shared_v4(to + ((c0 ^ (k & 7)) << 4), y[0], y[1], y[2], y[3]);
+                            st_shared_v4(to + (((c0 + 1) ^ (k & 7)) << 4), y[4], y[5], y[6], y[7]);
                         }
                     }
                     fence_proxy_async_smem();
@@ -739,7 +739,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 
 namespace {
 
-// Pages [n_pages][h_kv][page][d]: boxes of up to 64 tokens x 64 16-bit elements with the 128-byte swizzle, or d e4m3 ones.
+// Pages [n_pages][h_kv][page][d]: boxes of up to 64 tokens x 64 16-bit elements or d e4m3 ones, with the swizzle of the box's
+// width.
 bool tmap_pages(CUtensorMap *m, void *ptr, const PagedCache &c, int dtype, int d, int h_kv)
 {
     auto enc = tmap_encoder();
@@ -753,7 +754,7 @@ bool tmap_pages(CUtensorMap *m, void *ptr, const PagedCache &c, int dtype, int d
     const CUtensorMapDataType type = eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return enc(m, type, 4, ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               eight ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               eight && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
