@@ -21,9 +21,12 @@
 // looks up a page, a stage ahead, and issues its TMA boxes.  16 bits: 64 elements x page
 // rows with the 128-byte swizzle, straight to where the MMA reads them.  e4m3: rows of
 // d bytes to a ring of their own, with their scales (4-byte asynchronous copies), from which a
-// warpgroup makes 16-bit numbers in the swizzled layout: keys unscaled (e4m3 numbers are
-// 16-bit numbers exactly; their scales multiply S's columns), values times their scale,
-// rounded (half a step of the 16-bit type, as V of a 16-bit cache has it).
+// warpgroup makes 16-bit numbers in the swizzled layout.  Keys unscaled, of the queries'
+// type (e4m3 numbers are 16-bit numbers exactly); their scales multiply S's columns.
+// Values as half-precision numbers, times their scale relative to the stage's largest, rounded up
+// to a power of two 2^E: number, factor and product in one multiplication a pair, each
+// rounded by at most half a step of that type.  2^E goes into the weights: P' = exp2(x + E - m)
+// with m over x + E, so that O and l keep one reference; l takes P' 2^-E.
 // A page id out of range reads as zeros.
 //
 // A row's reference maximum m is raised only when a step's maximum exceeds it by more
@@ -68,7 +71,8 @@ template <int D, bool kEight, bool kSplit> struct ChunkCfg {
     static constexpr int OFF_MISC = OFF_BAR + 80 * 8;
     static constexpr int OFF_ML = OFF_MISC + 64;              // [2 groups][m, l][128 rows] floats
     static constexpr int OFF_KS = OFF_ML + 2 * 2 * 128 * 4;   // [NKS][64] floats
-    static constexpr int OFF_RANGE = OFF_KS + (kEight ? NKS * HN * 4 : 0);  // scratch of the range, then the range
+    static constexpr int OFF_KE = OFF_KS + (kEight ? NKS * HN * 4 : 0);   // [NKS] E and 2^-E of the values
+    static constexpr int OFF_RANGE = OFF_KE + (kEight ? NKS * 8 : 0);     // scratch of the range, then the range
     static constexpr int SMEM = OFF_RANGE + 256;
     // at least half the SM's shared memory: one CTA, which holds all of the TMEM, runs per SM
     static constexpr int SMEM_ALLOC = SMEM + 1024 > 116 * 1024 ? SMEM + 1024 : 116 * 1024;
@@ -115,21 +119,25 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// two e4m3 numbers as 16-bit ones: exactly, or times a scale and rounded
-template <class T> __device__ __forceinline__ uint32_t widen(uint32_t e4m3x2)
+// two e4m3 numbers as half-precision ones, and as numbers of type T
+__device__ __forceinline__ uint32_t half_pair(uint32_t e4m3x2)
 {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(e4m3x2)));
+    return h;
+}
+template <class T> __device__ __forceinline__ uint32_t widen(uint32_t e4m3x2)
+{
+    const uint32_t h = half_pair(e4m3x2);
     if (std::is_same<T, __half>::value) return h;
     const float2 y = unpack2<__half>(h);
     return pack2<T>(y.x, y.y);
 }
-template <class T> __device__ __forceinline__ uint32_t widen(uint32_t e4m3x2, float2 scale)
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(e4m3x2)));
-    const float2 y = mul2(unpack2<__half>(h), scale);
-    return pack2<T>(y.x, y.y);
+    uint32_t c;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
 }
 
 }  // namespace
@@ -141,6 +149,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
     constexpr int BM = Cfg::BM, HN = Cfg::HN, NS = Cfg::NS, NE = Cfg::NE, NKS = Cfg::NKS;
     constexpr int kStage = kSplit ? 2 : 1;  // stages of a step
     constexpr int kType = std::is_same<T, __half>::value ? 0 : 1;
+    using P16 = typename std::conditional<kEight, __half, T>::type;  // type of P and V
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
             // one add from values kept in registers, a piece starts at buffer 0 so that buffers are constants of the
             // (two-step) loop body, and phases are bits that flip with each wait.
             constexpr uint32_t idS = idesc_f16(128, HN, kType, 0, 0);
-            constexpr uint32_t idO = idesc_f16(128, D, kType, 0, 1);
+            constexpr uint32_t idO = idesc_f16(128, D, kEight ? 0 : kType, 0, 1);
             constexpr uint32_t STAGE = Cfg::STAGE_BYTES / 16, QROWS = Cfg::TILE_BYTES / 16;  // in descriptor units
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -435,6 +444,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
         const uint32_t tO = tmem + lane_addr + Cfg::T_O + grp * D;
         const float *scales = reinterpret_cast<const float *>(smem + Cfg::OFF_KS);
+        const float2 *sizes = reinterpret_cast<const float2 *>(smem + Cfg::OFF_KE);
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, nullptr);
@@ -469,7 +479,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 s_par ^= 1u << sb;
                 // the row of S (e4m3: in log2 units), masked, and its maximum
                 float x[HN];
-                float mx = -INFINITY;
+                float mx = -INFINITY, vexp = 0.f, vinv = 1.f;  // e4m3: E and 2^-E
                 if (ok) {
                     uint32_t v[2][32];
                     tmem_ld32(tS, v[0]);
@@ -479,6 +489,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 #pragma unroll
                     for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e / 32][e % 32]);
                     if (kEight) {
+                        const float2 size = sizes[stage % NKS];
+                        vexp = size.x;
+                        vinv = size.y;
                         const float4 *f = reinterpret_cast<const float4 *>(scales + (stage % NKS) * HN);
 #pragma unroll
                         for (int e = 0; e < HN; e += 4) {
@@ -501,7 +514,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mq[k] = max3(mq[k], x[e + 2 * k], x[e + 2 * k + 1]);
                     mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
-                    if (!kEight) mx *= c;
+                    mx = kEight ? mx + vexp : mx * c;
                 }
                 const float m_new = fmaxf(m_ref, mx);
                 const bool need = m_new > m_ref + 8.f;  // also the first finite max
@@ -537,7 +550,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 // P = exp2(x - m) over the columns S was read from
                 if (ok) {
                     const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // no visible key yet: every P is 0
-                    const float2 neg2 = make_float2(neg, neg), c2 = make_float2(c, c);
+                    const float2 neg2 = kEight ? make_float2(neg + vexp, neg + vexp) : make_float2(neg, neg), c2 = make_float2(c, c);
                     float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e0 = 0; e0 < HN; e0 += 16) {
@@ -548,13 +561,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                             const float2 t = kEight ? add2(z, neg2) : fma2(z, c2, neg2);
                             const float2 q = make_float2(ex2(t.x), ex2(t.y));
                             l2 = add2(l2, q);
-                            y[e / 2] = pack2<T>(q.x, q.y);
+                            y[e / 2] = pack2<P16>(q.x, q.y);
                         }
                         tmem_st8(tS + e0 / 2, y);
                     }
                     // a step's sum is added with what earlier additions lost: thousands of weights far below the largest
                     // would each be rounded away
-                    const float add = l2.x + l2.y - l_lost, sum = l + add;
+                    const float add = (l2.x + l2.y) * vinv - l_lost, sum = l + add;
                     l_lost = sum - l - add;
                     l = sum;
                     tmem_st_wait();
@@ -664,6 +677,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         const int wt = threadIdx.x - 384, k = wt & 63, col = wt >> 6;
         const float c = a.scale * kLog2e;
         float *scales = reinterpret_cast<float *>(smem + Cfg::OFF_KS);
+        float2 *sizes = reinterpret_cast<float2 *>(smem + Cfg::OFF_KE);
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, nullptr);
@@ -675,11 +689,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
             const Steps st = steps_of(w);
             for (int j = 0; j < st.stages; ++j, ++n) {
                 const int left = w.k1 - (w.k0 + j * HN);  // rows behind: zeros
+                // the values' scales, relative to the power of two at or above the largest
+                wait(&e_full[es], epar);
+                wait(&e_full[NE + es], epar);
+                const float *size = reinterpret_cast<const float *>(smem + Cfg::OFF_ES) + 2 * es * HN;
+                const float most = fmaxf(fabsf(size[HN + lane]), fabsf(size[HN + 32 + lane]));
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(fmaxf(most, 0x1p-100f), 0x1p+100f)));
+                const uint32_t e = (top + 0x7fffffu) >> 23;  // exponent, of bias 127
+                const float down = __uint_as_float((254u - e) << 23);
+                const uint32_t factor = pack2<__half>(size[HN + k] * down, size[HN + k] * down);
+                if (wt < HN) {
+                    scales[n % NKS * HN + wt] = size[wt] * c;
+                    if (wt == 0) sizes[n % NKS] = make_float2(float(int(e) - 127), down);
+                }
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
-                    wait(&e_full[side * NE + es], epar);
                     const uint8_t *src = smem + Cfg::OFF_E + (2 * es + side) * Cfg::E_BYTES;
-                    const float *sizes = reinterpret_cast<const float *>(smem + Cfg::OFF_ES) + (2 * es + side) * HN;
                     uint4 x[N];
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
@@ -687,8 +712,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                         x[i] = *reinterpret_cast<const uint4 *>(src + k * D + at * 16);
                         if (k >= left) x[i] = make_uint4(0, 0, 0, 0);
                     }
-                    const float2 f = make_float2(sizes[k], sizes[k]);
-                    if (!side && wt < HN) scales[n % NKS * HN + wt] = f.x * c;
                     if (n >= uint32_t(NS)) wait(side ? &v_empty[s] : &k_empty[s], par);
                     if (ok) {
                         const uint32_t dst = smem_u32(side ? sV(s) : sK(s)) + k * 128;
@@ -700,7 +723,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const uint32_t u = (e / 2 == 0 ? x[i].x : e / 2 == 1 ? x[i].y : e / 2 == 2 ? x[i].z : x[i].w) >> (16 * (e & 1));
-                                y[e] = side ? widen<T>(u, f) : widen<T>(u);
+                                y[e] = side ? mul_half2(half_pair(u), factor) : widen<T>(u);
                             }
                             st_shared_v4(to + ((c0 ^ (k & 7)) << 4), y[0], y[1], y[2], y[3]);
                             st_shared_v4(to + (((c0 + 1) ^ (k & 7)) << 4), y[4], y[5], y[6], y[7]);

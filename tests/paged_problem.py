@@ -3,9 +3,11 @@ bounds of the attention.
 
 Bounds (h: half a step of the 16-bit type, u = 2^-23).  The exponent of a key's weight is off by at most
 e = (d + 8) u (sum |q k| scale + |s| + |largest s|), the exponential by 2^-21; the weights are rounded to 16 bits
-(h), and in an e4m3 cache values may be too (h); a half-precision weight is also off by 2^-25 of the largest, which
-for e4m3 is relative to the largest value scale rounded up to a power of two:
-    |O err| <= h |O| + sum_j (2 h + 2 max e + 2^-20 + n u) P_j |v_j| + 2^-25 a,   a = sum_j |v_j|, e4m3: 2 (largest scale) sum_j |code_j|
+(h); values of an e4m3 cache may be half-precision numbers times their scale, both rounded (2^-11 each, together g); a
+half-precision weight is also off by 2^-25 of the largest, and such a value by 2^-25 of the largest value scale
+rounded up to a power of two, once for the scale's rounding and once for the product's:
+    |O err| <= h |O| + sum_j (h + g + 2 max e + 2^-20 + n u) P_j |v_j| + 2^-25 a,
+    a = sum_j |v_j|, e4m3: 3 * 2 (largest scale) sum_j max(|code_j|, 1)
     |LSE err| <= max e + 2^-20 + n u + 4 u |LSE|."""
 import numpy as np
 
@@ -131,7 +133,8 @@ class Problem:
             if self.eight:
                 r = self.rows_of[n]
                 code = np.abs(P.E4M3[self.pool[1].reshape(-1, self.hk, self.d)[r].numpy()])
-                tiny = 2 * (self.scales[1].reshape(-1, self.hk)[r].double().numpy().max(0, initial=0)[:, None] * code.sum(0))
+                code = np.where(code > 0, np.maximum(code, 1), 0)
+                tiny = 6 * (self.scales[1].reshape(-1, self.hk)[r].double().numpy().max(0, initial=0)[:, None] * code.sum(0))
             else:
                 tiny = np.abs(v).sum(0)
             tiny = np.repeat(tiny, grp, 0) * 2.0 ** -25
@@ -148,7 +151,7 @@ class Problem:
                     ref, rl, p, mag, s = P.attention(q, k[:upto], v[:upto], self.d ** -0.5, True)
                 e = (self.d + 8) * U * (mag + np.abs(s) + np.abs(s).max(-1, initial=0, keepdims=True))
                 e = e.max(-1, initial=0)
-                w = 2 * hf + 2 * e + 2.0 ** -20 + len(k) * U
+                w = hf + (2.0 ** -10 if self.eight else 0) + 2 * e + 2.0 ** -20 + len(k) * U
                 bound = hf * np.abs(ref) + w[..., None] * np.einsum("mhn,nhd->mhd", p, av[:upto] if self.causal else av) + tiny + 2.0 ** -24
                 err = np.abs(o[rows] - ref)
                 assert np.all(err <= bound), (n, i0, float(np.nanmax(err)), float(np.nanmax(err - bound)), int(np.isnan(err).sum()))
