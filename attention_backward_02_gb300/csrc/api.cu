@@ -986,6 +986,7 @@ attn_status_t check_paged(const attn_sdpa_desc_t *d, const attn_paged_cache_t *c
     out->type = c->type;
     out->n_pages = int(c->n_pages);
     out->shift = shift;
+    out->none = out->n_pages > 0 ? out->n_pages : 1;
     out->sp = c->sp; out->sh = int(c->sh); out->ss = int(c->ss);
     out->sc_sp = eight ? c->scale_sp : 0; out->sc_sh = eight ? int(c->scale_sh) : 0; out->sc_ss = eight ? int(c->scale_ss) : 0;
     return ATTN_OK;
@@ -1042,10 +1043,10 @@ struct PagedLayout {
     size_t flags, rec, ml, o, total;
 };
 
-// The kernel a call takes: from 17 rows (new tokens x query heads of a kv head) on the tensor-core one.
+// The kernel a call takes: from 33 rows (new tokens x query heads of a kv head) on the tensor-core one.
 PagedShape paged_shape(const attn_sdpa_desc_t *d)
 {
-    if (d->s_q * (d->h / d->h_kv) > 16) return paged_chunk_shape(d->h, d->h_kv, d->s_q);
+    if (d->s_q * (d->h / d->h_kv) > 32) return paged_chunk_shape(d->h, d->h_kv, d->s_q);
     return paged_decode_shape(d->h, d->h_kv, d->d, d->s_q);
 }
 
@@ -1093,7 +1094,7 @@ attn_status_t sdpa_paged_workspace_size(const attn_sdpa_desc_t *desc, const attn
     const attn_status_t st = check_paged(desc, cache, &c);
     if (st) return st;
     if (!bytes) return ATTN_ERR_NULLPTR;
-    // (a call without tokens or pages takes the other kernel; one of its shares' rows are always fewer)
+    // (a call without tokens takes the other kernel, whose partial results are always smaller)
     *bytes = paged_layout(desc, paged_shape(desc)).total;
     return ATTN_OK;
 }
@@ -1110,8 +1111,8 @@ attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cach
     if (reinterpret_cast<uintptr_t>(lse) & 3) return ATTN_ERR_ALIGN;
     PagedShape shape = paged_shape(desc);
     if ((st = check_ws(workspace, workspace_bytes, paged_layout(desc, shape).total))) return st;
-    // nothing to make a tensor map of: the other kernel writes the status, and reads no page
-    if (shape.chunk && (a.seqs.tokens == 0 || a.cache.n_pages == 0)) shape = paged_decode_shape(desc->h, desc->h_kv, desc->d, 1);
+    // no queries to make a tensor map of: the other kernel writes the status
+    if (shape.chunk && a.seqs.tokens == 0) shape = paged_decode_shape(desc->h, desc->h_kv, desc->d, 1);
     const PagedLayout L = paged_layout(desc, shape);
     a.dtype = desc->dtype;
     a.h = int(desc->h); a.h_kv = int(desc->h_kv); a.d = int(desc->d);
@@ -1121,6 +1122,7 @@ attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cach
     a.lse = lse;
     char *ws = static_cast<char *>(workspace);
     a.status = reinterpret_cast<uint32_t *>(ws);
+    if (a.cache.n_pages == 0) a.cache.k = a.cache.v = ws;  // (for the tensor maps: an address, which nothing reads)
     a.flags = reinterpret_cast<uint32_t *>(ws + L.flags);
     a.rec = reinterpret_cast<int4 *>(ws + L.rec);
     a.part_ml = reinterpret_cast<float2 *>(ws + L.ml);

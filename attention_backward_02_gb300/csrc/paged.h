@@ -15,6 +15,7 @@ struct PagedCache {
     float *k_scale, *v_scale;
     int type;                     // ATTN_F16, ATTN_BF16 or ATTN_E4M3
     int n_pages, shift;           // page size: 1 << shift tokens
+    int none;                     // a page coordinate out of every range: max(n_pages, 1)
     int64_t sp, sc_sp;            // stride of a page; within one, offsets fit 32 bits:
     int sh, ss, sc_sh, sc_ss;     // strides of a head and a token
 };

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                     if (lane == 0) mbar_arrive_expect_tx(&full[s], kEight ? Cfg::E_BYTES : Cfg::STAGE_BYTES);
                     __syncwarp();
                     if (lane < boxes) {
-                        const int page = good ? id : cache.n_pages;  // (out of range: zeros)
+                        const int page = good ? id : cache.none;  // (out of range: zeros)
                         if (kEight) {
                             tma_load_4d(smem + Cfg::OFF_E + (2 * s + !isk) * Cfg::E_BYTES + lane * pr * D, tm, &full[s], 0,
                                         key & in_page, w.x, page);
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                     a.part_ml[part] = make_float2(m, l);
                 else if (a.lse)
                     a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + w.u.first + ti : (int64_t(w.n) * a.h + head) * a.seqs.s_q + ti] =
-                        l == 0.f ? INFINITY : (m + __log2f(l)) / kLog2e;
+                        lse_of(m, l);
             }
             k_base += st.stages;
             // the next piece's first product overwrites O once this group's P of it is there, which is behind these
@@ -770,7 +770,7 @@ bool tmap_pages(CUtensorMap *m, void *ptr, const PagedCache &c, int dtype, int d
     if (!enc) return false;
     const bool eight = c.type == ATTN_E4M3;
     const int page = 1 << c.shift, size = eight ? 1 : 2;
-    cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(h_kv), cuuint64_t(c.n_pages)};
+    cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(h_kv), cuuint64_t(c.none)};
     cuuint64_t strides[3] = {cuuint64_t(c.ss) * size, cuuint64_t(c.sh) * size, cuuint64_t(c.sp) * size};
     cuuint32_t box[4] = {cuuint32_t(eight ? d : 64), cuuint32_t(page < 64 ? page : 64), 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};

@@ -7,14 +7,17 @@
 //   s_j = scale q.k_j over the keys j <= its position,  O = sum_j exp(s_j) v_j / sum_j exp(s_j).
 //
 // Bound by HBM: every cached key and value is read once a row block against 4 d ROWS
-// operations.  A CTA takes its range of keys, four warps striding over it 16 keys (e4m3:
-// 2 x 16) at a time.  Both products are mma.sync m16n8k16, which keeps the operations off
-// the critical path; the tcgen05 path would need the tile staged through shared memory.
-// S = Q K^T has the rows as its rows; its accumulator is, as it stands, the second operand
-// of O^T = V^T P^T, whose rows are head dims and whose eight columns are rows of S.  K and V
-// go from global memory to registers as 16-byte loads that are operand fragments as they
-// stand: the order of the contraction over d is free, so a lane's 16 bytes of a key serve
-// several steps, and V's key pairs are joined by byte permutes.
+// operations.  A CTA takes its range of keys in stages of 64, which a producing warp brings into a
+// ring in shared memory by TMA (a lane looks up a page, a stage ahead, and issues its
+// boxes), so that loads run under the arithmetic and over the ends of pieces; four warps (32 rows: four pairs)
+// take 16 keys of a stage each.  Both products are mma.sync m16n8k16, which keeps the
+// operations off the critical path.  S = Q K^T has the rows as its rows; its accumulator is, as it
+// stands, the second operand of O^T = V^T P^T, whose rows are head dims and whose eight
+// columns are rows of S.  The operands are 16-byte reads of shared memory as they stand: the order of the
+// contraction over d is free, so a lane's 16 bytes of a key serve several steps, and V's key
+// pairs are joined by byte permutes.  Keys lie in blocks of 64 bytes a row, in which the eight lanes of a
+// read take two whole rows; values in rows of 128 bytes with the 128-byte swizzle, in which they take
+// pieces of four rows: neither has bank conflicts (values of 64 e4m3 numbers have two-way ones).
 //
 // e4m3: a number is a half-precision number exactly, one conversion a pair, so both products
 // are of that type whatever the queries' is.  bf16 queries are scaled by a power of two per row that
@@ -29,16 +32,54 @@
 
 #include "paged.h"
 #include "paged_sched.cuh"
+#include "sm103.cuh"
+#include "tc_util.cuh"
+#include "tmap.h"
 
 namespace attn {
-namespace {
 
 using namespace paged;
+using namespace sm103;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+namespace {
+
 constexpr int kKeys = 16;        // keys of a warp's product
+constexpr int kStage = 64;       // keys of a stage
+constexpr int kKeyWarps = kStage / kKeys;
 constexpr int kUnitCost = 128;   // what a unit's start and end take, in keys
+constexpr int kJoin = 128;       // threads of the join
+
+// CTAs an SM holds: set by a lane's registers (Q, sums) and the rings.
+constexpr int decode_blocks(int d, int rows) { return rows == 8 ? (d == 64 ? 4 : 3) : rows == 16 ? (d == 64 ? 3 : 2) : d == 64 ? 2 : 1; }
+
+template <int D, bool kEight, int ROWS> struct DecodeCfg {
+    static constexpr int RW = ROWS > 16 ? ROWS / 16 : 1;   // warps that share 16 keys, each with 8 or 16 of the rows
+    static constexpr int NR = ROWS / RW / 8;               // rows of a lane
+    static constexpr int CONSUMERS = 32 * kKeyWarps * RW, THREADS = CONSUMERS + 32;
+    static constexpr int ESIZE = kEight ? 1 : 2;
+    static constexpr int SIDE = kStage * D * ESIZE;        // keys, or values, of a stage
+    static constexpr int O_BYTES = 2 * ROWS * D * 4;       // [2][ROWS][D] floats
+    static constexpr int BLOCKS = decode_blocks(D, ROWS);
+    static constexpr int OTHER = O_BYTES + 2 * kKeyWarps * ROWS * 4 + 512 + 1024;
+    static constexpr int STAGE = 2 * SIDE + (kEight ? 2 * kStage * 4 : 0) + 16;
+    static constexpr int FIT = ((227 * 1024 / BLOCKS - 1024) - OTHER) / STAGE;
+    static constexpr int NST = FIT > 12 ? 12 : FIT;
+    static_assert(NST >= 2, "a ring of two stages");
+    static constexpr int OFF_V = NST * SIDE;               // after the ring of keys
+    static constexpr int OFF_SCALE = OFF_V + NST * SIDE;   // [NST][keys, values][64]
+    static constexpr int OFF_O = OFF_SCALE + (kEight ? NST * 2 * kStage * 4 : 0);
+    static constexpr int OFF_M = OFF_O + O_BYTES;          // [key warp][ROWS] maxima, then sums
+    static constexpr int OFF_BAR = OFF_M + 2 * kKeyWarps * ROWS * 4;
+    static constexpr int OFF_MISC = OFF_BAR + 2 * NST * 8;
+    static constexpr int OFF_RANGE = OFF_MISC + 16;        // scratch of the range
+    static constexpr int SMEM = OFF_RANGE + (THREADS / 32 + 5) * 8 + 1024;
+    static_assert(SMEM <= 227 * 1024 / BLOCKS - 1024, "shared memory budget");
+};
+
+struct DecodeParams {
+    CUtensorMap tm_k, tm_v;
+    PagedAttnArgs a;
+};
 
 __device__ __forceinline__ float ex2f(float x)
 {
@@ -47,18 +88,16 @@ __device__ __forceinline__ float ex2f(float x)
     return y;
 }
 
-// 16 (8) bytes of the cache: read once, not kept in L1
-__device__ __forceinline__ uint4 load16(const void *p)
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ uint4 load8(const void *p)
+__device__ __forceinline__ uint4 lds8(uint32_t addr)
 {
     uint4 v = make_uint4(0, 0, 0, 0);
-    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
 }
 
@@ -68,6 +107,17 @@ __device__ __forceinline__ uint32_t to_half2(uint32_t e4m3x2)
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(e4m3x2)));
     return h;
+}
+
+// 4 bytes, global to shared, asynchronous (zeros where `on` is false; the address is then not read)
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src, bool on)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+// One arrival on the barrier once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // c += a b for a 16 x 16 a (rows lane / 4 and lane / 4 + 8) and a 16 x 8 b
@@ -85,9 +135,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint32_t part(const uint4 &u, int k) { return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w; }
 
-// Registers of a lane (K and V in flight, Q, sums) set the CTAs an SM holds.
-constexpr int decode_blocks(int d, int rows) { return d == 64 ? 4 : rows == 8 ? 3 : 2; }
-
 // A power of two that brings |x| <= most to 2^14 .. 2^15.
 __device__ __forceinline__ float half_range(float most)
 {
@@ -95,335 +142,446 @@ __device__ __forceinline__ float half_range(float most)
     return __uint_as_float((127u + 14u + 127u - e) << 23);
 }
 
-// ROWS: rows of a unit, 8 (the second half of S's rows is zero and never looked at) or 16.
+// ROWS: rows of a unit, 8 (the second half of S's rows is zero and never looked at), 16 or 32.
 template <class T, bool kEight, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads, decode_blocks(D, ROWS)) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a)
+__global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg<D, kEight, ROWS>::BLOCKS)
+    paged_decode_kernel(const __grid_constant__ DecodeParams p)
 {
+    using Cfg = DecodeCfg<D, kEight, ROWS>;
     using M = typename std::conditional<kEight, __half, T>::type;  // the products' type
     constexpr int NQ = D / 8;                // 32-bit words of a query row in a lane
     constexpr int NE = D / 16;               // products of O^T
-    constexpr int NR = ROWS / 8;             // rows of a lane
-    constexpr int SUB = kEight ? 2 : 1;      // blocks of 16 keys a step
-    constexpr int KL = kEight ? D / 64 : D / 32, VL = kEight ? 1 : D / 64;  // loads of a key, of a value
-    constexpr int kStep = kWarps * kKeys * SUB;
-    __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-    __shared__ float sm_o[kWarps][ROWS][D];
-    __shared__ int64_t scratch[kWarps + 5];
+    constexpr int NR = Cfg::NR, RW = Cfg::RW, NST = Cfg::NST;
+    constexpr int KL = D * Cfg::ESIZE / 64;  // reads of a key
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR), *empty = full + NST;
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC);
+    volatile int *bad_page = abort + 1;
+    const PagedAttnArgs &a = p.a;
+    const PagedCache &cache = a.cache;
 
     pdl_trigger();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        *bad_page = 0;
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&full[s], kEight ? 1 + 32 : 1);  // the boxes, and the scales of each lane
+            mbar_init(&empty[s], kKeyWarps * RW);
+        }
+        fence_mbar_init();
+    }
     const int G = a.h / a.h_kv, hb = G < ROWS ? G : ROWS, nrb = (G + ROWS - 1) / ROWS;
     const Sched<kUnitCost> sched = {a.seqs, ROWS / hb, a.h_kv * nrb, a.causal};
     bool bad = false;
-    const Range range = sched.range<kThreads, kStep, kStep, 2 * kUnitCost>(blockIdx.x, gridDim.x, scratch, &bad);
-    if (blockIdx.x != 0) bad = false;  // one CTA reports the lengths
-    const float sc = a.scale * kLog2e;
-    const PagedCache &cache = a.cache;
-    const int esize = kEight ? 1 : 2;
+    const Range range = sched.range<Cfg::THREADS, kStage, kStage, 2 * kUnitCost>(
+        blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(smem + Cfg::OFF_RANGE), &bad);  // (two barriers inside)
+    if (bad && blockIdx.x == 0) *bad_page = 1;  // (one CTA reports the lengths)
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {  // the whole warp
+        if (ok && !(ok = mbar_wait(bar, parity, abort))) tc::flag_abort(abort, nullptr);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    uint32_t s = 0, par = 0;  // ring position and phase
 
-    int4 named[2] = {unit_name(0, 0, 0, kNone), unit_name(0, 0, 0, kNone)};
-    Walk<kUnitCost> w(sched, range);
-    while (w.next()) {
-        const int kvh = w.x / nrb, rb = w.x - kvh * nrb;
-        // ---- the lane's rows: query words, last visible key, factor of the scores
-        uint32_t qa[NR][NQ];
-        int lim[NR];
-        float fs[NR];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int r = g + 8 * i, tok = r / hb, ti = w.t * sched.tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
-            const bool on = tok < sched.tokens && ti < w.u.m && rb * ROWS + r - tok * hb < G;
-            lim[i] = !on ? -1 : a.causal ? w.u.len - w.u.m + ti : w.u.len - 1;
-            const int64_t row = a.seqs.cu ? int64_t(w.u.first + ti) * a.q.ss : w.n * a.q.sb + ti * a.q.ss;
-            const T *p = static_cast<const T *>(a.q.ptr) + row + head * a.q.sh;
-            // 16-bit caches: 8 elements from 32 n + 8 q on; e4m3: 16 from 64 n + 16 q on
-#pragma unroll
-            for (int n = 0; n < NQ / 4; ++n) {
-                const int at = kEight ? 64 * (n / 2) + 16 * q + 8 * (n % 2) : 32 * n + 8 * q;
-                const uint4 v = on ? *reinterpret_cast<const uint4 *>(p + at) : make_uint4(0, 0, 0, 0);
-                qa[i][4 * n] = v.x; qa[i][4 * n + 1] = v.y; qa[i][4 * n + 2] = v.z; qa[i][4 * n + 3] = v.w;
-            }
-            fs[i] = sc;
-            if (kEight && !std::is_same<T, __half>::value) {
-                float most = 0.f;
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    const float2 y = unpack2<T>(qa[i][n]);
-                    most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
-                }
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                const float up = half_range(most);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    const float2 y = unpack2<T>(qa[i][n]);
-                    qa[i][n] = pack2<__half>(y.x * up, y.y * up);
-                }
-                fs[i] = sc / up;
-            }
+    if (warp == kKeyWarps * RW) {
+        // ================================================= producer
+        const int in_page = (1 << cache.shift) - 1, pr = cache.shift < 6 ? 1 << cache.shift : kStage;  // keys of a box
+        const int boxes = kStage / pr;
+        if (lane == 0) {
+            prefetch_tmap(&p.tm_k);
+            prefetch_tmap(&p.tm_v);
         }
-
-        float m[NR], l[NR], vmax = 0x1p-120f;  // vmax: a power of two, at least every value scale so far
-        float acc[NR][NE][4];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < NE; ++e) acc[i][e][0] = acc[i][e][1] = acc[i][e][2] = acc[i][e][3] = 0.f;
-        }
-        const int32_t *table = a.seqs.table + w.n * a.seqs.table_stride;
-        const char *kp = static_cast<const char *>(cache.k) + int64_t(kvh) * cache.sh * esize;
-        const char *vp = static_cast<const char *>(cache.v) + int64_t(kvh) * cache.sh * esize;
-        const float *sp = lane < 16 ? cache.k_scale : cache.v_scale;
-        auto page_of = [&](int key) -> int { return key < w.k1 ? table[key >> cache.shift] : -1; };
-
-        int base = w.k0 + warp * kKeys * SUB;
-        int id[SUB];
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) id[u] = page_of(base + u * kKeys);
-        for (; base < w.k1; base += kStep) {
-            uint4 kr[SUB][2][KL], vr[SUB][4][VL];
-            float size[SUB];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                const int kb = base + u * kKeys, tok = kb & ((1 << cache.shift) - 1);
-                int left = w.k1 - kb < kKeys ? w.k1 - kb : kKeys;
-                if (id[u] < 0 || id[u] >= cache.n_pages) {  // such a page reads as zeros
-                    bad |= left > 0;
-                    left = 0;
+        uint32_t n_stage = 0;
+        Walk<kUnitCost> w(sched, range);
+        while (ok && w.next()) {
+            const int kvh = w.x / nrb;
+            const int32_t *table = a.seqs.table + w.n * a.seqs.table_stride;
+            auto page_of = [&](int k) -> int {
+                const int key = k + lane * pr;
+                return lane < boxes && key < w.k1 ? table[key >> cache.shift] : -1;
+            };
+            int id = page_of(w.k0);
+            for (int k0 = w.k0; k0 < w.k1; k0 += kStage) {
+                const int next = page_of(k0 + kStage);
+                if (n_stage >= uint32_t(NST)) wait(&empty[s], par ^ 1);
+                if (!ok) break;
+                ++n_stage;
+                const int key = k0 + lane * pr;
+                const bool good = id >= 0 && id < cache.n_pages;
+                if (!good && lane < boxes && key < w.k1) *bad_page = 1;
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * Cfg::SIDE);
+                __syncwarp();
+                if (lane < boxes) {
+                    const int page = good ? id : cache.none;  // (out of range: zeros)
+                    uint8_t *kd = smem + s * Cfg::SIDE + lane * pr * 64, *vd = smem + Cfg::OFF_V + s * Cfg::SIDE;
+                    for (int c = 0; c < KL; ++c)
+                        tma_load_4d(kd + c * kStage * 64, &p.tm_k, &full[s], c * 64 / Cfg::ESIZE, key & in_page, kvh, page);
+                    if (D * Cfg::ESIZE == 64)
+                        tma_load_4d(vd + lane * pr * 64, &p.tm_v, &full[s], 0, key & in_page, kvh, page);
+                    else
+                        for (int c = 0; c < KL / 2; ++c)
+                            tma_load_4d(vd + c * kStage * 128 + lane * pr * 128, &p.tm_v, &full[s], c * 128 / Cfg::ESIZE, key & in_page,
+                                        kvh, page);
                 }
-                const int64_t page = id[u] * cache.sp;
-                const char *kb0 = kp + (page + (tok + g) * cache.ss) * esize;
-                const char *vb0 = vp + (page + (tok + 2 * q) * cache.ss) * esize;
+                if (kEight) {  // scales of keys lane and lane + 32; 0 behind the piece's end
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int n = 0; n < KL; ++n)
-                        kr[u][t][n] = 8 * t + g < left ? load16(kb0 + 8 * t * cache.ss * esize + 64 * n + 16 * q) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = (i & 1) + 8 * (i >> 1);
-#pragma unroll
-                    for (int j = 0; j < VL; ++j) {
-                        const char *p = vb0 + key * cache.ss * esize;
-                        vr[u][i][j] = !(2 * q + key < left) ? make_uint4(0, 0, 0, 0)
-                                      : !kEight            ? load16(p + 128 * j + 16 * g)
-                                      : D == 128           ? load16(p + 16 * g)
-                                                           : load8(p + 8 * g);
+                    for (int e = 0; e < 4; ++e) {
+                        const float *scale = e < 2 ? cache.k_scale : cache.v_scale;
+                        const int x = lane + 32 * (e & 1), pg = __shfl_sync(0xffffffffu, good ? id : -1, x / pr);
+                        const bool on = pg >= 0 && k0 + x < w.k1;
+                        copy4(smem_u32(smem + Cfg::OFF_SCALE) + ((2 * s + e / 2) * kStage + x) * 4,
+                              on ? scale + pg * cache.sc_sp + (kvh * cache.sc_sh + ((k0 + x) & in_page) * cache.sc_ss) : scale, on);
                     }
+                    copies_arrive(&full[s]);
                 }
-                size[u] = 0.f;
-                if (kEight && lane % 16 < left)
-                    size[u] = __ldg(sp + id[u] * cache.sc_sp + (kvh * cache.sc_sh + (tok + lane % 16) * cache.sc_ss));
+                id = next;
+                if (++s == NST) {
+                    s = 0;
+                    par ^= 1;
+                }
             }
+        }
+        // (a CTA does not end before its copies: the consumers wait for every stage, or, if they gave up, this warp does)
+        if (!ok && lane == 0) {
+            volatile int never = 0;
+            for (uint32_t j = n_stage > uint32_t(NST) ? n_stage - NST : 0; j < n_stage; ++j)
+                mbar_wait(&full[j % NST], (j / NST) & 1, &never, 100000000ull);
+        }
+    } else {
+        // ================================================= consumers
+        const int g = lane / 4, q = lane % 4, kw = warp / RW, rw = warp % RW;
+        const float sc = a.scale * kLog2e;
+        float *sm_m = reinterpret_cast<float *>(smem + Cfg::OFF_M), *sm_l = sm_m + kKeyWarps * ROWS;
+        float *sm_o = reinterpret_cast<float *>(smem + Cfg::OFF_O);
+        int4 named0 = unit_name(0, 0, 0, kNone), named1 = named0;
+        auto sync = []() { named_bar_sync(1, Cfg::CONSUMERS); };
+        Walk<kUnitCost> w(sched, range);
+        while (w.next()) {
+            const int kvh = w.x / nrb, rb = w.x - kvh * nrb;
+            // ---- the lane's rows: query words, last visible key, factor of the scores
+            uint32_t qa[NR][NQ];
+            int lim[NR];
+            float fs[NR];
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) id[u] = page_of(base + kStep + u * kKeys);
+            for (int i = 0; i < NR; ++i) {
+                const int r = rw * 16 + g + 8 * i, tok = r / hb, ti = w.t * sched.tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
+                const bool on = tok < sched.tokens && ti < w.u.m && rb * ROWS + r - tok * hb < G;
+                lim[i] = !on ? -1 : a.causal ? w.u.len - w.u.m + ti : w.u.len - 1;
+                const int64_t row = a.seqs.cu ? int64_t(w.u.first + ti) * a.q.ss : w.n * a.q.sb + ti * a.q.ss;
+                const T *src = static_cast<const T *>(a.q.ptr) + row + head * a.q.sh;
+                // 16-bit caches: 8 elements from 32 n + 8 q on; e4m3: 16 from 64 n + 16 q on
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                const int kb = base + u * kKeys;
-                if (u > 0 && kb >= w.k1) break;
-                // scores: lane (g, q) gets rows g, g + 8 and keys 2q, 2q + 1 of both tiles
-                float s[2][4];
+                for (int n = 0; n < NQ / 4; ++n) {
+                    const int at = kEight ? 64 * (n / 2) + 16 * q + 8 * (n % 2) : 32 * n + 8 * q;
+                    const uint4 v = on ? *reinterpret_cast<const uint4 *>(src + at) : make_uint4(0, 0, 0, 0);
+                    qa[i][4 * n] = v.x; qa[i][4 * n + 1] = v.y; qa[i][4 * n + 2] = v.z; qa[i][4 * n + 3] = v.w;
+                }
+                fs[i] = sc;
+                if (kEight && !std::is_same<T, __half>::value) {
+                    float most = 0.f;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                    for (int n = 0; n < NQ; ++n) {
+                        const float2 y = unpack2<T>(qa[i][n]);
+                        most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
+                    }
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    const float up = half_range(most);
 #pragma unroll
-                    for (int n = 0; n < NQ / 2; ++n) {
-                        uint32_t b0, b1;
-                        if (kEight) {
-                            const uint32_t x = part(kr[u][t][n / 4], n % 4);
-                            b0 = to_half2(x);
-                            b1 = to_half2(x >> 16);
-                        } else {
-                            b0 = part(kr[u][t][n / 2], 2 * (n % 2));
-                            b1 = part(kr[u][t][n / 2], 2 * (n % 2) + 1);
+                    for (int n = 0; n < NQ; ++n) {
+                        const float2 y = unpack2<T>(qa[i][n]);
+                        qa[i][n] = pack2<__half>(y.x * up, y.y * up);
+                    }
+                    fs[i] = sc / up;
+                }
+            }
+
+            float m[NR], l[NR], vmax = 0x1p-120f;  // vmax: a power of two, at least every value scale so far
+            float acc[NR][NE][4];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) acc[i][e][0] = acc[i][e][1] = acc[i][e][2] = acc[i][e][3] = 0.f;
+            }
+
+            for (int k0 = w.k0; k0 < w.k1; k0 += kStage) {
+                const int kb = k0 + kw * kKeys;  // this warp's keys
+                const int left = w.k1 - kb < kKeys ? w.k1 - kb : kKeys;
+                wait(&full[s], par);
+                const uint32_t ks = smem_u32(smem) + s * Cfg::SIDE + kw * kKeys * 64;
+                const uint32_t vs = smem_u32(smem) + Cfg::OFF_V + s * Cfg::SIDE;
+                if (ok && left > 0) {
+                    // scores: lane (g, q) gets rows g, g + 8 and keys 2q, 2q + 1 of both tiles
+                    float sa[2][4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        uint4 kr[KL];
+#pragma unroll
+                        for (int n = 0; n < KL; ++n) kr[n] = lds16(ks + n * kStage * 64 + (8 * t + g) * 64 + 16 * q);
+                        sa[t][0] = sa[t][1] = sa[t][2] = sa[t][3] = 0.f;
+#pragma unroll
+                        for (int n = 0; n < NQ / 2; ++n) {
+                            uint32_t b0, b1;
+                            if (kEight) {
+                                const uint32_t x = part(kr[n / 4 % KL], n % 4);
+                                b0 = to_half2(x);
+                                b1 = to_half2(x >> 16);
+                            } else {
+                                b0 = part(kr[n / 2 % KL], 2 * (n % 2));
+                                b1 = part(kr[n / 2 % KL], 2 * (n % 2) + 1);
+                            }
+                            mma16816<M>(sa[t], qa[0][2 * n], NR > 1 ? qa[NR - 1][2 * n] : 0u, qa[0][2 * n + 1],
+                                        NR > 1 ? qa[NR - 1][2 * n + 1] : 0u, b0, b1);
                         }
-                        mma16816<M>(s[t], qa[0][2 * n], NR > 1 ? qa[NR - 1][2 * n] : 0u, qa[0][2 * n + 1],
-                                    NR > 1 ? qa[NR - 1][2 * n + 1] : 0u, b0, b1);
                     }
-                }
-                float ks[4], vs[4];  // scales of the lane's keys
-                if (kEight) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = 8 * (e >> 1) + 2 * q + (e & 1);
-                        ks[e] = __shfl_sync(0xffffffffu, size[u], key);
-                        vs[e] = __shfl_sync(0xffffffffu, size[u], 16 + key);
-                    }
-                }
-                float x[NR][4], mx[NR];
-                bool raise = false;
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    mx[i] = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = kb + 8 * (e >> 1) + 2 * q + (e & 1);
-                        const float f = kEight ? fs[i] * ks[e] : fs[i];
-                        // (behind k1 the keys are another CTA's, or hidden from all rows)
-                        x[i][e] = key <= lim[i] && key < w.k1 ? s[e >> 1][2 * i + (e & 1)] * f : -INFINITY;
-                        mx[i] = fmaxf(mx[i], x[i][e]);
-                    }
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-                    raise |= mx[i] > m[i];
-                }
-                float vm = 0.f;
-                if (kEight) {
-                    vm = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-                    raise |= vm > vmax;
-                }
-                if (__any_sync(0xffffffffu, raise)) {
-                    float fv = 1.f;
+                    float fk[4], fv[4];  // scales of the lane's keys
                     if (kEight) {
-                        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-                        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-                        if (vm > vmax) {  // the next power of two
-                            const float up = __uint_as_float((__float_as_uint(fminf(vm, 0x1p+126f)) + 0x7fffffu) & 0xff800000u);
-                            fv = vmax / up;
-                            vmax = up;
+                        const float *size = reinterpret_cast<const float *>(smem + Cfg::OFF_SCALE) + 2 * s * kStage + kw * kKeys + 2 * q;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const float2 x = *reinterpret_cast<const float2 *>(size + 8 * t);
+                            const float2 y = *reinterpret_cast<const float2 *>(size + kStage + 8 * t);
+                            fk[2 * t] = x.x; fk[2 * t + 1] = x.y; fv[2 * t] = y.x; fv[2 * t + 1] = y.y;
                         }
+                    }
+                    float x[NR][4], mx[NR];
+                    bool raise = false;
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        mx[i] = -INFINITY;
+                        // (behind k1 the keys are another CTA's, or hidden from all rows)
+                        const int last = lim[i] < w.k1 - 1 ? lim[i] - kb : w.k1 - 1 - kb;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float f = kEight ? fs[i] * fk[e] : fs[i];
+                            x[i][e] = 8 * (e >> 1) + 2 * q + (e & 1) <= last ? sa[e >> 1][2 * i + (e & 1)] * f : -INFINITY;
+                            mx[i] = fmaxf(mx[i], x[i][e]);
+                        }
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                        raise |= mx[i] > m[i];
+                    }
+                    float vm = 0.f;
+                    if (kEight) {
+                        vm = fmaxf(fmaxf(fv[0], fv[1]), fmaxf(fv[2], fv[3]));
+                        raise |= vm > vmax;
+                    }
+                    if (__any_sync(0xffffffffu, raise)) {
+                        float fr = 1.f;
+                        if (kEight) {
+                            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+                            if (vm > vmax) {  // the next power of two
+                                const float up = __uint_as_float((__float_as_uint(fminf(vm, 0x1p+126f)) + 0x7fffffu) & 0xff800000u);
+                                fr = vmax / up;
+                                vmax = up;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < NR; ++i) {
+                            const float nm = fmaxf(m[i], mx[i]);
+                            const float f = nm == -INFINITY ? 1.f : ex2f(m[i] - nm);
+                            m[i] = nm;
+                            l[i] *= f;
+                            // (the accumulator holds rows 2 q and 2 q + 1 of the eight)
+                            const float f0 = __shfl_sync(0xffffffffu, f, 8 * q) * fr, f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4) * fr;
+#pragma unroll
+                            for (int e = 0; e < NE; ++e) {
+                                acc[i][e][0] *= f0;
+                                acc[i][e][1] *= f1;
+                                acc[i][e][2] *= f0;
+                                acc[i][e][3] *= f1;
+                            }
+                        }
+                    }
+                    // P, rounded (see above) for the product with V; its sum is taken before
+                    uint32_t pa[2][2] = {{0u, 0u}, {0u, 0u}};  // [key tile][row]
+                    if (kEight) {
+                        const float down = __uint_as_float((254u << 23) - __float_as_uint(vmax));  // 1 / vmax
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) fv[e] *= down;
                     }
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
-                        const float nm = fmaxf(m[i], mx[i]);
-                        const float f = nm == -INFINITY ? 1.f : ex2f(m[i] - nm);
-                        m[i] = nm;
-                        l[i] *= f;
-                        // (the accumulator holds rows 2 q and 2 q + 1 of the eight)
-                        const float f0 = __shfl_sync(0xffffffffu, f, 8 * q) * fv, f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4) * fv;
+                        const float ref = m[i] == -INFINITY ? 0.f : m[i];
+                        float e4[4];
 #pragma unroll
-                        for (int e = 0; e < NE; ++e) {
-                            acc[i][e][0] *= f0;
-                            acc[i][e][1] *= f1;
-                            acc[i][e][2] *= f0;
-                            acc[i][e][3] *= f1;
+                        for (int e = 0; e < 4; ++e) e4[e] = ex2f(x[i][e] - ref);
+                        l[i] += (e4[0] + e4[1]) + (e4[2] + e4[3]);
+                        if (kEight) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) e4[e] *= fv[e];
+                        }
+                        pa[0][i] = pack2<M>(e4[0], e4[1]);
+                        pa[1][i] = pack2<M>(e4[2], e4[3]);
+                    }
+                    // values of keys 2 q, 2 q + 1 (and + 8), head dims by g
+#pragma unroll
+                    for (int j = 0; j < (KL > 2 ? 2 : 1); ++j) {  // blocks of 128 bytes
+                        uint4 vr[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = 2 * q + (i & 1) + 8 * (i >> 1), row = kw * kKeys + key;
+                            if (D * Cfg::ESIZE == 64) vr[i] = lds8(vs + row * 64 + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
+                            else vr[i] = lds16(vs + j * kStage * 128 + row * 128 + ((g ^ (row & 7)) << 4));
+                            if (left < kKeys && key >= left) vr[i] = make_uint4(0, 0, 0, 0);  // (may be anything there)
+                        }
+                        constexpr int PER = kEight ? NE : 4;
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) {
+                            uint32_t a0, a1, a2, a3;
+                            if (kEight) {
+                                const uint32_t sel = e % 2 ? 0x7362 : 0x5140;
+                                const uint32_t x0 = __byte_perm(part(vr[0], e / 2), part(vr[1], e / 2), sel);
+                                const uint32_t x1 = __byte_perm(part(vr[2], e / 2), part(vr[3], e / 2), sel);
+                                a0 = to_half2(x0);
+                                a1 = to_half2(x0 >> 16);
+                                a2 = to_half2(x1);
+                                a3 = to_half2(x1 >> 16);
+                            } else {
+                                const uint32_t u0 = part(vr[0], e), u1 = part(vr[1], e), u2 = part(vr[2], e), u3 = part(vr[3], e);
+                                a0 = __byte_perm(u0, u1, 0x5410);
+                                a1 = __byte_perm(u0, u1, 0x7632);
+                                a2 = __byte_perm(u2, u3, 0x5410);
+                                a3 = __byte_perm(u2, u3, 0x7632);
+                            }
+#pragma unroll
+                            for (int i = 0; i < NR; ++i) mma16816<M>(acc[i][PER * j + e], a0, a1, a2, a3, pa[0][i], pa[1][i]);
                         }
                     }
                 }
-                // P, rounded (see above) for the product with V; its sum is taken before
-                uint32_t pa[2][2] = {{0u, 0u}, {0u, 0u}};  // [key tile][row]
-                if (kEight) {
-                    const float down = 1.f / vmax;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) vs[e] *= down;
-                }
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    const float ref = m[i] == -INFINITY ? 0.f : m[i];
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2f(x[i][e] - ref);
-                        l[i] += p[e];
-                        if (kEight) p[e] *= vs[e];
-                    }
-                    pa[0][i] = pack2<M>(p[0], p[1]);
-                    pa[1][i] = pack2<M>(p[2], p[3]);
-                }
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {  // keys 2 q, 2 q + 1 (and + 8) of two head dims
-                    uint32_t a0, a1, a2, a3;
-                    if (kEight) {
-                        const uint32_t sel = e % 2 ? 0x7362 : 0x5140;
-                        const uint32_t x0 = __byte_perm(part(vr[u][0][0], e / 2), part(vr[u][1][0], e / 2), sel);
-                        const uint32_t x1 = __byte_perm(part(vr[u][2][0], e / 2), part(vr[u][3][0], e / 2), sel);
-                        a0 = to_half2(x0);
-                        a1 = to_half2(x0 >> 16);
-                        a2 = to_half2(x1);
-                        a3 = to_half2(x1 >> 16);
-                    } else {
-                        const uint32_t u0 = part(vr[u][0][e / 4 % VL], e % 4), u1 = part(vr[u][1][e / 4 % VL], e % 4);
-                        const uint32_t u2 = part(vr[u][2][e / 4 % VL], e % 4), u3 = part(vr[u][3][e / 4 % VL], e % 4);
-                        a0 = __byte_perm(u0, u1, 0x5410);
-                        a1 = __byte_perm(u0, u1, 0x7632);
-                        a2 = __byte_perm(u2, u3, 0x5410);
-                        a3 = __byte_perm(u2, u3, 0x7632);
-                    }
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) mma16816<M>(acc[i][e], a0, a1, a2, a3, pa[0][i], pa[1][i]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+                if (++s == NST) {
+                    s = 0;
+                    par ^= 1;
                 }
             }
-        }
 
-        // ---- join the warps: lane (g, q) holds the sums of row g (+ 8 i), and dims of rows 2 q and 2 q + 1
+            // ---- join the key warps: maxima and sums of all rows first, then the outputs, brought to the joint maximum,
+            // of the upper two warps into the lower ones and of the second into the first.  Lane (g, q) holds the sums of row
+            // g (+ 8 i), and dims of rows 2 q and 2 q + 1.
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (q == 0) {
-                sm_m[warp][g + 8 * i] = m[i];
-                sm_l[warp][g + 8 * i] = l[i];
-            }
-            // (a lane's rows 2 q, 2 q + 1 are of the same warp: one vmax)
-            const float f = kEight ? vmax : 1.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    const int dim = kEight ? D / 8 * g + 2 * e : 64 * (e / 4) + 8 * g + 2 * (e % 4);
-                    *reinterpret_cast<float2 *>(&sm_o[warp][2 * q + c + 8 * i][dim]) =
-                        make_float2(acc[i][e][c] * f, acc[i][e][2 + c] * f);
+            for (int i = 0; i < NR; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                if (q == 0) {
+                    sm_m[kw * ROWS + rw * 16 + g + 8 * i] = m[i];
+                    sm_l[kw * ROWS + rw * 16 + g + 8 * i] = l[i];
                 }
-        }
-        __syncthreads();
-        const bool whole = w.begins() && w.ends();
-        const int slot = w.begins() ? 1 : 0;
-        if (!whole) named[slot] = unit_name(w.n, w.x, w.t, w.ends() ? kEnds : kGoesOn);
-        for (int t = threadIdx.x; t < ROWS * (D / 8); t += kThreads) {
-            const int r = t / (D / 8), c = t % (D / 8) * 8;
-            const int tok = r / hb, ti = w.t * sched.tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
-            if (tok >= sched.tokens || ti >= w.u.m || rb * ROWS + r - tok * hb >= G) continue;
-            float mm = -INFINITY, ll = 0.f, o[8] = {};
-            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, sm_m[k][r]);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            for (int k = 0; k < kWarps; ++k) {
-                const float f = ex2f(sm_m[k][r] - ref);
-                ll += f * sm_l[k][r];
+            }
+            sync();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = fmaf(f, sm_o[k][r][c + e], o[e]);
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int r = rw * 16 + 2 * q + c + 8 * i;
+                    float mm = sm_m[r];
+#pragma unroll
+                    for (int k = 1; k < kKeyWarps; ++k) mm = fmaxf(mm, sm_m[k * ROWS + r]);
+                    const float f = mm == -INFINITY ? 0.f : ex2f(sm_m[kw * ROWS + r] - mm) * (kEight ? vmax : 1.f);
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        acc[i][e][c] *= f;
+                        acc[i][e][2 + c] *= f;
+                    }
+                }
+            auto slot_of = [&](int slot, int i, int c, int e) -> float2 * {
+                const int dim = kEight ? D / 8 * g + 2 * e : 64 * (e / 4) + 8 * g + 2 * (e % 4);
+                return reinterpret_cast<float2 *>(sm_o + (slot * ROWS + rw * 16 + 2 * q + c + 8 * i) * D + dim);
+            };
+            auto put = [&](int slot) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < NE; ++e) *slot_of(slot, i, c, e) = make_float2(acc[i][e][c], acc[i][e][2 + c]);
+            };
+            auto add = [&](int slot) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < NE; ++e) {
+                            const float2 y = *slot_of(slot, i, c, e);
+                            acc[i][e][c] += y.x;
+                            acc[i][e][2 + c] += y.y;
+                        }
+            };
+            if (kw >= 2) put(kw - 2);
+            sync();
+            if (kw < 2) {
+                add(kw);
+                put(kw);
             }
-            if (whole) {
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                const int64_t row = a.seqs.cu ? int64_t(w.u.first + ti) * a.o.ss : w.n * a.o.sb + ti * a.o.ss;
-                T *dst = static_cast<T *>(a.o.ptr) + row + head * a.o.sh + c;
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
-                                                             pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
-                if (a.lse && c == 0)
-                    a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + w.u.first + ti
-                                    : (int64_t(w.n) * a.h + head) * a.seqs.s_q + ti] =
-                        ll == 0.f ? INFINITY : (mm + __log2f(ll)) / kLog2e;
-            } else {
-                const int64_t row = (int64_t(blockIdx.x) * 2 + slot) * ROWS + r;
-                if (c == 0) a.part_ml[row] = make_float2(mm, ll);
-                float4 *dst = reinterpret_cast<float4 *>(a.part_o + row * D + c);
-                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+            sync();
+            const bool whole = w.begins() && w.ends();
+            const int slot = w.begins() ? 1 : 0;
+            if (!whole) {
+                const int4 name = unit_name(w.n, w.x, w.t, w.ends() ? kEnds : kGoesOn);
+                if (slot) named1 = name;
+                else named0 = name;
             }
+            for (int t = threadIdx.x; t < ROWS * (D / 8); t += Cfg::CONSUMERS) {
+                const int r = t / (D / 8), c = t % (D / 8) * 8;
+                const int tok = r / hb, ti = w.t * sched.tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
+                if (tok >= sched.tokens || ti >= w.u.m || rb * ROWS + r - tok * hb >= G) continue;
+                float mm = sm_m[r], ll = 0.f, o[8];
+#pragma unroll
+                for (int k = 1; k < kKeyWarps; ++k) mm = fmaxf(mm, sm_m[k * ROWS + r]);
+                const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+                for (int k = 0; k < kKeyWarps; ++k) ll = fmaf(ex2f(sm_m[k * ROWS + r] - ref), sm_l[k * ROWS + r], ll);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = sm_o[r * D + c + e] + sm_o[(ROWS + r) * D + c + e];
+                if (whole) {
+                    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                    const int64_t row = a.seqs.cu ? int64_t(w.u.first + ti) * a.o.ss : w.n * a.o.sb + ti * a.o.ss;
+                    T *dst = static_cast<T *>(a.o.ptr) + row + head * a.o.sh + c;
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                                                 pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+                    if (a.lse && c == 0)
+                        a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + w.u.first + ti
+                                        : (int64_t(w.n) * a.h + head) * a.seqs.s_q + ti] =
+                            lse_of(mm, ll);
+                } else {
+                    const int64_t row = (int64_t(blockIdx.x) * 2 + slot) * ROWS + r;
+                    if (c == 0) a.part_ml[row] = make_float2(mm, ll);
+                    float4 *dst = reinterpret_cast<float4 *>(a.part_o + row * D + c);
+                    dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                    dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                }
+            }
+            sync();
         }
-        __syncthreads();
+        if (threadIdx.x == 0) {
+            a.rec[2 * blockIdx.x] = named0;
+            a.rec[2 * blockIdx.x + 1] = named1;
+        }
     }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        a.flags[blockIdx.x] = bad ? ATTN_DEV_INDEX_RANGE : 0u;
-        a.rec[2 * blockIdx.x] = named[0];
-        a.rec[2 * blockIdx.x + 1] = named[1];
-    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.flags[blockIdx.x] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
 }
 
 // Outputs of the units that several shares hold, a block for every share that holds a unit's first piece and every 16
 // rows: the pieces' maxima, then their sums in order of the shares, D / 8 lanes a row.  The first block gathers the
 // call's status.
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, const PagedShape shape)
+__global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, const PagedShape shape)
 {
-    constexpr int LPR = D / 8, NG = kThreads / LPR;
+    constexpr int LPR = D / 8, NG = kJoin / LPR;
     const int c0 = blockIdx.x, shares = shape.shares, rows = shape.rows;
     pdl_wait();
     if (c0 == 0 && blockIdx.y == 0) {
         uint32_t flags = 0;
-        for (int k = threadIdx.x; k < shares; k += kThreads) flags |= a.flags[k];
+        for (int k = threadIdx.x; k < shares; k += kJoin) flags |= a.flags[k];
         const int range = __syncthreads_or(flags & ATTN_DEV_INDEX_RANGE), timeout = __syncthreads_or(flags & ATTN_DEV_TIMEOUT);
         if (threadIdx.x == 0) *a.status = (range ? ATTN_DEV_INDEX_RANGE : 0u) | (timeout ? ATTN_DEV_TIMEOUT : 0u);
     }
@@ -465,19 +623,48 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
                                                      pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
         if (a.lse && c == 0)
             a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + first + ti : (int64_t(name.x) * a.h + head) * a.seqs.s_q + ti] =
-                ll == 0.f ? INFINITY : (mm + __log2f(ll)) / kLog2e;
+                lse_of(mm, ll);
     }
+}
+
+// Pages [n_pages][h_kv][page][d] in boxes of up to 64 tokens x `bytes` bytes, swizzled over that width or not.
+bool tmap_boxes(CUtensorMap *m, void *ptr, const PagedCache &c, int d, int h_kv, int bytes, bool swizzle)
+{
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    const int page = 1 << c.shift, size = c.type == ATTN_E4M3 ? 1 : 2;
+    cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(h_kv), cuuint64_t(c.none)};
+    cuuint64_t strides[3] = {cuuint64_t(c.ss) * size, cuuint64_t(c.sh) * size, cuuint64_t(c.sp) * size};
+    cuuint32_t box[4] = {cuuint32_t(bytes / size), cuuint32_t(page < kStage ? page : kStage), 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    return enc(m, type, 4, ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class T, bool kEight, int D, int ROWS> cudaError_t run(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    return launch_kernel(paged_decode_kernel<T, kEight, D, ROWS>, dim3(unsigned(p.shares)), dim3(kThreads), 0, s, false, a);
+    using Cfg = DecodeCfg<D, kEight, ROWS>;
+    DecodeParams prm;
+    prm.a = a;
+    if (!tmap_boxes(&prm.tm_k, a.cache.k, a.cache, D, a.h_kv, 64, false) ||
+        !tmap_boxes(&prm.tm_v, a.cache.v, a.cache, D, a.h_kv, D * Cfg::ESIZE < 128 ? 64 : 128, true))
+        return cudaErrorInvalidValue;
+    auto k = paged_decode_kernel<T, kEight, D, ROWS>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(k, dim3(unsigned(p.shares)), dim3(Cfg::THREADS), Cfg::SMEM, s, false, prm);
+}
+
+template <class T, bool kEight, int D> cudaError_t pick_rows(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
+{
+    return p.rows == 32 ? run<T, kEight, D, 32>(a, p, s) : p.rows == 16 ? run<T, kEight, D, 16>(a, p, s) : run<T, kEight, D, 8>(a, p, s);
 }
 
 template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    if (a.d == 64) return p.rows == 16 ? run<T, kEight, 64, 16>(a, p, s) : run<T, kEight, 64, 8>(a, p, s);
-    return p.rows == 16 ? run<T, kEight, 128, 16>(a, p, s) : run<T, kEight, 128, 8>(a, p, s);
+    return a.d == 64 ? pick_rows<T, kEight, 64>(a, p, s) : pick_rows<T, kEight, 128>(a, p, s);
 }
 
 }  // namespace
@@ -485,9 +672,10 @@ template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, const P
 PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q)
 {
     const int group = int(h / h_kv);
+    const int64_t rows = group * (s_q < 32 ? s_q : 32);
     PagedShape p;
     p.chunk = false;
-    p.rows = group * (s_q < 16 ? s_q : 16) > 8 ? 16 : 8;
+    p.rows = rows > 16 ? 32 : rows > 8 ? 16 : 8;
     p.shares = kPagedCtas * decode_blocks(int(d), p.rows);
     p.groups = 1;
     p.heads = group < p.rows ? group : p.rows;
@@ -506,7 +694,7 @@ cudaError_t launch_paged_join(const PagedAttnArgs &a, const PagedShape &p, cudaS
 {
     auto k = a.d == 64 ? (a.dtype == ATTN_F16 ? paged_join_kernel<__half, 64> : paged_join_kernel<__nv_bfloat16, 64>)
                        : (a.dtype == ATTN_F16 ? paged_join_kernel<__half, 128> : paged_join_kernel<__nv_bfloat16, 128>);
-    return launch_kernel(k, dim3(unsigned(p.shares), unsigned((p.rows + 15) / 16)), dim3(kThreads), 0, s, true, a, p);
+    return launch_kernel(k, dim3(unsigned(p.shares), unsigned((p.rows + 15) / 16)), dim3(kJoin), 0, s, true, a, p);
 }
 
 }  // namespace attn

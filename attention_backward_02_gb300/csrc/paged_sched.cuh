@@ -202,6 +202,16 @@ template <int kUnitCost> struct Walk {
     __host__ __device__ __forceinline__ bool ends() const { return k1 == all; }
 };
 
+// Natural log of l 2^m (+inf where no key was seen).  The exponent of l joins m before the logarithm of its fraction
+// is added: m and it may be far apart and cancel.
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    if (l == 0.f) return INFINITY;
+    const uint32_t u = __float_as_uint(l);
+    if ((u >> 23) - 1u >= 254u) return (m + __log2f(l)) / kLog2e;  // (no normal number: as it comes)
+    return ((m + float(int(u >> 23) - 127)) + __log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u))) / kLog2e;
+}
+
 // The unit's name in a share's record, for the join.
 __host__ __device__ __forceinline__ int4 unit_name(int n, int x, int t, int state) { return make_int4(n, x, t, state); }
 enum { kNone = 0, kGoesOn = 1, kEnds = 2 };  // state: no partial result, one that others follow, a unit's last

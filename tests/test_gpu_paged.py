@@ -206,6 +206,33 @@ def test_a_bad_page_reads_as_zeros(new):
     p.check(o, lse)
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_no_pages_and_no_tokens(eight):
+    """A cache without pages: every key reads as zeros, and the call says so.  A call without new tokens: its status."""
+    import torch
+    import attention_backward_02_gb300 as ab
+    pool = torch.empty(0, 16, 2, 64, dtype=torch.uint8 if eight else torch.float16, device="cuda")
+    pool = pool.view(torch.float8_e4m3fn) if eight else pool
+    sc = torch.empty(0, 16, 2, device="cuda") if eight else None
+    cache = ab.paged_cache(pool, pool, k_scale=sc, v_scale=sc)
+    table, lens = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.tensor([60], dtype=torch.int32, device="cuda")
+    for new in (1, 50):
+        desc = ab.sdpa_desc(dtype=ab.ATTN_F16, b=1, h=4, h_kv=2, s_q=new, s_kv=64, d=64, scale=0.125, mask=ab.ATTN_MASK_NONE)
+        q = torch.randn(1, 4, new, 64, dtype=torch.float16, device="cuda")
+        o, lse = torch.full_like(q, 3), torch.empty(1, 4, new, device="cuda")
+        ws = ab.sdpa_paged_fwd(desc, cache, table, lens, q, o, lse=lse)
+        assert ab.attn_query_status(ws) == 2
+        assert bool((o == 0).all()) and bool(((lse - np.log(60.0)).abs() <= 2.0 ** -18).all())
+        cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+        none = torch.empty(0, 4, 64, dtype=torch.float16, device="cuda")
+        ws = ab.sdpa_paged_fwd(desc, cache, table, lens, none, none, cu_new=cu)
+        assert ab.attn_query_status(ws) == 0
+        lens[0] = 65
+        ws = ab.sdpa_paged_fwd(desc, cache, table, lens, none, none, cu_new=cu, workspace=ws)
+        assert ab.attn_query_status(ws) == 2
+        lens[0] = 60
+
+
 @pytest.mark.parametrize("new", [1, 6, 90])
 def test_shared_pages_and_strided_rows(new):
     """Two sequences with the same first pages; queries as a slice of a fused projection, outputs into one."""
