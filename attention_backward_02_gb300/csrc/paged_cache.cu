@@ -13,11 +13,10 @@
 // the 8-bit side), d / 8 lanes a row.  A block takes a run of rows in the order token, keys and values, head, up to
 // eight a lane group; the write's are all loaded before the places in the cache are looked up (cumulative
 // counts, length, page id: three dependent loads), the read's behind it.
+#include <cstring>
 #include <type_traits>
 
 #include "paged.h"
-
-#include <cuda_fp8.h>
 
 namespace attn {
 namespace {
@@ -86,120 +85,165 @@ __device__ void check_call(const PagedSeqs &s, const PagedCache &c, uint32_t *st
     if (threadIdx.x == 0) *status = bad ? ATTN_DEV_INDEX_RANGE : 0u;
 }
 
-// T: the dense rows' type; kEight: e4m3 cache (else T); a block takes `most` rows, at most kMost a lane group.
+// The largest |x| of a lane's eight elements, NaN left out (the two-element maximum does that); kFinite: infinities too.
+template <class T, bool kFinite> __device__ __forceinline__ float most_of(const uint4 &x)
+{
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const uint32_t u[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
+    float most = 0.f;
+    if (kFinite) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 y = unpack2<T>(u[e]);
+            most = fmaxf(most, fmaxf(y.x < INFINITY ? y.x : 0.f, y.y < INFINITY ? y.y : 0.f));  // (false for NaN too)
+        }
+        return most;
+    }
+    T2 v[4];
+    memcpy(v, u, sizeof v);
+    const T2 m = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
+    uint32_t w;
+    memcpy(&w, &m, sizeof w);
+    const float2 y = unpack2<T>(w);
+    return fmaxf(fmaxf(y.x, y.y), 0.f);
+}
+
+// T: the dense rows' type; kEight: e4m3 cache (else T); a block takes `most` rows, at most kMost a lane group.  A lane
+// group's rows are kThreads / (D / 8) apart, which is step_t tokens and step_r rows of one.
 template <class T, bool kEight, int D, bool kWrite>
-__global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_constant__ PagedCopyArgs a, int most)
+__global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_constant__ PagedCopyArgs a, int most, int step_t, int step_r)
 {
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
     constexpr int kTokens = GROUPS * kMost / 2 + 1;            // that a block's rows may belong to
-    __shared__ int sm_page[kTokens], sm_tok[kTokens];          // page -1: no place; -2: no sequence's row
+    constexpr int kNone = -1, kNotOurs = -2;                   // page: no place; no sequence's row
+    __shared__ int64_t sm_dense[2][kTokens], sm_place[kTokens], sm_scale[kTokens];  // element offsets of head 0
+    __shared__ int sm_page[kTokens];
     const int group = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int per = 2 * a.h_kv, all = a.seqs.tokens * per;     // rows of a token, and of the call
     const int row0 = blockIdx.x * most, rows = all - row0 < most ? all - row0 : most;
     const int token0 = row0 / per, here = rows > 0 ? (row0 + rows - 1) / per - token0 + 1 : 0;
+    if (int(threadIdx.x) < here) {
+        const int row = token0 + threadIdx.x;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const View &v = e ? a.v : a.k;
+            sm_dense[e][threadIdx.x] = a.seqs.cu ? row * v.ss : (row / a.seqs.s_q) * v.sb + (row % a.seqs.s_q) * v.ss;
+        }
+    }
+    __syncthreads();
 
-    auto dense = [&](int t, int side, int head) -> T * {
+    // this lane group's rows: token, and row of the token (keys, then values; heads)
+    struct At {
+        int t, r;
+    };
+    At at0;
+    at0.t = (row0 + group) / per;
+    at0.r = row0 + group - at0.t * per;
+    at0.t -= token0;
+    auto next = [&](At &at) {
+        at.t += step_t;
+        at.r += step_r;
+        if (at.r >= per) {
+            at.r -= per;
+            ++at.t;
+        }
+    };
+    auto dense = [&](const At &at) -> T * {
+        const bool side = at.r >= a.h_kv;
         const View &v = side ? a.v : a.k;
-        const int row = token0 + t;
-        int64_t at = int64_t(head) * v.sh + l * 8;
-        if (a.seqs.cu) at += int64_t(row) * v.ss;
-        else at += int64_t(row / a.seqs.s_q) * v.sb + int64_t(row % a.seqs.s_q) * v.ss;
-        return static_cast<T *>(v.ptr) + at;
+        return static_cast<T *>(v.ptr) + sm_dense[side][at.t] + (side ? at.r - a.h_kv : at.r) * v.sh + l * 8;
     };
-    auto split = [&](int r, int *t, int *side, int *head) {
-        const int th = (row0 + r) / a.h_kv;
-        *head = row0 + r - th * a.h_kv;
-        *t = (th >> 1) - token0;
-        *side = th & 1;
-    };
+    const int count = rows > group ? (rows - group + GROUPS - 1) / GROUPS : 0;
 
     uint4 x[kMost];
     if (kWrite) {
+        At at = at0;
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
-            const int r = group + i * GROUPS;
-            int t, side, head;
-            split(r, &t, &side, &head);
-            x[i] = r < rows ? __ldcs(reinterpret_cast<const uint4 *>(dense(t, side, head))) : make_uint4(0, 0, 0, 0);
+            x[i] = i < count ? __ldcs(reinterpret_cast<const uint4 *>(dense(at))) : make_uint4(0, 0, 0, 0);
+            next(at);
         }
     }
     if (int(threadIdx.x) < here) {
         const int row = token0 + threadIdx.x;
-        int page = -1, tok = 0;
-        if (!place_of(a.seqs, a.cache, row, &page, &tok)) page = -1;
-        if (!kWrite && a.seqs.cu && (row >= a.seqs.cu[a.seqs.b] || row < a.seqs.cu[0])) page = -2;
+        int page = kNone, tok = 0;
+        if (!place_of(a.seqs, a.cache, row, &page, &tok)) page = kNone;
+        if (!kWrite && a.seqs.cu && (row >= a.seqs.cu[a.seqs.b] || row < a.seqs.cu[0])) page = kNotOurs;
         sm_page[threadIdx.x] = page;
-        sm_tok[threadIdx.x] = tok;
+        sm_place[threadIdx.x] = page * a.cache.sp + tok * a.cache.ss;
+        if (kEight) sm_scale[threadIdx.x] = page * a.cache.sc_sp + tok * a.cache.sc_ss;
     }
     __syncthreads();
 
-    auto scale_at = [&](int t, int side, int head) -> float * {
-        return (side ? a.cache.v_scale : a.cache.k_scale) + sm_page[t] * a.cache.sc_sp +
-               (head * a.cache.sc_sh + sm_tok[t] * a.cache.sc_ss);
+    struct Place {
+        int64_t at, scale;
+        bool side;
     };
-    auto cached = [&](int t, int side, int head) -> int64_t {
-        return sm_page[t] * a.cache.sp + (head * a.cache.sh + sm_tok[t] * a.cache.ss + l * 8);
+    auto place = [&](const At &at) -> Place {
+        Place p;
+        p.side = at.r >= a.h_kv;
+        const int head = p.side ? at.r - a.h_kv : at.r;
+        p.at = sm_place[at.t] + head * a.cache.sh + l * 8;
+        p.scale = kEight ? sm_scale[at.t] + head * a.cache.sc_sh : 0;
+        return p;
     };
 
+    At at = at0;
     if (kWrite) {
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int r = group + i * GROUPS;
+        for (int i = 0; i < kMost; ++i, next(at)) {
             if (i * GROUPS >= rows) break;  // (the same for the whole block: the shuffles below need all lanes)
-            int t, side, head;
-            split(r, &t, &side, &head);
-            const bool on = r < rows && sm_page[r < rows ? t : 0] >= 0;
-            void *pool = side ? a.cache.v : a.cache.k;
+            const bool on = i < count && sm_page[i < count ? at.t : 0] >= 0;
             if (!kEight) {
-                if (on) *reinterpret_cast<uint4 *>(static_cast<T *>(pool) + cached(t, side, head)) = x[i];
+                if (on) {
+                    const Place p = place(at);
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.side ? a.cache.v : a.cache.k) + p.at) = x[i];
+                }
                 continue;
             }
-            float2 y[4] = {unpack2<T>(x[i].x), unpack2<T>(x[i].y), unpack2<T>(x[i].z), unpack2<T>(x[i].w)};
-            float most = kFloor;
+            float top = most_of<T, false>(x[i]);
+            if (__any_sync(0xffffffffu, top == INFINITY)) top = most_of<T, true>(x[i]);
+            top = fmaxf(top, kFloor);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float u = fabsf(y[e].x), w = fabsf(y[e].y);
-                most = fmaxf(most, u < INFINITY ? u : 0.f);  // (false for NaN too)
-                most = fmaxf(most, w < INFINITY ? w : 0.f);
-            }
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float up = kTop / most;
+            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float up = kTop / top;
             uint16_t c[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = to_e4m3x2(y[e].x * up, y[e].y * up);
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = unpack2<T>(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w);
+                c[e] = to_e4m3x2(y.x * up, y.y * up);
+            }
             if (on) {
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + cached(t, side, head)) =
+                const Place p = place(at);
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.side ? a.cache.v : a.cache.k) + p.at) =
                     make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
-                if (l == 0) *scale_at(t, side, head) = most / kTop;
+                if (l == 0) (p.side ? a.cache.v_scale : a.cache.k_scale)[p.scale] = top / kTop;
             }
         }
     } else {
         uint2 c[kMost];
         float size[kMost];
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int r = group + i * GROUPS;
-            int t, side, head;
-            split(r, &t, &side, &head);
-            const bool on = r < rows && sm_page[r < rows ? t : 0] >= 0;
-            const void *pool = side ? a.cache.v : a.cache.k;
+        for (int i = 0; i < kMost; ++i, next(at)) {
+            const bool on = i < count && sm_page[i < count ? at.t : 0] >= 0;
+            x[i] = make_uint4(0, 0, 0, 0);
+            c[i] = make_uint2(0, 0);
+            size[i] = 0.f;
+            if (!on) continue;
+            const Place p = place(at);
+            const void *pool = p.side ? a.cache.v : a.cache.k;
             if (kEight) {
-                c[i] = on ? __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + cached(t, side, head)))
-                          : make_uint2(0, 0);
-                size[i] = on ? *scale_at(t, side, head) : 0.f;
+                c[i] = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + p.at));
+                size[i] = __ldg((p.side ? a.cache.v_scale : a.cache.k_scale) + p.scale);
             } else {
-                x[i] = on ? __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(pool) + cached(t, side, head)))
-                          : make_uint4(0, 0, 0, 0);
+                x[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(pool) + p.at));
             }
         }
+        at = at0;
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int r = group + i * GROUPS;
-            if (r >= rows) break;
-            int t, side, head;
-            split(r, &t, &side, &head);
-            if (sm_page[t] == -2) continue;
+        for (int i = 0; i < kMost; ++i, next(at)) {
+            if (i >= count) break;
+            if (sm_page[at.t] == kNotOurs) continue;
             if (kEight) {
                 uint32_t w[4];
 #pragma unroll
@@ -209,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_const
                 }
                 x[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4 *>(dense(t, side, head)) = x[i];
+            __stcs(reinterpret_cast<uint4 *>(dense(at)), x[i]);
         }
     }
     if (blockIdx.x == 0) check_call(a.seqs, a.cache, a.status);  // the call's only status writer
@@ -224,7 +268,7 @@ template <class T, bool kEight, int D> cudaError_t run(const PagedCopyArgs &a, b
     most = (most < 1 ? 1 : most > kMost ? kMost : most) * GROUPS;
     const int blocks = all > 0 ? (all + most - 1) / most : 1;
     return launch_kernel(write ? paged_copy_kernel<T, kEight, D, true> : paged_copy_kernel<T, kEight, D, false>,
-                         dim3(unsigned(blocks)), dim3(kThreads), 0, s, false, a, most);
+                         dim3(unsigned(blocks)), dim3(kThreads), 0, s, false, a, most, GROUPS / (2 * a.h_kv), GROUPS % (2 * a.h_kv));
 }
 
 template <class T> cudaError_t pick(const PagedCopyArgs &a, bool write, cudaStream_t s)

@@ -47,7 +47,7 @@ constexpr int kKeys = 16;        // keys of a warp's product
 constexpr int kStage = 64;       // keys of a stage
 constexpr int kKeyWarps = kStage / kKeys;
 constexpr int kUnitCost = 128;   // what a unit's start and end take, in keys
-constexpr int kJoin = 128;       // threads of the join
+constexpr int kJoin = 256;       // threads of the join
 
 // CTAs an SM holds: set by a lane's registers (Q, sums) and the rings.
 constexpr int decode_blocks(int d, int rows) { return rows == 8 ? (d == 64 ? 4 : 3) : rows == 16 ? (d == 64 ? 3 : 2) : d == 64 ? 2 : 1; }
@@ -570,61 +570,99 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
     if (threadIdx.x == 0) a.flags[blockIdx.x] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
 }
 
-// Outputs of the units that several shares hold, a block for every share that holds a unit's first piece and every 16
-// rows: the pieces' maxima, then their sums in order of the shares, D / 8 lanes a row.  The first block gathers the
-// call's status.
-template <class T, int D>
+// Outputs of the units that several shares hold: a block for every share that may hold a unit's first piece, every 8 rows
+// and every COLS columns, COLS / 4 lanes a row.  Groups of lanes take every kGroups-th piece; a row's group sums are added
+// in order.  Three round trips to L2: the records of the next shares side by side, the pieces' maxima side by side,
+// their outputs several at a time.  The first block gathers the call's status.
+template <class T, int D, int COLS>
 __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, const PagedShape shape)
 {
-    constexpr int LPR = D / 8, NG = kJoin / LPR;
-    const int c0 = blockIdx.x, shares = shape.shares, rows = shape.rows;
+    constexpr int LPR = COLS / 4, kGroups = kJoin / (8 * LPR), kBatch = 32;
+    __shared__ float sm_m[8], sm_f[kBatch][8], sm_s[kBatch][8], sm_l[kGroups][8];
+    __shared__ float4 sm_o[kGroups][8][LPR];
+    const int c0 = blockIdx.x, shares = shape.shares, rows = shape.rows, t = threadIdx.x, lane = t % 32;
     pdl_wait();
-    if (c0 == 0 && blockIdx.y == 0) {
+    if (c0 == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
         uint32_t flags = 0;
-        for (int k = threadIdx.x; k < shares; k += kJoin) flags |= a.flags[k];
+        for (int k = t; k < shares; k += kJoin) flags |= a.flags[k];
         const int range = __syncthreads_or(flags & ATTN_DEV_INDEX_RANGE), timeout = __syncthreads_or(flags & ATTN_DEV_TIMEOUT);
-        if (threadIdx.x == 0) *a.status = (range ? ATTN_DEV_INDEX_RANGE : 0u) | (timeout ? ATTN_DEV_TIMEOUT : 0u);
+        if (t == 0) *a.status = (range ? ATTN_DEV_INDEX_RANGE : 0u) | (timeout ? ATTN_DEV_TIMEOUT : 0u);
     }
+    // the shares that hold the rest: up to the one whose first piece ends the unit (every warp finds it for itself)
     const int4 name = a.rec[2 * c0 + 1];
+    int next = c0 + 1 + lane < shares ? a.rec[2 * (c0 + 1 + lane)].w : kEnds;
     if (name.w == kNone) return;
-    // the shares that hold the rest: up to the one whose first piece ends the unit
     int end = c0 + 1;
-    while (end < shares && a.rec[2 * end].w != kEnds) ++end;
+    for (uint32_t found; (found = __ballot_sync(0xffffffffu, next == kEnds)) == 0;) {
+        end += 32;
+        next = end + lane < shares ? a.rec[2 * (end + lane)].w : kEnds;
+        if (end >= shares) break;
+    }
+    end += __ffs(__ballot_sync(0xffffffffu, next == kEnds)) - 1;
+    const int n = (end < shares ? end : shares - 1) - c0 + 1;  // pieces (a share in between may hold none)
+
     const int G = a.h / a.h_kv, kvh = name.y / shape.row_blocks, block = name.y - kvh * shape.row_blocks;
     bool none = false;
     int first, m;
     a.seqs.rows(name.x, &first, &m, &none);
-    const int g = threadIdx.x / LPR, c = threadIdx.x % LPR * 8, group_rows = rows / shape.groups;
-    for (int r = blockIdx.y * 16 + g; r < int(blockIdx.y) * 16 + 16 && r < rows; r += NG) {
-        const int grp = r / group_rows, in = r - grp * group_rows, tok = in / shape.heads;
-        const int x = block * shape.heads + in - tok * shape.heads, head = kvh * G + x;
-        const int ti = (name.z * shape.groups + grp) * shape.tokens + tok;
-        if (tok >= shape.tokens || ti >= m || x >= G) continue;
+    const int row = t / LPR % 8, grp = t / (8 * LPR), col = blockIdx.z * COLS + t % LPR * 4, r0 = blockIdx.y * 8;
+    const float *po = a.part_o + (int64_t(c0) * 2 + 1) * rows * D + int64_t(r0 + row) * D + col;
+    const int64_t step = 2 * int64_t(rows) * D;  // from a share's first result to the next one's
+    auto ml = [&](int k, int r) -> float2 {       // maximum and sum of piece k
+        if (k > 0 && a.rec[2 * (c0 + k)].w == kNone) return make_float2(-INFINITY, 0.f);
+        return a.part_ml[(int64_t(c0 + k) * 2 + (k == 0)) * rows + r0 + r];
+    };
+    // the rows' maxima: warp w row w (kJoin / 32 warps)
+    for (int r = t / 32; r < 8; r += kJoin / 32) {
         float mm = -INFINITY;
-        for (int k = c0; k <= end && k < shares; ++k)
-            if (k == c0 || a.rec[2 * k].w != kNone) mm = fmaxf(mm, a.part_ml[(int64_t(k) * 2 + (k == c0)) * rows + r].x);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f, o[8] = {};
-        for (int k = c0; k <= end && k < shares; ++k) {
-            if (k != c0 && a.rec[2 * k].w == kNone) continue;
-            const int64_t row = (int64_t(k) * 2 + (k == c0)) * rows + r;
-            const float2 x = a.part_ml[row];
-            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + row * D + c);
-            const float4 u = src[0], v = src[1];
-            const float f = ex2f(x.x - ref);
-            ll = fmaf(f, x.y, ll);
-            o[0] = fmaf(f, u.x, o[0]); o[1] = fmaf(f, u.y, o[1]); o[2] = fmaf(f, u.z, o[2]); o[3] = fmaf(f, u.w, o[3]);
-            o[4] = fmaf(f, v.x, o[4]); o[5] = fmaf(f, v.y, o[5]); o[6] = fmaf(f, v.z, o[6]); o[7] = fmaf(f, v.w, o[7]);
-        }
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        const int64_t row = a.seqs.cu ? int64_t(first + ti) * a.o.ss : name.x * a.o.sb + ti * a.o.ss;
-        T *dst = static_cast<T *>(a.o.ptr) + row + head * a.o.sh + c;
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
-                                                     pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
-        if (a.lse && c == 0)
-            a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + first + ti : (int64_t(name.x) * a.h + head) * a.seqs.s_q + ti] =
-                lse_of(mm, ll);
+        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, ml(k, r).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        if (lane == 0) sm_m[r] = mm;
     }
+    __syncthreads();
+    const float mm = sm_m[row];
+    float ll = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+        const int here = n - k0 < kBatch ? n - k0 : kBatch;
+        if (k0 > 0) __syncthreads();
+        for (int x = t; x < here * 8; x += kJoin) {
+            const int r = x % 8;
+            const float2 y = ml(k0 + x / 8, r);
+            sm_f[x / 8][r] = y.y != y.y ? y.y : y.x == -INFINITY ? 0.f : ex2f(y.x - sm_m[r]);  // (NaN stays NaN)
+            sm_s[x / 8][r] = y.y;
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int k = grp; k < here; k += kGroups) {
+            const float f = sm_f[k][row];
+            const float4 u = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                      : *reinterpret_cast<const float4 *>(po + (k0 + k) * step - (k0 + k > 0 ? int64_t(rows) * D : 0));
+            o.x = fmaf(f, u.x, o.x); o.y = fmaf(f, u.y, o.y); o.z = fmaf(f, u.z, o.z); o.w = fmaf(f, u.w, o.w);
+            ll = fmaf(f, sm_s[k][row], ll);
+        }
+    }
+    if (t % LPR == 0) sm_l[grp][row] = ll;
+    sm_o[grp][row][t % LPR] = o;
+    __syncthreads();
+    if (grp > 0) return;
+    ll = sm_l[0][row];
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) {
+        const float4 u = sm_o[k][row][t % LPR];
+        o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
+        ll += sm_l[k][row];
+    }
+    const int group_rows = rows / shape.groups, r = r0 + row, g = r / group_rows, in = r - g * group_rows, tok = in / shape.heads;
+    const int x = block * shape.heads + in - tok * shape.heads, head = kvh * G + x;
+    const int ti = (name.z * shape.groups + g) * shape.tokens + tok;
+    if (tok >= shape.tokens || ti >= m || x >= G) return;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    T *dst = static_cast<T *>(a.o.ptr) + (a.seqs.cu ? int64_t(first + ti) * a.o.ss : name.x * a.o.sb + ti * a.o.ss) + head * a.o.sh;
+    *reinterpret_cast<uint2 *>(dst + col) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (a.lse && col == 0)
+        a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + first + ti : (int64_t(name.x) * a.h + head) * a.seqs.s_q + ti] = lse_of(mm, ll);
 }
 
 // Pages [n_pages][h_kv][page][d] in boxes of up to 64 tokens x `bytes` bytes, swizzled over that width or not.
@@ -640,7 +678,7 @@ bool tmap_boxes(CUtensorMap *m, void *ptr, const PagedCache &c, int d, int h_kv,
     const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     return enc(m, type, 4, ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               tmap_promotion(d * size), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class T, bool kEight, int D, int ROWS> cudaError_t run(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
@@ -690,11 +728,20 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a, const PagedShape &p, cud
     return a.dtype == ATTN_F16 ? pick<__half, false>(a, p, s) : pick<__nv_bfloat16, false>(a, p, s);
 }
 
+namespace {
+template <class T, int D> cudaError_t join(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
+{
+    // many blocks for the few rows of the small kernel, whose units may have hundreds of pieces
+    const dim3 grid(unsigned(p.shares), unsigned(p.rows / 8), p.chunk ? 1u : unsigned(D / 32));
+    if (p.chunk) return launch_kernel(paged_join_kernel<T, D, D>, grid, dim3(kJoin), 0, s, true, a, p);
+    return launch_kernel(paged_join_kernel<T, D, 32>, grid, dim3(kJoin), 0, s, true, a, p);
+}
+}  // namespace
+
 cudaError_t launch_paged_join(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    auto k = a.d == 64 ? (a.dtype == ATTN_F16 ? paged_join_kernel<__half, 64> : paged_join_kernel<__nv_bfloat16, 64>)
-                       : (a.dtype == ATTN_F16 ? paged_join_kernel<__half, 128> : paged_join_kernel<__nv_bfloat16, 128>);
-    return launch_kernel(k, dim3(unsigned(p.shares), unsigned((p.rows + 15) / 16)), dim3(kJoin), 0, s, true, a, p);
+    if (a.d == 64) return a.dtype == ATTN_F16 ? join<__half, 64>(a, p, s) : join<__nv_bfloat16, 64>(a, p, s);
+    return a.dtype == ATTN_F16 ? join<__half, 128>(a, p, s) : join<__nv_bfloat16, 128>(a, p, s);
 }
 
 }  // namespace attn

@@ -26,6 +26,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder()
     return fn;
 }
 
+// What a load may widen its reads of DRAM to: no more than a row, behind which another head's lies.
+inline CUtensorMapL2promotion tmap_promotion(int row_bytes)
+{
+    return row_bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+           : row_bytes >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+}
+
 // A 16-bit [B][H][S][D] view (element strides) as a 4-D map (d, s, h, b) with
 // boxes of 64 elements x `rows` rows and the 128-byte swizzle.  A stride of 0 (an
 // input that is one and the same for all sequences, heads or tokens) is one the map takes.
