@@ -1044,10 +1044,10 @@ struct PagedLayout {
 };
 
 // The kernel a call takes: from 33 rows (new tokens x query heads of a kv head) on the tensor-core one.
-PagedShape paged_shape(const attn_sdpa_desc_t *d)
+PagedShape paged_shape(const attn_sdpa_desc_t *d, bool eight)
 {
     if (d->s_q * (d->h / d->h_kv) > 32) return paged_chunk_shape(d->h, d->h_kv, d->s_q);
-    return paged_decode_shape(d->h, d->h_kv, d->d, d->s_q);
+    return paged_decode_shape(d->h, d->h_kv, d->d, d->s_q, eight);
 }
 
 PagedLayout paged_layout(const attn_sdpa_desc_t *d, const PagedShape &p)
@@ -1095,7 +1095,7 @@ attn_status_t sdpa_paged_workspace_size(const attn_sdpa_desc_t *desc, const attn
     if (st) return st;
     if (!bytes) return ATTN_ERR_NULLPTR;
     // (a call without tokens takes the other kernel, whose partial results are always smaller)
-    *bytes = paged_layout(desc, paged_shape(desc)).total;
+    *bytes = paged_layout(desc, paged_shape(desc, c.type == ATTN_E4M3)).total;
     return ATTN_OK;
 }
 
@@ -1109,10 +1109,11 @@ attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cach
     if (st || (st = check_paged_call(desc, cache, seqs, &a.seqs))) return st;
     if ((st = check_view(q, a.seqs.tokens)) || (st = check_view(o, a.seqs.tokens))) return st;
     if (reinterpret_cast<uintptr_t>(lse) & 3) return ATTN_ERR_ALIGN;
-    PagedShape shape = paged_shape(desc);
+    const bool eight = a.cache.type == ATTN_E4M3;
+    PagedShape shape = paged_shape(desc, eight);
     if ((st = check_ws(workspace, workspace_bytes, paged_layout(desc, shape).total))) return st;
     // no queries to make a tensor map of: the other kernel writes the status
-    if (shape.chunk && a.seqs.tokens == 0) shape = paged_decode_shape(desc->h, desc->h_kv, desc->d, 1);
+    if (shape.chunk && a.seqs.tokens == 0) shape = paged_decode_shape(desc->h, desc->h_kv, desc->d, 1, eight);
     const PagedLayout L = paged_layout(desc, shape);
     a.dtype = desc->dtype;
     a.h = int(desc->h); a.h_kv = int(desc->h_kv); a.d = int(desc->d);

@@ -88,7 +88,7 @@ struct PagedShape {
     int rows, shares;
     int groups, tokens, heads, row_blocks;
 };
-PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q);
+PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q, bool eight);
 PagedShape paged_chunk_shape(int64_t h, int64_t h_kv, int64_t s_q);
 
 cudaError_t launch_paged_copy(const PagedCopyArgs &a, bool write, cudaStream_t s);

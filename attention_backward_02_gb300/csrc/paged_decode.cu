@@ -10,8 +10,9 @@
 // operations.  A CTA takes its range of keys in stages of 64, which a producing warp brings into a
 // ring in shared memory by TMA (a lane looks up a page, a stage ahead, and issues its
 // boxes), so that loads run under the arithmetic and over the ends of pieces; four warps (32 rows: four pairs)
-// take 16 keys of a stage each.  Both products are mma.sync m16n8k16, which keeps the
-// operations off the critical path.  S = Q K^T has the rows as its rows; its accumulator is, as it
+// take 16 or 32 keys of a stage each.  Both products are mma.sync m16n8k16, which keeps the
+// operations off the critical path; what a warp's step takes is their latency and the softmax's (650 + 500 + 400
+// cycles, whether numbers are converted or not), so where a key has at most 128 bytes it takes 32 keys.  S = Q K^T has the rows as its rows; its accumulator is, as it
 // stands, the second operand of O^T = V^T P^T, whose rows are head dims and whose eight
 // columns are rows of S.  The operands are 16-byte reads of shared memory as they stand: the order of the
 // contraction over d is free, so a lane's 16 bytes of a key serve several steps, and V's key
@@ -43,31 +44,37 @@ using namespace sm103;
 
 namespace {
 
-constexpr int kKeys = 16;        // keys of a warp's product
-constexpr int kStage = 64;       // keys of a stage
-constexpr int kKeyWarps = kStage / kKeys;
-constexpr int kUnitCost = 128;   // what a unit's start and end take, in keys
+constexpr int kKeyWarps = 4;     // warps that share a stage's keys
+constexpr int kUnitCost = 256;   // what a unit's start and end take, in keys (128: 32 e4m3 sequences of 1 to 8192 keys 87 us, 256: 73, 512: 71)
+constexpr int kShare = 256;      // a share worth a start
 constexpr int kJoin = 256;       // threads of the join
 
-// CTAs an SM holds: set by a lane's registers (Q, sums) and the rings.
-constexpr int decode_blocks(int d, int rows) { return rows == 8 ? (d == 64 ? 4 : 3) : rows == 16 ? (d == 64 ? 3 : 2) : d == 64 ? 2 : 1; }
+// CTAs an SM holds: as many as the rings leave room for two stages or more, and a lane's registers (Q, sums) allow.
+constexpr int decode_blocks(int d, int esize, int rows)
+{
+    if (rows == 32) return d == 64 ? 2 : 1;
+    return d * esize == 64 || (d * esize == 256 && rows == 8) ? 3 : 2;
+}
 
 template <int D, bool kEight, int ROWS> struct DecodeCfg {
     static constexpr int RW = ROWS > 16 ? ROWS / 16 : 1;   // warps that share 16 keys, each with 8 or 16 of the rows
     static constexpr int NR = ROWS / RW / 8;               // rows of a lane
     static constexpr int CONSUMERS = 32 * kKeyWarps * RW, THREADS = CONSUMERS + 32;
     static constexpr int ESIZE = kEight ? 1 : 2;
-    static constexpr int SIDE = kStage * D * ESIZE;        // keys, or values, of a stage
-    static constexpr int O_BYTES = 2 * ROWS * D * 4;       // [2][ROWS][D] floats
-    static constexpr int BLOCKS = decode_blocks(D, ROWS);
+    static constexpr int SUB = D * ESIZE <= 128 ? 2 : 1;   // blocks of 16 keys that a warp takes at once
+    static constexpr int KEYS = 16 * SUB, STAGE_KEYS = kKeyWarps * KEYS;
+    static constexpr int SIDE = STAGE_KEYS * D * ESIZE;    // keys, or values, of a stage
+    static constexpr int OS = D + 2;                       // a row of sums: two rows of a lane lie in other banks
+    static constexpr int O_BYTES = 2 * ROWS * OS * 4;      // [2][ROWS][OS] floats
+    static constexpr int BLOCKS = decode_blocks(D, ESIZE, ROWS);
     static constexpr int OTHER = O_BYTES + 2 * kKeyWarps * ROWS * 4 + 512 + 1024;
-    static constexpr int STAGE = 2 * SIDE + (kEight ? 2 * kStage * 4 : 0) + 16;
+    static constexpr int STAGE = 2 * SIDE + (kEight ? 2 * STAGE_KEYS * 4 : 0) + 16;
     static constexpr int FIT = ((227 * 1024 / BLOCKS - 1024) - OTHER) / STAGE;
     static constexpr int NST = FIT > 12 ? 12 : FIT;
     static_assert(NST >= 2, "a ring of two stages");
     static constexpr int OFF_V = NST * SIDE;               // after the ring of keys
-    static constexpr int OFF_SCALE = OFF_V + NST * SIDE;   // [NST][keys, values][64]
-    static constexpr int OFF_O = OFF_SCALE + (kEight ? NST * 2 * kStage * 4 : 0);
+    static constexpr int OFF_SCALE = OFF_V + NST * SIDE;   // [NST][keys, values][STAGE_KEYS]
+    static constexpr int OFF_O = OFF_SCALE + (kEight ? NST * 2 * STAGE_KEYS * 4 : 0);
     static constexpr int OFF_M = OFF_O + O_BYTES;          // [key warp][ROWS] maxima, then sums
     static constexpr int OFF_BAR = OFF_M + 2 * kKeyWarps * ROWS * 4;
     static constexpr int OFF_MISC = OFF_BAR + 2 * NST * 8;
@@ -153,6 +160,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
     constexpr int NE = D / 16;               // products of O^T
     constexpr int NR = Cfg::NR, RW = Cfg::RW, NST = Cfg::NST;
     constexpr int KL = D * Cfg::ESIZE / 64;  // reads of a key
+    constexpr int SUB = Cfg::SUB, kKeys = Cfg::KEYS, kStage = Cfg::STAGE_KEYS;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -176,7 +184,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
     const int G = a.h / a.h_kv, hb = G < ROWS ? G : ROWS, nrb = (G + ROWS - 1) / ROWS;
     const Sched<kUnitCost> sched = {a.seqs, ROWS / hb, a.h_kv * nrb, a.causal};
     bool bad = false;
-    const Range range = sched.range<Cfg::THREADS, kStage, kStage, 2 * kUnitCost>(
+    const Range range = sched.range<Cfg::THREADS, kStage, kStage, kShare>(
         blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(smem + Cfg::OFF_RANGE), &bad);  // (two barriers inside)
     if (bad && blockIdx.x == 0) *bad_page = 1;  // (one CTA reports the lengths)
     bool ok = true;
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
 
     if (warp == kKeyWarps * RW) {
         // ================================================= producer
-        const int in_page = (1 << cache.shift) - 1, pr = cache.shift < 6 ? 1 << cache.shift : kStage;  // keys of a box
+        const int in_page = (1 << cache.shift) - 1, pr = 1 << cache.shift < kStage ? 1 << cache.shift : kStage;  // keys of a box
         const int boxes = kStage / pr;
         if (lane == 0) {
             prefetch_tmap(&p.tm_k);
@@ -226,13 +234,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                             tma_load_4d(vd + c * kStage * 128 + lane * pr * 128, &p.tm_v, &full[s], c * 128 / Cfg::ESIZE, key & in_page,
                                         kvh, page);
                 }
-                if (kEight) {  // scales of keys lane and lane + 32; 0 behind the piece's end
+                if (kEight) {  // scales of keys lane, lane + 32 ..; 0 behind the piece's end
+                    constexpr int PER = kStage / 32;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float *scale = e < 2 ? cache.k_scale : cache.v_scale;
-                        const int x = lane + 32 * (e & 1), pg = __shfl_sync(0xffffffffu, good ? id : -1, x / pr);
+                    for (int e = 0; e < 2 * PER; ++e) {
+                        const float *scale = e < PER ? cache.k_scale : cache.v_scale;
+                        const int x = lane + 32 * (e % PER), pg = __shfl_sync(0xffffffffu, good ? id : -1, x / pr);
                         const bool on = pg >= 0 && k0 + x < w.k1;
-                        copy4(smem_u32(smem + Cfg::OFF_SCALE) + ((2 * s + e / 2) * kStage + x) * 4,
+                        copy4(smem_u32(smem + Cfg::OFF_SCALE) + ((2 * s + e / PER) * kStage + x) * 4,
                               on ? scale + pg * cache.sc_sp + (kvh * cache.sc_sh + ((k0 + x) & in_page) * cache.sc_ss) : scale, on);
                     }
                     copies_arrive(&full[s]);
@@ -316,50 +325,52 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 const uint32_t ks = smem_u32(smem) + s * Cfg::SIDE + kw * kKeys * 64;
                 const uint32_t vs = smem_u32(smem) + Cfg::OFF_V + s * Cfg::SIDE;
                 if (ok && left > 0) {
-                    // scores: lane (g, q) gets rows g, g + 8 and keys 2q, 2q + 1 of both tiles
-                    float sa[2][4];
+                    // scores: lane (g, q) gets rows g, g + 8 and keys 2q, 2q + 1 of every tile of eight
+                    float sa[2 * SUB][4];
+                    uint4 kr[2 * SUB][KL];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        uint4 kr[KL];
+                    for (int t = 0; t < 2 * SUB; ++t) {
 #pragma unroll
-                        for (int n = 0; n < KL; ++n) kr[n] = lds16(ks + n * kStage * 64 + (8 * t + g) * 64 + 16 * q);
+                        for (int n = 0; n < KL; ++n) kr[t][n] = lds16(ks + n * kStage * 64 + (8 * t + g) * 64 + 16 * q);
                         sa[t][0] = sa[t][1] = sa[t][2] = sa[t][3] = 0.f;
+                    }
 #pragma unroll
-                        for (int n = 0; n < NQ / 2; ++n) {
+                    for (int n = 0; n < NQ / 2; ++n)
+#pragma unroll
+                        for (int t = 0; t < 2 * SUB; ++t) {
                             uint32_t b0, b1;
                             if (kEight) {
-                                const uint32_t x = part(kr[n / 4 % KL], n % 4);
+                                const uint32_t x = part(kr[t][n / 4 % KL], n % 4);
                                 b0 = to_half2(x);
                                 b1 = to_half2(x >> 16);
                             } else {
-                                b0 = part(kr[n / 2 % KL], 2 * (n % 2));
-                                b1 = part(kr[n / 2 % KL], 2 * (n % 2) + 1);
+                                b0 = part(kr[t][n / 2 % KL], 2 * (n % 2));
+                                b1 = part(kr[t][n / 2 % KL], 2 * (n % 2) + 1);
                             }
                             mma16816<M>(sa[t], qa[0][2 * n], NR > 1 ? qa[NR - 1][2 * n] : 0u, qa[0][2 * n + 1],
                                         NR > 1 ? qa[NR - 1][2 * n + 1] : 0u, b0, b1);
                         }
-                    }
-                    float fk[4], fv[4];  // scales of the lane's keys
+                    float fk[4 * SUB], fv[4 * SUB];  // scales of the lane's keys
                     if (kEight) {
                         const float *size = reinterpret_cast<const float *>(smem + Cfg::OFF_SCALE) + 2 * s * kStage + kw * kKeys + 2 * q;
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
+                        for (int t = 0; t < 2 * SUB; ++t) {
                             const float2 x = *reinterpret_cast<const float2 *>(size + 8 * t);
                             const float2 y = *reinterpret_cast<const float2 *>(size + kStage + 8 * t);
                             fk[2 * t] = x.x; fk[2 * t + 1] = x.y; fv[2 * t] = y.x; fv[2 * t + 1] = y.y;
                         }
                     }
-                    float x[NR][4], mx[NR];
+                    float x[NR][4 * SUB], mx[NR];
                     bool raise = false;
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
                         mx[i] = -INFINITY;
                         // (behind k1 the keys are another CTA's, or hidden from all rows)
-                        const int last = lim[i] < w.k1 - 1 ? lim[i] - kb : w.k1 - 1 - kb;
+                        const int last = (lim[i] < w.k1 - 1 ? lim[i] : w.k1 - 1) - kb - 2 * q;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 4 * SUB; ++e) {
                             const float f = kEight ? fs[i] * fk[e] : fs[i];
-                            x[i][e] = 8 * (e >> 1) + 2 * q + (e & 1) <= last ? sa[e >> 1][2 * i + (e & 1)] * f : -INFINITY;
+                            x[i][e] = 8 * (e >> 1) + (e & 1) <= last ? sa[e >> 1][2 * i + (e & 1)] * f : -INFINITY;
                             mx[i] = fmaxf(mx[i], x[i][e]);
                         }
                         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
@@ -368,7 +379,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                     }
                     float vm = 0.f;
                     if (kEight) {
-                        vm = fmaxf(fmaxf(fv[0], fv[1]), fmaxf(fv[2], fv[3]));
+#pragma unroll
+                        for (int e = 0; e < 4 * SUB; ++e) vm = fmaxf(vm, fv[e]);
                         raise |= vm > vmax;
                     }
                     if (__any_sync(0xffffffffu, raise)) {
@@ -400,60 +412,64 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                         }
                     }
                     // P, rounded (see above) for the product with V; its sum is taken before
-                    uint32_t pa[2][2] = {{0u, 0u}, {0u, 0u}};  // [key tile][row]
+                    uint32_t pa[2 * SUB][2];  // [key tile][row]
                     if (kEight) {
                         const float down = __uint_as_float((254u << 23) - __float_as_uint(vmax));  // 1 / vmax
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) fv[e] *= down;
+                        for (int e = 0; e < 4 * SUB; ++e) fv[e] *= down;
                     }
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
                         const float ref = m[i] == -INFINITY ? 0.f : m[i];
-                        float e4[4];
+                        float sum[SUB];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) e4[e] = ex2f(x[i][e] - ref);
-                        l[i] += (e4[0] + e4[1]) + (e4[2] + e4[3]);
-                        if (kEight) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) e4[e] *= fv[e];
-                        }
-                        pa[0][i] = pack2<M>(e4[0], e4[1]);
-                        pa[1][i] = pack2<M>(e4[2], e4[3]);
-                    }
-                    // values of keys 2 q, 2 q + 1 (and + 8), head dims by g
-#pragma unroll
-                    for (int j = 0; j < (KL > 2 ? 2 : 1); ++j) {  // blocks of 128 bytes
-                        uint4 vr[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int key = 2 * q + (i & 1) + 8 * (i >> 1), row = kw * kKeys + key;
-                            if (D * Cfg::ESIZE == 64) vr[i] = lds8(vs + row * 64 + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
-                            else vr[i] = lds16(vs + j * kStage * 128 + row * 128 + ((g ^ (row & 7)) << 4));
-                            if (left < kKeys && key >= left) vr[i] = make_uint4(0, 0, 0, 0);  // (may be anything there)
-                        }
-                        constexpr int PER = kEight ? NE : 4;
-#pragma unroll
-                        for (int e = 0; e < PER; ++e) {
-                            uint32_t a0, a1, a2, a3;
+                        for (int t = 0; t < 2 * SUB; ++t) {
+                            float e0 = ex2f(x[i][2 * t] - ref), e1 = ex2f(x[i][2 * t + 1] - ref);
+                            sum[t / 2] = t % 2 ? sum[t / 2] + (e0 + e1) : e0 + e1;
                             if (kEight) {
-                                const uint32_t sel = e % 2 ? 0x7362 : 0x5140;
-                                const uint32_t x0 = __byte_perm(part(vr[0], e / 2), part(vr[1], e / 2), sel);
-                                const uint32_t x1 = __byte_perm(part(vr[2], e / 2), part(vr[3], e / 2), sel);
-                                a0 = to_half2(x0);
-                                a1 = to_half2(x0 >> 16);
-                                a2 = to_half2(x1);
-                                a3 = to_half2(x1 >> 16);
-                            } else {
-                                const uint32_t u0 = part(vr[0], e), u1 = part(vr[1], e), u2 = part(vr[2], e), u3 = part(vr[3], e);
-                                a0 = __byte_perm(u0, u1, 0x5410);
-                                a1 = __byte_perm(u0, u1, 0x7632);
-                                a2 = __byte_perm(u2, u3, 0x5410);
-                                a3 = __byte_perm(u2, u3, 0x7632);
+                                e0 *= fv[2 * t];
+                                e1 *= fv[2 * t + 1];
                             }
-#pragma unroll
-                            for (int i = 0; i < NR; ++i) mma16816<M>(acc[i][PER * j + e], a0, a1, a2, a3, pa[0][i], pa[1][i]);
+                            pa[t][i] = pack2<M>(e0, e1);
                         }
+                        l[i] += SUB > 1 ? sum[0] + sum[SUB - 1] : sum[0];
                     }
+                    // values of keys 2 q, 2 q + 1 (and + 8) of 16, head dims by g
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int j = 0; j < (KL > 2 ? 2 : 1); ++j) {  // blocks of 128 bytes
+                            uint4 vr[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int key = 16 * u + 2 * q + (i & 1) + 8 * (i >> 1), row = kw * kKeys + key;
+                                if (D * Cfg::ESIZE == 64) vr[i] = lds8(vs + row * 64 + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
+                                else vr[i] = lds16(vs + j * kStage * 128 + row * 128 + ((g ^ (row & 7)) << 4));
+                                if (left < kKeys && key >= left) vr[i] = make_uint4(0, 0, 0, 0);  // (may be anything there)
+                            }
+                            constexpr int PER = kEight ? NE : 4;
+#pragma unroll
+                            for (int e = 0; e < PER; ++e) {
+                                uint32_t a0, a1, a2, a3;
+                                if (kEight) {
+                                    const uint32_t sel = e % 2 ? 0x7362 : 0x5140;
+                                    const uint32_t x0 = __byte_perm(part(vr[0], e / 2), part(vr[1], e / 2), sel);
+                                    const uint32_t x1 = __byte_perm(part(vr[2], e / 2), part(vr[3], e / 2), sel);
+                                    a0 = to_half2(x0);
+                                    a1 = to_half2(x0 >> 16);
+                                    a2 = to_half2(x1);
+                                    a3 = to_half2(x1 >> 16);
+                                } else {
+                                    const uint32_t u0 = part(vr[0], e), u1 = part(vr[1], e), u2 = part(vr[2], e), u3 = part(vr[3], e);
+                                    a0 = __byte_perm(u0, u1, 0x5410);
+                                    a1 = __byte_perm(u0, u1, 0x7632);
+                                    a2 = __byte_perm(u2, u3, 0x5410);
+                                    a3 = __byte_perm(u2, u3, 0x7632);
+                                }
+#pragma unroll
+                                for (int i = 0; i < NR; ++i) mma16816<M>(acc[i][PER * j + e], a0, a1, a2, a3, pa[2 * u][i], pa[2 * u + 1][i]);
+                            }
+                        }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
@@ -493,7 +509,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 }
             auto slot_of = [&](int slot, int i, int c, int e) -> float2 * {
                 const int dim = kEight ? D / 8 * g + 2 * e : 64 * (e / 4) + 8 * g + 2 * (e % 4);
-                return reinterpret_cast<float2 *>(sm_o + (slot * ROWS + rw * 16 + 2 * q + c + 8 * i) * D + dim);
+                return reinterpret_cast<float2 *>(sm_o + (slot * ROWS + rw * 16 + 2 * q + c + 8 * i) * Cfg::OS + dim);
             };
             auto put = [&](int slot) {
 #pragma unroll
@@ -540,7 +556,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
 #pragma unroll
                 for (int k = 0; k < kKeyWarps; ++k) ll = fmaf(ex2f(sm_m[k * ROWS + r] - ref), sm_l[k * ROWS + r], ll);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = sm_o[r * D + c + e] + sm_o[(ROWS + r) * D + c + e];
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 y = *reinterpret_cast<const float2 *>(sm_o + r * Cfg::OS + c + e);
+                    const float2 z = *reinterpret_cast<const float2 *>(sm_o + (ROWS + r) * Cfg::OS + c + e);
+                    o[e] = y.x + z.x;
+                    o[e + 1] = y.y + z.y;
+                }
                 if (whole) {
                     const float inv = ll == 0.f ? 0.f : 1.f / ll;
                     const int64_t row = a.seqs.cu ? int64_t(w.u.first + ti) * a.o.ss : w.n * a.o.sb + ti * a.o.ss;
@@ -665,15 +686,15 @@ __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant
         a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + first + ti : (int64_t(name.x) * a.h + head) * a.seqs.s_q + ti] = lse_of(mm, ll);
 }
 
-// Pages [n_pages][h_kv][page][d] in boxes of up to 64 tokens x `bytes` bytes, swizzled over that width or not.
-bool tmap_boxes(CUtensorMap *m, void *ptr, const PagedCache &c, int d, int h_kv, int bytes, bool swizzle)
+// Pages [n_pages][h_kv][page][d] in boxes of up to `keys` tokens x `bytes` bytes, swizzled over that width or not.
+bool tmap_boxes(CUtensorMap *m, void *ptr, const PagedCache &c, int d, int h_kv, int keys, int bytes, bool swizzle)
 {
     auto enc = tmap_encoder();
     if (!enc) return false;
     const int page = 1 << c.shift, size = c.type == ATTN_E4M3 ? 1 : 2;
     cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(h_kv), cuuint64_t(c.none)};
     cuuint64_t strides[3] = {cuuint64_t(c.ss) * size, cuuint64_t(c.sh) * size, cuuint64_t(c.sp) * size};
-    cuuint32_t box[4] = {cuuint32_t(bytes / size), cuuint32_t(page < kStage ? page : kStage), 1, 1};
+    cuuint32_t box[4] = {cuuint32_t(bytes / size), cuuint32_t(page < keys ? page : keys), 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     return enc(m, type, 4, ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -686,8 +707,8 @@ template <class T, bool kEight, int D, int ROWS> cudaError_t run(const PagedAttn
     using Cfg = DecodeCfg<D, kEight, ROWS>;
     DecodeParams prm;
     prm.a = a;
-    if (!tmap_boxes(&prm.tm_k, a.cache.k, a.cache, D, a.h_kv, 64, false) ||
-        !tmap_boxes(&prm.tm_v, a.cache.v, a.cache, D, a.h_kv, D * Cfg::ESIZE < 128 ? 64 : 128, true))
+    if (!tmap_boxes(&prm.tm_k, a.cache.k, a.cache, D, a.h_kv, Cfg::STAGE_KEYS, 64, false) ||
+        !tmap_boxes(&prm.tm_v, a.cache.v, a.cache, D, a.h_kv, Cfg::STAGE_KEYS, D * Cfg::ESIZE < 128 ? 64 : 128, true))
         return cudaErrorInvalidValue;
     auto k = paged_decode_kernel<T, kEight, D, ROWS>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
@@ -707,14 +728,14 @@ template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, const P
 
 }  // namespace
 
-PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q)
+PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q, bool eight)
 {
     const int group = int(h / h_kv);
     const int64_t rows = group * (s_q < 32 ? s_q : 32);
     PagedShape p;
     p.chunk = false;
     p.rows = rows > 16 ? 32 : rows > 8 ? 16 : 8;
-    p.shares = kPagedCtas * decode_blocks(int(d), p.rows);
+    p.shares = kPagedCtas * decode_blocks(int(d), eight ? 1 : 2, p.rows);
     p.groups = 1;
     p.heads = group < p.rows ? group : p.rows;
     p.tokens = p.rows / p.heads;

@@ -29,17 +29,34 @@ struct SeqUnits {
     int first, m, len, nt;
 };
 
-// a / b and the remainder, b > 0; 32-bit division (a fifth of the instructions) where both fit.
-__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b, int64_t *rest)
+// a / b (less than 2^20) and the remainder: an estimate in fp32, which is off by one at most, put right.  (The code of a
+// 64-bit division is long, and a CTA runs it once: fetching it took longer than the rest of the range's arithmetic.)
+__host__ __device__ __forceinline__ int quotient(int64_t a, int64_t b, int64_t *rest)
 {
-    if ((uint64_t(a) | uint64_t(b)) >> 32 == 0) {
-        const uint32_t q = uint32_t(a) / uint32_t(b);
-        *rest = uint32_t(a) - q * uint32_t(b);
-        return q;
+    int q = int(float(a) / float(b));
+    int64_t r = a - q * b;
+    if (r < 0) {
+        --q;
+        r += b;
+    } else if (r >= b) {
+        ++q;
+        r -= b;
     }
-    const int64_t q = a / b;
-    *rest = a - q * b;
+    *rest = r;
     return q;
+}
+
+// Cost of the tiles before t of one head block.  (Not inlined: it is called from several places that a CTA passes once.)
+template <int kUnitCost>
+__host__ __device__ __noinline__ int64_t cost_before(int causal, int tokens, int m, int len, int nt, int t)
+{
+    int64_t c = int64_t(t) * kUnitCost;
+    if (!causal) return c + int64_t(t) * len;
+    const int full = t < nt ? t : nt - 1;  // tiles of `tokens` tokens each
+    const int past = len - m;
+    const int from = past < 0 ? (-past / tokens < full ? -past / tokens : full) : 0;  // the first that sees keys
+    c += int64_t(full - from) * past + int64_t(tokens) * (int64_t(full) * (full + 1) - int64_t(from) * (from + 1)) / 2;
+    return t < nt ? c : c + len;
 }
 
 template <int kUnitCost> struct Sched {
@@ -67,13 +84,7 @@ template <int kUnitCost> struct Sched {
     // cost of the tiles before t of one head block
     __host__ __device__ __forceinline__ int64_t before(const SeqUnits &u, int t) const
     {
-        int64_t c = int64_t(t) * kUnitCost;
-        if (!causal) return c + int64_t(t) * u.len;
-        const int full = t < u.nt ? t : u.nt - 1;                            // tiles of `tokens` tokens each
-        const int past = u.len - u.m;
-        const int from = past < 0 ? (-past / tokens < full ? -past / tokens : full) : 0;  // the first that sees keys
-        c += int64_t(full - from) * past + int64_t(tokens) * (int64_t(full) * (full + 1) - int64_t(from) * (from + 1)) / 2;
-        return t < u.nt ? c : c + u.len;
+        return cost_before<kUnitCost>(causal, tokens, u.m, u.len, u.nt, t);
     }
     __host__ __device__ __forceinline__ int64_t cost(const SeqUnits &u) const { return u.nt ? heads * before(u, u.nt) : 0; }
 
@@ -81,7 +92,7 @@ template <int kUnitCost> struct Sched {
     template <int kStep, int kLeast>
     __host__ __device__ __forceinline__ void locate(const SeqUnits &u, int64_t at, int *x, int *t, int *k) const
     {
-        *x = int(quotient(at, before(u, u.nt), &at));
+        *x = quotient(at, before(u, u.nt), &at);
         int lo = 0, hi = u.nt - 1;  // the last tile that begins at or before
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
@@ -98,16 +109,18 @@ template <int kUnitCost> struct Sched {
     }
 
     // CTAs that have a share worth a start, and where the range of CTA c begins, of a total cost.
-    template <int kShare> static __host__ __device__ __forceinline__ int64_t shares(int64_t total, int ctas)
+    template <int kShare> static __host__ __device__ __forceinline__ int shares(int64_t total, int ctas)
     {
+        static_assert((kShare & (kShare - 1)) == 0, "a shift");
         const int64_t n = (total + kShare - 1) / kShare;
-        return n > ctas ? ctas : n < 1 ? 1 : n;
+        return n > ctas ? ctas : n < 1 ? 1 : int(n);
     }
-    static __host__ __device__ __forceinline__ int64_t border(int64_t total, int64_t n, int64_t c)
+    // (total c / n, in fractions of 2^-32)
+    static __host__ __device__ __forceinline__ int64_t border(int64_t total, int n, int c)
     {
-        int64_t rest;
-        const int64_t q = quotient(total, n, &rest);
-        return q * c + quotient(rest * c, n, &rest);
+        if (c >= n) return total;
+        const uint64_t part = uint64_t(0xffffffffu / uint32_t(n)) * uint32_t(c);
+        return int64_t((uint64_t(total) >> 32) * part + ((uint64_t(total) & 0xffffffffu) * part >> 32));
     }
 
     // The range of CTA c.  All threads of the block; `scratch`: 40 words of shared memory.  *bad: counts or lengths
@@ -135,20 +148,21 @@ template <int kUnitCost> struct Sched {
             if (w < warp) base += scratch[w];
             total += scratch[w];
         }
-        const int64_t n_cta = shares<kShare>(total, ctas);
+        const int n_cta = shares<kShare>(total, ctas);
         if (c < n_cta) {
             bool none = false;
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < 2; ++e) {
                 const int64_t at = border(total, n_cta, c + e);
                 if (at < base || at >= base + mine) continue;  // another thread's, or the end of the last unit
                 int64_t off = at - base;
                 int n = lo;
                 SeqUnits u = units(n, &none);
-                for (int64_t w = cost(u); off >= w; w = cost(u)) {
-                    off -= w;
-                    u = units(++n, &none);
-                }
+                if (hi - lo > 1)  // (else it is this one)
+                    for (int64_t w = cost(u); off >= w; w = cost(u)) {
+                        off -= w;
+                        u = units(++n, &none);
+                    }
                 int x, t, k;
                 locate<kStep, kLeast>(u, off, &x, &t, &k);
                 out[4 * e] = n;

@@ -30,8 +30,9 @@ void check(const std::vector<int> &lens, const std::vector<int> &news, bool pack
     bool bad = false;
     std::vector<int64_t> base(1, 0);
     for (int n = 0; n < s.b; ++n) base.push_back(base.back() + sc.cost(sc.units(n, &bad)));
-    const int64_t total = base.back(), n_cta = Sched<kUnitCost>::template shares<kShare>(total, ctas);
-    auto at = [&](int64_t c, int *n, int *x, int *t, int *k) {
+    const int64_t total = base.back();
+    const int n_cta = Sched<kUnitCost>::template shares<kShare>(total, ctas);
+    auto at = [&](int c, int *n, int *x, int *t, int *k) {
         const int64_t pos = Sched<kUnitCost>::border(total, n_cta, c);
         *n = s.b;
         *x = *t = *k = 0;
@@ -45,7 +46,7 @@ void check(const std::vector<int> &lens, const std::vector<int> &news, bool pack
     bool open = false;  // a unit begun and not ended
     std::vector<std::vector<int>> taken(s.b);  // times a unit's end was reached
     for (int n = 0; n < s.b; ++n) taken[n].assign(size_t(heads) * sc.units(n, &bad).nt, 0);
-    for (int64_t c = 0; c < n_cta; ++c) {
+    for (int c = 0; c < n_cta; ++c) {
         Range r;
         r.any = total > 0;
         at(c, &r.n0, &r.x0, &r.t0, &r.k0);
@@ -74,7 +75,8 @@ void check(const std::vector<int> &lens, const std::vector<int> &news, bool pack
             ++in_share;
         }
         const int64_t part = (total + n_cta - 1) / n_cta;
-        if (load > part + 2 * kLeast + 2 * kStep + kUnitCost * (in_share + 1)) ++heavy;
+        // (borders are fractions of 2^-32 of the work, of which the last share gets what is rounded off)
+        if (load > part + total / (int64_t(1) << 32) * n_cta + n_cta + 2 * kLeast + 2 * kStep + kUnitCost * (in_share + 1)) ++heavy;
     }
     if (open) ++holes;
     for (auto &v : taken)
