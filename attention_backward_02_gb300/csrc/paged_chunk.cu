@@ -73,7 +73,7 @@ template <int D, bool kEight, bool kSplit> struct ChunkCfg {
     static constexpr int OFF_KS = OFF_ML + 2 * 2 * 128 * 4;   // [NKS][64] floats
     static constexpr int OFF_KE = OFF_KS + (kEight ? NKS * HN * 4 : 0);   // [NKS] E and 2^-E of the values
     static constexpr int OFF_RANGE = OFF_KE + (kEight ? NKS * 8 : 0);     // scratch of the range, then the range
-    static constexpr int SMEM = OFF_RANGE + 256;
+    static constexpr int SMEM = OFF_RANGE + 320;
     // at least half the SM's shared memory: one CTA, which holds all of the TMEM, runs per SM
     static constexpr int SMEM_ALLOC = SMEM + 1024 > 116 * 1024 ? SMEM + 1024 : 116 * 1024;
     static constexpr int T_S = 0, T_O = 256;  // S (and P) of group g, step parity b at T_S + 128 g + 64 b, O at T_O + D g
@@ -81,7 +81,7 @@ template <int D, bool kEight, bool kSplit> struct ChunkCfg {
     static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
     static_assert(3 + 4 * NS + 12 + NKS + 4 * NE <= 80, "barrier slots");
     static_assert(!kEight || NKS >= NS + 4, "key scale slots");
-    static_assert((THREADS / 32 + 5) * 8 <= 256 - sizeof(Range) && sizeof(Range) <= 64, "range scratch");
+    static_assert((THREADS / 32 + 12) * 8 <= 256 && sizeof(Range) <= 64, "range scratch");
 };
 
 // What a unit's start and end take, in keys; pieces of fewer than kLeast keys are avoided; a share worth a start.
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
     const int G = a.h / a.h_kv;
     const Sched<kChunkCost> sched = {a.seqs, kSplit ? p.tokens : 2 * p.tokens, a.h_kv, a.causal};
     bool bad = false;
-    Range *range = reinterpret_cast<Range *>(smem + Cfg::OFF_RANGE + 192);
+    Range *range = reinterpret_cast<Range *>(smem + Cfg::OFF_RANGE + 256);
     {
         const Range r = sched.template range<Cfg::THREADS, 2 * HN, kChunkLeast, kChunkShare>(
             blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(smem + Cfg::OFF_RANGE), &bad);

@@ -79,7 +79,7 @@ template <int D, bool kEight, int ROWS> struct DecodeCfg {
     static constexpr int OFF_BAR = OFF_M + 2 * kKeyWarps * ROWS * 4;
     static constexpr int OFF_MISC = OFF_BAR + 2 * NST * 8;
     static constexpr int OFF_RANGE = OFF_MISC + 16;        // scratch of the range
-    static constexpr int SMEM = OFF_RANGE + (THREADS / 32 + 5) * 8 + 1024;
+    static constexpr int SMEM = OFF_RANGE + (THREADS / 32 + 12) * 8 + 1024;
     static_assert(SMEM <= 227 * 1024 / BLOCKS - 1024, "shared memory budget");
 };
 

@@ -33,7 +33,11 @@ struct SeqUnits {
 // 64-bit division is long, and a CTA runs it once: fetching it took longer than the rest of the range's arithmetic.)
 __host__ __device__ __forceinline__ int quotient(int64_t a, int64_t b, int64_t *rest)
 {
+#ifdef __CUDA_ARCH__
+    int q = int(__fdividef(float(a), float(b)));
+#else
     int q = int(float(a) / float(b));
+#endif
     int64_t r = a - q * b;
     if (r < 0) {
         --q;
@@ -123,7 +127,7 @@ template <int kUnitCost> struct Sched {
         return int64_t((uint64_t(total) >> 32) * part + ((uint64_t(total) & 0xffffffffu) * part >> 32));
     }
 
-    // The range of CTA c.  All threads of the block; `scratch`: 40 words of shared memory.  *bad: counts or lengths
+    // The range of CTA c.  All threads of the block; `scratch`: kThreads / 32 + 12 64-bit words of shared memory.  *bad: counts or lengths
     // out of range (known to CTA 0's threads only).
     template <int kThreads, int kStep, int kLeast, int kShare>
     __device__ Range range(int c, int ctas, int64_t *scratch, bool *bad) const
@@ -132,16 +136,28 @@ template <int kUnitCost> struct Sched {
         const int each = (s.b + kThreads - 1) / kThreads;  // sequences of a thread, in order
         const int lo = tid * each < s.b ? tid * each : s.b, hi = lo + each < s.b ? lo + each : s.b;
         int64_t mine = 0;
-        for (int n = lo; n < hi; ++n) mine += cost(units(n, bad));
+        SeqUnits u = {0, 0, 0, 0};
+        for (int n = lo; n < hi; ++n) {
+            u = units(n, bad);
+            mine += cost(u);
+        }
         int64_t sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += v;
         }
+        // scratch: the warps' sums; where the two borders lie (sequences, cost from the first's start on, the last one's
+        // units); the range
+        struct Found {
+            int64_t off;
+            int lo, hi;
+            SeqUnits u;
+        };
+        Found *found = reinterpret_cast<Found *>(scratch + kThreads / 32);
+        int *out = reinterpret_cast<int *>(found + 2);
         if (lane == 31) scratch[warp] = sum;
-        int *out = reinterpret_cast<int *>(scratch + kThreads / 32);
-        if (tid < 10) out[tid] = tid == 4 ? s.b : 0;
+        if (tid < 2) found[tid].lo = s.b;
         __syncthreads();
         int64_t base = sum - mine, total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
@@ -149,27 +165,34 @@ template <int kUnitCost> struct Sched {
             total += scratch[w];
         }
         const int n_cta = shares<kShare>(total, ctas);
-        if (c < n_cta) {
-            bool none = false;
-#pragma unroll 1
+        if (c < n_cta && mine > 0) {
+#pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int64_t at = border(total, n_cta, c + e);
-                if (at < base || at >= base + mine) continue;  // another thread's, or the end of the last unit
-                int64_t off = at - base;
-                int n = lo;
-                SeqUnits u = units(n, &none);
-                if (hi - lo > 1)  // (else it is this one)
+                if (at >= base && at < base + mine) found[e] = {at - base, lo, hi, u};  // (else another thread's, or the end)
+            }
+        }
+        __syncthreads();
+        if (lane == 0 && warp < 2) {  // a warp each: one after the other took 1500 cycles more
+            const Found f = found[warp];
+            int n = f.lo, x = 0, t = 0, k = 0;
+            if (n < s.b) {
+                bool none = false;
+                u = f.u;
+                int64_t off = f.off;
+                if (f.hi - f.lo > 1) {
+                    u = units(n, &none);
                     for (int64_t w = cost(u); off >= w; w = cost(u)) {
                         off -= w;
                         u = units(++n, &none);
                     }
-                int x, t, k;
+                }
                 locate<kStep, kLeast>(u, off, &x, &t, &k);
-                out[4 * e] = n;
-                out[4 * e + 1] = x;
-                out[4 * e + 2] = t;
-                out[4 * e + 3] = k;
             }
+            out[4 * warp] = n;
+            out[4 * warp + 1] = x;
+            out[4 * warp + 2] = t;
+            out[4 * warp + 3] = k;
         }
         __syncthreads();
         Range r;
