@@ -10,11 +10,12 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+import struct
 
 from . import _lib
 from ._lib import (ATTN_BF16, ATTN_CAUSAL_BOTTOM_RIGHT, ATTN_CAUSAL_TOP_LEFT, ATTN_DQ_ATOMIC, ATTN_DQ_ORDERED,
                    ATTN_DQ_SPLIT, ATTN_E4M3, ATTN_F16, ATTN_F32, ATTN_MASK_NONE, AttnError, attn_nsa_desc_t,
-                   attn_paged_cache_t, attn_paged_seqs_t, attn_qk_norm_desc_t, attn_relbias_t, attn_sdpa_desc_t,
+                   attn_paged_cache_t, attn_qk_norm_desc_t, attn_relbias_t, attn_sdpa_desc_t,
                    attn_view_t, check)
 
 __all__ = ["sdpa_desc", "nsa_desc", "view_bhsd", "view_tnd", "sdpa_workspace_size", "sdpa_fwd_stats",
@@ -428,60 +429,74 @@ def paged_cache(k, v, *, k_scale=None, v_scale=None):
     transposed); float8: k_scale, v_scale fp32 [n_pages, page_size, h_kv], strides alike in both.  The tensors
     are held by the result, and read anew by every call."""
     cache = attn_paged_cache_t()
-    cache.tensors = (k, v, k_scale, v_scale)
+    cache.tensors, cache.as_read = (k, v, k_scale, v_scale), None
     _read_cache(cache)
     return cache
 
 
 def _read_cache(cache):
-    """The pages' addresses, type and strides, as their tensors are now."""
-    torch = _torch()
+    """The pages' addresses, type and strides, as their tensors are now: their memory may have been replaced
+    (tensor.data = ...) since the last call.  The struct is written where something has changed (most of a call's
+    time here goes into its fields)."""
     k, v, ks, vs = cache.tensors
+    now = (k.data_ptr(), v.data_ptr(), k.dtype, v.dtype, k.shape, v.shape, k.stride(), v.stride(), k.get_device(),
+           v.get_device())
+    if ks is not None and vs is not None:
+        now += (ks.data_ptr(), vs.data_ptr(), ks.dtype, vs.dtype, ks.shape, vs.shape, ks.stride(), vs.stride(),
+                ks.get_device(), vs.get_device())
+    if now == cache.as_read:
+        return now[8]
+    torch = _torch()
     code = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16, torch.float8_e4m3fn: ATTN_E4M3}.get(k.dtype)
-    st, dev = k.stride(), k.get_device()
-    if (code is None or k.dim() != 4 or v.dtype is not k.dtype or v.shape != k.shape or v.stride() != st or
-            v.get_device() != dev or (st[3] != 1 and k.shape[3] > 1)):
+    shape, st = k.shape, k.stride()
+    if (code is None or k.dim() != 4 or v.dtype is not k.dtype or v.shape != shape or v.stride() != st or
+            now[8] != now[9] or (st[3] != 1 and shape[3] > 1)):
         raise ValueError("paged_cache: k, v [n_pages, page_size, h_kv, d] of fp16, bf16 or float8_e4m3fn with the same "
-                         f"strides on one device, got {k.dtype} {tuple(k.shape)} {st} and {v.dtype} {tuple(v.shape)} "
+                         f"strides on one device, got {k.dtype} {tuple(shape)} {st} and {v.dtype} {tuple(v.shape)} "
                          f"{v.stride()}")
-    cache.k, cache.v, cache.type = k.data_ptr(), v.data_ptr(), code
-    cache.n_pages, cache.page_size = k.shape[0], k.shape[1]
+    if code == ATTN_E4M3 and (len(now) == 10 or ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or
+                              ks.shape != shape[:3] or vs.shape != ks.shape or vs.stride() != ks.stride() or
+                              now[18] != now[8] or now[19] != now[8]):
+        raise ValueError("paged_cache: float8 pages need k_scale, v_scale fp32 [n_pages, page_size, h_kv] with the "
+                         "same strides on the pages' device")
+    cache.k, cache.v, cache.type = now[0], now[1], code
+    cache.n_pages, cache.page_size = shape[0], shape[1]
     cache.sp, cache.ss, cache.sh = st[0], st[1], st[2]
     if code == ATTN_E4M3:
-        if (ks is None or vs is None or ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or
-                ks.shape != k.shape[:3] or vs.shape != ks.shape or vs.stride() != ks.stride() or
-                ks.get_device() != dev or vs.get_device() != dev):
-            raise ValueError("paged_cache: float8 pages need k_scale, v_scale fp32 [n_pages, page_size, h_kv] with the "
-                             "same strides on the pages' device")
-        cache.k_scale, cache.v_scale = ks.data_ptr(), vs.data_ptr()
+        cache.k_scale, cache.v_scale = now[10], now[11]
         cache.scale_sp, cache.scale_ss, cache.scale_sh = ks.stride()
-    return dev
+    cache.as_read = now
+    return now[8]
+
+
+# an attn_paged_seqs_t's fields (six of 64 bits): packed in a third of the time that a ctypes structure takes
+_pack_seqs = struct.Struct("=QqqQQq").pack
 
 
 def _paged_call(where, desc, cache, page_table, lens, cu_new, tokens, stream):
     """The call on the device of the pages, and its attn_paged_seqs_t."""
-    torch = _torch()
+    int32 = _torch().int32
     call = _Call(where, desc.dtype, _read_cache(cache), stream)
-    k = cache.tensors[0]
-    if k.shape[2] != desc.h_kv or k.shape[3] != desc.d:
-        raise ValueError(f"{where}: pages {tuple(k.shape)}, {desc.h_kv} kv heads of {desc.d}")
-    b = desc.b
-    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != b or
-            page_table.get_device() != call.device or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        call.refuse("page_table", page_table, torch.int32, (b, -1))
-    seqs = attn_paged_seqs_t(page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                             call.ptr("lens", lens, torch.int32, (b,)), call.ptr("cu_new", cu_new, torch.int32, (b + 1,)),
-                             tokens)
-    return call, seqs
+    shape, dev, b = cache.as_read[4], call.device, desc.b
+    if shape[2] != desc.h_kv or shape[3] != desc.d:
+        raise ValueError(f"{where}: pages {tuple(shape)}, {desc.h_kv} kv heads of {desc.d}")
+    ts, st = page_table.shape, page_table.stride()
+    if (page_table.dtype is not int32 or len(ts) != 2 or ts[0] != b or page_table.get_device() != dev or
+            (ts[1] > 1 and st[1] != 1)):
+        call.refuse("page_table", page_table, int32, (b, -1))
+    cu = 0 if cu_new is None else call.ptr("cu_new", cu_new, int32, (b + 1,))
+    return call, _pack_seqs(page_table.data_ptr(), st[0], ts[1], call.ptr("lens", lens, int32, (b,)) or 0, cu,
+                            tokens)
 
 
 def _paged_rows(call, desc, name, x, heads, packed, tokens):
     """View of the new tokens' rows: [B, heads, S_q, D], packed [tokens, heads, D]."""
     if not packed:
         return call.view(name, x, (desc.b, heads, desc.s_q, desc.d))
-    if x.dtype is not call.dtype or x.shape != (tokens, heads, desc.d) or x.get_device() != call.device or x.stride(2) != 1:
+    st = x.stride()
+    if x.dtype is not call.dtype or x.shape != (tokens, heads, desc.d) or x.get_device() != call.device or st[2] != 1:
         call.refuse(name, x, call.dtype, (tokens, heads, desc.d))
-    return attn_view_t(x.data_ptr(), 0, x.stride(1), x.stride(0))
+    return attn_view_t(x.data_ptr(), 0, st[1], st[0])
 
 
 def paged_cache_workspace_size(desc, cache):
@@ -497,7 +512,7 @@ def _paged_copy(where, fn, desc, cache, page_table, lens, k, v, cu_new, workspac
     call, seqs = _paged_call(where, desc, cache, page_table, lens, cu_new, tokens, stream)
     ws = call.workspace(256, workspace)
     views = [_paged_rows(call, desc, n, x, desc.h_kv, packed, tokens) for n, x in (("k", k), ("v", v))]
-    call.run(fn, C.byref(desc), C.byref(cache), C.byref(seqs), *views, ws.data_ptr(), ws.numel())
+    call.run(fn, C.byref(desc), C.byref(cache), seqs, *views, ws.data_ptr(), ws.numel())
     return ws
 
 
@@ -539,8 +554,7 @@ def sdpa_paged_fwd(desc, cache, page_table, lens, q, o, *, lse=None, cu_new=None
     ws = call.workspace(sdpa_paged_workspace_size(desc, cache) if workspace is None else 0, workspace)
     views = [_paged_rows(call, desc, n, x, desc.h, packed, tokens) for n, x in (("q", q), ("o", o))]
     stats = call.ptr("lse", lse, torch.float32, (desc.h, tokens) if packed else (desc.b, desc.h, desc.s_q))
-    call.run(_lib.load().sdpa_paged_fwd, C.byref(desc), C.byref(cache), C.byref(seqs), *views, stats, ws.data_ptr(),
-             ws.numel())
+    call.run(_lib.load().sdpa_paged_fwd, C.byref(desc), C.byref(cache), seqs, *views, stats, ws.data_ptr(), ws.numel())
     return ws
 
 

@@ -90,7 +90,7 @@ def load() -> C.CDLL:
     P, V, S, I = C.POINTER, C.c_void_p, C.c_size_t, C.c_int
     D, N, view = P(attn_sdpa_desc_t), P(attn_nsa_desc_t), attn_view_t
     K, R = P(attn_qk_norm_desc_t), P(attn_relbias_t)
-    G, Q = P(attn_paged_cache_t), P(attn_paged_seqs_t)
+    G = P(attn_paged_cache_t)
     sig = {
         "sdpa_workspace_size": [D, P(S), P(S)],
         "sdpa_fwd_stats": [D, view, view, view, view, P(C.c_float), V, S, V],
@@ -115,10 +115,11 @@ def load() -> C.CDLL:
         "sdpa_relbias_decode_workspace_size": [D, R, P(S)],
         "sdpa_relbias_decode": [D, R, view, view, view, V, view, V, S, V],
         "paged_cache_workspace_size": [D, G, P(S)],
-        "paged_cache_write": [D, G, Q, view, view, V, S, V],
-        "paged_cache_read": [D, G, Q, view, view, V, S, V],
+        # (an attn_paged_seqs_t by its address, or as packed bytes)
+        "paged_cache_write": [D, G, V, view, view, V, S, V],
+        "paged_cache_read": [D, G, V, view, view, V, S, V],
         "sdpa_paged_workspace_size": [D, G, P(S)],
-        "sdpa_paged_fwd": [D, G, Q, view, view, V, V, S, V],
+        "sdpa_paged_fwd": [D, G, V, view, view, V, V, S, V],
         "qk_norm_rope_workspace_size": [K, P(S), P(S)],
         "qk_norm_rope_fwd": [K, view, view, V, V, V, V, V, view, view, V, S, V],
         "qk_norm_rope_bwd": [K, view, view, view, view, V, V, V, V, V, view, view, V, V, V, S, V],
