@@ -17,10 +17,10 @@
 // P overwrites the S it came from; the tensor pipe runs the MMAs in the order they were
 // issued, so S of step j + 2 follows O += P V of step j into the same columns without a wait.
 //
-// A stage of 64 keys is 1 to 4 pages (part of a larger one).  A lane of the producing warp
-// looks up a page, a stage ahead, and issues its TMA boxes.  16 bits: 64 elements x page
-// rows with the 128-byte swizzle, straight to where the MMA reads them.  e4m3: rows of
-// d bytes to a ring of their own, with their scales (4-byte asynchronous copies), from which a
+// A stage is one to eight pages (or part of one).  A lane of the producing warp looks up a
+// page, a stage ahead, and issues its TMA boxes.  16 bits: stages of 128 keys, 64 elements x page
+// rows with the 128-byte swizzle, straight to where the MMA reads them (stages of 64: 930 us for 896,
+// each wait of the MMA thread takes it 100 cycles).  e4m3: stages of 64, rows of d bytes to a ring of their own, with their scales (4-byte asynchronous copies), from which a
 // warpgroup makes 16-bit numbers in the swizzled layout.  Keys unscaled, of the queries'
 // type (e4m3 numbers are 16-bit numbers exactly); their scales multiply S's columns.
 // Values as half-precision numbers, times their scale relative to the stage's largest, rounded up
@@ -55,12 +55,13 @@ using namespace paged;
 
 template <int D, bool kEight, bool kSplit> struct ChunkCfg {
     static constexpr int BM = 128, HN = 64;          // rows of a group, keys of a stage (and of a step)
-    static constexpr int NS = kEight ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 4);  // K and V ring stages
+    static constexpr int SN = kEight ? 64 : 128;     // keys of a K or V stage
+    static constexpr int NS = kEight ? (D == 64 ? 4 : 3) : (D == 64 ? 4 : 2);  // K and V ring stages
     static constexpr int NE = !kEight ? 0 : D == 64 ? 8 : kSplit ? 5 : 3;      // e4m3 ring stages
     static constexpr int NKS = 8;                    // key scales: read until two steps behind S
     static constexpr int THREADS = kEight ? 512 : 384;
     static constexpr int TILE_BYTES = BM * D * 2;    // 128 query rows
-    static constexpr int STAGE_BYTES = HN * D * 2;   // a K or V stage
+    static constexpr int STAGE_BYTES = SN * D * 2;   // a K or V stage
     static constexpr int E_BYTES = HN * D;           // and as e4m3
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + (kSplit ? 1 : 2) * TILE_BYTES;
@@ -146,8 +147,7 @@ template <class T, int D, bool kEight, bool kSplit>
 __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p)
 {
     using Cfg = ChunkCfg<D, kEight, kSplit>;
-    constexpr int BM = Cfg::BM, HN = Cfg::HN, NS = Cfg::NS, NE = Cfg::NE, NKS = Cfg::NKS;
-    constexpr int kStage = kSplit ? 2 : 1;  // stages of a step
+    constexpr int BM = Cfg::BM, HN = Cfg::HN, SN = Cfg::SN, NS = Cfg::NS, NE = Cfg::NE, NKS = Cfg::NKS;
     constexpr int kType = std::is_same<T, __half>::value ? 0 : 1;
     using P16 = typename std::conditional<kEight, __half, T>::type;  // type of P and V
 
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         Steps st;
         if (kSplit) {
             st.s0 = st.s1 = st.n = (w.k1 - w.k0 + 2 * HN - 1) / (2 * HN);
-            st.stages = 2 * st.n;
+            st.stages = kEight ? 2 * st.n : st.n;
             return st;
         }
         auto of = [&](int grp) -> int {
@@ -239,12 +239,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         st.s0 = of(0);
         st.s1 = of(1);
         st.n = st.s0 > st.s1 ? st.s0 : st.s1;
-        st.stages = st.n;
+        st.stages = kEight ? st.n : (st.n + 1) / 2;
         return st;
     };
+    // stage of a step's keys, from the piece's first on, and which half of it (e4m3: it has but one)
+    auto stage_of = [](int j, int grp) { return kEight ? (kSplit ? 2 * j + grp : j) : kSplit ? j : j >> 1; };
+    auto half_of = [](int j, int grp) { return kEight ? 0 : kSplit ? grp : j & 1; };
 
-    // (e4m3: 512 threads are launched with 128 registers each; the warpgroups' shares add up to that)
-    constexpr uint32_t kRegsIssue = 72, kRegsSoftmax = 160, kRegsConvert = 120;
+    // (e4m3: 512 threads are launched with 128 registers each; the warpgroups' shares add up to that.  The MMA thread's
+    // count: 2048 tokens on 32768 with 72 registers 1422 us, 96: 1287, 112: 1222, 128: 1310, when the softmax has too few)
+    constexpr uint32_t kRegsIssue = 112, kRegsSoftmax = 152, kRegsConvert = 96;
     static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert == 4 * 128, "register shares");
     if (warp < 4) {
         if (kEight) regs_decrease<kRegsIssue>();
@@ -255,8 +259,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
             uint64_t *full = kEight ? e_full + (isk ? 0 : NE) : isk ? k_full : v_full;
             uint64_t *empty = kEight ? e_empty + (isk ? 0 : NE) : isk ? k_empty : v_empty;
             const CUtensorMap *tm = isk ? &p.tm_k : &p.tm_v;
-            const int in_page = (1 << cache.shift) - 1, pr = cache.shift < 6 ? 1 << cache.shift : HN;  // keys of a box
-            const int boxes = HN / pr;
+            const int in_page = (1 << cache.shift) - 1, pr = 1 << cache.shift < SN ? 1 << cache.shift : SN;  // keys of a box
+            const int boxes = SN / pr;
             if (lane == 0) {
                 prefetch_tmap(tm);
                 if (isk) prefetch_tmap(&p.tm_q);
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                     }
                 }
                 for (int j = 0; j < st.stages; ++j) {
-                    const int k0 = w.k0 + j * HN, next = page_of(k0 + HN);
+                    const int k0 = w.k0 + j * SN, next = page_of(k0 + SN);
                     if (n_stage >= uint32_t(NR)) wait(&empty[s], par);
                     if (!ok) break;
                     ++n_stage;
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                         } else {
                             uint8_t *dst = (isk ? sK(s) : sV(s)) + lane * pr * 128;
                             for (int c = 0; c < D / 64; ++c)
-                                tma_load_4d(dst + c * HN * 128, tm, &full[s], c * 64, key & in_page, w.x, page);
+                                tma_load_4d(dst + c * SN * 128, tm, &full[s], c * 64, key & in_page, w.x, page);
                         }
                     }
                     if (kEight) {  // scales of keys lane and lane + 32; 0 behind the piece's end
@@ -354,8 +358,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 if (ok && !mbar_test_wait(bar, parity) && !(ok = chunk_wait_slow(bar, parity, abort))) flag_abort(abort, nullptr);
                 tc_fence_after();
             };
-            const uint64_t kQ = desc_kmaj(smem_u32(sQ), BM, 0), kK = desc_kmaj(smem_u32(sK(0)), HN, 0);
-            const uint64_t mV = desc_mn(smem_u32(sV(0)), HN, 0);
+            const uint64_t kQ = desc_kmaj(smem_u32(sQ), BM, 0), kK = desc_kmaj(smem_u32(sK(0)), SN, 0);
+            const uint64_t mV = desc_mn(smem_u32(sV(0)), SN, 0);
             uint32_t ks = 0, vs = 0, k_par = 0, v_par = 0, q_par = 0, p_par = 0;  // p_par: bit 2 group + buffer
             Walk<kChunkCost> w(sched, *range);
             while (w.next()) {
@@ -382,37 +386,40 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 };
                 auto round = [&](int j, auto sb_tag) {
                     constexpr int sb = decltype(sb_tag)::value, xb = sb ^ 1;
+                    // a stage is waited for by its first user and released by its last: a group of its own (e4m3, kSplit),
+                    // both groups of a step, or both groups of two steps
+                    constexpr bool kOwn = kEight && kSplit, kTwo = !kEight && !kSplit;
                     if (j < n_steps) {
-                        if (!kSplit) wait(&k_full[ks], k_par);
+                        if (!kOwn && (!kTwo || sb == 0)) wait(&k_full[ks], k_par);
 #pragma unroll
                         for (int grp = 0; grp < 2; ++grp) {
                             if (j >= (grp ? steps1 : steps0)) continue;
-                            if (kSplit) wait(&k_full[ks], k_par);
+                            if (kOwn) wait(&k_full[ks], k_par);
                             if (ok) {
-                                const uint64_t dk = kK + ks * STAGE, dq = kQ + (kSplit ? 0 : grp * QROWS);
+                                const uint64_t dk = kK + ks * STAGE + half_of(sb, grp) * (HN * 128 / 16), dq = kQ + (kSplit ? 0 : grp * QROWS);
 #pragma unroll
                                 for (int kk = 0; kk < D / 16; ++kk)
-                                    mma_f16_ss(tmem + Cfg::T_S + grp * 128 + sb * 64, kmaj_step(dq, BM, kk), kmaj_step(dk, HN, kk), idS,
+                                    mma_f16_ss(tmem + Cfg::T_S + grp * 128 + sb * 64, kmaj_step(dq, BM, kk), kmaj_step(dk, SN, kk), idS,
                                                kk > 0);
                                 mma_commit(&s_full[grp * 2 + sb]);
                             }
-                            if (kSplit) k_next();
+                            if (kOwn) k_next();
                         }
-                        if (!kSplit) k_next();
+                        if (!kOwn && (!kTwo || sb || j == n_steps - 1)) k_next();
                         if (ok && j == n_steps - 1) mma_commit(q_empty);
                     }
                     if (j > 0) {
                         const int x = j - 1;
-                        if (!kSplit) wait(&v_full[vs], v_par);
+                        if (!kOwn && (!kTwo || xb == 0)) wait(&v_full[vs], v_par);
 #pragma unroll
                         for (int grp = 0; grp < 2; ++grp) {
                             const int steps = grp ? steps1 : steps0;
                             if (x >= steps) continue;
-                            if (kSplit) wait(&v_full[vs], v_par);
+                            if (kOwn) wait(&v_full[vs], v_par);
                             wait(&p_full[grp * 2 + xb], p_par >> (grp * 2 + xb) & 1);
                             p_par ^= 1u << (grp * 2 + xb);
                             if (ok) {
-                                const uint64_t dv = mV + vs * STAGE;
+                                const uint64_t dv = mV + vs * STAGE + half_of(xb, grp) * (HN / 16) * 128;
 #pragma unroll
                                 for (int kk = 0; kk < HN / 16; ++kk)
                                     mma_f16_ts(tmem + Cfg::T_O + grp * D, tmem + Cfg::T_S + grp * 128 + xb * 64 + kk * 8,
@@ -420,9 +427,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                                 // (earlier ones are behind S of step x + 2)
                                 if (x >= steps - 2) mma_commit(x == steps - 1 ? &o_last[grp] : &o_prev[grp]);
                             }
-                            if (kSplit) v_next();
+                            if (kOwn) v_next();
                         }
-                        if (!kSplit) v_next();
+                        if (!kOwn && (!kTwo || xb || x == n_steps - 1)) v_next();
                     }
                 };
                 for (int j = 0; j <= n_steps; j += 2) {
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
             const int ti = w.t * sched.tokens + (kSplit ? 0 : grp * p.tokens) + row_tok;  // the row's new token
             const bool row_ok = row_tok < p.tokens && ti < w.u.m;
             // step j's first key is kfirst + j kstep, of which this row sees those up to kmax
-            constexpr int kstep = kStage * HN;
+            constexpr int kstep = kSplit ? 2 * HN : HN;
             const int kfirst = w.k0 + (kSplit ? grp * HN : 0);
             const int kmax = !row_ok ? -1 : a.causal ? w.u.len - w.u.m + ti : w.u.len - 1;
             float m_ref = -INFINITY, l = 0.f, l_lost = 0.f;  // l: sum of P, and what its additions have rounded off
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 const uint32_t tS = tmem + lane_addr + Cfg::T_S + grp * 128 + sb * 64;
                 const int lim = kmax - kfirst - j * kstep;  // columns <= lim are visible
                 const bool whole = __all_sync(0xffffffffu, lim >= HN - 1);
-                const uint32_t stage = k_base + kStage * j + (kSplit ? grp : 0);
+                const uint32_t stage = k_base + stage_of(j, grp);
                 if (kEight) wait(&ks_full[stage % NKS], (stage / NKS) & 1);
                 wait(&s_full[grp * 2 + sb], s_par >> sb & 1);
                 s_par ^= 1u << sb;
@@ -574,10 +581,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                     if (!kEight && kfirst + j * kstep + HN > w.u.len) {  // values from the sequence's end on
                         const uint32_t s = stage % NS;
                         wait(&v_full[s], (stage / NS) & 1);
+                        const int row = half_of(j, grp) * HN + r;  // of the stage
                         if (r < HN && kfirst + j * kstep + r >= w.u.len)
                             for (int q = 0; q < D / 64; ++q)
                                 for (int e = 0; e < 8; ++e)
-                                    st_shared_v4(smem_u32(sV(s)) + q * HN * 128 + r * 128 + e * 16, 0, 0, 0, 0);
+                                    st_shared_v4(smem_u32(sV(s)) + q * SN * 128 + row * 128 + e * 16, 0, 0, 0, 0);
                         fence_proxy_async_smem();
                     }
                 }
@@ -762,7 +770,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 
 namespace {
 
-// Pages [n_pages][h_kv][page][d]: boxes of up to 64 tokens x 64 16-bit elements or d e4m3 ones, with the swizzle of the box's
+// Pages [n_pages][h_kv][page][d]: boxes of up to 128 tokens x 64 16-bit elements or 64 x d e4m3 ones, with the swizzle of the box's
 // width.
 bool tmap_pages(CUtensorMap *m, void *ptr, const PagedCache &c, int dtype, int d, int h_kv)
 {
@@ -772,7 +780,7 @@ bool tmap_pages(CUtensorMap *m, void *ptr, const PagedCache &c, int dtype, int d
     const int page = 1 << c.shift, size = eight ? 1 : 2;
     cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page), cuuint64_t(h_kv), cuuint64_t(c.none)};
     cuuint64_t strides[3] = {cuuint64_t(c.ss) * size, cuuint64_t(c.sh) * size, cuuint64_t(c.sp) * size};
-    cuuint32_t box[4] = {cuuint32_t(eight ? d : 64), cuuint32_t(page < 64 ? page : 64), 1, 1};
+    cuuint32_t box[4] = {cuuint32_t(eight ? d : 64), cuuint32_t(page < (eight ? 64 : 128) ? page : (eight ? 64 : 128)), 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     const CUtensorMapDataType type = eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : dtype == ATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
