@@ -86,7 +86,7 @@ template <int D, bool kEight, bool kSplit> struct ChunkCfg {
 };
 
 // What a unit's start and end take, in keys; pieces of fewer than kLeast keys are avoided; a share worth a start.
-constexpr int kChunkCost = 256, kChunkLeast = 256, kChunkShare = 512;
+constexpr int kChunkCost = 256, kChunkLeast = 512, kChunkShare = 1024;
 
 struct ChunkParams {
     CUtensorMap tm_q, tm_k, tm_v;

@@ -591,16 +591,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
     if (threadIdx.x == 0) a.flags[blockIdx.x] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
 }
 
-// Outputs of the units that several shares hold: a block for every share that may hold a unit's first piece, every 8 rows
-// and every COLS columns, COLS / 4 lanes a row.  Groups of lanes take every kGroups-th piece; a row's group sums are added
-// in order.  Three round trips to L2: the records of the next shares side by side, the pieces' maxima side by side,
-// their outputs several at a time.  The first block gathers the call's status.
-template <class T, int D, int COLS>
+// Outputs of the units that several shares hold: a block for every share that may hold a unit's first piece, some of its
+// rows (RPT a thread) and COLS columns, COLS / 4 lanes a row.  kGroups groups of lanes take every kGroups-th piece; a row's
+// group sums are added in order.  Three round trips to L2: the records of the next shares side by side, the pieces'
+// maxima and sums side by side, their outputs several at a time.  The first block gathers the call's status.
+// (Rows of the tensor-core kernel: 32 or 64 a block, one wave of blocks; 8 a block, four waves, took 25 us behind 2048
+// tokens on 32768 where this takes REPLACEJ.)
+template <class T, int D, int COLS, int RPT>
 __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, const PagedShape shape)
 {
-    constexpr int LPR = COLS / 4, kGroups = kJoin / (8 * LPR), kBatch = 32;
-    __shared__ float sm_m[8], sm_f[kBatch][8], sm_s[kBatch][8], sm_l[kGroups][8];
-    __shared__ float4 sm_o[kGroups][8][LPR];
+    constexpr int LPR = COLS / 4, kGroups = RPT > 1 ? 1 : kJoin / (8 * LPR), SLOTS = kJoin / LPR / kGroups, ROWS = SLOTS * RPT;
+    constexpr int kBatch = kJoin / ROWS;  // pieces whose maxima and sums are fetched at once
+    __shared__ float2 sm_ml[kBatch][ROWS];
+    __shared__ float sm_l[kGroups][SLOTS];
+    __shared__ float4 sm_o[kGroups][SLOTS][LPR];
     const int c0 = blockIdx.x, shares = shape.shares, rows = shape.rows, t = threadIdx.x, lane = t % 32;
     pdl_wait();
     if (c0 == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
@@ -614,76 +618,89 @@ __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant
     int next = c0 + 1 + lane < shares ? a.rec[2 * (c0 + 1 + lane)].w : kEnds;
     if (name.w == kNone) return;
     int end = c0 + 1;
-    for (uint32_t found; (found = __ballot_sync(0xffffffffu, next == kEnds)) == 0;) {
+    while (__ballot_sync(0xffffffffu, next == kEnds) == 0) {
         end += 32;
         next = end + lane < shares ? a.rec[2 * (end + lane)].w : kEnds;
-        if (end >= shares) break;
     }
     end += __ffs(__ballot_sync(0xffffffffu, next == kEnds)) - 1;
     const int n = (end < shares ? end : shares - 1) - c0 + 1;  // pieces (a share in between may hold none)
 
-    const int G = a.h / a.h_kv, kvh = name.y / shape.row_blocks, block = name.y - kvh * shape.row_blocks;
-    bool none = false;
-    int first, m;
-    a.seqs.rows(name.x, &first, &m, &none);
-    const int row = t / LPR % 8, grp = t / (8 * LPR), col = blockIdx.z * COLS + t % LPR * 4, r0 = blockIdx.y * 8;
-    const float *po = a.part_o + (int64_t(c0) * 2 + 1) * rows * D + int64_t(r0 + row) * D + col;
-    const int64_t step = 2 * int64_t(rows) * D;  // from a share's first result to the next one's
-    auto ml = [&](int k, int r) -> float2 {       // maximum and sum of piece k
-        if (k > 0 && a.rec[2 * (c0 + k)].w == kNone) return make_float2(-INFINITY, 0.f);
-        return a.part_ml[(int64_t(c0 + k) * 2 + (k == 0)) * rows + r0 + r];
+    const int slot = t / LPR % SLOTS, grp = t / (SLOTS * LPR), col = blockIdx.z * COLS + t % LPR * 4, r0 = blockIdx.y * ROWS;
+    const int64_t step = 2 * int64_t(rows);  // rows from a share's results to the next one's
+    auto row_of = [&](int k, int r) { return (int64_t(c0) * 2 + (k == 0)) * rows + k * step + r0 + r; };
+    auto fetch = [&](int k0, int here) {  // maxima and sums of pieces k0 ..
+        const int k = t / ROWS, r = t % ROWS;
+        if (k < here)
+            sm_ml[k][r] = k0 + k > 0 && a.rec[2 * (c0 + k0 + k)].w == kNone ? make_float2(-INFINITY, 0.f) : a.part_ml[row_of(k0 + k, r)];
+        __syncthreads();
     };
-    // the rows' maxima: warp w row w (kJoin / 32 warps)
-    for (int r = t / 32; r < 8; r += kJoin / 32) {
-        float mm = -INFINITY;
-        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, ml(k, r).x);
+    float mm[RPT], ll[RPT];
+    float4 o[RPT];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-        if (lane == 0) sm_m[r] = mm;
+    for (int i = 0; i < RPT; ++i) {
+        mm[i] = -INFINITY;
+        ll[i] = 0.f;
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __syncthreads();
-    const float mm = sm_m[row];
-    float ll = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < n; k0 += kBatch) {
         const int here = n - k0 < kBatch ? n - k0 : kBatch;
         if (k0 > 0) __syncthreads();
-        for (int x = t; x < here * 8; x += kJoin) {
-            const int r = x % 8;
-            const float2 y = ml(k0 + x / 8, r);
-            sm_f[x / 8][r] = y.y != y.y ? y.y : y.x == -INFINITY ? 0.f : ex2f(y.x - sm_m[r]);  // (NaN stays NaN)
-            sm_s[x / 8][r] = y.y;
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int k = grp; k < here; k += kGroups) {
-            const float f = sm_f[k][row];
-            const float4 u = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                      : *reinterpret_cast<const float4 *>(po + (k0 + k) * step - (k0 + k > 0 ? int64_t(rows) * D : 0));
-            o.x = fmaf(f, u.x, o.x); o.y = fmaf(f, u.y, o.y); o.z = fmaf(f, u.z, o.z); o.w = fmaf(f, u.w, o.w);
-            ll = fmaf(f, sm_s[k][row], ll);
-        }
-    }
-    if (t % LPR == 0) sm_l[grp][row] = ll;
-    sm_o[grp][row][t % LPR] = o;
-    __syncthreads();
-    if (grp > 0) return;
-    ll = sm_l[0][row];
+        fetch(k0, here);
+        for (int k = 0; k < here; ++k)
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) {
-        const float4 u = sm_o[k][row][t % LPR];
-        o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
-        ll += sm_l[k][row];
+            for (int i = 0; i < RPT; ++i) mm[i] = fmaxf(mm[i], sm_ml[k][slot + i * SLOTS].x);
     }
-    const int group_rows = rows / shape.groups, r = r0 + row, g = r / group_rows, in = r - g * group_rows, tok = in / shape.heads;
-    const int x = block * shape.heads + in - tok * shape.heads, head = kvh * G + x;
-    const int ti = (name.z * shape.groups + g) * shape.tokens + tok;
-    if (tok >= shape.tokens || ti >= m || x >= G) return;
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    T *dst = static_cast<T *>(a.o.ptr) + (a.seqs.cu ? int64_t(first + ti) * a.o.ss : name.x * a.o.sb + ti * a.o.ss) + head * a.o.sh;
-    *reinterpret_cast<uint2 *>(dst + col) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-    if (a.lse && col == 0)
-        a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + first + ti : (int64_t(name.x) * a.h + head) * a.seqs.s_q + ti] = lse_of(mm, ll);
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+        const int here = n - k0 < kBatch ? n - k0 : kBatch;
+        if (n > kBatch) {
+            __syncthreads();
+            fetch(k0, here);
+        }
+#pragma unroll 4
+        for (int k = grp; k < here; k += kGroups)
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const int r = slot + i * SLOTS;
+                const float2 x = sm_ml[k][r];
+                const float f = x.y != x.y ? x.y : x.x == -INFINITY ? 0.f : ex2f(x.x - mm[i]);  // (NaN stays NaN)
+                const float4 u = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                          : *reinterpret_cast<const float4 *>(a.part_o + row_of(k0 + k, r) * D + col);
+                o[i].x = fmaf(f, u.x, o[i].x); o[i].y = fmaf(f, u.y, o[i].y);
+                o[i].z = fmaf(f, u.z, o[i].z); o[i].w = fmaf(f, u.w, o[i].w);
+                ll[i] = fmaf(f, x.y, ll[i]);
+            }
+    }
+    if (kGroups > 1) {
+        if (t % LPR == 0) sm_l[grp][slot] = ll[0];
+        sm_o[grp][slot][t % LPR] = o[0];
+        __syncthreads();
+        if (grp > 0) return;
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) {
+            const float4 u = sm_o[k][slot][t % LPR];
+            o[0].x += u.x; o[0].y += u.y; o[0].z += u.z; o[0].w += u.w;
+        }
+        ll[0] = sm_l[0][slot];
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) ll[0] += sm_l[k][slot];
+    }
+    const int G = a.h / a.h_kv, kvh = name.y / shape.row_blocks, block = name.y - kvh * shape.row_blocks, group_rows = rows / shape.groups;
+    bool none = false;
+    int first, m;
+    a.seqs.rows(name.x, &first, &m, &none);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + slot + i * SLOTS, g = r / group_rows, in = r - g * group_rows, tok = in / shape.heads;
+        const int x = block * shape.heads + in - tok * shape.heads, head = kvh * G + x;
+        const int ti = (name.z * shape.groups + g) * shape.tokens + tok;
+        if (tok >= shape.tokens || ti >= m || x >= G) continue;
+        const float inv = ll[i] == 0.f ? 0.f : 1.f / ll[i];
+        T *dst = static_cast<T *>(a.o.ptr) + (a.seqs.cu ? int64_t(first + ti) * a.o.ss : name.x * a.o.sb + ti * a.o.ss) + head * a.o.sh;
+        *reinterpret_cast<uint2 *>(dst + col) = make_uint2(pack2<T>(o[i].x * inv, o[i].y * inv), pack2<T>(o[i].z * inv, o[i].w * inv));
+        if (a.lse && col == 0)
+            a.lse[a.seqs.cu ? int64_t(head) * a.seqs.tokens + first + ti : (int64_t(name.x) * a.h + head) * a.seqs.s_q + ti] =
+                lse_of(mm[i], ll[i]);
+    }
 }
 
 // Pages [n_pages][h_kv][page][d] in boxes of up to `keys` tokens x `bytes` bytes, swizzled over that width or not.
@@ -752,10 +769,14 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a, const PagedShape &p, cud
 namespace {
 template <class T, int D> cudaError_t join(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    // many blocks for the few rows of the small kernel, whose units may have hundreds of pieces
-    const dim3 grid(unsigned(p.shares), unsigned(p.rows / 8), p.chunk ? 1u : unsigned(D / 32));
-    if (p.chunk) return launch_kernel(paged_join_kernel<T, D, D>, grid, dim3(kJoin), 0, s, true, a, p);
-    return launch_kernel(paged_join_kernel<T, D, 32>, grid, dim3(kJoin), 0, s, true, a, p);
+    if (p.chunk) {
+        constexpr int RPT = 4, ROWS = kJoin / (D / 4) * RPT;
+        return launch_kernel(paged_join_kernel<T, D, D, RPT>, dim3(unsigned(p.shares), unsigned(p.rows / ROWS)), dim3(kJoin), 0, s, true,
+                             a, p);
+    }
+    // (many blocks for the few rows of the small kernel, whose units may have hundreds of pieces)
+    return launch_kernel(paged_join_kernel<T, D, 32, 1>, dim3(unsigned(p.shares), unsigned(p.rows / 8), unsigned(D / 32)), dim3(kJoin), 0,
+                         s, true, a, p);
 }
 }  // namespace
 
