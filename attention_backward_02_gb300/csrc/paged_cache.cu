@@ -9,9 +9,10 @@
 // relative to it.)  Both factors are rounded fp32 quotients, so a row's codes do not
 // depend on how it is shared out.
 //
-// Bound by HBM: a row is read once and written once.  A lane takes 16 bytes of the 16-bit side (8 elements; 8 of
-// the 8-bit side), d / 8 lanes a row.  A block takes a run of rows in the order token, keys and values, head, up to
-// eight a lane group; the write's are all loaded before the places in the cache are looked up (cumulative
+// Bound by HBM: a row is read once and written once; what has to be kept low for that is the instructions a row takes
+// (with 8 elements a lane 116 for 16 bytes of 32 lanes, and 75 % of the issue slots).  A lane takes two pieces of a row, 16
+// bytes of the 16-bit side each (8 elements; 8 bytes of the 8-bit side), d / 16 lanes a row.  A block takes a run of rows in the order token, keys and values, head, up to
+// four a lane group; the write's are all loaded before the places in the cache are looked up (cumulative
 // counts, length, page id: three dependent loads), the read's behind it.
 #include <cstring>
 #include <type_traits>
@@ -22,7 +23,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMost = 8;           // rows of a lane group in a block
+constexpr int kMost = 4;           // rows of a lane group in a block
 constexpr float kTop = 448.f;
 constexpr float kFloor = 0x1p-110f;
 
@@ -109,11 +110,11 @@ template <class T, bool kFinite> __device__ __forceinline__ float most_of(const 
 }
 
 // T: the dense rows' type; kEight: e4m3 cache (else T); a block takes `most` rows, at most kMost a lane group.  A lane
-// group's rows are kThreads / (D / 8) apart, which is step_t tokens and step_r rows of one.
+// group's rows are kThreads / (D / 16) apart, which is step_t tokens and step_r rows of one.
 template <class T, bool kEight, int D, bool kWrite>
 __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_constant__ PagedCopyArgs a, int most, int step_t, int step_r)
 {
-    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    constexpr int LPR = D / 16, GROUPS = kThreads / LPR, HALF = D / 2;
     constexpr int kTokens = GROUPS * kMost / 2 + 1;            // that a block's rows may belong to
     constexpr int kNone = -1, kNotOurs = -2;                   // page: no place; no sequence's row
     __shared__ int64_t sm_dense[2][kTokens], sm_place[kTokens], sm_scale[kTokens];  // element offsets of head 0
@@ -155,12 +156,18 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_const
     };
     const int count = rows > group ? (rows - group + GROUPS - 1) / GROUPS : 0;
 
-    uint4 x[kMost];
+    uint4 x[kMost][2];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     if (kWrite) {
         At at = at0;
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
-            x[i] = i < count ? __ldcs(reinterpret_cast<const uint4 *>(dense(at))) : make_uint4(0, 0, 0, 0);
+            x[i][0] = x[i][1] = zero;
+            if (i < count) {
+                const T *src = dense(at);
+                x[i][0] = __ldcs(reinterpret_cast<const uint4 *>(src));
+                x[i][1] = __ldcs(reinterpret_cast<const uint4 *>(src + HALF));
+            }
             next(at);
         }
     }
@@ -197,46 +204,55 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_const
             if (!kEight) {
                 if (on) {
                     const Place p = place(at);
-                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.side ? a.cache.v : a.cache.k) + p.at) = x[i];
+                    T *dst = static_cast<T *>(p.side ? a.cache.v : a.cache.k) + p.at;
+                    *reinterpret_cast<uint4 *>(dst) = x[i][0];
+                    *reinterpret_cast<uint4 *>(dst + HALF) = x[i][1];
                 }
                 continue;
             }
-            float top = most_of<T, false>(x[i]);
-            if (__any_sync(0xffffffffu, top == INFINITY)) top = most_of<T, true>(x[i]);
+            float top = fmaxf(most_of<T, false>(x[i][0]), most_of<T, false>(x[i][1]));
+            if (__any_sync(0xffffffffu, top == INFINITY)) top = fmaxf(most_of<T, true>(x[i][0]), most_of<T, true>(x[i][1]));
             top = fmaxf(top, kFloor);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float up = kTop / top;
-            uint16_t c[4];
+            uint32_t c[2][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 y = unpack2<T>(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w);
-                c[e] = to_e4m3x2(y.x * up, y.y * up);
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 y = unpack2<T>(e ? x[i][h].z : x[i][h].x), z = unpack2<T>(e ? x[i][h].w : x[i][h].y);
+                    c[h][e] = to_e4m3x2(y.x * up, y.y * up) | uint32_t(to_e4m3x2(z.x * up, z.y * up)) << 16;
+                }
             if (on) {
                 const Place p = place(at);
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.side ? a.cache.v : a.cache.k) + p.at) =
-                    make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
+                uint8_t *dst = static_cast<uint8_t *>(p.side ? a.cache.v : a.cache.k) + p.at;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0][0], c[0][1]);
+                *reinterpret_cast<uint2 *>(dst + HALF) = make_uint2(c[1][0], c[1][1]);
                 if (l == 0) (p.side ? a.cache.v_scale : a.cache.k_scale)[p.scale] = top / kTop;
             }
         }
     } else {
-        uint2 c[kMost];
+        uint2 c[kMost][2];
         float size[kMost];
 #pragma unroll
         for (int i = 0; i < kMost; ++i, next(at)) {
             const bool on = i < count && sm_page[i < count ? at.t : 0] >= 0;
-            x[i] = make_uint4(0, 0, 0, 0);
-            c[i] = make_uint2(0, 0);
+            x[i][0] = x[i][1] = zero;
+            c[i][0] = c[i][1] = make_uint2(0, 0);
             size[i] = 0.f;
             if (!on) continue;
             const Place p = place(at);
             const void *pool = p.side ? a.cache.v : a.cache.k;
             if (kEight) {
-                c[i] = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + p.at));
+                const uint8_t *src = static_cast<const uint8_t *>(pool) + p.at;
+                c[i][0] = __ldcs(reinterpret_cast<const uint2 *>(src));
+                c[i][1] = __ldcs(reinterpret_cast<const uint2 *>(src + HALF));
                 size[i] = __ldg((p.side ? a.cache.v_scale : a.cache.k_scale) + p.scale);
             } else {
-                x[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(pool) + p.at));
+                const T *src = static_cast<const T *>(pool) + p.at;
+                x[i][0] = __ldcs(reinterpret_cast<const uint4 *>(src));
+                x[i][1] = __ldcs(reinterpret_cast<const uint4 *>(src + HALF));
             }
         }
         at = at0;
@@ -244,16 +260,20 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_const
         for (int i = 0; i < kMost; ++i, next(at)) {
             if (i >= count) break;
             if (sm_page[at.t] == kNotOurs) continue;
-            if (kEight) {
-                uint32_t w[4];
+            T *dst = dense(at);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 y = from_e4m3x2(uint16_t((e < 2 ? c[i].x : c[i].y) >> (16 * (e & 1))));
-                    w[e] = pack2<T>(y.x * size[i], y.y * size[i]);
+            for (int h = 0; h < 2; ++h) {
+                if (kEight) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = from_e4m3x2(uint16_t((e < 2 ? c[i][h].x : c[i][h].y) >> (16 * (e & 1))));
+                        w[e] = pack2<T>(y.x * size[i], y.y * size[i]);
+                    }
+                    x[i][h] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                __stcs(reinterpret_cast<uint4 *>(dst + h * HALF), x[i][h]);
             }
-            __stcs(reinterpret_cast<uint4 *>(dense(at)), x[i]);
         }
     }
     if (blockIdx.x == 0) check_call(a.seqs, a.cache, a.status);  // the call's only status writer
@@ -262,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_const
 template <class T, bool kEight, int D> cudaError_t run(const PagedCopyArgs &a, bool write, cudaStream_t s)
 {
     // as many rows a lane group as leave four blocks an SM
-    constexpr int GROUPS = kThreads / (D / 8);
+    constexpr int GROUPS = kThreads / (D / 16);
     const int all = a.seqs.tokens * 2 * a.h_kv, share = (all + 4 * kPagedCtas - 1) / (4 * kPagedCtas);
     int most = (share + GROUPS - 1) / GROUPS;
     most = (most < 1 ? 1 : most > kMost ? kMost : most) * GROUPS;
