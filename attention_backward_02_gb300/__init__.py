@@ -489,6 +489,12 @@ def _paged_call(where, desc, cache, page_table, lens, cu_new, tokens, stream):
                             tokens)
 
 
+def _packed_tokens(where, x):
+    if type(x) is attn_view_t:
+        raise ValueError(f"{where}: packed rows are passed as [T, heads, D] tensors")
+    return x.shape[0]
+
+
 def _paged_rows(call, desc, name, x, heads, packed, tokens):
     """View of the new tokens' rows: [B, heads, S_q, D], packed [tokens, heads, D]."""
     if not packed:
@@ -508,7 +514,7 @@ def paged_cache_workspace_size(desc, cache):
 
 def _paged_copy(where, fn, desc, cache, page_table, lens, k, v, cu_new, workspace, stream):
     packed = cu_new is not None
-    tokens = k.shape[0] if packed else 0
+    tokens = _packed_tokens(where, k) if packed else 0
     call, seqs = _paged_call(where, desc, cache, page_table, lens, cu_new, tokens, stream)
     ws = call.workspace(256, workspace)
     views = [_paged_rows(call, desc, n, x, desc.h_kv, packed, tokens) for n, x in (("k", k), ("v", v))]
@@ -549,7 +555,7 @@ def sdpa_paged_fwd(desc, cache, page_table, lens, q, o, *, lse=None, cu_new=None
     attn_query_status."""
     torch = _torch()
     packed = cu_new is not None
-    tokens = q.shape[0] if packed else 0
+    tokens = _packed_tokens("sdpa_paged_fwd", q) if packed else 0
     call, seqs = _paged_call("sdpa_paged_fwd", desc, cache, page_table, lens, cu_new, tokens, stream)
     ws = call.workspace(sdpa_paged_workspace_size(desc, cache) if workspace is None else 0, workspace)
     views = [_paged_rows(call, desc, n, x, desc.h, packed, tokens) for n, x in (("q", q), ("o", o))]

@@ -26,6 +26,7 @@ class Problem:
         self.dt = dt = torch.float16 if dtype == "float16" else torch.bfloat16
         self.lens, self.new = list(lens), list(new)
         self.h, self.hk, self.d, self.page, self.packed, self.causal, self.eight = h, hk, d, page, packed, causal, cache == "e4m3"
+        self.scale = d ** -0.5
         b = len(self.lens)
         self.cap = cap if cap is not None else max(1, max(self.lens))
         g = torch.Generator().manual_seed(seed)
@@ -146,9 +147,9 @@ class Problem:
                 upto = max(upto, 0)
                 q = self.q[rows].double().numpy()
                 if not self.causal:
-                    ref, rl, p, mag, s = P.attention(q, k, v, self.d ** -0.5, False)
+                    ref, rl, p, mag, s = P.attention(q, k, v, self.scale, False)
                 else:
-                    ref, rl, p, mag, s = P.attention(q, k[:upto], v[:upto], self.d ** -0.5, True)
+                    ref, rl, p, mag, s = P.attention(q, k[:upto], v[:upto], self.scale, True)
                 e = (self.d + 8) * U * (mag + np.abs(s) + np.abs(s).max(-1, initial=0, keepdims=True))
                 e = e.max(-1, initial=0)
                 w = hf + (2.0 ** -10 if self.eight else 0) + 2 * e + 2.0 ** -20 + len(k) * U

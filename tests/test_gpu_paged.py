@@ -195,6 +195,48 @@ def test_attention_parity(case):
     assert torch.equal(o.nan_to_num(9), alone.nan_to_num(9))
 
 
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [-0.17, 0.0, 3.0])
+def test_scales_of_every_sign(cache, new, scale):
+    """A negative scale, one of zero (the mean of the visible values) and a large one."""
+    p = Problem("bfloat16", cache, [200, 77], [new, new], 4, 2, 64, packed=False, seed=11)
+    p.desc.scale = scale
+    p.scale = scale
+    p.check(*p.attend())
+
+
+@pytest.mark.parametrize("new", [3, 50])
+def test_padded_in_front_and_queries_by_head(new):
+    """Fixed-length calls whose sequences have fewer cached tokens than new ones, with [B, h, S, D] storage."""
+    import torch
+    p = Problem("float16", "e4m3", [2, 0, 60], [new] * 3, 8, 2, 128, packed=False, seed=12)
+    q = p.dense(p.q).contiguous()
+    o, lse = p.attend(q=q, o=torch.full_like(q, float("nan")))
+    p.check(o, lse)
+    x = _rows(p, 13)
+    ws = p.ab.paged_cache_write(p.desc, p.cache, p.dtable, p.dlens, p.dense(x).contiguous(), p.dense(x), cu_new=p.cu)
+    assert p.ab.attn_query_status(ws) == 0
+    for i in range(2):
+        pool, scales = _expected_pool(p, i, x)
+        assert torch.equal(_bits(p.cpool[i]).reshape(-1, 2, 128), pool)
+
+
+def test_packed_views_are_refused():
+    import torch
+    p = Problem("float16", "same", [5], [5], 2, 2, 64)
+    v = p.ab.attn_view_t(p.dense(p.q).data_ptr(), 0, 64, 128)
+    with pytest.raises(ValueError):
+        p.ab.sdpa_paged_fwd(p.desc, p.cache, p.dtable, p.dlens, v, v, cu_new=p.cu)
+    with pytest.raises(ValueError):  # a page table of another type
+        p.ab.sdpa_paged_fwd(p.desc, p.cache, p.dtable.long(), p.dlens, p.dense(p.q), p.dense(p.q), cu_new=p.cu)
+    with pytest.raises(ValueError):  # rows of another head count
+        p.ab.paged_cache_write(p.desc, p.cache, p.dtable, p.dlens, p.dense(p.q)[:, :1], p.dense(p.q)[:, :1], cu_new=p.cu)
+    with pytest.raises(p.ab.AttnError):  # too small a workspace
+        p.ab.sdpa_paged_fwd(p.desc, p.cache, p.dtable, p.dlens, p.dense(p.q), p.dense(p.q), cu_new=p.cu,
+                            workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_a_bad_page_reads_as_zeros(new):
     p = Problem("bfloat16", "same", [200, 300], [new, new], 4, 2, 128, seed=3)
