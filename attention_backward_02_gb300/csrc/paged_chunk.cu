@@ -246,10 +246,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
     auto stage_of = [](int j, int grp) { return kEight ? (kSplit ? 2 * j + grp : j) : kSplit ? j : j >> 1; };
     auto half_of = [](int j, int grp) { return kEight ? 0 : kSplit ? grp : j & 1; };
 
-    constexpr int NR = kEight ? NE : NS;   // the producers' ring
-    // stages of K and of V and pieces with keys that have been issued (in shared memory: a register of every role costs the
-    // MMA thread 3 % of a long chunk)
-    volatile uint32_t *issued = reinterpret_cast<volatile uint32_t *>(smem + Cfg::OFF_MISC + 16);
     // (e4m3: 512 threads are launched with 128 registers each; the warpgroups' shares add up to that.  The MMA thread's
     // count: 2048 tokens on 32768 with 72 registers 1422 us, 96: 1287, 112: 1222, 128: 1310, when the softmax has too few)
     constexpr uint32_t kRegsIssue = 112, kRegsSoftmax = 152, kRegsConvert = 96;
@@ -259,6 +255,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         if (warp == 0 || warp == 2) {
             // ============================================= producers: Q and K (warp 0), V (warp 2)
             const bool isk = warp == 0;
+            constexpr int NR = kEight ? NE : NS;  // ring
             uint64_t *full = kEight ? e_full + (isk ? 0 : NE) : isk ? k_full : v_full;
             uint64_t *empty = kEight ? e_empty + (isk ? 0 : NE) : isk ? k_empty : v_empty;
             const CUtensorMap *tm = isk ? &p.tm_k : &p.tm_v;
@@ -339,10 +336,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                     }
                 }
             }
-            if (lane == 0) {
-                issued[!isk] = n_stage;
-                if (isk) issued[2] = n_unit;
+            if (lane == 0) {  // a CTA does not end before its copies, whoever may have given up
+                volatile int never = 0;
+                if (isk && n_unit > 0) mbar_wait(q_full, (n_unit - 1) & 1, &never, 100000000ull);
+                for (uint32_t j = n_stage > uint32_t(NR) ? n_stage - NR : 0; j < n_stage; ++j)
+                    mbar_wait(&full[j % NR], (j / NR) & 1, &never, 100000000ull);
             }
+            __syncwarp();
         } else if (warp == 1 && elect_one()) {
             // ============================================= MMA issuer
             // One thread, and the time it takes between two MMAs is the tensor pipe's to lose: descriptors are
@@ -757,14 +757,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 
     tc_fence_before();
     __syncthreads();
-    if (*abort && (warp == 0 || warp == 2) && lane == 0) {  // (a CTA does not end before its copies)
-        volatile int never = 0;
-        uint64_t *full = kEight ? e_full + (warp ? NE : 0) : warp ? v_full : k_full;
-        const uint32_t n_stage = issued[warp != 0], n_unit = issued[2];
-        if (warp == 0 && n_unit > 0) mbar_wait(q_full, (n_unit - 1) & 1, &never, 100000000ull);
-        for (uint32_t j = n_stage > uint32_t(NR) ? n_stage - NR : 0; j < n_stage; ++j)
-            mbar_wait(&full[j % NR], (j / NR) & 1, &never, 100000000ull);
-    }
     if (threadIdx.x == 0) a.flags[blockIdx.x] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
     if (warp == 1) {
         tc_fence_after();

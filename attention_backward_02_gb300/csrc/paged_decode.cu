@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         if (ok && !(ok = mbar_wait(bar, parity, abort))) tc::flag_abort(abort, nullptr);
         ok = __all_sync(0xffffffffu, ok);
     };
-    uint32_t s = 0, par = 0, n_stage = 0;  // ring position and phase; stages the producer has issued
+    uint32_t s = 0, par = 0;  // ring position and phase
 
     if (warp == kKeyWarps * RW) {
         // ================================================= producer
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
             prefetch_tmap(&p.tm_k);
             prefetch_tmap(&p.tm_v);
         }
+        uint32_t n_stage = 0;
         Walk<kUnitCost> w(sched, range);
         while (ok && w.next()) {
             const int kvh = w.x / nrb;
@@ -252,6 +253,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 }
             }
         }
+        if (lane == 0) {  // a CTA does not end before its copies, whoever may have given up
+            volatile int never = 0;
+            for (uint32_t j = n_stage > uint32_t(NST) ? n_stage - NST : 0; j < n_stage; ++j)
+                mbar_wait(&full[j % NST], (j / NST) & 1, &never, 100000000ull);
+        }
+        __syncwarp();
     } else {
         // ================================================= consumers
         const int g = lane / 4, q = lane % 4, kw = warp / RW, rw = warp % RW;
@@ -581,12 +588,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         }
     }
     __syncthreads();
-    // (a CTA does not end before its copies: the consumers wait for every stage, or, if anyone gave up, the producer does)
-    if (*abort && warp == kKeyWarps * RW && lane == 0) {
-        volatile int never = 0;
-        for (uint32_t j = n_stage > uint32_t(NST) ? n_stage - NST : 0; j < n_stage; ++j)
-            mbar_wait(&full[j % NST], (j / NST) & 1, &never, 100000000ull);
-    }
     if (threadIdx.x == 0) a.flags[blockIdx.x] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
 }
 
