@@ -9,7 +9,7 @@
 // Bound by HBM: every cached key and value is read once a row block against 4 d ROWS
 // operations.  A CTA takes its range of keys in stages of 64, which a producing warp brings into a
 // ring in shared memory by TMA (a lane looks up a page, a stage ahead, and issues its
-// boxes), so that loads run under the arithmetic and over the ends of pieces; four warps (32 rows: four pairs)
+// boxes), so that loads run under the arithmetic and over the ends of pieces; four warps
 // take 16 or 32 keys of a stage each.  Both products are mma.sync m16n8k16, which keeps the
 // operations off the critical path; what a warp's step takes is their latency and the softmax's (650 + 500 + 400
 // cycles, whether numbers are converted or not), so where a key has at most 128 bytes it takes 32 keys.  S = Q K^T has the rows as its rows; its accumulator is, as it
@@ -45,28 +45,27 @@ using namespace sm103;
 namespace {
 
 constexpr int kKeyWarps = 4;     // warps that share a stage's keys
-constexpr int kUnitCost = 256;   // what a unit's start and end take, in keys (128: 32 e4m3 sequences of 1 to 8192 keys 87 us, 256: 73, 512: 71)
+constexpr int kUnitCost = 384;   // what a unit's start and end take, in keys (32 e4m3 sequences of 1 to 8192 keys: 128 85 us, 256 73, 384 69)
 constexpr int kShare = 256;      // a share worth a start
 constexpr int kJoin = 256;       // threads of the join
 
-// CTAs an SM holds: as many as the rings leave room for two stages or more, and a lane's registers (Q, sums) allow.
-constexpr int decode_blocks(int d, int esize, int rows)
+// CTAs an SM holds: as many as leave each a ring of two stages or more.  (16 bits, d = 128: three with two stages 100 us for
+// 32 sequences of 1 to 8192 keys, two with three 97.)
+constexpr int decode_blocks(int d, int esize)
 {
-    if (rows == 32) return d == 64 ? 2 : 1;
-    return d * esize == 64 || (d * esize == 256 && rows == 8) ? 3 : 2;
+    return d * esize == 64 ? 3 : 2;
 }
 
 template <int D, bool kEight, int ROWS> struct DecodeCfg {
-    static constexpr int RW = ROWS > 16 ? ROWS / 16 : 1;   // warps that share 16 keys, each with 8 or 16 of the rows
-    static constexpr int NR = ROWS / RW / 8;               // rows of a lane
-    static constexpr int CONSUMERS = 32 * kKeyWarps * RW, THREADS = CONSUMERS + 32;
+    static constexpr int NR = ROWS / 8;                    // rows of a lane
+    static constexpr int CONSUMERS = 32 * kKeyWarps, THREADS = CONSUMERS + 32;
     static constexpr int ESIZE = kEight ? 1 : 2;
     static constexpr int SUB = D * ESIZE <= 128 ? 2 : 1;   // blocks of 16 keys that a warp takes at once
     static constexpr int KEYS = 16 * SUB, STAGE_KEYS = kKeyWarps * KEYS;
     static constexpr int SIDE = STAGE_KEYS * D * ESIZE;    // keys, or values, of a stage
     static constexpr int OS = D + 2;                       // a row of sums: two rows of a lane lie in other banks
     static constexpr int O_BYTES = 2 * ROWS * OS * 4;      // [2][ROWS][OS] floats
-    static constexpr int BLOCKS = decode_blocks(D, ESIZE, ROWS);
+    static constexpr int BLOCKS = decode_blocks(D, ESIZE);
     static constexpr int OTHER = O_BYTES + 2 * kKeyWarps * ROWS * 4 + 512 + 1024;
     static constexpr int STAGE = 2 * SIDE + (kEight ? 2 * STAGE_KEYS * 4 : 0) + 16;
     static constexpr int FIT = ((227 * 1024 / BLOCKS - 1024) - OTHER) / STAGE;
@@ -149,7 +148,8 @@ __device__ __forceinline__ float half_range(float most)
     return __uint_as_float((127u + 14u + 127u - e) << 23);
 }
 
-// ROWS: rows of a unit, 8 (the second half of S's rows is zero and never looked at), 16 or 32.
+// ROWS: rows of a unit, 8 (the second half of S's rows is zero and never looked at) or 16.  (32, two warps to the same
+// keys: drafted tokens of 28 rows 67 us, as two units of 16 that read the keys twice 52.)
 template <class T, bool kEight, int D, int ROWS>
 __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg<D, kEight, ROWS>::BLOCKS)
     paged_decode_kernel(const __grid_constant__ DecodeParams p)
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
     using M = typename std::conditional<kEight, __half, T>::type;  // the products' type
     constexpr int NQ = D / 8;                // 32-bit words of a query row in a lane
     constexpr int NE = D / 16;               // products of O^T
-    constexpr int NR = Cfg::NR, RW = Cfg::RW, NST = Cfg::NST;
+    constexpr int NR = Cfg::NR, NST = Cfg::NST;
     constexpr int KL = D * Cfg::ESIZE / 64;  // reads of a key
     constexpr int SUB = Cfg::SUB, kKeys = Cfg::KEYS, kStage = Cfg::STAGE_KEYS;
 
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         *bad_page = 0;
         for (int s = 0; s < NST; ++s) {
             mbar_init(&full[s], kEight ? 1 + 32 : 1);  // the boxes, and the scales of each lane
-            mbar_init(&empty[s], kKeyWarps * RW);
+            mbar_init(&empty[s], kKeyWarps);
         }
         fence_mbar_init();
     }
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
     };
     uint32_t s = 0, par = 0;  // ring position and phase
 
-    if (warp == kKeyWarps * RW) {
+    if (warp == kKeyWarps) {
         // ================================================= producer
         const int in_page = (1 << cache.shift) - 1, pr = 1 << cache.shift < kStage ? 1 << cache.shift : kStage;  // keys of a box
         const int boxes = kStage / pr;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         __syncwarp();
     } else {
         // ================================================= consumers
-        const int g = lane / 4, q = lane % 4, kw = warp / RW, rw = warp % RW;
+        const int g = lane / 4, q = lane % 4, kw = warp;
         const float sc = a.scale * kLog2e;
         float *sm_m = reinterpret_cast<float *>(smem + Cfg::OFF_M), *sm_l = sm_m + kKeyWarps * ROWS;
         float *sm_o = reinterpret_cast<float *>(smem + Cfg::OFF_O);
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
             float fs[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                const int r = rw * 16 + g + 8 * i, tok = r / hb, ti = w.t * sched.tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
+                const int r = g + 8 * i, tok = r / hb, ti = w.t * sched.tokens + tok, head = kvh * G + rb * ROWS + r - tok * hb;
                 const bool on = tok < sched.tokens && ti < w.u.m && rb * ROWS + r - tok * hb < G;
                 lim[i] = !on ? -1 : a.causal ? w.u.len - w.u.m + ti : w.u.len - 1;
                 const int64_t row = a.seqs.cu ? int64_t(w.u.first + ti) * a.q.ss : w.n * a.q.sb + ti * a.q.ss;
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
                 if (q == 0) {
-                    sm_m[kw * ROWS + rw * 16 + g + 8 * i] = m[i];
-                    sm_l[kw * ROWS + rw * 16 + g + 8 * i] = l[i];
+                    sm_m[kw * ROWS + g + 8 * i] = m[i];
+                    sm_l[kw * ROWS + g + 8 * i] = l[i];
                 }
             }
             sync();
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
             for (int i = 0; i < NR; ++i)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int r = rw * 16 + 2 * q + c + 8 * i;
+                    const int r = 2 * q + c + 8 * i;
                     float mm = sm_m[r];
 #pragma unroll
                     for (int k = 1; k < kKeyWarps; ++k) mm = fmaxf(mm, sm_m[k * ROWS + r]);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 }
             auto slot_of = [&](int slot, int i, int c, int e) -> float2 * {
                 const int dim = kEight ? D / 8 * g + 2 * e : 64 * (e / 4) + 8 * g + 2 * (e % 4);
-                return reinterpret_cast<float2 *>(sm_o + (slot * ROWS + rw * 16 + 2 * q + c + 8 * i) * Cfg::OS + dim);
+                return reinterpret_cast<float2 *>(sm_o + (slot * ROWS + 2 * q + c + 8 * i) * Cfg::OS + dim);
             };
             auto put = [&](int slot) {
 #pragma unroll
@@ -735,7 +735,7 @@ template <class T, bool kEight, int D, int ROWS> cudaError_t run(const PagedAttn
 
 template <class T, bool kEight, int D> cudaError_t pick_rows(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
 {
-    return p.rows == 32 ? run<T, kEight, D, 32>(a, p, s) : p.rows == 16 ? run<T, kEight, D, 16>(a, p, s) : run<T, kEight, D, 8>(a, p, s);
+    return p.rows == 16 ? run<T, kEight, D, 16>(a, p, s) : run<T, kEight, D, 8>(a, p, s);
 }
 
 template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, const PagedShape &p, cudaStream_t s)
@@ -748,11 +748,11 @@ template <class T, bool kEight> cudaError_t pick(const PagedAttnArgs &a, const P
 PagedShape paged_decode_shape(int64_t h, int64_t h_kv, int64_t d, int64_t s_q, bool eight)
 {
     const int group = int(h / h_kv);
-    const int64_t rows = group * (s_q < 32 ? s_q : 32);
+    const int64_t rows = group * (s_q < 16 ? s_q : 16);
     PagedShape p;
     p.chunk = false;
-    p.rows = rows > 16 ? 32 : rows > 8 ? 16 : 8;
-    p.shares = kPagedCtas * decode_blocks(int(d), eight ? 1 : 2, p.rows);
+    p.rows = rows > 8 ? 16 : 8;
+    p.shares = kPagedCtas * decode_blocks(int(d), eight ? 1 : 2);
     p.groups = 1;
     p.heads = group < p.rows ? group : p.rows;
     p.tokens = p.rows / p.heads;

@@ -102,12 +102,12 @@ int main()
             if (news.back() > lens.back() && upto(3)) lens.back() += news.back();
         }
         if (b > 1 && packed) news[0] = std::max(news[0], 1);
-        check<128, 64, 64, 256>(lens, news, packed, 1 + upto(15), 1 + upto(40), i & 1, 456);
-        check<128, 128, 128, 256>(lens, news, packed, 1 + upto(15), 1 + upto(7), i & 1, 608);
+        check<384, 64, 64, 256>(lens, news, packed, 1 + upto(15), 1 + upto(40), i & 1, 456);
+        check<384, 128, 128, 256>(lens, news, packed, 1 + upto(15), 1 + upto(7), i & 1, 608);
         check<256, 128, 512, 1024>(lens, news, packed, 1 + upto(255), 1 + upto(40), i & 1, 152);
     }
     // no tokens at all, and a cost past 32 bits
-    check<128, 64, 64, 256>({5, 0}, {0, 0}, true, 2, 3, 1, 456);
+    check<384, 64, 64, 256>({5, 0}, {0, 0}, true, 2, 3, 1, 456);
     check<256, 128, 512, 1024>({1 << 30, 1 << 29}, {200000, 100000}, true, 8, 128, 1, 152);
     printf("batches %lld pieces %lld holes %lld twice %lld empty %lld slot %lld chain %lld heavy %lld\n", batches, pieces, holes,
            twice, empty_wrong, slot_wrong, chain_wrong, heavy);
