@@ -191,3 +191,143 @@ def test_the_binding_refuses(ab):
     cache, d = ab.paged_cache(kv, kv), _desc(ab, d=64, s_kv=64)
     with pytest.raises(ValueError):  # not CUDA tensors
         ab.paged_cache_write(d, cache, torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), kv, kv)
+
+
+class _Memory:
+    """A CUDA tensor as the argument checks see it."""
+
+    def __init__(self, ptr, dtype, shape, stride=None, device=0):
+        self.ptr, self.dtype, self.shape, self.index = ptr, dtype, tuple(shape), device
+        self.strides, self.device = stride, f"cuda:{device}"
+
+    def data_ptr(self):
+        return self.ptr
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        if self.strides is None:
+            s, n = [], 1
+            for x in reversed(self.shape):
+                s.insert(0, n)
+                n *= x
+            self.strides = tuple(s)
+        return self.strides if i is None else self.strides[i]
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+    def numel(self):
+        return 1 << 40
+
+
+def _fakes(torch, **kw):
+    """(a descriptor's cache, and the arguments of a call) of made-up CUDA tensors."""
+    m = lambda dt, *shape, ptr=A: _Memory(ptr, dt, shape, device=kw.get("device", 0))
+    bf, i32, e4 = torch.bfloat16, torch.int32, torch.float8_e4m3fn
+    pool = [m(e4, 50, 64, 2, 128, ptr=A * (i + 1)) for i in range(2)]
+    size = [m(torch.float32, 50, 64, 2, ptr=A * (i + 3)) for i in range(2)]
+    return pool, size, dict(table=m(i32, 2, 16), lens=m(i32, 2), q=m(bf, 2, 8, 1, 128), kv=m(bf, 2, 2, 1, 128))
+
+
+def test_a_cache_whose_memory_was_replaced(ab):
+    """tensor.data = ... gives pages other memory, strides and type: a call reads what the tensors are then, and refuses
+    what no longer fits together."""
+    import types
+    torch = pytest.importorskip("torch")
+    pool, size, t = _fakes(torch)
+    cache = ab.paged_cache(*pool, k_scale=size[0], v_scale=size[1])
+    stream = types.SimpleNamespace(cuda_stream=0, device=types.SimpleNamespace(index=0))
+    call = lambda: ab._paged_call("call", _desc(ab), cache, t["table"], t["lens"], None, 0, stream)
+    call()
+    assert (cache.k, cache.v, cache.k_scale, cache.type, cache.n_pages, cache.ss, cache.scale_ss) == (A, 2 * A, 3 * A, 3, 50, 256, 2)
+    pool[0].ptr, size[1].ptr = 7 * A, 9 * A
+    call()
+    assert (cache.k, cache.v_scale) == (7 * A, 9 * A)
+    for x in pool:
+        x.dtype, x.shape, x.strides = torch.bfloat16, (60, 64, 2, 128), (1 << 20, 512, 128, 1)
+    call()
+    assert (cache.type, cache.n_pages, cache.sp, cache.ss, cache.sh) == (1, 60, 1 << 20, 512, 128)
+    for name, value in (("dtype", torch.float16), ("shape", (60, 64, 2, 64)), ("strides", (1 << 20, 256, 128, 1)), ("index", 1)):
+        old = getattr(pool[1], name)
+        setattr(pool[1], name, value)
+        with pytest.raises(ValueError):
+            call()
+        setattr(pool[1], name, old)
+    call()
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("table", dict(index=1)), ("lens", dict(index=1)), ("table", dict(shape=(3, 16))), ("lens", dict(shape=(3,))),
+    ("table", dict(strides=(32, 2))), ("q", dict(index=1)), ("q", dict(shape=(2, 4, 1, 128))), ("kv", dict(index=1)),
+    ("kv", dict(shape=(2, 2, 2, 128)))])
+def test_tensors_of_another_device_or_shape_are_refused(ab, name, kw):
+    torch = pytest.importorskip("torch")
+    import types
+    pool, size, t = _fakes(torch)
+    cache = ab.paged_cache(*pool, k_scale=size[0], v_scale=size[1])
+    for k, v in kw.items():
+        setattr(t[name], k, v)
+    stream = types.SimpleNamespace(cuda_stream=0, device=types.SimpleNamespace(index=0))
+    with pytest.raises(ValueError):
+        if name == "kv":
+            ab.paged_cache_write(_desc(ab), cache, t["table"], t["lens"], t["kv"], t["kv"], workspace=_Memory(A, torch.uint8, (1,)),
+                                 stream=stream)
+        else:
+            ab.sdpa_paged_fwd(_desc(ab), cache, t["table"], t["lens"], t["q"], t["q"], workspace=_Memory(A, torch.uint8, (1,)),
+                              stream=stream)
+
+
+def test_calls_run_on_the_pages_device_and_their_workspace_on_the_stream(ab, monkeypatch):
+    """With the tensors on device 1 and device 0 current: the device is made current for the call, the stream is that of
+    device 1, and a workspace that the call makes is memory of the stream it is given.  torch and the launches are stood in for."""
+    import contextlib
+    import types
+    torch = pytest.importorskip("torch")
+    current, made, seen, at = [0], [], [], [None]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    @contextlib.contextmanager
+    def use(stream):
+        before, at[0] = at[0], stream
+        yield
+        at[0] = before
+
+    def empty(n, dtype, device):
+        made.append(at[0])
+        return _Memory(A, dtype, (n,), device=1)
+
+    names = ("float16", "bfloat16", "float32", "int32", "uint8", "float8_e4m3fn", "device")
+    raw = types.SimpleNamespace(_cuda_getDevice=lambda: current[0], _cuda_getCurrentRawStream=lambda d: 100 + d)
+    fake = types.SimpleNamespace(empty=empty, _C=raw, **{n: getattr(torch, n) for n in names},
+                                 cuda=types.SimpleNamespace(stream=use, device=device))
+    real = ab._lib.load()
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return getattr(real, name)
+            return lambda *a: seen.append((name, current[0], a[-1])) or 0
+
+    pool, size, t = _fakes(torch, device=1)
+    cache = ab.paged_cache(*pool, k_scale=size[0], v_scale=size[1])
+    monkeypatch.setattr(ab, "_torch_module", fake)
+    monkeypatch.setattr(ab._lib, "load", Lib)
+    stream = types.SimpleNamespace(cuda_stream=5, device=types.SimpleNamespace(index=1))
+    args = (_desc(ab), cache, t["table"], t["lens"])
+    for i, (fn, x) in enumerate(((ab.paged_cache_write, t["kv"]), (ab.paged_cache_read, t["kv"]), (ab.sdpa_paged_fwd, t["q"]))):
+        fn(*args, x, x)
+        fn(*args, x, x, stream=stream)
+        assert made[-2] is None and made[-1] is stream and seen[-2:] == [(fn.__name__, 1, 101), (fn.__name__, 1, 5)], i
+        with pytest.raises(ValueError):  # a stream of another device
+            fn(*args, x, x, stream=types.SimpleNamespace(cuda_stream=5, device=types.SimpleNamespace(index=0)))
+    assert current == [0]
