@@ -9,11 +9,15 @@
 // relative to it.)  Both factors are rounded fp32 quotients, so a row's codes do not
 // depend on how it is shared out.
 //
-// Bound by HBM: a row is read once and written once; what has to be kept low for that is the instructions a row takes
-// (with 8 elements a lane 116 for 16 bytes of 32 lanes, and 75 % of the issue slots).  A lane takes two pieces of a row, 16
-// bytes of the 16-bit side each (8 elements; 8 bytes of the 8-bit side), d / 16 lanes a row.  A block takes a run of rows in the order token, keys and values, head, up to
-// four a lane group; the write's are all loaded before the places in the cache are looked up (cumulative
-// counts, length, page id: three dependent loads), the read's behind it.
+// Bound by HBM: a row is read once and written once; what has to be kept low for that is
+// the instructions a row takes (with 8 elements a lane 116 for two rows, 75 % of the issue
+// slots).  A lane takes two pieces of a row, 16 bytes of the 16-bit side each (8 elements;
+// 8 bytes of the 8-bit side), d / 16 lanes a row.  A block takes a run of rows in the order
+// token, keys and values, head, up to four a lane group; the write's are all loaded before
+// the places in the cache are looked up (cumulative counts, length, page id: three
+// dependent loads), the read's behind it.  131104 tokens of 8 heads of 128 read from e4m3:
+// 124 us, 0.96 of the measured copy rate; 17408 tokens written: 25 us, 0.64 (the start and
+// end of the run).
 #include <cstring>
 #include <type_traits>
 

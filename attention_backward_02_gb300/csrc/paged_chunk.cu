@@ -1,6 +1,6 @@
 // paged_chunk.cu -- tensor-core attention of chunks of new tokens over a paged key /
-// value cache, 16-bit or e4m3, for sm_103a: tcgen05 MMAs with TMEM accumulators, 16-bit
-// pages by TMA.
+// value cache, 16-bit or e4m3, for sm_103a: tcgen05 MMAs with TMEM accumulators, pages by
+// TMA.
 //
 //   s_ij = scale q_i.k_j,  O = softmax(s) V  over the keys j <= position of i (or all)
 //
@@ -19,15 +19,24 @@
 //
 // A stage is one to eight pages (or part of one).  A lane of the producing warp looks up a
 // page, a stage ahead, and issues its TMA boxes.  16 bits: stages of 128 keys, 64 elements x page
-// rows with the 128-byte swizzle, straight to where the MMA reads them (stages of 64: 930 us for 896,
-// each wait of the MMA thread takes it 100 cycles).  e4m3: stages of 64, rows of d bytes to a ring of their own, with their scales (4-byte asynchronous copies), from which a
-// warpgroup makes 16-bit numbers in the swizzled layout.  Keys unscaled, of the queries'
-// type (e4m3 numbers are 16-bit numbers exactly); their scales multiply S's columns.
+// rows with the 128-byte swizzle, straight to where the MMA reads them (stages of 64: 930 us for 905,
+// each wait of the MMA thread takes it 100 cycles).  e4m3: stages of 64, rows of d bytes to a
+// ring of their own, with their scales (4-byte asynchronous copies), from which a warpgroup
+// makes 16-bit numbers in the swizzled layout (a lane a row, so that neither side has bank
+// conflicts: 1512 -> 1445 us).  Keys unscaled, of the queries' type (e4m3 numbers are
+// 16-bit numbers exactly); their scales multiply S's columns.
 // Values as half-precision numbers, times their scale relative to the stage's largest, rounded up
 // to a power of two 2^E: number, factor and product in one multiplication a pair, each
 // rounded by at most half a step of that type.  2^E goes into the weights: P' = exp2(x + E - m)
 // with m over x + E, so that O and l keep one reference; l takes P' 2^-E.
 // A page id out of range reads as zeros.
+//
+// Bound: 16 bits, the chain S -> softmax -> P -> O of a group, 2000 cycles for 64 keys and 256
+// rows against 1260 of MMAs (2048 tokens on 32768, 32 / 8 heads of 128: 905 us, 0.65 of the measured tensor
+// rate).  e4m3, 1225 us: the converting warps share the issue slots with the softmax and shared memory's
+// bandwidth with the MMAs.  Measured and dropped: 128 keys a step with one S a group, whose MMAs run at the full rate
+// (M=128 N=64 from shared memory reads 128 rows of Q for 64 of K: two thirds), 876 and 1470 us; the same with two threads a
+// row, 865 and 1900; a warp that tells the MMA thread its steps, 913 and 1290.
 //
 // A row's reference maximum m is raised only when a step's maximum exceeds it by more
 // than 8 (log2 units), and then l and the row of O in TMEM are scaled by exp2(m_old - m_new):

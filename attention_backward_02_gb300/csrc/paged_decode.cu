@@ -7,18 +7,24 @@
 //   s_j = scale q.k_j over the keys j <= its position,  O = sum_j exp(s_j) v_j / sum_j exp(s_j).
 //
 // Bound by HBM: every cached key and value is read once a row block against 4 d ROWS
-// operations.  A CTA takes its range of keys in stages of 64, which a producing warp brings into a
-// ring in shared memory by TMA (a lane looks up a page, a stage ahead, and issues its
-// boxes), so that loads run under the arithmetic and over the ends of pieces; four warps
-// take 16 or 32 keys of a stage each.  Both products are mma.sync m16n8k16, which keeps the
-// operations off the critical path; what a warp's step takes is their latency and the softmax's (650 + 500 + 400
-// cycles, whether numbers are converted or not), so where a key has at most 128 bytes it takes 32 keys.  S = Q K^T has the rows as its rows; its accumulator is, as it
-// stands, the second operand of O^T = V^T P^T, whose rows are head dims and whose eight
-// columns are rows of S.  The operands are 16-byte reads of shared memory as they stand: the order of the
-// contraction over d is free, so a lane's 16 bytes of a key serve several steps, and V's key
-// pairs are joined by byte permutes.  Keys lie in blocks of 64 bytes a row, in which the eight lanes of a
-// read take two whole rows; values in rows of 128 bytes with the 128-byte swizzle, in which they take
-// pieces of four rows: neither has bank conflicts (values of 64 e4m3 numbers have two-way ones).
+// operations.  A CTA takes its range of keys in stages of 64 or 128, which a producing warp
+// brings into a ring in shared memory by TMA (a lane looks up a page, a stage ahead, and
+// issues its boxes), so that loads run under the arithmetic and over the ends of pieces;
+// four warps take 16 or 32 keys of a stage each.  Both products are mma.sync m16n8k16,
+// which keeps the operations off the critical path; what a warp's step takes is their
+// latency and the softmax's (650 + 500 + 400 cycles for 16 keys, whether numbers are
+// converted or not), so where a key has at most 128 bytes it takes 32.  S = Q K^T has the
+// rows as its rows; its accumulator is, as it stands, the second operand of O^T = V^T P^T,
+// whose rows are head dims and whose eight columns are rows of S.  The operands are 16-byte
+// reads of shared memory as they stand: the order of the contraction over d is free, so a
+// lane's 16 bytes of a key serve several steps, and V's key pairs are joined by byte
+// permutes.  Keys lie in blocks of 64 bytes a row, in which the eight lanes of a read take
+// two whole rows; values in rows of 128 bytes with the 128-byte swizzle, in which they take
+// pieces of four rows: neither has bank conflicts (values of 64 e4m3 numbers have two-way
+// ones).  32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 97 us for 537 MB, 0.81 of the
+// measured copy rate (all of 8192: 173, 0.91), e4m3 66 us for 277 MB, 0.62: once under way
+// both read at that rate, the rest is the start (a share's range, first loads), units that
+// end early and the join.
 //
 // e4m3: a number is a half-precision number exactly, one conversion a pair, so both products
 // are of that type whatever the queries' is.  bf16 queries are scaled by a power of two per row that
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
 // group sums are added in order.  Three round trips to L2: the records of the next shares side by side, the pieces'
 // maxima and sums side by side, their outputs several at a time.  The first block gathers the call's status.
 // (Rows of the tensor-core kernel: 32 or 64 a block, one wave of blocks; 8 a block, four waves, took 25 us behind 2048
-// tokens on 32768 where this takes REPLACEJ.)
+// tokens on 32768 where this takes 19.)
 template <class T, int D, int COLS, int RPT>
 __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, const PagedShape shape)
 {

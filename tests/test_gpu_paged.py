@@ -222,6 +222,63 @@ def test_padded_in_front_and_queries_by_head(new):
         assert torch.equal(_bits(p.cpool[i]).reshape(-1, 2, 128), pool)
 
 
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+@pytest.mark.parametrize("hint,new", [(1, [300, 1, 7]), (1000, [1, 2, 1]), (0, [5, 40, 1])])
+def test_an_expected_count_only_chooses_the_kernel(cache, hint, new):
+    """desc.s_q of packed calls: longer and shorter chunks than it says are computed all the same."""
+    p = Problem("bfloat16", cache, [400, 90, 50], new, 8, 2, 64, seed=14)
+    p.desc.s_q = hint
+    p.check(*p.attend())
+
+
+def test_a_cache_without_room():
+    """s_kv = 0: nothing is read, every row is empty."""
+    import torch
+    for new in (1, 40):
+        p = Problem("float16", "same", [3, 2], [new, new], 4, 2, 64, packed=False)
+        p.desc.s_kv = 0
+        table, lens = torch.empty(2, 0, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+        q = p.dense(p.q)
+        o, lse = torch.full_like(q, 3), torch.empty(2, 4, new, device="cuda")
+        ws = p.ab.sdpa_paged_fwd(p.desc, p.cache, table, lens, q, o, lse=lse)
+        assert p.ab.attn_query_status(ws) == 0
+        assert bool((o == 0).all()) and bool(lse.isposinf().all())
+        lens[1] = 1
+        ws = p.ab.sdpa_paged_fwd(p.desc, p.cache, table, lens, q, o, lse=lse)
+        assert p.ab.attn_query_status(ws) == 2
+
+
+def test_two_threads_on_two_streams():
+    """Two host threads, each with a stream and a workspace, over one cache handle."""
+    import threading
+    import torch
+    p = Problem("bfloat16", "e4m3", [3000, 700], [60, 60], 8, 2, 128, packed=False, seed=15)
+    one = Problem("bfloat16", "e4m3", [3000, 700], [1, 1], 8, 2, 128, packed=False, seed=15)
+    one.cache, one.dtable = p.cache, p.dtable  # (the same seed: the same pages)
+    want = [p.attend()[0], one.attend()[0]]
+    got, errors = [[], []], []
+
+    def work(i, x):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(30):
+                    got[i].append(x.attend(flags=None, stream=s)[0])
+                s.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i, x)) for i, x in enumerate((p, one))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for i in range(2):
+        assert len(got[i]) == 30 and all(torch.equal(o, want[i]) for o in got[i])
+
+
 def test_packed_views_are_refused():
     import torch
     p = Problem("float16", "same", [5], [5], 2, 2, 64)
