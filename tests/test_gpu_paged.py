@@ -346,6 +346,29 @@ def test_shared_pages_and_strided_rows(new):
     assert torch.equal(fused[:, :, :4], p.q.view(2, new, 4, 64).cuda())
 
 
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+@pytest.mark.parametrize("new", [1, 5, 70])
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_inputs_that_repeat(cache, new, dim):
+    """Queries, and rows to write, that are the same for all sequences, heads or tokens (a stride of 0, as expand makes
+    them): the bits of the same calls on copies."""
+    import torch
+    runs = []
+    for copies in (False, True):
+        p = Problem("bfloat16", cache, [90 + new, 7 + new, 200], [new] * 3, 8, 2, 128, packed=False, seed=15)
+        g = torch.Generator().manual_seed(16)
+        def rows(heads):
+            shape = [3, heads, new, 128]
+            x = torch.randn(*(1 if i == dim else n for i, n in enumerate(shape)), generator=g).to(p.dt).cuda().expand(*shape)
+            return x.contiguous() if copies else x
+        ws = p.ab.paged_cache_write(p.desc, p.cache, p.dtable, p.dlens, rows(2), rows(2))
+        assert p.ab.attn_query_status(ws) == 0
+        q = rows(8)
+        runs.append([*p.cpool, *p.attend(q=q, o=torch.full((3, 8, new, 128), float("nan"), dtype=p.dt, device="cuda"))])
+    for a, b in zip(*runs):
+        assert torch.equal(_bits(a), _bits(b))
+
+
 def test_extreme_scores_and_scales():
     """Scores far apart and values of very different size: e4m3 scales from 2^-20 to 2^10 in one sequence."""
     import torch
