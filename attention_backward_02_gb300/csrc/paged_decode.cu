@@ -21,10 +21,12 @@
 // permutes.  Keys lie in blocks of 64 bytes a row, in which the eight lanes of a read take
 // two whole rows; values in rows of 128 bytes with the 128-byte swizzle, in which they take
 // pieces of four rows: neither has bank conflicts (values of 64 e4m3 numbers have two-way
-// ones).  32 sequences of 1 to 8192 keys, 32 / 8 heads of 128: 97 us for 537 MB, 0.81 of the
-// measured copy rate (all of 8192: 173, 0.91), e4m3 66 us for 277 MB, 0.62: once under way
-// both read at that rate, the rest is the start (a share's range, first loads), units that
-// end early and the join.
+// ones).  CTAs that start together take the same keys of neighbouring heads (Lanes): a head's
+// 128 bytes of e4m3 numbers alone came at 0.66 of the measured copy rate even with the
+// arithmetic left out, side by side at 0.78 with it.  32 sequences of 1 to 8192 keys, 32 / 8
+// heads of 128: 95 us for 537 MB, 0.83 of that rate (all of 8192: 171, 0.92), e4m3 65 us for
+// 277 MB, 0.63 (105, 0.78): beside the reading stand the start (a share's range, first loads),
+// units that end early and the join.
 //
 // e4m3: a number is a half-precision number exactly, one conversion a pair, so both products
 // are of that type whatever the queries' is.  bf16 queries are scaled by a power of two per row that
@@ -188,10 +190,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         fence_mbar_init();
     }
     const int G = a.h / a.h_kv, hb = G < ROWS ? G : ROWS, nrb = (G + ROWS - 1) / ROWS;
-    const Sched<kUnitCost> sched = {a.seqs, ROWS / hb, a.h_kv * nrb, a.causal};
+    const Lanes side(a.h_kv * nrb, gridDim.x, blockIdx.x);
+    const Sched<kUnitCost> sched = {a.seqs, ROWS / hb, a.h_kv * nrb / side.lanes, a.causal};
     bool bad = false;
     const Range range = sched.range<Cfg::THREADS, kStage, kStage, kShare>(
-        blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(smem + Cfg::OFF_RANGE), &bad);  // (two barriers inside)
+        side.share, side.per, reinterpret_cast<int64_t *>(smem + Cfg::OFF_RANGE), &bad);  // (two barriers inside)
     if (bad && blockIdx.x == 0) *bad_page = 1;  // (one CTA reports the lengths)
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {  // the whole warp
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         uint32_t n_stage = 0;
         Walk<kUnitCost> w(sched, range);
         while (ok && w.next()) {
-            const int kvh = w.x / nrb;
+            const int kvh = (w.x * side.lanes + side.lane) / nrb;
             const int32_t *table = a.seqs.table + w.n * a.seqs.table_stride;
             auto page_of = [&](int k) -> int {
                 const int key = k + lane * pr;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
         auto sync = []() { named_bar_sync(1, Cfg::CONSUMERS); };
         Walk<kUnitCost> w(sched, range);
         while (w.next()) {
-            const int kvh = w.x / nrb, rb = w.x - kvh * nrb;
+            const int x = w.x * side.lanes + side.lane, kvh = x / nrb, rb = x - kvh * nrb;
             // ---- the lane's rows: query words, last visible key, factor of the scores
             uint32_t qa[NR][NQ];
             int lim[NR];
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
             const bool whole = w.begins() && w.ends();
             const int slot = w.begins() ? 1 : 0;
             if (!whole) {
-                const int4 name = unit_name(w.n, w.x, w.t, w.ends() ? kEnds : kGoesOn);
+                const int4 name = unit_name(w.n, x, w.t, w.ends() ? kEnds : kGoesOn);
                 if (slot) named1 = name;
                 else named0 = name;
             }
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                                         : (int64_t(w.n) * a.h + head) * a.seqs.s_q + ti] =
                             lse_of(mm, ll);
                 } else {
-                    const int64_t row = (int64_t(blockIdx.x) * 2 + slot) * ROWS + r;
+                    const int64_t row = (int64_t(side.me) * 2 + slot) * ROWS + r;
                     if (c == 0) a.part_ml[row] = make_float2(mm, ll);
                     float4 *dst = reinterpret_cast<float4 *>(a.part_o + row * D + c);
                     dst[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -589,12 +592,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
             sync();
         }
         if (threadIdx.x == 0) {
-            a.rec[2 * blockIdx.x] = named0;
-            a.rec[2 * blockIdx.x + 1] = named1;
+            a.rec[2 * side.me] = named0;
+            a.rec[2 * side.me + 1] = named1;
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) a.flags[blockIdx.x] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
+    if (threadIdx.x == 0) a.flags[side.me] = (*bad_page ? ATTN_DEV_INDEX_RANGE : 0u) | (*abort ? ATTN_DEV_TIMEOUT : 0u);
 }
 
 // Outputs of the units that several shares hold: a block for every share that may hold a unit's first piece, some of its

@@ -12,7 +12,7 @@
 using namespace attn;
 using namespace attn::paged;
 
-static long long batches, pieces, holes, twice, empty_wrong, slot_wrong, chain_wrong, heavy;
+static long long batches, pieces, holes, twice, empty_wrong, slot_wrong, chain_wrong, heavy, lane_wrong;
 
 template <int kUnitCost, int kStep, int kLeast, int kShare>
 void check(const std::vector<int> &lens, const std::vector<int> &news, bool packed, int tokens, int heads, int causal, int ctas)
@@ -87,8 +87,32 @@ void check(const std::vector<int> &lens, const std::vector<int> &news, bool pack
     if (bad) ++chain_wrong;
 }
 
+// Every share of every lane has one CTA, and every CTA a number of its own.
+static void check_lanes(int heads, int ctas)
+{
+    std::vector<int> numbers(ctas, 0), shares(ctas, 0);
+    for (int c = 0; c < ctas; ++c) {
+        const Lanes x(heads, ctas, c);
+        if (x.lanes < 1 || heads % x.lanes || x.lane >= x.lanes || x.per < 1 || x.share > x.per || x.me < 0 || x.me >= ctas) {
+            ++lane_wrong;
+            continue;
+        }
+        ++numbers[x.me];
+        if (x.share < x.per) {
+            if (x.me != x.lane * x.per + x.share) ++lane_wrong;
+            ++shares[x.me];
+        }
+    }
+    const Lanes x(heads, ctas, 0);
+    for (int c = 0; c < ctas; ++c)
+        if (numbers[c] != 1 || shares[c] != (c < x.per * x.lanes)) ++lane_wrong;
+    if (x.per * x.lanes * 20 < ctas * 19) ++lane_wrong;  // at most a twentieth of the CTAs without work
+}
+
 int main()
 {
+    for (int heads = 1; heads < 400; ++heads)
+        for (int ctas : {304, 456}) check_lanes(heads, ctas);
     std::mt19937 rng(5);
     auto upto = [&](int n) { return int(rng() % unsigned(n + 1)); };
     for (int i = 0; i < 4000; ++i) {
@@ -109,7 +133,7 @@ int main()
     // no tokens at all, and a cost past 32 bits
     check<384, 64, 64, 256>({5, 0}, {0, 0}, true, 2, 3, 1, 456);
     check<256, 128, 512, 1024>({1 << 30, 1 << 29}, {200000, 100000}, true, 8, 128, 1, 152);
-    printf("batches %lld pieces %lld holes %lld twice %lld empty %lld slot %lld chain %lld heavy %lld\n", batches, pieces, holes,
-           twice, empty_wrong, slot_wrong, chain_wrong, heavy);
+    printf("batches %lld pieces %lld holes %lld twice %lld empty %lld slot %lld chain %lld heavy %lld lanes %lld\n", batches, pieces, holes,
+           twice, empty_wrong, slot_wrong, chain_wrong, heavy, lane_wrong);
     return 0;
 }

@@ -29,7 +29,7 @@ def test_every_key_is_taken_once():
         f = subprocess.run([exe], check=True, capture_output=True, text=True, timeout=300).stdout.split()
     got = dict(zip(f[::2], map(int, f[1::2])))
     assert got["batches"] > 10000 and got["pieces"] > 10 ** 6
-    for k in ("holes", "twice", "empty", "slot", "chain", "heavy"):
+    for k in ("holes", "twice", "empty", "slot", "chain", "heavy", "lanes"):
         assert got[k] == 0, got
 
 
