@@ -206,8 +206,8 @@ template <int kUnitCost> struct Sched {
 // Where the pages' rows are short (a head's 128 bytes), reading one head's alone uses little of what DRAM opens for it.
 // So up to 16 neighbouring head blocks, which cost the same, are shared out alike, a lane each, and CTAs that start together
 // read the same keys of neighbouring heads (32 e4m3 sequences of 8192 keys, 8 heads of 128: 122 us, so 105; not for the
-// tensor-core kernel, which its arithmetic binds: mixed chunks 330 us, so 345).  A lane's units hold the head blocks lane, lane + lanes ..; the CTAs'
-// numbers are in the lanes' order, so that a unit's pieces lie one behind the other.
+// tensor-core kernel, which its arithmetic binds: mixed chunks 330 us, so 345).  A lane's units hold the head blocks lane,
+// lane + lanes ..; the CTAs' numbers are in the lanes' order, so that a unit's pieces lie one behind the other.
 struct Lanes {
     int lanes, lane;  // this CTA's lane
     int per, share;   // shares of a lane, and this CTA's (per: it has none)
