@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 }
             }
 
-            float m[NR], l[NR], vmax = 0x1p-120f;  // vmax: a power of two, at least every value scale so far
+            float m[NR], l[NR], vmax = 0x1p-120f;  // vmax: a power of two, at least the size of every value scale so far
             float acc[NR][NE][4];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                     float vm = 0.f;
                     if (kEight) {
 #pragma unroll
-                        for (int e = 0; e < 4 * SUB; ++e) vm = fmaxf(vm, fv[e]);
+                        for (int e = 0; e < 4 * SUB; ++e) vm = fmaxf(vm, fabsf(fv[e]));
                         raise |= vm > vmax;
                     }
                     if (__any_sync(0xffffffffu, raise)) {

@@ -1,0 +1,85 @@
+"""Scales of an e4m3 cache that its caller made: of either sign, and far from one another.  A value's scale may only matter
+as far as its key's weight does.
+
+Bounds (u = 2^-23, g = 2^-11, half a step of the half-precision type): a key's score is off by at most
+e = (d + 8) u (sum |q k| scale + |s|) + 2 u |s - largest s| + 4 u (|E| + largest |E|), E the exponents of the value scales
+(they are added to the scores where the weights are taken); its weight is rounded to half precision, which is off by
+g of it or by 2^-25 of the largest weight times scale that the row sees, E rounding that up by less than 2; its value may be a
+number times the scale's fraction, both rounded (2 g):
+    |O err| <= h |O| + sum_j (3 g + e_j + sum P e + 2^-20 + n u) P_j |v_j| + 2^-24 max_j (P_j |scale_j|) sum_j |code_j|
+    |LSE err| <= sum P e + 2^-20 + n u + 4 u (|LSE| + largest |E|)
+over the keys j that the row sees (h: half a step of the output's type; fp16 outputs are off by 2^-25 at least)."""
+import numpy as np
+import pytest
+
+from oracle import paged as P
+from tests.paged_problem import HALF, U, Problem
+
+pytestmark = pytest.mark.gpu
+
+# new tokens, query heads: 8 and 16 rows of the mma.sync kernel, 128 and 256 of the tensor-core kernel
+FORMS = [(1, 4), (5, 4), (30, 4), (150, 4)]
+
+
+def _set(p, side, scales):
+    """The cache's key (0) or value (1) scales: scales [slot, head] where a sequence has a token."""
+    import torch
+    live = ~p.scales[side].isnan()
+    p.scales[side][live] = torch.as_tensor(scales, dtype=torch.float32).reshape(p.scales[side].shape)[live]
+    p.cscales[side].copy_(p.scales[side])
+
+
+def _slot_scales(p, side):
+    return p.scales[side].reshape(-1, p.hk).numpy().copy()
+
+
+def _check(p, o, lse):
+    o = p.packed_of(o).double().cpu().numpy()
+    lse = lse.double().cpu().numpy() if p.packed else lse.permute(1, 0, 2).reshape(p.h, -1).double().cpu().numpy()
+    grp, g, h = p.h // p.hk, 2.0 ** -11, HALF[p.dtype]
+    for n, m in enumerate(p.new):
+        k, v = p.contents(n)
+        rows = slice(p.starts[n], p.starts[n] + m)
+        size = np.repeat(np.abs(p.scales[1].reshape(-1, p.hk)[p.rows_of[n]].double().numpy()), grp, 1).T  # [h, n]
+        code = np.repeat(np.abs(P.E4M3[p.pool[1].reshape(-1, p.hk, p.d)[p.rows_of[n]].numpy()]), grp, 1)
+        ref, rl, w, mag, s = P.attention(p.q[rows].double().numpy(), k, v, p.scale, p.causal)
+        seen = np.arange(len(k))[None, :] <= (np.arange(m) + len(k) - m)[:, None] if p.causal else np.ones((m, len(k)), bool)
+        seen = seen[:, None, :]
+        top = np.where(seen, s, -np.inf).max(-1, keepdims=True)
+        exps = np.abs(np.log2(np.clip(size, 2.0 ** -80, None)))
+        most = np.where(seen, exps, 0).max(-1, initial=0, keepdims=True)
+        e = np.where(seen, (p.d + 8) * U * (mag + np.abs(s)) + 2 * U * np.abs(s - top) + 4 * U * (exps + most), 0)
+        pe = (w * e).sum(-1, keepdims=True)
+        av = np.repeat(np.abs(v), grp, 1)
+        small = 2.0 ** -24 * (w * size).max(-1)[..., None] * np.einsum("mhn,nhd->mhd", np.where(seen, 1.0, 0.0) + 0 * w, code)
+        bound = (h * np.abs(ref) + np.einsum("mhn,nhd->mhd", (3 * g + e + pe + 2.0 ** -20 + len(k) * U) * w, av) + small +
+                 (2.0 ** -25 if p.dtype == "float16" else 2.0 ** -126))
+        err = np.abs(o[rows] - ref)
+        assert np.all(err <= bound), (n, float(np.nanmax(err)), float(np.nanmax(err / bound)), int(np.isnan(err).sum()))
+        lim = pe[..., 0] + 2.0 ** -20 + len(k) * U + 4 * U * (np.abs(rl) + most[..., 0])
+        err = np.abs(lse[:, rows].T - rl)
+        assert np.all(err <= lim), (n, float(np.nanmax(err)), float(np.nanmax(err / lim)))
+    return ref
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,h", FORMS)
+@pytest.mark.parametrize("signs", ["all", "mixed"])
+def test_scales_below_zero(dtype, d, new, h, signs):
+    """A row stands for code * scale whatever the scale's sign."""
+    import torch
+    p = Problem(dtype, "e4m3", [300, 170], [new, new], h, 1, d, packed=False, seed=21)
+    rng = np.random.default_rng(22)
+    for side in range(2):
+        x = _slot_scales(p, side)
+        sign = -1.0 if signs == "all" else rng.choice([-1.0, 1.0], x.shape)
+        _set(p, side, x * sign * (2.0 ** rng.integers(-3, 4, x.shape) if side else 1.0))
+    o, lse = p.attend()
+    _check(p, o, lse)
+    back = [torch.empty(2, 1, new, d, dtype=p.dt, device="cuda") for _ in range(2)]
+    p.ab.paged_cache_read(p.desc, p.cache, p.dtable, p.dlens, *back)
+    for n in range(2):
+        for side in range(2):
+            want = p.contents(n)[side][-new:]
+            assert np.all(np.abs(back[side][n, 0].double().cpu().numpy() - want[:, 0]) <= HALF[dtype] * np.abs(want[:, 0]) + 2.0 ** -25)
