@@ -31,9 +31,11 @@
 // e4m3: a number is a half-precision number exactly, one conversion a pair, so both products
 // are of that type whatever the queries' is.  bf16 queries are scaled by a power of two per row that
 // brings their largest element to 2^14 .. 2^15 (exact but for elements 2^-38 below it);
-// a key's scale and that power multiply its score; a value's scale multiplies its weight,
-// relative to a running power of two of the warp (the largest value scale so far), so that the
-// weights are at most 1 and those of 16 bits.
+// a key's scale and that power multiply its score.  A value's scale is 2^E f, |f| in [1, 2), and its key's
+// weight e^s 2^E f: E joins the score s (log2 units), so that the row's running maximum R is that of s + E over the keys
+// that it sees, and P = 2^(s + E - R) says what a key counts for in O.  (Relative to the largest value scale the
+// weights lost bits to keys of no weight and to keys that the row does not see.)  l takes P 2^-E, O the products of
+// P f and the numbers; both are in units of 2^R.  E is held between -80 and 126, so that l stays in range.
 //
 // The weights P are rounded to the 16-bit type of the product with V, after their sum is taken: its
 // operands are 16-bit, and a weight is off by half a step of that type.
@@ -112,6 +114,13 @@ __device__ __forceinline__ uint4 lds8(uint32_t addr)
 {
     uint4 v = make_uint4(0, 0, 0, 0);
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float2 lds_pair(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
     return v;
 }
 
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                 }
             }
 
-            float m[NR], l[NR], vmax = 0x1p-120f;  // vmax: a power of two, at least the size of every value scale so far
+            float m[NR], l[NR];  // (m: R above, of the scores alone over a 16-bit cache)
             float acc[NR][NE][4];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -359,14 +368,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                             mma16816<M>(sa[t], qa[0][2 * n], NR > 1 ? qa[NR - 1][2 * n] : 0u, qa[0][2 * n + 1],
                                         NR > 1 ? qa[NR - 1][2 * n + 1] : 0u, b0, b1);
                         }
-                    float fk[4 * SUB], fv[4 * SUB];  // scales of the lane's keys
+                    float fk[4 * SUB], ve[4 * SUB];  // scales of the lane's keys, and E of the values'
+                    const uint32_t size = smem_u32(smem) + Cfg::OFF_SCALE + (2 * s * kStage + kw * kKeys + 2 * q) * 4;
                     if (kEight) {
-                        const float *size = reinterpret_cast<const float *>(smem + Cfg::OFF_SCALE) + 2 * s * kStage + kw * kKeys + 2 * q;
 #pragma unroll
                         for (int t = 0; t < 2 * SUB; ++t) {
-                            const float2 x = *reinterpret_cast<const float2 *>(size + 8 * t);
-                            const float2 y = *reinterpret_cast<const float2 *>(size + kStage + 8 * t);
-                            fk[2 * t] = x.x; fk[2 * t + 1] = x.y; fv[2 * t] = y.x; fv[2 * t + 1] = y.y;
+                            const float2 x = lds_pair(size + 32 * t), y = lds_pair(size + 4 * kStage + 32 * t);
+                            fk[2 * t] = x.x; fk[2 * t + 1] = x.y;
+                            ve[2 * t] = exponent_of(exponent_bits(y.x)); ve[2 * t + 1] = exponent_of(exponent_bits(y.y));
                         }
                     }
                     float x[NR][4 * SUB], mx[NR];
@@ -378,31 +387,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                         const int last = (lim[i] < w.k1 - 1 ? lim[i] : w.k1 - 1) - kb - 2 * q;
 #pragma unroll
                         for (int e = 0; e < 4 * SUB; ++e) {
-                            const float f = kEight ? fs[i] * fk[e] : fs[i];
-                            x[i][e] = 8 * (e >> 1) + (e & 1) <= last ? sa[e >> 1][2 * i + (e & 1)] * f : -INFINITY;
+                            const float y = sa[e >> 1][2 * i + (e & 1)];
+                            x[i][e] = 8 * (e >> 1) + (e & 1) <= last ? (kEight ? fmaf(y, fs[i] * fk[e], ve[e]) : y * fs[i]) : -INFINITY;
                             mx[i] = fmaxf(mx[i], x[i][e]);
                         }
                         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
                         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
                         raise |= mx[i] > m[i];
                     }
-                    float vm = 0.f;
-                    if (kEight) {
-#pragma unroll
-                        for (int e = 0; e < 4 * SUB; ++e) vm = fmaxf(vm, fabsf(fv[e]));
-                        raise |= vm > vmax;
-                    }
                     if (__any_sync(0xffffffffu, raise)) {
-                        float fr = 1.f;
-                        if (kEight) {
-                            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-                            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-                            if (vm > vmax) {  // the next power of two
-                                const float up = __uint_as_float((__float_as_uint(fminf(vm, 0x1p+126f)) + 0x7fffffu) & 0xff800000u);
-                                fr = vmax / up;
-                                vmax = up;
-                            }
-                        }
 #pragma unroll
                         for (int i = 0; i < NR; ++i) {
                             const float nm = fmaxf(m[i], mx[i]);
@@ -410,7 +403,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                             m[i] = nm;
                             l[i] *= f;
                             // (the accumulator holds rows 2 q and 2 q + 1 of the eight)
-                            const float f0 = __shfl_sync(0xffffffffu, f, 8 * q) * fr, f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4) * fr;
+                            const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
 #pragma unroll
                             for (int e = 0; e < NE; ++e) {
                                 acc[i][e][0] *= f0;
@@ -422,10 +415,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                     }
                     // P, rounded (see above) for the product with V; its sum is taken before
                     uint32_t pa[2 * SUB][2];  // [key tile][row]
+                    float fv[4 * SUB], vinv[4 * SUB];  // f and 2^-E (the scales read again: registers are what is short)
                     if (kEight) {
-                        const float down = __uint_as_float((254u << 23) - __float_as_uint(vmax));  // 1 / vmax
 #pragma unroll
-                        for (int e = 0; e < 4 * SUB; ++e) fv[e] *= down;
+                        for (int t = 0; t < 2 * SUB; ++t) {
+                            const float2 y = lds_pair(size + 4 * kStage + 32 * t);
+                            vinv[2 * t] = exponent_inv(exponent_bits(y.x)); vinv[2 * t + 1] = exponent_inv(exponent_bits(y.y));
+                            fv[2 * t] = y.x * vinv[2 * t]; fv[2 * t + 1] = y.y * vinv[2 * t + 1];
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
@@ -434,7 +431,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
 #pragma unroll
                         for (int t = 0; t < 2 * SUB; ++t) {
                             float e0 = ex2f(x[i][2 * t] - ref), e1 = ex2f(x[i][2 * t + 1] - ref);
-                            sum[t / 2] = t % 2 ? sum[t / 2] + (e0 + e1) : e0 + e1;
+                            const float both = kEight ? fmaf(e0, vinv[2 * t], e1 * vinv[2 * t + 1]) : e0 + e1;
+                            sum[t / 2] = t % 2 ? sum[t / 2] + both : both;
                             if (kEight) {
                                 e0 *= fv[2 * t];
                                 e1 *= fv[2 * t + 1];
@@ -509,7 +507,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kEight, ROWS>::THREADS, DecodeCfg
                     float mm = sm_m[r];
 #pragma unroll
                     for (int k = 1; k < kKeyWarps; ++k) mm = fmaxf(mm, sm_m[k * ROWS + r]);
-                    const float f = mm == -INFINITY ? 0.f : ex2f(sm_m[kw * ROWS + r] - mm) * (kEight ? vmax : 1.f);
+                    const float f = mm == -INFINITY ? 0.f : ex2f(sm_m[kw * ROWS + r] - mm);
 #pragma unroll
                     for (int e = 0; e < NE; ++e) {
                         acc[i][e][c] *= f;

@@ -272,6 +272,15 @@ template <int kUnitCost> struct Walk {
     __host__ __device__ __forceinline__ bool ends() const { return k1 == all; }
 };
 
+// A value's scale is 2^E f, |f| in [1, 2): E + 127 as an exponent's bits, E, and 2^-E.  (E is held between -80 and 126, so that sums of
+// 2^-E stay in range; |f| is below 1 for smaller scales and up to 4 for larger ones.)
+__device__ __forceinline__ uint32_t exponent_bits(float scale)
+{
+    return min(max(__float_as_uint(scale) & 0x7f800000u, (127u - 80u) << 23), (127u + 126u) << 23);
+}
+__device__ __forceinline__ float exponent_of(uint32_t u) { return __uint_as_float(0x4b000000u | u >> 23) - (8388608.f + 127.f); }
+__device__ __forceinline__ float exponent_inv(uint32_t u) { return __uint_as_float((254u << 23) - u); }
+
 // Natural log of l 2^m (+inf where no key was seen).  The exponent of l joins m before the logarithm of its fraction
 // is added: m and it may be far apart and cancel.
 __device__ __forceinline__ float lse_of(float m, float l)

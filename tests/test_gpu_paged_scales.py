@@ -19,6 +19,7 @@ pytestmark = pytest.mark.gpu
 
 # new tokens, query heads: 8 and 16 rows of the mma.sync kernel, 128 and 256 of the tensor-core kernel
 FORMS = [(1, 4), (5, 4), (30, 4), (150, 4)]
+HEAVY = FORMS[:2]  # (the tensor-core kernel's values share an exponent for 64 keys)
 
 
 def _set(p, side, scales):
@@ -83,3 +84,82 @@ def test_scales_below_zero(dtype, d, new, h, signs):
         for side in range(2):
             want = p.contents(n)[side][-new:]
             assert np.all(np.abs(back[side][n, 0].double().cpu().numpy() - want[:, 0]) <= HALF[dtype] * np.abs(want[:, 0]) + 2.0 ** -25)
+
+
+def _light_key(p, n, key, head=0):
+    """Puts a cached key where every query's score is about -45: element 0 of the queries is 4, of the key the rest."""
+    import torch
+    slot = p.rows_of[n][key]
+    code, size = P.quantise(np.array([[-45.0 / (4 * p.scale)] + [0.0] * (p.d - 1)], np.float32))
+    p.pool[0].reshape(-1, p.hk, p.d)[slot, head] = torch.from_numpy(code[0])
+    p.scales[0].reshape(-1, p.hk)[slot, head] = float(size[0])
+    p.cpool[0].view(torch.uint8).copy_(p.pool[0])
+    p.cscales[0].copy_(p.scales[0])
+
+
+@pytest.mark.parametrize("dtype,up", [("bfloat16", 22), ("bfloat16", 40), ("float16", 20)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,h", HEAVY)
+@pytest.mark.parametrize("where", [3, 70, 200])
+def test_a_large_value_of_negligible_weight(dtype, up, d, new, h, where):
+    """One key of a weight of about 2^-65 whose value's scale is 2^20 to 2^40 above the rest: 2^-25 of them at most."""
+    p = Problem(dtype, "e4m3", [400], [new], h, 1, d, packed=False, seed=23)
+    p.q[..., 0] = 4
+    _light_key(p, 0, where)
+    x = _slot_scales(p, 1) * (2.0 ** -8 if dtype == "float16" else 1.0)  # (its value within the type's range)
+    x[p.rows_of[0][where]] = np.nanmedian(x) * 2.0 ** up
+    _set(p, 1, x)
+    o, lse = p.attend()
+    _check(p, o, lse)
+
+
+@pytest.mark.parametrize("dtype,up", [("bfloat16", 22), ("bfloat16", 60), ("float16", 20)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,h", [f for f in HEAVY if f[0] > 1])
+def test_a_large_value_that_earlier_tokens_do_not_see(dtype, up, d, new, h):
+    """The last token's value is 2^20 to 2^60 above the rest: the rows before it do not see it, and their outputs are
+    those of a cache without it."""
+    import torch
+    outs = []
+    for raised in (False, True):
+        p = Problem(dtype, "e4m3", [300, 128 + new], [new, new], h, 1, d, packed=False, seed=24)
+        x = _slot_scales(p, 1) * (2.0 ** -8 if dtype == "float16" else 1.0)
+        if raised:
+            for n in range(2):
+                x[p.rows_of[n][-1]] = np.nanmedian(x) * 2.0 ** up
+        _set(p, 1, x)
+        o, lse = p.attend()
+        _check(p, o, lse)
+        outs.append(o[:, :, :-1])
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,h", HEAVY)
+def test_dominant_keys_of_small_scales(d, new, h):
+    """Value scales from 2^-30 to 2^30, larger the lighter their key: weight times scale is about the same for all."""
+    p = Problem("bfloat16", "e4m3", [500], [new], h, 1, d, packed=False, seed=25)
+    p.q[:] = p.q[:1, :1]  # (one query for all rows, so that its weights are known)
+    k, _ = p.contents(0)
+    s = (k[:, 0] @ p.q[0, 0].double().numpy()) * p.scale
+    x = _slot_scales(p, 1)
+    x[p.rows_of[0], 0] = np.clip(np.exp(-(s - s.mean()) * 3), 2.0 ** -30, 2.0 ** 30)
+    p.causal, p.desc.mask = False, p.ab.ATTN_MASK_NONE
+    _set(p, 1, x)
+    o, lse = p.attend()
+    _check(p, o, lse)
+
+
+@pytest.mark.parametrize("new,h", HEAVY)
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -118, 2.0 ** -70, 2.0 ** 70])
+def test_scales_alike_and_far_from_one(new, h, scale):
+    """A sequence whose value scales are all zero or the least there is (rows of zeros), or all small or large."""
+    p = Problem("bfloat16", "e4m3", [700, 33], [min(new, 33)] * 2, h, 1, 128, packed=False, seed=26)
+    x = np.full_like(_slot_scales(p, 1), scale)
+    _set(p, 1, x)
+    o, lse = p.attend()
+    if scale in (0.0, 2.0 ** -118):  # (values below 2^-109: their outputs are what is left of them)
+        assert bool((o.abs() <= 2.0 ** -100).all())
+        o = o * 0
+        p.scales[1][~p.scales[1].isnan()] = 0
+    _check(p, o, lse)
