@@ -25,16 +25,19 @@
 // makes 16-bit numbers in the swizzled layout (a lane a row, so that neither side has bank
 // conflicts: 1512 -> 1445 us).  Keys unscaled, of the queries' type (e4m3 numbers are
 // 16-bit numbers exactly); their scales multiply S's columns.
-// Values as half-precision numbers, times their scale relative to the stage's largest, rounded up
-// to a power of two 2^E: number, factor and product in one multiplication a pair, each
-// rounded by at most half a step of that type.  2^E goes into the weights: P' = exp2(x + E - m)
-// with m over x + E, so that O and l keep one reference; l takes P' 2^-E.
+// Values as half-precision numbers times f, where their scale is 2^E f, |f| in [1, 2): number,
+// factor and product in one multiplication a pair, the latter two rounded by at most half a step of that
+// type.  2^E goes into the weight of its key: P' = exp2(x + E - m) with m over x + E, so that O and l keep one
+// reference, which is what the row's keys weigh with their scales; l takes P' 2^-E.  (One E for a stage, that of its
+// largest scale, needs two numbers less a key in the softmax and takes 1220 us for 1360, but lets a key of no weight,
+// or one that a row does not see, take the bits of the others.  One E where the scales are near one another, and each its
+// own elsewhere: 1410 and more, in one loop or two; the code of both is too much for the instruction cache.)
 // A page id out of range reads as zeros.
 //
 // Bound: 16 bits, the chain S -> softmax -> P -> O of a group, 2000 cycles for 64 keys and 256
 // rows against 1260 of MMAs (2048 tokens on 32768, 32 / 8 heads of 128: 905 us, 0.65 of the measured tensor
-// rate).  e4m3, 1225 us: the converting warps share the issue slots with the softmax and shared memory's
-// bandwidth with the MMAs.  Measured and dropped: 128 keys a step with one S a group, whose MMAs run at the full rate
+// rate).  e4m3, 1360 us: the converting warps share the issue slots with the softmax, whose chain has the scales
+// of 64 keys to read, and shared memory's bandwidth with the MMAs.  Measured and dropped: 128 keys a step with one S a group, whose MMAs run at the full rate
 // (M=128 N=64 from shared memory reads 128 rows of Q for 64 of K: two thirds), 876 and 1470 us; the same with two threads a
 // row, 865 and 1900; a warp that tells the MMA thread its steps, 913 and 1290.
 //
@@ -80,9 +83,8 @@ template <int D, bool kEight, bool kSplit> struct ChunkCfg {
     static constexpr int OFF_BAR = OFF_ES + NE * 2 * HN * 4;
     static constexpr int OFF_MISC = OFF_BAR + 80 * 8;
     static constexpr int OFF_ML = OFF_MISC + 64;              // [2 groups][m, l][128 rows] floats
-    static constexpr int OFF_KS = OFF_ML + 2 * 2 * 128 * 4;   // [NKS][64] floats
-    static constexpr int OFF_KE = OFF_KS + (kEight ? NKS * HN * 4 : 0);   // [NKS] E and 2^-E of the values
-    static constexpr int OFF_RANGE = OFF_KE + (kEight ? NKS * 8 : 0);     // scratch of the range, then the range
+    static constexpr int OFF_KS = OFF_ML + 2 * 2 * 128 * 4;   // [NKS][key scale, E, 2^-E][64] floats
+    static constexpr int OFF_RANGE = OFF_KS + (kEight ? NKS * 3 * HN * 4 : 0);  // scratch of the range, then the range
     static constexpr int SMEM = OFF_RANGE + 320;
     // at least half the SM's shared memory: one CTA, which holds all of the TMEM, runs per SM
     static constexpr int SMEM_ALLOC = SMEM + 1024 > 116 * 1024 ? SMEM + 1024 : 116 * 1024;
@@ -127,6 +129,14 @@ __device__ __forceinline__ void copy4(uint32_t dst, const float *src, bool on)
 __device__ __forceinline__ void copies_arrive(uint64_t *bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// (volatile: read where it is used, not held in registers)
+__device__ __forceinline__ float4 lds4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 
 // two e4m3 numbers as half-precision ones, and as numbers of type T
@@ -256,8 +266,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
     auto half_of = [](int j, int grp) { return kEight ? 0 : kSplit ? grp : j & 1; };
 
     // (e4m3: 512 threads are launched with 128 registers each; the warpgroups' shares add up to that.  The MMA thread's
-    // count: 2048 tokens on 32768 with 72 registers 1422 us, 96: 1287, 112: 1222, 128: 1310, when the softmax has too few)
-    constexpr uint32_t kRegsIssue = 112, kRegsSoftmax = 152, kRegsConvert = 96;
+    // count: 2048 tokens on 32768 with 112 registers, and 152 for the softmax, 1390 us, 120: 1381, 128: 1361)
+    constexpr uint32_t kRegsIssue = 128, kRegsSoftmax = 144, kRegsConvert = 96;
     static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert == 4 * 128, "register shares");
     if (warp < 4) {
         if (kEight) regs_decrease<kRegsIssue>();
@@ -457,8 +467,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         // (scores in log2 units are c times S; a scale below zero turns S's sign; c > 0, so that a masked -inf stays one)
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
         const uint32_t tO = tmem + lane_addr + Cfg::T_O + grp * D;
-        const float *scales = reinterpret_cast<const float *>(smem + Cfg::OFF_KS);
-        const float2 *sizes = reinterpret_cast<const float2 *>(smem + Cfg::OFF_KE);
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, nullptr);
@@ -491,9 +499,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 if (kEight) wait(&ks_full[stage % NKS], (stage / NKS) & 1);
                 wait(&s_full[grp * 2 + sb], s_par >> sb & 1);
                 s_par ^= 1u << sb;
-                // the row of S (e4m3: in log2 units), masked, and its maximum
+                // the row of S (e4m3: in log2 units, plus E), masked, and its maximum
                 float x[HN];
-                float mx = -INFINITY, vexp = 0.f, vinv = 1.f;  // e4m3: E and 2^-E
+                float mx = -INFINITY;
+                const uint32_t scales = smem_u32(smem) + Cfg::OFF_KS + stage % NKS * (3 * HN * 4);
                 if (ok) {
                     uint32_t v[2][32];
                     tmem_ld32(tS, v[0]);
@@ -503,15 +512,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 #pragma unroll
                     for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e / 32][e % 32]);
                     if (kEight) {
-                        const float2 size = sizes[stage % NKS];
-                        vexp = size.x;
-                        vinv = size.y;
-                        const float4 *f = reinterpret_cast<const float4 *>(scales + (stage % NKS) * HN);
 #pragma unroll
                         for (int e = 0; e < HN; e += 4) {
-                            const float4 q = f[e / 4];
-                            const float2 y0 = mul2(make_float2(x[e], x[e + 1]), make_float2(q.x, q.y));
-                            const float2 y1 = mul2(make_float2(x[e + 2], x[e + 3]), make_float2(q.z, q.w));
+                            const float4 q = lds4(scales + e * 4), ve = lds4(scales + (HN + e) * 4);
+                            const float2 y0 = fma2(make_float2(x[e], x[e + 1]), make_float2(q.x, q.y), make_float2(ve.x, ve.y));
+                            const float2 y1 = fma2(make_float2(x[e + 2], x[e + 3]), make_float2(q.z, q.w), make_float2(ve.z, ve.w));
                             x[e] = y0.x; x[e + 1] = y0.y; x[e + 2] = y1.x; x[e + 3] = y1.y;
                         }
                     } else if (a.scale < 0.f) {
@@ -528,7 +533,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mq[k] = max3(mq[k], x[e + 2 * k], x[e + 2 * k + 1]);
                     mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
-                    mx = kEight ? mx + vexp : mx * c;
+                    if (!kEight) mx *= c;
                 }
                 const float m_new = fmaxf(m_ref, mx);
                 const bool need = m_new > m_ref + 8.f;  // also the first finite max
@@ -564,8 +569,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                 // P = exp2(x - m) over the columns S was read from
                 if (ok) {
                     const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // no visible key yet: every P is 0
-                    const float2 neg2 = kEight ? make_float2(neg + vexp, neg + vexp) : make_float2(neg, neg), c2 = make_float2(c, c);
+                    const float2 neg2 = make_float2(neg, neg), c2 = make_float2(c, c);
                     float2 l2 = make_float2(0.f, 0.f);
+                    float4 inv = make_float4(1.f, 1.f, 1.f, 1.f);  // e4m3: 2^-E of four keys
 #pragma unroll
                     for (int e0 = 0; e0 < HN; e0 += 16) {
                         uint32_t y[8];
@@ -574,14 +580,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
                             const float2 z = make_float2(x[e0 + e], x[e0 + e + 1]);
                             const float2 t = kEight ? add2(z, neg2) : fma2(z, c2, neg2);
                             const float2 q = make_float2(ex2(t.x), ex2(t.y));
-                            l2 = add2(l2, q);
+                            if (kEight) {
+                                if (e % 4 == 0) inv = lds4(scales + (2 * HN + e0 + e) * 4);
+                                l2 = fma2(q, e % 4 ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y), l2);
+                            } else {
+                                l2 = add2(l2, q);
+                            }
                             y[e / 2] = pack2<P16>(q.x, q.y);
                         }
                         tmem_st8(tS + e0 / 2, y);
                     }
                     // a step's sum is added with what earlier additions lost: thousands of weights far below the largest
                     // would each be rounded away
-                    const float add = (l2.x + l2.y) * vinv - l_lost, sum = l + add;
+                    const float add = l2.x + l2.y - l_lost, sum = l + add;
                     l_lost = sum - l - add;
                     l = sum;
                     tmem_st_wait();
@@ -692,7 +703,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
         const int wt = threadIdx.x - 384, k = wt & 63, col = wt >> 6;
         const float c = a.scale * kLog2e;
         float *scales = reinterpret_cast<float *>(smem + Cfg::OFF_KS);
-        float2 *sizes = reinterpret_cast<float2 *>(smem + Cfg::OFF_KE);
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok && !(ok = mbar_wait(bar, parity, abort))) flag_abort(abort, nullptr);
@@ -704,18 +714,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, kEight, kSplit>::THREADS, 1) paged
             const Steps st = steps_of(w);
             for (int j = 0; j < st.stages; ++j, ++n) {
                 const int left = w.k1 - (w.k0 + j * HN);  // rows behind: zeros
-                // the values' scales, relative to the power of two at or above the largest
                 wait(&e_full[es], epar);
                 wait(&e_full[NE + es], epar);
                 const float *size = reinterpret_cast<const float *>(smem + Cfg::OFF_ES) + 2 * es * HN;
-                const float most = fmaxf(fabsf(size[HN + lane]), fabsf(size[HN + 32 + lane]));
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(fmaxf(most, 0x1p-100f), 0x1p+100f)));
-                const uint32_t e = (top + 0x7fffffu) >> 23;  // exponent, of bias 127
-                const float down = __uint_as_float((254u - e) << 23);
-                const uint32_t factor = pack2<__half>(size[HN + k] * down, size[HN + k] * down);
-                if (wt < HN) {
-                    scales[n % NKS * HN + wt] = size[wt] * c;
-                    if (wt == 0) sizes[n % NKS] = make_float2(float(int(e) - 127), down);
+                const uint32_t eb = exponent_bits(size[HN + k]);
+                const float f = size[HN + k] * exponent_inv(eb);
+                const uint32_t factor = pack2<__half>(f, f);
+                float *to = scales + n % NKS * 3 * HN + k;
+                if (col == 0) {
+                    *to = size[k] * c;
+                } else {
+                    to[HN] = exponent_of(eb);
+                    to[2 * HN] = exponent_inv(eb);
                 }
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {

@@ -19,7 +19,6 @@ pytestmark = pytest.mark.gpu
 
 # new tokens, query heads: 8 and 16 rows of the mma.sync kernel, 128 and 256 of the tensor-core kernel
 FORMS = [(1, 4), (5, 4), (30, 4), (150, 4)]
-HEAVY = FORMS[:2]  # (the tensor-core kernel's values share an exponent for 64 keys)
 
 
 def _set(p, side, scales):
@@ -99,7 +98,7 @@ def _light_key(p, n, key, head=0):
 
 @pytest.mark.parametrize("dtype,up", [("bfloat16", 22), ("bfloat16", 40), ("float16", 20)])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("new,h", HEAVY)
+@pytest.mark.parametrize("new,h", FORMS)
 @pytest.mark.parametrize("where", [3, 70, 200])
 def test_a_large_value_of_negligible_weight(dtype, up, d, new, h, where):
     """One key of a weight of about 2^-65 whose value's scale is 2^20 to 2^40 above the rest: 2^-25 of them at most."""
@@ -115,7 +114,7 @@ def test_a_large_value_of_negligible_weight(dtype, up, d, new, h, where):
 
 @pytest.mark.parametrize("dtype,up", [("bfloat16", 22), ("bfloat16", 60), ("float16", 20)])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("new,h", [f for f in HEAVY if f[0] > 1])
+@pytest.mark.parametrize("new,h", [f for f in FORMS if f[0] > 1])
 def test_a_large_value_that_earlier_tokens_do_not_see(dtype, up, d, new, h):
     """The last token's value is 2^20 to 2^60 above the rest: the rows before it do not see it, and their outputs are
     those of a cache without it."""
@@ -135,7 +134,7 @@ def test_a_large_value_that_earlier_tokens_do_not_see(dtype, up, d, new, h):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("new,h", HEAVY)
+@pytest.mark.parametrize("new,h", FORMS)
 def test_dominant_keys_of_small_scales(d, new, h):
     """Value scales from 2^-30 to 2^30, larger the lighter their key: weight times scale is about the same for all."""
     p = Problem("bfloat16", "e4m3", [500], [new], h, 1, d, packed=False, seed=25)
@@ -150,7 +149,7 @@ def test_dominant_keys_of_small_scales(d, new, h):
     _check(p, o, lse)
 
 
-@pytest.mark.parametrize("new,h", HEAVY)
+@pytest.mark.parametrize("new,h", FORMS)
 @pytest.mark.parametrize("scale", [0.0, 2.0 ** -118, 2.0 ** -70, 2.0 ** 70])
 def test_scales_alike_and_far_from_one(new, h, scale):
     """A sequence whose value scales are all zero or the least there is (rows of zeros), or all small or large."""
