@@ -1008,9 +1008,9 @@ attn_status_t check_paged_call(const attn_sdpa_desc_t *d, const attn_paged_cache
     if ((reinterpret_cast<uintptr_t>(s->page_table) | reinterpret_cast<uintptr_t>(s->lens) |
          reinterpret_cast<uintptr_t>(s->cu_new)) & 3)
         return ATTN_ERR_ALIGN;
-    const int64_t tokens = s->cu_new ? s->tokens : d->b * d->s_q, lim = int64_t(1) << 31;
-    // 32-bit row indices inside the kernels
-    if (tokens >= lim || tokens * (d->h > 2 * d->h_kv ? d->h : 2 * d->h_kv) >= lim) return ATTN_ERR_UNSUPPORTED;
+    // 32-bit row indices inside the kernels, which round them up to a block's rows and the number of blocks
+    const int64_t tokens = s->cu_new ? s->tokens : d->b * d->s_q, lim = (int64_t(1) << 31) - 4096;
+    if (tokens > lim || tokens * (d->h > 2 * d->h_kv ? d->h : 2 * d->h_kv) > lim) return ATTN_ERR_UNSUPPORTED;
     out->table = s->page_table;
     out->table_stride = s->table_stride;
     out->lens = s->lens;

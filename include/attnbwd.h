@@ -419,6 +419,7 @@ typedef struct {
  * NULL): s_kv = the most tokens a sequence may have cached (up to 2^30), s_q = the new
  * tokens of every sequence or, with cu_new, the most that a sequence is expected to
  * have (a longer one is computed all the same: it chooses the kernel); h / h_kv <= 128;
+ * the new tokens times h, and times 2 h_kv, at most 2^31 - 4096;
  * mask ATTN_MASK_NONE (a new token sees all of its sequence) or
  * ATTN_CAUSAL_BOTTOM_RIGHT (up to its own position); deterministic is ignored: the
  * results are always bitwise reproducible.
