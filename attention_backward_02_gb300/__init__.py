@@ -527,7 +527,8 @@ def paged_cache_write(desc, cache, page_table, lens, k, v, *, cu_new=None, works
     lens [B] (int32 CUDA) cached tokens they are counted in, page_table [B, pages] (int32 CUDA) naming its pages
     in order.  desc: an sdpa_desc with s_kv = the most tokens a sequence may have cached, s_q = the new tokens
     of each.  k, v: [B, h_kv, S_q, D] tensors or views; with cu_new (int32 CUDA [B + 1], first rows) packed
-    [T, h_kv, D] tensors.  float8 pages: each row rounded to e4m3 with a scale of its own.  Returns the
+    [T, h_kv, D] tensors.  float8 pages: each row rounded to e4m3 with a scale of its own (expanded scales, of
+    stride 0, can be read through but not written: AttnError).  Returns the
     workspace, for attn_query_status (lengths, counts or page ids out of range)."""
     return _paged_copy("paged_cache_write", _lib.load().paged_cache_write, desc, cache, page_table, lens, k, v, cu_new,
                        workspace, stream)

@@ -1020,6 +1020,16 @@ attn_status_t check_paged_call(const attn_sdpa_desc_t *d, const attn_paged_cache
     return ATTN_OK;
 }
 
+// A cache to be written has a place for every row and every scale: no stride of 0, which a cache that is read may have (one
+// scale for all rows), along what it has several of.
+bool own_places(const attn_sdpa_desc_t *d, const attn_paged_cache_t *c)
+{
+    auto apart = [&](int64_t sp, int64_t ss, int64_t sh) {
+        return (c->n_pages < 2 || sp > 0) && (c->page_size < 2 || ss > 0) && (d->h_kv < 2 || sh > 0);
+    };
+    return apart(c->sp, c->ss, c->sh) && (c->type != ATTN_E4M3 || apart(c->scale_sp, c->scale_ss, c->scale_sh));
+}
+
 constexpr size_t kPagedCopyBytes = 256;
 
 attn_status_t paged_copy_call(bool write, const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
@@ -1030,6 +1040,7 @@ attn_status_t paged_copy_call(bool write, const attn_sdpa_desc_t *desc, const at
     std::memset(&a, 0, sizeof a);
     attn_status_t st = check_paged(desc, cache, &a.cache);
     if (st || (st = check_paged_call(desc, cache, seqs, &a.seqs))) return st;
+    if (write && !own_places(desc, cache)) return ATTN_ERR_INVALID;
     if ((st = check_view(k, a.seqs.tokens)) || (st = check_view(v, a.seqs.tokens))) return st;
     if ((st = check_ws(workspace, workspace_bytes, kPagedCopyBytes))) return st;
     a.dtype = desc->dtype;

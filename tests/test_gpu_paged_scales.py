@@ -162,3 +162,25 @@ def test_scales_alike_and_far_from_one(new, h, scale):
         o = o * 0
         p.scales[1][~p.scales[1].isnan()] = 0
     _check(p, o, lse)
+
+
+@pytest.mark.parametrize("new,h", FORMS)
+def test_one_scale_for_all_rows(new, h):
+    """Scales of stride 0, as expand makes them, are read through: the bits of the same calls on copies.  A write is refused."""
+    import torch
+    outs = []
+    for copies in (False, True):
+        p = Problem("bfloat16", "e4m3", [300, 170], [new, new], h, 1, 128, packed=False, seed=27)
+        size = [torch.full((1, 1, 1), x, device="cuda").expand(p.cscales[0].shape) for x in (0.011, 0.0075)]
+        if copies:
+            size = [t.contiguous() for t in size]
+        cache = p.ab.paged_cache(*p.cpool, k_scale=size[0], v_scale=size[1])
+        p.cache = cache
+        o, lse = p.attend()
+        back = [torch.empty(2, 1, new, 128, dtype=p.dt, device="cuda") for _ in range(2)]
+        p.ab.paged_cache_read(p.desc, cache, p.dtable, p.dlens, *back)
+        outs.append([o, lse, *back])
+        if not copies:
+            with pytest.raises(p.ab.AttnError):
+                p.ab.paged_cache_write(p.desc, cache, p.dtable, p.dlens, *back)
+    assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*outs))
