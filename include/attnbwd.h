@@ -400,8 +400,9 @@ typedef struct {
  * lens[n] - m + i, and position x lies in page page_table[n*table_stride + x /
  * page_size].  The new tokens' rows: cu_new NULL: s_q of each sequence, in [b,h,s_q,d]
  * views.  Else packed views, token row t at t*ss: rows cu_new[n] .. cu_new[n+1] - 1,
- * of `tokens` in all; rows that belong to no sequence are neither read nor
- * written.  A new token at a position below 0 (a sequence with more new tokens than
+ * of `tokens` in all; rows that belong to no sequence are not written, and what they
+ * hold changes no result, but all `tokens` rows of a view that a call reads have to be
+ * memory that it may read (it may load them and not use them).  A new token at a position below 0 (a sequence with more new tokens than
  * cached ones, padded in front) is not written to the cache, is read back as zeros
  * and sees no key.  Table entries of pages that hold no needed position are not
  * read.  Lengths outside [0, s_kv] and counts out of order or range are brought
