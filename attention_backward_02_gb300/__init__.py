@@ -426,7 +426,7 @@ def sdpa_relbias_decode(desc, bias, q, k, v, lens, o, *, workspace=None, stream=
 def paged_cache(k, v, *, k_scale=None, v_scale=None):
     """An attn_paged_cache_t: a key / value cache in pages.  k, v: [n_pages, page_size, h_kv, d] of the calls' dtype
     or float8_e4m3fn, any strides with a unit innermost one, alike in both (a cache stored by heads is passed
-    transposed); float8: k_scale, v_scale fp32 [n_pages, page_size, h_kv], strides alike in both.  The tensors
+    transposed); float8: k_scale, v_scale fp32 [n_pages, page_size, h_kv] of either sign, strides alike in both.  The tensors
     are held by the result, and read anew by every call."""
     cache = attn_paged_cache_t()
     cache.tensors, cache.as_read = (k, v, k_scale, v_scale), None

@@ -1056,8 +1056,8 @@ struct PagedLayout {
 
 // The kernel a call takes, by its rows (new tokens x query heads of a kv head): the tensor-core one from 17 on, or from 49
 // over an e4m3 cache, whose conversion takes it longer than the other takes to read the keys once for every 16 rows.
-// (us, 16 sequences of 500 to 6000 tokens, 32 / 8 heads of 128, mma.sync / tcgen05: 16 bits, 16 rows 54 / 63, 24 rows 77 / 65;
-// e4m3, 16 rows 46 / 102, 48 rows 87 / 104, 64 rows 108 / 104.)
+// (us, cold L2, 16 sequences of 500 to 6000 tokens, 32 / 8 heads of 128, mma.sync / tcgen05: 16 bits, 16 rows 60 / 80, 24 rows
+// 82 / 82, 48 rows 110 / 83; e4m3, 16 rows 46 / 109, 48 rows 89 / 112, 64 rows 108 / 109.)
 PagedShape paged_shape(const attn_sdpa_desc_t *d, bool eight)
 {
     if (d->s_q * (d->h / d->h_kv) > (eight ? 48 : 16)) return paged_chunk_shape(d->h, d->h_kv, d->s_q);

@@ -37,9 +37,10 @@
 // Bound: 16 bits, the chain S -> softmax -> P -> O of a group, 2000 cycles for 64 keys and 256
 // rows against 1260 of MMAs (2048 tokens on 32768, 32 / 8 heads of 128: 905 us, 0.65 of the measured tensor
 // rate).  e4m3, 1360 us: the converting warps share the issue slots with the softmax, whose chain has the scales
-// of 64 keys to read, and shared memory's bandwidth with the MMAs.  Measured and dropped: 128 keys a step with one S a group, whose MMAs run at the full rate
-// (M=128 N=64 from shared memory reads 128 rows of Q for 64 of K: two thirds), 876 and 1470 us; the same with two threads a
-// row, 865 and 1900; a warp that tells the MMA thread its steps, 913 and 1290.
+// of 64 keys to read, and shared memory's bandwidth with the MMAs.  Measured and not taken (16 bits, and e4m3 where that had
+// one E a stage and 1225 us): 128 keys a step with one S a group, whose MMAs run at the full rate (M=128 N=64 from shared
+// memory reads 128 rows of Q for 64 of K: two thirds), 876 and 1470 us; the same with two threads a row, 865 and 1900; a
+// warp that tells the MMA thread its steps, 913 and 1290.
 //
 // A row's reference maximum m is raised only when a step's maximum exceeds it by more
 // than 8 (log2 units), and then l and the row of O in TMEM are scaled by exp2(m_old - m_new):

@@ -23,9 +23,9 @@
 // pieces of four rows: neither has bank conflicts (values of 64 e4m3 numbers have two-way
 // ones).  CTAs that start together take the same keys of neighbouring heads (Lanes): a head's
 // 128 bytes of e4m3 numbers alone came at 0.66 of the measured copy rate even with the
-// arithmetic left out, side by side at 0.78 with it.  32 sequences of 1 to 8192 keys, 32 / 8
-// heads of 128: 95 us for 537 MB, 0.83 of that rate (all of 8192: 171, 0.92), e4m3 65 us for
-// 277 MB, 0.63 (105, 0.78): beside the reading stand the start (a share's range, first loads),
+// arithmetic left out, side by side at 0.81 with it.  32 sequences of 1 to 8192 keys, 32 / 8
+// heads of 128: 95 us for 537 MB, 0.83 of that rate (all of 8192: 166, 0.95), e4m3 62 us for
+// 277 MB, 0.66 (101, 0.81): beside the reading stand the start (a share's range, first loads),
 // units that end early and the join.
 //
 // e4m3: a number is a half-precision number exactly, one conversion a pair, so both products

@@ -452,8 +452,9 @@ attn_status_t paged_cache_read(const attn_sdpa_desc_t *desc, const attn_paged_ca
  * to 16 bits for their product with the values: to dtype, or over ATTN_E4M3 to half
  * precision, times their value's scale, relative to the largest such product that the
  * row sees (below 2^-25 of it, or of the largest weight of an ATTN_F16 cache, they
- * vanish).  Value scales may be of either sign and far apart; of those below 2^-80 bits
- * are lost.                                                                  */
+ * vanish).  Value scales may be of either sign, and a key's scale matters as far as its
+ * weight does; weights are lost beside a key of a scale 2^100 larger, and bits of
+ * scales below 2^-80.                                                        */
 attn_status_t sdpa_paged_workspace_size(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache, size_t *bytes);
 attn_status_t sdpa_paged_fwd(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache,
                              const attn_paged_seqs_t *seqs, attn_view_t q, attn_view_t o, float *lse, void *workspace,
