@@ -431,8 +431,8 @@ typedef struct {
  * in fp32, codes rounded to nearest even, the maximum over the finite elements (an
  * infinity becomes the largest code of its sign, a NaN stays one): the row stands for
  * code * scale.  No two of the call's tokens may have one place, nor two pages, tokens
- * or heads of the cache (a stride of 0 is refused here; the other calls read
- * through it).
+ * or heads of the cache, nor a key and a value (a stride of 0 is refused here; the
+ * other calls read through it).
  * paged_cache_read: the same rows from the cache, code * scale rounded to dtype.
  * Workspace of both: paged_cache_workspace_size bytes.                       */
 attn_status_t paged_cache_workspace_size(const attn_sdpa_desc_t *desc, const attn_paged_cache_t *cache, size_t *bytes);

@@ -184,3 +184,33 @@ def test_one_scale_for_all_rows(new, h):
             with pytest.raises(p.ab.AttnError):
                 p.ab.paged_cache_write(p.desc, cache, p.dtable, p.dlens, *back)
     assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,h", [(1, 4), (5, 4), (30, 4), (70, 4)])
+def test_scales_far_apart_over_many_pieces(d, new, h):
+    """A long sequence, whose pieces several blocks hold and join: one key in a hundred has a value scale up to 2^30 above or
+    below the others, of either sign, one in a hundred has a scale of zero."""
+    p = Problem("bfloat16", "e4m3", [9000, 77], [new, new], h, 1, d, packed=False, page=64, seed=28)
+    rng = np.random.default_rng(29)
+    x = _slot_scales(p, 1)
+    at = rng.random(x.shape)
+    x = np.where(at < 0.01, x * 2.0 ** rng.integers(-30, 31, x.shape) * rng.choice([-1.0, 1.0], x.shape), x)
+    x = np.where(at > 0.99, 0.0 * x, x)
+    _set(p, 1, x)
+    o, lse = p.attend()
+    _check(p, o, lse)
+
+
+@pytest.mark.parametrize("new,h", FORMS)
+def test_a_bad_page_of_an_e4m3_cache_reads_as_zeros(new, h):
+    """Its keys have the score 0 and its values are zeros, and the call says so."""
+    p = Problem("bfloat16", "e4m3", [400, 300], [new, new], h, 1, 128, packed=False, seed=30)
+    for n, i in ((0, 2), (1, 0)):
+        p.dtable[n, i] = -3
+        slots = p.rows_of[n][16 * i:16 * i + 16]
+        for side in range(2):
+            p.pool[side].reshape(-1, 1, 128)[slots] = 0
+            p.scales[side].reshape(-1, 1)[slots] = 0
+    o, lse = p.attend(flags=2)
+    _check(p, o, lse)
